@@ -28,7 +28,9 @@ __all__ = ["gdn_gating", "gdn_chunk_fwd", "gdn_recurrent_decode", "chunk_fwd_wor
            "gdn_recurrent_decode_mtp", "gdn_chunk_bwd", "chunk_bwd_workspace_size",
            "gdn_chunk_fwd_gated", "chunk_gated_delta_rule", "GDNError", "lib_path", "load_library", "status_string", "DEV_BAD_CU_SEQLENS",
            "DEV_BAD_SLOT", "DEV_WAIT_TIMEOUT", "DEV_DRAIN_TIMEOUT", "EXPORTED_SYMBOLS",
-           "testing_force_wait_expiry"]
+           "testing_force_wait_expiry", "DEV_NO_PAGE", "DEV_BAD_SEQ_LEN",
+           "gdn_norm_gate", "gdn_norm_gate_bwd", "norm_gate", "gdn_rope", "rotary_embedding", "rope_frequencies",
+           "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention", "kv8_attention_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libgdn.so")
@@ -37,6 +39,7 @@ _lock = threading.Lock()
 
 GDN_OK, GDN_EINVAL, GDN_EUNSUPPORTED, GDN_ECUDA, GDN_EWORKSPACE, GDN_ESCRATCH_LIMIT = 0, 1, 2, 3, 4, 5
 DEV_BAD_CU_SEQLENS, DEV_BAD_SLOT, DEV_WAIT_TIMEOUT, DEV_DRAIN_TIMEOUT = 1, 2, 4, 8
+DEV_NO_PAGE, DEV_BAD_SEQ_LEN = 16, 32
 
 #: Every symbol include/gdn.h declares (checked by the tests).
 EXPORTED_SYMBOLS = ("gdn_status_string", "gdn_version", "gdn_gating", "gdn_chunk_fwd_workspace_size",
@@ -45,7 +48,9 @@ EXPORTED_SYMBOLS = ("gdn_status_string", "gdn_version", "gdn_gating", "gdn_chunk
                     "gdn_causal_conv1d_fwd", "gdn_causal_conv1d_update", "gdn_conv_decode_pack",
                     "gdn_recurrent_decode_bf16", "gdn_recurrent_decode_mtp", "gdn_chunk_bwd_workspace_size",
                     "gdn_chunk_bwd", "gdn_chunk_fwd_gated", "gdn_testing_force_wait_expiry",
-                    "gdn_causal_conv1d_update_spec")
+                    "gdn_causal_conv1d_update_spec",
+                    "gdn_norm_gate", "gdn_norm_gate_bwd_workspace_size", "gdn_norm_gate_bwd", "gdn_rope",
+                    "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention_workspace_size", "gdn_kv8_attention")
 
 #: Size of the fixed scratch buffer behind gdn_chunk_fwd_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -64,6 +69,8 @@ def lib_path() -> str:
 def load_library():
     """Load libgdn.so (built by ``build.py``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -113,6 +120,22 @@ def load_library():
         lib.gdn_chunk_bwd.argtypes = [P, P, P, P, P, F, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P, P, P, P,
                                       P, SZ, P, P]
         lib.gdn_chunk_bwd.restype = I
+        lib.gdn_norm_gate.argtypes = [P, P, P, P, F, F, I, I64, I, I64, I64, P, P, P]
+        lib.gdn_norm_gate.restype = I
+        lib.gdn_norm_gate_bwd_workspace_size.argtypes = [I64, I]
+        lib.gdn_norm_gate_bwd_workspace_size.restype = SZ
+        lib.gdn_norm_gate_bwd.argtypes = [P, P, P, P, P, F, F, I, I64, I, I64, I64, P, P, P, P, P, SZ, P]
+        lib.gdn_norm_gate_bwd.restype = I
+        lib.gdn_rope.argtypes = [P, P, P, P, I64, I, I, I, I, I, I, F, I64, I64, P, P, P]
+        lib.gdn_rope.restype = I
+        lib.gdn_paged_plan.argtypes = [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P]
+        lib.gdn_paged_plan.restype = I
+        lib.gdn_kv8_append.argtypes = [P, P, I64, I64, P, P, P, P, P, I64, I, I, I, I, P, P]
+        lib.gdn_kv8_append.restype = I
+        lib.gdn_kv8_attention_workspace_size.argtypes = [I, I, I, I, I, I, I]
+        lib.gdn_kv8_attention_workspace_size.restype = SZ
+        lib.gdn_kv8_attention.argtypes = [P, I64, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P, P]
+        lib.gdn_kv8_attention.restype = I
         _lib = lib
         return lib
 
@@ -681,3 +704,8 @@ def chunk_gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     if isinstance(out, tuple):
         return out
     return out, None
+
+
+# Norms, rotary positions and the paged 8-bit cache (after the helpers above, which they use).
+from .stack import (gdn_kv8_append, gdn_kv8_attention, gdn_norm_gate, gdn_norm_gate_bwd, gdn_paged_plan,  # noqa: E402
+                    gdn_rope, kv8_attention_workspace_size, norm_gate, rope_frequencies, rotary_embedding)

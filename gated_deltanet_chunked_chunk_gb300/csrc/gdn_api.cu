@@ -282,4 +282,112 @@ int gdn_recurrent_decode_mtp(const uint16_t *q, const uint16_t *k, const uint16_
   return cuda_status(gdn_host::launch_decode_general(d, static_cast<cudaStream_t>(stream)));
 }
 
+int gdn_norm_gate(const uint16_t *x, const uint16_t *residual, const uint16_t *z, const float *weight, float res_scale,
+                  float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride, uint16_t *y,
+                  uint16_t *h, void *stream) {
+  if (rows < 0 || D <= 0 || activation < 0 || activation > 2 || !(eps >= 0.f)) return GDN_EINVAL;
+  if ((activation != 0) != (z != nullptr) || (residual != nullptr) != (h != nullptr)) return GDN_EINVAL;
+  if (z && z_rows < 0) return GDN_EINVAL;
+  if (rows == 0) return GDN_OK;
+  if (!x || !weight || !y) return GDN_EINVAL;
+  if (z_rows == 0) { z_rows = rows; z_stride = 0; }
+  return cuda_status(gdn_host::launch_norm_fwd(x, residual, z, weight, res_scale, eps, activation, rows, D, z_rows, z_stride,
+                                               y, h, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_norm_gate_bwd_workspace_size(int64_t rows, int D) {
+  return rows < 0 || D <= 0 ? 0 : gdn_host::norm_bwd_workspace_bytes(rows, D);
+}
+
+int gdn_norm_gate_bwd(const uint16_t *dy, const uint16_t *h, const uint16_t *z, const uint16_t *dh, const float *weight,
+                      float res_scale, float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride,
+                      uint16_t *dx, uint16_t *dresidual, uint16_t *dz, float *dweight, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+  if (rows < 0 || D <= 0 || activation < 0 || activation > 2 || !(eps >= 0.f)) return GDN_EINVAL;
+  if ((activation != 0) != (dz != nullptr) || (dh != nullptr) != (dresidual != nullptr) || !dweight) return GDN_EINVAL;
+  if (z && z_rows < 0) return GDN_EINVAL;
+  if (rows > 0 && ((activation != 0) != (z != nullptr) || !dy || !h || !weight || !dx)) return GDN_EINVAL;
+  const size_t need = gdn_host::norm_bwd_workspace_bytes(rows, D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
+  if (!aligned16({workspace})) return GDN_EINVAL;
+  if (z_rows == 0) { z_rows = rows > 0 ? rows : 1; z_stride = 0; }
+  return cuda_status(gdn_host::launch_norm_bwd(dy, h, z, dh, weight, res_scale, eps, activation, rows, D, z_rows, z_stride,
+                                               dx, dresidual, dz, dweight, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_rope(const uint16_t *q, const uint16_t *k, const int32_t *positions, const float *inv_freq, int64_t T, int HQ,
+             int HK, int D, int rotary_dim, int interleaved, int inverse, float attention_factor, int64_t ldq,
+             int64_t ldk, uint16_t *q_out, uint16_t *k_out, void *stream) {
+  if (T < 0 || HQ <= 0 || HK < 0 || D <= 0 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > D) return GDN_EINVAL;
+  if (ldq < (int64_t)HQ * D || (HK > 0 && ldk < (int64_t)HK * D)) return GDN_EINVAL;
+  if (rotary_dim > 8192) return GDN_EUNSUPPORTED;
+  if (T == 0) return GDN_OK;
+  if (!q || !q_out || !positions || !inv_freq || (HK > 0 && (!k || !k_out))) return GDN_EINVAL;
+  // in place only where input and output have the same layout
+  if ((q == q_out && ldq != (int64_t)HQ * D) || (HK > 0 && k == k_out && ldk != (int64_t)HK * D)) return GDN_EINVAL;
+  if (HK == 0) { k = nullptr; k_out = nullptr; ldk = 0; }
+  return cuda_status(gdn_host::launch_rope(q, k, positions, inv_freq, T, HQ, HK, D, rotary_dim, interleaved ? 1 : 0,
+                                           inverse ? 1 : 0, attention_factor, ldq, ldk, q_out, k_out,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_paged_plan(const int32_t *cached_lens, const int32_t *cu_seqlens, int N, int T, int32_t *block_table, int width,
+                   const int32_t *free_pages, int F, const int32_t *num_free, int page_size, int32_t *seq_lens,
+                   int32_t *slot_mapping, int32_t *positions, int32_t *num_free_out, int32_t *dev_status, void *stream) {
+  if (N < 0 || T < 0 || width < 0 || F < 0 || page_size <= 0) return GDN_EINVAL;
+  if (!num_free || !num_free_out || num_free == num_free_out || (F > 0 && !free_pages)) return GDN_EINVAL;
+  if (N > 0 && (!cached_lens || !cu_seqlens || !seq_lens || (width > 0 && !block_table))) return GDN_EINVAL;
+  if (T > 0 && (!slot_mapping || !positions)) return GDN_EINVAL;
+  return cuda_status(gdn_host::launch_paged_plan(cached_lens, cu_seqlens, N, T, block_table, width, free_pages, F, num_free,
+                                                 page_size, seq_lens, slot_mapping, positions, num_free_out, dev_status,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ldv, uint8_t *k_cache, uint8_t *v_cache,
+                   float *k_scale, float *v_scale, const int32_t *slot_mapping, int64_t T, int P, int HK, int D,
+                   int page_size, int32_t *dev_status, void *stream) {
+  if (T < 0 || P <= 0 || HK <= 0 || D <= 0 || page_size <= 0) return GDN_EINVAL;
+  if (ldk < (int64_t)HK * D || ldv < (int64_t)HK * D || (int64_t)P * page_size > 2147483647LL) return GDN_EINVAL;
+  if (T == 0) return GDN_OK;
+  if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !slot_mapping) return GDN_EINVAL;
+  return cuda_status(gdn_host::launch_kv8_append(k, v, ldk, ldv, k_cache, v_cache, k_scale, v_scale, slot_mapping, T, P, HK,
+                                                 D, page_size, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int max_q_len, int max_seq_len) {
+  if (N <= 0 || T <= 0 || HK <= 0 || HQ <= 0 || HQ % HK || !head_dim_ok(D) || max_q_len <= 0 || max_seq_len < 0) return 0;
+  return gdn_host::kv8_attn_workspace_bytes(N, HK, HQ / HK, D, max_q_len < T ? max_q_len : T, max_seq_len);
+}
+
+int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, const uint8_t *v_cache,
+                      const float *k_scale, const float *v_scale, const int32_t *block_table, int width,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, int N, int T, int P, int HQ, int HK, int D,
+                      int page_size, int max_q_len, int max_seq_len, float scale, uint16_t *o, float *lse,
+                      void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  if (N < 0 || T < 0 || P < 0 || HQ <= 0 || HK <= 0 || D <= 0 || HQ % HK || width < 0 || page_size <= 0) return GDN_EINVAL;
+  if (max_q_len < 0 || max_seq_len < 0 || (int64_t)max_seq_len > (int64_t)width * page_size) return GDN_EINVAL;
+  if (!cu_seqlens && T != N) return GDN_EINVAL;
+  if (!head_dim_ok(D)) return GDN_EUNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return GDN_EUNSUPPORTED;
+  if (N > 65535 || HK > 65535) return GDN_EUNSUPPORTED;
+  if (N == 0 || T == 0) return GDN_OK;
+  if (ldq < (int64_t)HQ * D || ldq % 8) return GDN_EINVAL;
+  if (P <= 0 || max_q_len <= 0 || !q || !k_cache || !v_cache || !k_scale || !v_scale || !seq_lens || !o) return GDN_EINVAL;
+  if (width > 0 && !block_table) return GDN_EINVAL;
+  if (!aligned16({q, k_cache, v_cache, o, workspace})) return GDN_EINVAL;
+  const int max_q = max_q_len < T ? max_q_len : T;
+  if ((int64_t)P * HK > 2147483646LL || (int64_t)max_q * (HQ / HK) > (1 << 30)) return GDN_EUNSUPPORTED;
+  const size_t need = gdn_host::kv8_attn_workspace_bytes(N, HK, HQ / HK, D, max_q, max_seq_len);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
+  if (!(scale > 0.f)) scale = 1.f / sqrtf((float)D);  // also catches NaN
+  gdn_host::Kv8AttnArgs a{};
+  a.q = q; a.ldq = ldq; a.kc = k_cache; a.vc = v_cache; a.ks = k_scale; a.vs = v_scale;
+  a.table = block_table; a.width = width; a.seq_lens = seq_lens; a.cu = cu_seqlens;
+  a.N = N; a.T = T; a.P = P; a.HQ = HQ; a.HK = HK; a.D = D; a.bs = page_size; a.max_q = max_q; a.max_seq = max_seq_len;
+  a.scale = scale; a.o = o; a.lse = lse; a.ws = workspace; a.dev_status = dev_status;
+  a.force_expiry = g_force_wait_expiry.load();
+  if (!bind_context()) return GDN_ECUDA;
+  return cuda_status(gdn_host::launch_kv8_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

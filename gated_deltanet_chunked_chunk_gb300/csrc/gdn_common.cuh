@@ -141,4 +141,42 @@ struct ChunkBwdArgs {
 };
 size_t chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int K, int V, int N, int varlen);
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a, cudaStream_t s);
+// Norms, rotary positions and the paged 8-bit cache (gdn_norm.cu, gdn_rope.cu,
+// gdn_paged.cu, gdn_kv8_attn.cu).  Row r of z starts at (r / z_group) z_stride +
+// (r % z_group) D elements; act: 0 none, 1 SiLU, 2 sigmoid.
+size_t norm_bwd_workspace_bytes(int64_t rows, int D);
+cudaError_t launch_norm_fwd(const uint16_t *x, const uint16_t *res, const uint16_t *z, const float *w, float res_scale,
+                            float eps, int act, int64_t rows, int D, int64_t z_group, int64_t z_stride, uint16_t *y,
+                            uint16_t *h, cudaStream_t s);
+cudaError_t launch_norm_bwd(const uint16_t *dy, const uint16_t *h, const uint16_t *z, const uint16_t *dh, const float *w,
+                            float res_scale, float eps, int act, int64_t rows, int D, int64_t z_group, int64_t z_stride,
+                            uint16_t *dx, uint16_t *dres, uint16_t *dz, float *dw, void *ws, cudaStream_t s);
+cudaError_t launch_rope(const uint16_t *q, const uint16_t *k, const int32_t *pos, const float *inv_freq, int64_t T, int HQ,
+                        int HK, int D, int rot, int interleaved, int inverse, float factor, int64_t ldq, int64_t ldk,
+                        uint16_t *qo, uint16_t *ko, cudaStream_t s);
+cudaError_t launch_paged_plan(const int32_t *cached, const int32_t *cu, int N, int T, int32_t *table, int width,
+                              const int32_t *free_pages, int F, const int32_t *num_free, int bs, int32_t *seq_lens,
+                              int32_t *slots, int32_t *positions, int32_t *num_free_out, int32_t *dev_status,
+                              cudaStream_t s);
+cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ldv, uint8_t *kc, uint8_t *vc,
+                              float *ks, float *vs, const int32_t *slots, int64_t T, int P, int HK, int D, int bs,
+                              int32_t *dev_status, cudaStream_t s);
+struct Kv8AttnArgs {
+  const uint16_t *q;
+  int64_t ldq;  // token stride in elements
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  const int32_t *table;
+  int width;
+  const int32_t *seq_lens, *cu;
+  int N, T, P, HQ, HK, D, bs, max_q, max_seq;
+  float scale;
+  uint16_t *o;
+  float *lse;
+  void *ws;
+  int32_t *dev_status;
+  int force_expiry;  // testing hook: the first bounded wait of every block runs out
+};
+size_t kv8_attn_workspace_bytes(int N, int HK, int G, int D, int max_q, int max_seq);
+cudaError_t launch_kv8_attn(const Kv8AttnArgs &a, cudaStream_t s);
 }  // namespace gdn_host

@@ -57,11 +57,14 @@ enum gdn_device_status_bits {
   GDN_DEV_BAD_CU_SEQLENS = 1, /* cu_seqlens not non-decreasing from 0, or past T */
   GDN_DEV_BAD_SLOT = 2,       /* decode slot index < -1 or >= P (row treated as PAD) */
   GDN_DEV_WAIT_TIMEOUT = 4,   /* a bounded wait inside a kernel gave up */
-  GDN_DEV_DRAIN_TIMEOUT = 8   /* after GDN_DEV_WAIT_TIMEOUT, the wait for the
+  GDN_DEV_DRAIN_TIMEOUT = 8,  /* after GDN_DEV_WAIT_TIMEOUT, the wait for the
                                  block's own copies (or tensor-core products)
                                  in flight gave up too: shared or tensor memory
                                  of that block may still have been written after
                                  it exited; treat the context as suspect */
+  GDN_DEV_NO_PAGE = 16,       /* gdn_paged_plan: the free list, or a table row, is too
+                                 short; the tokens left out have slot -1 */
+  GDN_DEV_BAD_SEQ_LEN = 32    /* a context length < 0 or > max_seq_len (request skipped) */
 };
 
 /* Static text for a gdn_status_code.  Never NULL. */
@@ -477,6 +480,164 @@ int gdn_conv_decode_pack(const uint16_t *mixed_qkv, uint16_t *conv_state, int P,
                          const int32_t *conv_state_indices, int R, int H, int HV, int K, int V,
                          int width, int activation, uint16_t *q, uint16_t *k, uint16_t *v,
                          int32_t *dev_status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Around the recurrence: what a stack of gated-delta-rule and attention layers
+ * needs next to it.  The pages describe the layers' own kernels only, so these
+ * have no counterpart there; they follow the conventions above.
+ */
+
+/*
+ * gdn_norm_gate -- RMS norm with a gate and a scaled residual, before or after
+ * a block.  For every row of D elements:
+ *     h = x                       (residual == NULL)
+ *     h = residual + res_scale x  (stored to h, rounded to bf16; the norm uses
+ *                                  the value before that rounding)
+ *     y = h / sqrt(mean(h^2) + eps) * weight * act(z)
+ * activation: 0 none (z must be NULL), 1 SiLU, z sigmoid(z), 2 sigmoid(z).
+ *
+ *   x, residual, y, h : bf16 [rows, D]; residual and h are both NULL or both
+ *                       set.  y may be x, and h may be residual.
+ *   z                 : bf16, row r at (r / z_rows) z_stride + (r % z_rows) D
+ *                       elements: a dense [rows, D] with z_rows = 0, or a slice
+ *                       of a wider projection ([tokens, z_rows heads, D] with
+ *                       z_stride elements between tokens)
+ *   weight            : fp32 [D]
+ * Any D >= 1; rows of D % 8 == 0 up to 16384 on 16-byte boundaries (z_stride %
+ * 8 == 0) move in 16-byte accesses, others element by element.  rows = 0 is a
+ * no-op.  One launch.  GDN_EINVAL: null pointers, D <= 0, a bad activation,
+ * eps < 0 or NaN.
+ */
+int gdn_norm_gate(const uint16_t *x, const uint16_t *residual, const uint16_t *z, const float *weight, float res_scale,
+                  float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride, uint16_t *y,
+                  uint16_t *h, void *stream);
+
+/* gdn_norm_gate_bwd_workspace_size -- bytes of device workspace gdn_norm_gate_bwd needs. */
+size_t gdn_norm_gate_bwd_workspace_size(int64_t rows, int D);
+
+/*
+ * gdn_norm_gate_bwd -- gradients of gdn_norm_gate.  h is what was normed (x
+ * itself, or the stream that the forward stored).
+ *   dy             : bf16 [rows, D]
+ *   dh             : bf16 [rows, D], the gradient that reaches h from its other
+ *                    uses, or NULL (none; dresidual must then be NULL too)
+ *   dx, dresidual  : bf16 [rows, D]; dx = res_scale dH and dresidual = dH, with
+ *                    dH the gradient of h (dresidual NULL when dh is)
+ *   dz             : bf16 [rows, D], dense; required with a gate, else NULL
+ *   dweight        : fp32 [D]
+ *   workspace      : gdn_norm_gate_bwd_workspace_size() bytes, 16-byte aligned
+ * Sums have a fixed order: two runs agree bit for bit.  Two launches.  dx may
+ * be dy, dresidual may be dh.  GDN_EWORKSPACE for a small workspace.
+ */
+int gdn_norm_gate_bwd(const uint16_t *dy, const uint16_t *h, const uint16_t *z, const uint16_t *dh, const float *weight,
+                      float res_scale, float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride,
+                      uint16_t *dx, uint16_t *dresidual, uint16_t *dz, float *dweight, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_rope -- rotary positions of queries and keys, one launch for both.
+ *     (a, b) -> f (a cos t - b sin t, a sin t + b cos t),  t = positions[n] inv_freq[i]
+ * for the pairs i < rotary_dim / 2 of a head: elements (i, i + rotary_dim / 2),
+ * or (2 i, 2 i + 1) with interleaved != 0.  Elements from rotary_dim on pass
+ * unchanged (they are not scaled).  inverse != 0 turns by -t (f stays): the
+ * gradient of the call without it.  The angle is exact for any int32 position.
+ *   q [T, HQ, D], k [T, HK, D] : bf16, ldq, ldk elements between tokens (>= HQ
+ *                                D, HK D), heads dense; k may be NULL with HK = 0
+ *   positions                  : int32 [T];  inv_freq: fp32 [rotary_dim / 2], finite
+ *   attention_factor           : f
+ *   q_out, k_out               : bf16, dense [T, HQ, D], [T, HK, D]; may be q, k
+ *                                where those are dense
+ * T = 0 is a no-op.  GDN_EINVAL: null pointers, rotary_dim odd, < 2 or > D, a
+ * stride below a token's width, HQ <= 0, HK < 0.  GDN_EUNSUPPORTED:
+ * rotary_dim > 8192.
+ */
+int gdn_rope(const uint16_t *q, const uint16_t *k, const int32_t *positions, const float *inv_freq, int64_t T, int HQ,
+             int HK, int D, int rotary_dim, int interleaved, int inverse, float attention_factor, int64_t ldq,
+             int64_t ldk, uint16_t *q_out, uint16_t *k_out, void *stream);
+
+/*
+ * gdn_paged_plan -- block tables, slot map and positions of one step, on the
+ * device, from request lengths.  Request n holds cached_lens[n] tokens in its
+ * pages and gets cu_seqlens[n + 1] - cu_seqlens[n] more.  It keeps its
+ * ceil(cached / page_size) pages (entries of its table row) and takes, up to
+ * ceil((cached + new) / page_size), further ones from the end of the free list,
+ * requests in order.
+ *   cached_lens   : int32 [N];  cu_seqlens: int32 [N + 1] (0, ..., T)
+ *   block_table   : int32 [N, width]; the entries of the pages taken are written
+ *   free_pages    : int32 [F], num_free: int32 [1], the free ones are the first num_free
+ *   seq_lens      : int32 [N]   cached + new
+ *   slot_mapping  : int32 [T]   page * page_size + place in the page, -1: no page
+ *   positions     : int32 [T]   place in the request's context (0 without a request)
+ *   num_free_out  : int32 [1]   pages left; another address than num_free
+ * No input but the table is written, so a call can be repeated.  Too few free
+ * pages, or a row too short: table entry and slots -1, GDN_DEV_NO_PAGE.  Offsets
+ * that break the rules and negative lengths: GDN_DEV_BAD_CU_SEQLENS, the
+ * request counts as having no new tokens.  Slots must fit int32 (caller's
+ * pages x page_size < 2^31).  N = 0 writes num_free_out and T slots of -1.
+ * One launch.
+ */
+int gdn_paged_plan(const int32_t *cached_lens, const int32_t *cu_seqlens, int N, int T, int32_t *block_table, int width,
+                   const int32_t *free_pages, int F, const int32_t *num_free, int page_size, int32_t *seq_lens,
+                   int32_t *slot_mapping, int32_t *positions, int32_t *num_free_out, int32_t *dev_status, void *stream);
+
+/*
+ * The paged 8-bit cache.  k_cache, v_cache: e4m3 codes [P, HK, page_size, D];
+ * k_scale, v_scale: fp32 [P, HK]; value = code * scale.  gdn_kv8_append writes
+ * scales that are powers of two; the attention takes any positive ones.
+ *
+ * gdn_kv8_append -- the write of new keys and values.  For each page and head
+ * that a call writes to:
+ *     e     = the least exponent >= -60 with every finite new |x| <= 448 2^e, and,
+ *             where the page holds earlier tokens, not below its present one
+ *     codes = earlier codes 2^(e_before - e), new x 2^-e, rounded to e4m3 (to
+ *             nearest, ties to even; infinities become +-448, NaN stays NaN)
+ *     scale = 2^e
+ * A write to place 0 begins the page anew: what it held does not count.
+ *   k, v          : bf16 [T, HK, D], ldk, ldv elements between tokens
+ *   slot_mapping  : int32 [T] as gdn_paged_plan writes it; -1 skips the token,
+ *                   others outside [0, P page_size) set GDN_DEV_BAD_SLOT and are
+ *                   skipped.  The tokens of one page must be consecutive and in
+ *                   the order of their places, and must not belong to two runs.
+ * Codes past a page's last token are left as they were.  T = 0 is a no-op.  One
+ * launch.  GDN_EINVAL: null pointers, sizes <= 0, strides below a token's width.
+ */
+int gdn_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ldv, uint8_t *k_cache, uint8_t *v_cache,
+                   float *k_scale, float *v_scale, const int32_t *slot_mapping, int64_t T, int P, int HK, int D,
+                   int page_size, int32_t *dev_status, void *stream);
+
+/* gdn_kv8_attention_workspace_size -- bytes of device workspace
+ * gdn_kv8_attention needs for these sizes (0: none, pass NULL). */
+size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int max_q_len, int max_seq_len);
+
+/*
+ * gdn_kv8_attention -- causal attention of new tokens over the paged 8-bit
+ * cache, which holds them already.  Request n has tokens [cu_seqlens[n],
+ * cu_seqlens[n + 1]) of q (one token each, T = N, where cu_seqlens is NULL) and
+ * a context of seq_lens[n] tokens, the new ones last; its token i of m sees the
+ * places 0 .. seq_lens[n] - m + i.
+ *     o = softmax(scale q K^T) V,  lse = log sum exp(scale q K^T)
+ * A token that sees nothing has o = 0 and lse = -inf.
+ *   q             : bf16 [T, HQ, D], ldq elements between tokens; query head h
+ *                   reads kv head h / (HQ / HK)
+ *   block_table   : int32 [N, width]; a needed entry outside [0, P) sets
+ *                   GDN_DEV_BAD_SLOT, its places are not seen
+ *   seq_lens      : int32 [N], 0 .. max_seq_len (else GDN_DEV_BAD_SEQ_LEN and the
+ *                   request is skipped); what a page holds past a context is
+ *                   never used
+ *   max_q_len, max_seq_len : host bounds on a request's new tokens and context
+ *                   (more new tokens: GDN_DEV_BAD_CU_SEQLENS and the request is
+ *                   skipped); max_seq_len <= width page_size
+ *   scale         : <= 0 or NaN selects 1/sqrt(D)
+ *   o             : bf16 [T, HQ, D];  lse: fp32 [T, HQ] or NULL
+ * D 64 or 128, page_size 16, 32, 64 or 128 (else GDN_EUNSUPPORTED, as for N >
+ * 65535 or HK > 65535); HQ % HK == 0.  q, the caches, o and the workspace must
+ * start on a 16-byte boundary and ldq be a multiple of 8 (else GDN_EINVAL).
+ */
+int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, const uint8_t *v_cache,
+                      const float *k_scale, const float *v_scale, const int32_t *block_table, int width,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, int N, int T, int P, int HQ, int HK, int D,
+                      int page_size, int max_q_len, int max_seq_len, float scale, uint16_t *o, float *lse,
+                      void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,597 @@
+"""The operators around the recurrence on the GPU against plain 64-bit implementations (tests/stack_util.py).
+
+Tolerances, from the roundings: a bf16 output is one rounding of an fp32 result, 2^-9 relative, and the fp32 result is
+off by some 2^-21 of the terms that were added, so 2^-8 of the value plus 2^-18 of the largest term.  fp32 sums over
+rows: 2^-19 of the sum of magnitudes.  Attention: p is rounded to 11 bits (2^-12 each, at most 2^-11 of
+sum p |v| with the fp32 errors of the logits) and o to bf16.  Codes, scales and whole numbers: equal."""
+import numpy as np
+import pytest
+import torch
+
+import stack_util as U
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_deltanet_chunked_chunk_gb300 import build
+    build.build()
+
+
+def _gdn():
+    import gated_deltanet_chunked_chunk_gb300 as gdn
+    return gdn
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _close_bf16(got, ref, extra=0.0, what=""):
+    got = U.f64(got)
+    tol = 2.0 ** -8 * np.abs(ref) + extra + 1e-37
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, worst {np.max(np.abs(got - ref) - tol):.3e}"
+
+
+# ------------------------------------------------------------------- norms
+@pytest.mark.parametrize("shape", [(1, 128), (257, 2, 128), (33, 4, 64), (5, 3, 96), (130, 256), (9, 512), (7, 1024), (5, 2048),
+                                   (3, 4096), (3, 8192), (2, 16384), (2, 16392), (4, 1), (6, 7), (3, 1001), (2, 3, 130)])
+@pytest.mark.parametrize("kind,res", [(None, False), ("silu", True), ("sigmoid", False)])
+def test_norm_gate_and_gradients(shape, kind, res):
+    gdn, g = _gdn(), _gen(sum(shape))
+    x = (2 * torch.randn(shape, generator=g)).to(BF)
+    w = 1 + 0.1 * torch.randn(shape[-1], generator=g)
+    z = torch.randn(shape, generator=g).to(BF) if kind else None
+    r = torch.randn(shape, generator=g).to(BF) if res else None
+    dy, dh = torch.randn(shape, generator=g).to(BF), torch.randn(shape, generator=g).to(BF) if res else None
+    c = lambda t: None if t is None else t.cuda()
+    y, h = gdn.gdn_norm_gate(c(x), c(w), residual=c(r), z=c(z), activation=kind, res_scale=0.5 if res else 1.0)
+    ry, rh = U.norm_fwd(U.f64(x), U.f64(w), U.f64(r), U.f64(z), kind, res_scale=0.5 if res else 1.0)
+    _close_bf16(y, ry, what="y")
+    if res:
+        _close_bf16(h, rh, 2.0 ** -18 * np.abs(rh).max(), what="h")
+    else:
+        assert h is None
+    hb = x if h is None else h.cpu()
+    dx, dres, dz, dw = gdn.gdn_norm_gate_bwd(c(dy), c(hb), c(w), z=c(z), dh=c(dh), activation=kind,
+                                             res_scale=0.5 if res else 1.0)
+    h64 = U.f64(hb)
+    rx, rr, rz, rw = U.norm_bwd(U.f64(dy), h64, U.f64(w), U.f64(z), U.f64(dh), kind, res_scale=0.5 if res else 1.0)
+    rstd = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + 1e-6)
+    terms = rstd * np.abs(U.f64(dy)).max(-1, keepdims=True) * 4 + (2.0 if res else 0.0)
+    _close_bf16(dx, rx, 2.0 ** -18 * terms, what="dx")
+    if res:
+        _close_bf16(dres, rr, 2.0 ** -18 * terms, what="dresidual")
+    if kind:
+        _close_bf16(dz, rz, 2.0 ** -18 * np.abs(U.f64(dy) * h64 * rstd), what="dz")
+    n = h64 * rstd
+    mags = np.abs(U.f64(dy) * n * (1.0 if kind is None else U.act(U.f64(z), kind)[0])).reshape(-1, shape[-1]).sum(0)
+    assert (np.abs(U.f64(dw) - rw) <= 2.0 ** -19 * mags + 1e-30).all()
+
+
+def test_norm_gate_of_a_packed_projection_in_place_and_misaligned():
+    gdn, g = _gdn(), _gen(3)
+    T, H, D = 37, 4, 128
+    wide = torch.randn(T, 3 * H * D + 8, generator=g).to(BF).cuda()
+    z = wide[:, H * D:2 * H * D].view(T, H, D)
+    assert not z.is_contiguous()
+    x = torch.randn(T, H, D, generator=g).to(BF).cuda()
+    w = torch.rand(D, generator=g).cuda() + 0.5
+    y, _ = gdn.gdn_norm_gate(x, w, z=z)
+    y2, _ = gdn.gdn_norm_gate(x, w, z=z.contiguous())
+    assert torch.equal(y, y2)
+    a = gdn.gdn_norm_gate_bwd(x, y, w, z=z)
+    b = gdn.gdn_norm_gate_bwd(x, y, w, z=z.contiguous())
+    assert all(torch.equal(p, q) for p, q in zip(a, b) if p is not None)
+    # the same values from buffers that are only 2-byte aligned (the element loop): equal up to fp32 order
+    buf = torch.empty(x.numel() + 1, dtype=BF, device="cuda")
+    odd = buf[1:].view(T, H, D)
+    odd.copy_(x)
+    y3, _ = gdn.gdn_norm_gate(odd, w, z=z)
+    ry, _ = U.norm_fwd(U.f64(x), U.f64(w), None, U.f64(z))
+    _close_bf16(y3, ry, what="misaligned")
+    # in place: y over x, h over the residual
+    r = torch.randn(T, H, D, generator=g).to(BF).cuda()
+    y4, h4 = gdn.gdn_norm_gate(x, w, residual=r, res_scale=0.25)
+    xi, ri = x.clone(), r.clone()
+    y5, h5 = gdn.gdn_norm_gate(xi, w, residual=ri, res_scale=0.25, y=xi, h=ri)
+    assert y5.data_ptr() == xi.data_ptr() and torch.equal(y4, y5) and torch.equal(h4, h5)
+
+
+def test_norm_gate_extremes():
+    gdn = _gdn()
+    D = 128
+    x = torch.zeros(4, D)
+    x[1, 5] = 1e30   # one large element: the others vanish, the row keeps its norm
+    x[2] = 1e-20     # far below eps
+    x[3] = 3.0
+    z = torch.zeros(4, D)
+    z[3, 0], z[3, 1] = 200.0, -200.0
+    x, z = x.to(BF), z.to(BF)
+    w = torch.ones(D)
+    y, _ = gdn.gdn_norm_gate(x[:1].cuda(), w.cuda())
+    assert (y == 0).all()
+    y, _ = gdn.gdn_norm_gate(x[2:].cuda(), w.cuda(), z=z[2:].cuda())
+    ry, _ = U.norm_fwd(U.f64(x[2:]), U.f64(w), None, U.f64(z[2:]))
+    _close_bf16(y, ry, 1e-30)
+    nan = x[3:].clone()
+    nan[0, 7] = float("nan")
+    y, _ = gdn.gdn_norm_gate(torch.cat([x[3:], nan]).cuda(), w.cuda())
+    assert torch.isfinite(y[0]).all() and torch.isnan(y[1]).all()
+    y, h = gdn.gdn_norm_gate(torch.empty(0, D, dtype=BF, device="cuda"), w.cuda())
+    assert y.shape == (0, D) and h is None
+    e = torch.empty(0, D, dtype=BF, device="cuda")
+    dx, _, _, dw = gdn.gdn_norm_gate_bwd(e, e, w.cuda())
+    assert dx.shape == (0, D) and (dw == 0).all()
+
+
+def test_norm_gate_autograd_against_differences_and_repeats():
+    """The gradient against central differences of the 64-bit forward, along random directions, and bit for bit twice."""
+    gdn, g = _gdn(), _gen(11)
+    T, D = 6, 64
+    x, r, z = (torch.randn(T, D, generator=g).to(BF) for _ in range(3))
+    w = 1 + 0.1 * torch.randn(D, generator=g)
+    cy, ch = torch.randn(T, D, generator=g).to(BF), torch.randn(T, D, generator=g).to(BF)
+    leaves = [t.cuda().requires_grad_() for t in (x, w, r, z)]
+    y, h = gdn.norm_gate(leaves[0], leaves[1], residual=leaves[2], z=leaves[3], res_scale=0.5)
+    grads = torch.autograd.grad([y, h], leaves, [cy.cuda(), ch.cuda()])
+    again = torch.autograd.grad(gdn.norm_gate(leaves[0], leaves[1], residual=leaves[2], z=leaves[3], res_scale=0.5), leaves,
+                                [cy.cuda(), ch.cuda()])
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+    def loss(x, w, r, z):
+        y, h = U.norm_fwd(x, w, r, z, "silu", res_scale=0.5)
+        return (y * U.f64(cy)).sum() + (h * U.f64(ch)).sum()
+
+    base = [U.f64(t) for t in (x, w, r, z)]
+    for i in range(4):
+        for k in range(3):
+            d = np.random.RandomState(10 * i + k).randn(*base[i].shape)
+            step = 1e-5
+            up, dn = list(base), list(base)
+            up[i], dn[i] = base[i] + step * d, base[i] - step * d
+            num = (loss(*up) - loss(*dn)) / (2 * step)
+            got = (U.f64(grads[i]) * d).sum()
+            # bf16 gradients of a stream that the forward stored in bf16: 2^-8 of each term, added at random
+            tol = 2.0 ** -8 * 4 * np.sqrt(((U.f64(grads[i]) * d) ** 2).sum()) + 2.0 ** -8 * np.abs(U.f64(grads[i])).max()
+            assert abs(num - got) <= tol, (i, k, num, got, tol)
+
+
+# ------------------------------------------------------------------ rotary
+@pytest.mark.parametrize("T,HQ,HK,D,rot", [(1, 1, 1, 64, 64), (3, 32, 4, 128, 32), (257, 8, 2, 128, 128), (5000, 4, 1, 64, 16),
+                                           (19, 3, 1, 256, 128), (7, 2, 2, 80, 20), (11, 2, 0, 10, 6), (40, 16, 16, 128, 64),
+                                           (2, 1, 1, 2, 2)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_and_inverse(T, HQ, HK, D, rot, interleaved):
+    gdn, g = _gdn(), _gen(T + D)
+    q = torch.randn(T, HQ, D, generator=g).to(BF)
+    k = torch.randn(T, HK, D, generator=g).to(BF) if HK else None
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, dtype=torch.int32)
+    pos[0] = 2147483647 if T > 1 else 0
+    pos[-1] = -5 if T > 2 else pos[-1]
+    inv, att = gdn.rope_frequencies(rot, scaling="yarn", factor=4.0)
+    att = 1.25
+    c = lambda t: None if t is None else t.cuda()
+    for inverse in (False, True):
+        qo, ko = gdn.gdn_rope(c(q), c(k), c(pos), c(inv), interleaved=interleaved, attention_factor=att, inverse=inverse)
+        for x, y in ((q, qo), (k, ko)):
+            if x is None:
+                assert y is None
+                continue
+            ref = U.rope(U.f64(x), pos.numpy(), inv.numpy(), interleaved, att, inverse)
+            _close_bf16(y, ref, 2.0 ** -18 * np.abs(U.f64(x)).max(), what="rope")
+            assert torch.equal(y[..., rot:].cpu(), x[..., rot:])
+
+
+def test_rope_views_in_place_and_gradient():
+    gdn, g = _gdn(), _gen(5)
+    T, HQ, HK, D = 70, 8, 2, 128
+    packed = torch.randn(T, (HQ + 2 * HK) * D, generator=g).to(BF).cuda()
+    q, k = packed[:, :HQ * D].view(T, HQ, D), packed[:, HQ * D:(HQ + HK) * D].view(T, HK, D)
+    pos = torch.arange(T, dtype=torch.int32).cuda() * 37
+    inv, _ = gdn.rope_frequencies(D, device="cuda")
+    a = gdn.gdn_rope(q, k, pos, inv)
+    qc, kc = q.contiguous(), k.contiguous()
+    b = gdn.gdn_rope(qc, kc, pos, inv, q_out=qc, k_out=kc)
+    assert b[0].data_ptr() == qc.data_ptr() and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # an odd element offset takes the element loop: the same formula in fp32, at most a rounding apart
+    buf = torch.empty(T * HQ * D + 1, dtype=BF, device="cuda")
+    buf[1:].copy_(q.reshape(-1))
+    odd, _ = gdn.gdn_rope(buf[1:].view(T, HQ, D), None, pos, inv)
+    _close_bf16(odd, U.rope(U.f64(q), pos.cpu().numpy(), inv.cpu().numpy(), False), 2.0 ** -16)
+    ql, kl = q.detach().clone().requires_grad_(), k.detach().clone().requires_grad_()
+    co = torch.randn(T, HQ, D, generator=g).to(BF).cuda(), torch.randn(T, HK, D, generator=g).to(BF).cuda()
+    out = gdn.rotary_embedding(ql, kl, pos, inv, attention_factor=1.5)
+    dq, dk = torch.autograd.grad(out, (ql, kl), co)
+    # <R x, c> = <x, R^T c>, and the difference quotient of a linear map is the map itself
+    for x, d, cc in ((q, dq, co[0]), (k, dk, co[1])):
+        lhs = U.rope(U.f64(x), pos.cpu().numpy(), inv.cpu().numpy(), False, 1.5) * U.f64(cc)
+        assert abs(lhs.sum() - (U.f64(x) * U.f64(d)).sum()) <= 4 * 2.0 ** -8 * np.sqrt((lhs ** 2).sum() + (U.f64(x) * U.f64(d)).var() * d.numel())
+    e = gdn.gdn_rope(q[:0], k[:0], pos[:0], inv)
+    assert e[0].shape == (0, HQ, D)
+
+
+# -------------------------------------------------------------------- plan
+def _plan_case(N, cached_hi, new_hi, bs, seed, extra=4):
+    r = np.random.RandomState(seed)
+    cached = r.randint(0, cached_hi + 1, N).tolist()
+    new = r.randint(0, new_hi + 1, N).tolist()
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(int).tolist()
+    width = max(1, max(-(-(c + m) // bs) for c, m in zip(cached, new))) + 1
+    ids = r.permutation(sum(-(-(c + m) // bs) for c, m in zip(cached, new)) + extra).tolist()
+    table = [[-1] * width for _ in range(N)]
+    for n, c in enumerate(cached):
+        for p in range(-(-c // bs)):
+            table[n][p] = ids.pop()
+    return cached, cu, table, ids, bs
+
+
+def _run_plan(case, left=None, width=None):
+    gdn = _gdn()
+    cached, cu, table, ids, bs = case
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    left = len(ids) if left is None else left
+    t = i(table)
+    if width is not None:
+        t = t[:, :width].contiguous()
+        table = [row[:width] for row in table]
+    st = i([0])
+    free = i(ids) if ids else torch.empty(0, dtype=torch.int32, device="cuda")
+    got = gdn.gdn_paged_plan(i(cached), i(cu), t, free, i([left]), bs, cu[-1], dev_status=st)
+    ref = U.plan(cached, cu, table, ids, left, bs, cu[-1])
+    return t, got, ref, int(st.item())
+
+
+@pytest.mark.parametrize("N,cached_hi,new_hi,bs", [(1, 0, 1, 16), (1, 300, 5000, 64), (7, 65, 1, 64), (300, 200, 3, 16), (1024, 70, 9, 32),
+                                                   (1025, 5, 2, 128), (3000, 40, 1, 16), (5, 100, 2000, 48)])
+def test_plan(N, cached_hi, new_hi, bs):
+    case = _plan_case(N, cached_hi, new_hi, bs, N)
+    t, got, ref, st = _run_plan(case)
+    assert st == 0
+    assert t.cpu().tolist() == ref[0]
+    for a, b in zip(got, (ref[1], ref[2], ref[3], [ref[4]])):
+        assert a.cpu().tolist() == b
+    # again on the table that now has the pages: nothing changes
+    t2, got2, _, _ = _run_plan((case[0], case[1], t.cpu().tolist(), case[3], bs))
+    assert torch.equal(t, t2) and all(torch.equal(a, b) for a, b in zip(got, got2))
+
+
+def test_plan_without_enough_pages_or_room():
+    gdn = _gdn()
+    case = _plan_case(40, 60, 50, 16, 3)
+    t, got, ref, st = _run_plan(case, left=5)
+    assert st == gdn.DEV_NO_PAGE and ref[5]
+    assert t.cpu().tolist() == ref[0] and got[1].cpu().tolist() == ref[2] and int(got[3]) == 0
+    t, got, ref, st = _run_plan(case, width=3)
+    assert st == gdn.DEV_NO_PAGE and got[1].cpu().tolist() == ref[2] and got[2].cpu().tolist() == ref[3]
+    assert t.cpu().tolist() == ref[0]
+
+
+def test_plan_bad_offsets_and_empty():
+    gdn = _gdn()
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    st = i([0])
+    t = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    # request 1 runs backwards; the tokens that no request has get slot -1
+    seq, slots, pos, left = gdn.gdn_paged_plan(i([0, 3, 0]), i([0, 2, 1, 4]), t, i([5, 6, 7, 8]), i([4]), 4, 4, dev_status=st)
+    assert int(st) == gdn.DEV_BAD_CU_SEQLENS and seq.tolist() == [2, 3, 3]
+    assert all(s == -1 or 0 <= s < 9 * 4 for s in slots.tolist())
+    st.zero_()
+    seq, slots, pos, left = gdn.gdn_paged_plan(i([-4]), i([0, 1]), t[:1], i([5]), i([1]), 4, 1, dev_status=st)
+    assert int(st) == gdn.DEV_BAD_CU_SEQLENS and slots.tolist() == [-1]
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    seq, slots, pos, left = gdn.gdn_paged_plan(e, i([0]), t[:0], i([5]), i([1]), 4, 2)
+    assert seq.numel() == 0 and slots.tolist() == [-1, -1] and left.tolist() == [1]
+    seq, slots, pos, left = gdn.gdn_paged_plan(i([3]), i([0, 0]), t[:1], i([5]), i([9]), 4, 0)
+    assert seq.tolist() == [3] and slots.numel() == 0 and left.tolist() == [1]  # num_free beyond the list counts as its length
+
+
+# ------------------------------------------------------------------ append
+def _same_cache(codes, scale, ref):
+    got = U.f64(codes.float())
+    assert np.array_equal(np.isnan(got), np.isnan(ref[0])) and np.array_equal(np.nan_to_num(got), np.nan_to_num(ref[0]))
+    assert np.array_equal(U.f64(scale), ref[1])
+
+
+@pytest.mark.parametrize("HK,D,bs,counts,offs", [
+    (1, 64, 16, [1], [0]), (2, 128, 64, [1, 1, 1, 1], [0, 5, 63, 17]), (4, 128, 64, [200, 64, 3], [30, 0, 61]),
+    (3, 64, 16, [1, 40, 2, 16], [15, 9, 14, 0]), (1, 128, 128, [300], [100]), (2, 72, 8, [20, 5], [3, 0]), (2, 10, 5, [9, 1], [1, 4])])
+@pytest.mark.parametrize("packed", [False, True])
+def test_append(HK, D, bs, counts, offs, packed):
+    gdn, g = _gdn(), _gen(D + bs)
+    T, need = sum(counts), [-(-(o + c) // bs) for o, c in zip(offs, counts)]
+    P = sum(need) + 2
+    ids = torch.randperm(P, generator=g).tolist()
+    slots, at = [], 0
+    for o, c, m in zip(offs, counts, need):
+        pages = ids[at:at + m]
+        at += m
+        slots += [pages[(o + i) // bs] * bs + (o + i) % bs for i in range(c)]
+    slots.insert(0, -1)  # a token without a place (a page's own tokens must follow one another)
+    T += 1
+    kc, ks = U.make_cache(P, HK, bs, D, g)
+    vc, vs = U.make_cache(P, HK, bs, D, g)
+    wide = torch.randn(T, 2 * HK * D, generator=g) * torch.exp(2 * torch.randn(T, 1, generator=g))
+    wide = wide.to(BF)
+    k, v = (wide[:, :HK * D].view(T, HK, D), wide[:, HK * D:].view(T, HK, D))
+    if not packed:
+        k, v = k.contiguous(), v.contiguous()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dev = [t.cuda() for t in (kc, vc, ks, vs)]
+    wd = wide.cuda()
+    kd, vd = (wd[:, :HK * D].view(T, HK, D), wd[:, HK * D:].view(T, HK, D)) if packed else (k.cuda(), v.cuda())
+    sl = torch.tensor(slots, dtype=torch.int32, device="cuda")
+    for _ in range(2):  # the second time the same tokens go to the same places
+        gdn.gdn_kv8_append(kd, vd, dev[0], dev[1], dev[2], dev[3], sl, dev_status=st)
+        assert int(st) == 0
+        _same_cache(dev[0], dev[2], U.append(U.f64(k), U.f64(kc.float()), U.f64(ks), slots))
+        _same_cache(dev[1], dev[3], U.append(U.f64(v), U.f64(vc.float()), U.f64(vs), slots))
+
+
+def test_append_values_at_the_edges():
+    """Zeros, infinities, NaN, values on the border of an exponent, growth of a page's scale by much, tiny values."""
+    gdn = _gdn()
+    bs, D, P = 16, 64, 6
+    kc, ks = U.make_cache(P, 1, bs, D, _gen(1))
+    rows = torch.zeros(8, 1, D)
+    rows[1] = 448.0
+    rows[2] = 450.0  # the next bf16
+    rows[3, 0, :4] = torch.tensor([float("inf"), float("-inf"), float("nan"), 2.0])
+    rows[4] = 1e30
+    rows[5] = 1e-30
+    rows[6] = torch.linspace(-1, 1, D)
+    rows[7, 0, 0] = float("nan")
+    x = rows.to(BF)
+    slots = [0 * bs, 1 * bs, 2 * bs, 3 * bs, 4 * bs + 7, 5 * bs]
+    dev = [t.cuda() for t in (kc, kc.clone(), ks, ks.clone())]
+    ref = U.f64(kc.float()), U.f64(ks)
+    for rows, at in ((x[:6], slots), (x[6:], [0 * bs + 1, 1 * bs + 1])):  # the second call adds to pages of the first
+        gdn.gdn_kv8_append(rows.cuda(), rows.cuda(), dev[0], dev[1], dev[2], dev[3], torch.tensor(at, dtype=torch.int32, device="cuda"))
+        ref = U.append(U.f64(rows), ref[0], ref[1], at)
+        _same_cache(dev[0], dev[2], ref)
+        _same_cache(dev[1], dev[3], ref)
+    assert float(dev[2][5, 0]) == 2.0 ** -60 and float(dev[2][1, 0]) == 1.0 and float(dev[2][2, 0]) == 2.0
+
+
+def test_append_refuses_places_outside_the_cache():
+    gdn = _gdn()
+    kc, ks = U.make_cache(3, 2, 16, 64, _gen(2))
+    x = torch.randn(4, 2, 64, generator=_gen(4)).to(BF).cuda()
+    dev = [t.cuda() for t in (kc, kc.clone(), ks, ks.clone())]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_kv8_append(x, x, *dev, torch.tensor([48, -7, -1, 2147483647], dtype=torch.int32, device="cuda"), dev_status=st)
+    assert int(st) == gdn.DEV_BAD_SLOT
+    assert torch.equal(dev[0].cpu().view(torch.uint8), kc.view(torch.uint8)) and torch.equal(dev[2].cpu(), ks)
+    gdn.gdn_kv8_append(x[:0], x[:0], *dev, torch.empty(0, dtype=torch.int32, device="cuda"))
+
+
+# --------------------------------------------------------------- attention
+def _attn_case(HK, G, D, bs, lens, news, seed, spread=0.5, nan_past=True):
+    g = _gen(seed)
+    N, T = len(lens), sum(news)
+    need = [-(-L // bs) for L in lens]
+    P, width = sum(need) + 3, max(1, max(need)) + 1
+    ids = torch.randperm(P, generator=g).tolist()
+    table = [[-1] * width for _ in range(N)]
+    for n, m in enumerate(need):
+        for p in range(m):
+            table[n][p] = ids.pop()
+    kc, ks = U.make_cache(P, HK, bs, D, g, spread)
+    vc, vs = U.make_cache(P, HK, bs, D, g, spread)
+    if nan_past:  # what a page holds past a context must not matter, NaN least of all
+        for n, L in enumerate(lens):
+            if L % bs:
+                for c in (kc, vc):
+                    c.view(torch.uint8)[table[n][L // bs], :, L % bs:] = 0x7f
+    q = torch.randn(T, HK * G, D, generator=g).to(BF)
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(int).tolist()
+    return dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=table, lens=lens, cu=cu, max_q=max(news), HK=HK, G=G, D=D, bs=bs)
+
+
+def _attn_run(c, use_cu=True, scale=None, **kw):
+    gdn = _gdn()
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    st = i([0])
+    lse = torch.full(c["q"].shape[:2], 7.0, dtype=torch.float32, device="cuda")
+    q = kw.pop("q", None)
+    o = gdn.gdn_kv8_attention(c["q"].cuda() if q is None else q, c["kc"].cuda(), c["vc"].cuda(), c["ks"].cuda(), c["vs"].cuda(),
+                              i(c["table"]), i(c["lens"]), cu_seqlens=i(c["cu"]) if use_cu else None, max_q_len=c["max_q"],
+                              scale=scale, lse=lse, dev_status=st, **kw)
+    return o, lse, int(st.item())
+
+
+def _attn_check(c, o, lse, scale=None):
+    scale = c["D"] ** -0.5 if scale is None else scale
+    ro, rl, mag = U.attention(U.f64(c["q"]), U.f64(c["kc"].float()), U.f64(c["vc"].float()), U.f64(c["ks"]), U.f64(c["vs"]),
+                              c["table"], c["lens"], c["cu"], scale)
+    got, gl = U.f64(o), U.f64(lse)
+    assert np.array_equal(np.isnan(got), np.isnan(ro))
+    fin = ~np.isnan(ro)
+    tol = 2.0 ** -8 * np.abs(ro) + 2.0 ** -10 * mag + 1e-37
+    bad = (np.abs(got - ro) > tol) & fin
+    assert not bad.any(), f"o: {bad.sum()} of {bad.size}, worst {np.nanmax(np.abs(got - ro) / np.maximum(mag, 1e-37)):.3e} of sum p|v|"
+    empty = np.isneginf(rl)
+    assert np.array_equal(empty, np.isneginf(gl)) and (got[empty] == 0).all()
+    ok = np.isfinite(rl)
+    assert (np.abs(gl[ok] - rl[ok]) <= 2.0 ** -17 * (1 + np.abs(rl[ok]))).all()
+
+
+@pytest.mark.parametrize("HK,G,D,bs,lens,news", [
+    (1, 1, 64, 16, [1], [1]), (2, 4, 128, 64, [1, 63, 64, 65, 0, 300], [1] * 6), (4, 8, 128, 16, [17, 1000, 129], [1] * 3),
+    (1, 7, 64, 32, [257, 4], [1, 1]), (2, 16, 128, 128, [700, 128, 127], [1] * 3), (1, 1, 128, 64, [5000], [1]),
+    (2, 8, 64, 64, [2500, 31], [1, 1]), (2, 4, 128, 64, [70, 5, 200], [4, 4, 4]), (1, 8, 128, 16, [900, 33], [4, 2]),
+    (1, 5, 64, 128, [400, 3, 77], [3, 5, 0]), (2, 8, 128, 32, [1111, 64], [8, 5]), (1, 64, 128, 64, [333], [1]),
+    (1, 3, 128, 64, [3000, 40], [20, 17])])
+def test_attention_of_a_few_tokens(HK, G, D, bs, lens, news):
+    c = _attn_case(HK, G, D, bs, lens, news, sum(lens) + D)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+    if all(m == 1 for m in news):
+        o2, lse2, _ = _attn_run(c, use_cu=False)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    o3, lse3, _ = _attn_run(c)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+@pytest.mark.parametrize("HK,G,D,bs,lens,news", [
+    (1, 1, 128, 64, [129], [129]), (2, 4, 128, 64, [500, 64, 130], [300, 64, 1]), (1, 8, 128, 16, [257, 700], [257, 33]),
+    (1, 7, 64, 32, [333, 90, 1], [150, 90, 1]), (2, 2, 64, 128, [640], [513]), (1, 4, 128, 128, [1000, 300], [100, 299]),
+    (1, 16, 64, 16, [200], [77])])
+def test_attention_of_many_tokens(HK, G, D, bs, lens, news):
+    c = _attn_case(HK, G, D, bs, lens, news, sum(lens) + D + 1)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+    o3, lse3, _ = _attn_run(c)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+@pytest.mark.parametrize("news", [[4, 6, 1], [150, 90, 33]])
+def test_attention_rows_that_see_nothing(news):
+    """Contexts shorter than the new tokens: the first tokens see nothing, their rows are 0 and -inf."""
+    c = _attn_case(2, 4, 128, 16, [max(1, news[0] - 3), 0, news[2]], news, 9)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+
+
+@pytest.mark.parametrize("news", [[3, 4], [200, 170]])
+def test_attention_nan_that_only_later_rows_see(news):
+    """NaN in a key or value reaches exactly the rows, and for a value the columns, that see it."""
+    lens = [news[0] + 40, news[1]]
+    c = _attn_case(1, 4, 128, 64, lens, news, 21)
+    at = lens[0] - 2                      # the last but one key of request 0: its first rows do not see it
+    c["vc"].view(torch.uint8)[c["table"][0][at // 64], 0, at % 64, 5] = 0xff
+    at = lens[0] - 1
+    c["kc"].view(torch.uint8)[c["table"][0][at // 64], 0, at % 64, 9] = 0x7f
+    at = 1
+    c["vc"].view(torch.uint8)[c["table"][1][at // 64], 0, at % 64, 77] = 0x7f
+    o, lse, st = _attn_run(c)
+    got = torch.isnan(o).cpu()
+    ref = torch.zeros_like(got)
+    ref[news[0] - 2:news[0], :, 5] = True
+    ref[news[0] - 1] = True
+    ref[news[0] + 1:, :, 77] = True
+    assert torch.equal(got, ref)
+
+
+def test_attention_scales_of_very_different_pages():
+    """Pages whose scales lie 2^80 apart, on both sides; logits in the hundreds; a tiny and a zero query."""
+    c = _attn_case(2, 4, 128, 16, [200, 90], [1, 3], 33)
+    e = torch.randint(-40, 40, c["vs"].shape, generator=_gen(1))
+    c["vs"] = torch.ldexp(torch.ones_like(c["vs"]), e)
+    c["q"][0] *= 64
+    c["q"][1] = 0
+    c["q"][2] = (c["q"][2].float() * 1e-30).to(BF)
+    o, lse, st = _attn_run(c)
+    _attn_check(c, o, lse)
+    o, lse, st = _attn_run(c, scale=0.5)
+    _attn_check(c, o, lse, scale=0.5)
+
+
+def test_attention_query_not_finite_and_missing_pages():
+    gdn = _gdn()
+    c = _attn_case(1, 4, 128, 64, [130, 130], [1, 1], 41)
+    c["q"][0, 1, 3] = float("inf")
+    c["q"][1, 2, 3] = float("nan")
+    o, lse, st = _attn_run(c)
+    nan = torch.isnan(o).all(-1).cpu()
+    assert nan.tolist() == [[False, True, False, False], [False, False, True, False]]
+    c = _attn_case(1, 4, 128, 64, [130, 200], [1, 1], 43)
+    c["table"][0][1] = -1                       # keys 64..127 are not there
+    c["table"][1][0] = len(c["ks"]) + 5
+    o, lse, st = _attn_run(c)
+    assert st == gdn.DEV_BAD_SLOT
+    _attn_check(c, o, lse)
+
+
+def test_attention_bad_lengths_leave_others_alone():
+    gdn = _gdn()
+    c = _attn_case(1, 4, 128, 64, [130, 200], [2, 2], 44)
+    o, lse, _ = _attn_run(c)
+    d = dict(c)
+    d["lens"] = [-1, 200]
+    o2, lse2, st = _attn_run(d)
+    assert st == gdn.DEV_BAD_SEQ_LEN and torch.equal(o[2:], o2[2:]) and torch.equal(lse[2:], lse2[2:])
+    d["lens"], d["max_q"] = [130, 200], 1
+    _, _, st = _attn_run(d)
+    assert st == gdn.DEV_BAD_CU_SEQLENS
+    d = dict(c)
+    d["cu"] = [0, 3, 2]
+    _, _, st = _attn_run(d)
+    assert st == gdn.DEV_BAD_CU_SEQLENS
+
+
+def test_attention_strided_queries_other_stream_and_graph():
+    gdn = _gdn()
+    c = _attn_case(2, 4, 128, 64, [300, 900, 4000], [2, 1, 3], 51)
+    o, lse, _ = _attn_run(c)
+    wide = torch.zeros(6, 8 * 128 + 64, dtype=BF, device="cuda")
+    wide[:, :1024].copy_(c["q"].reshape(6, -1))
+    o2, lse2, _ = _attn_run(c, q=wide[:, :1024].view(6, 8, 128))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    args = [c["q"].cuda(), c["kc"].cuda(), c["vc"].cuda(), c["ks"].cuda(), c["vs"].cuda(), i(c["table"]), i(c["lens"])]
+    kw = dict(cu_seqlens=i(c["cu"]), max_q_len=3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o3 = gdn.gdn_kv8_attention(*args, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(o, o3)
+    out = torch.empty_like(o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_kv8_attention(*args, o=out, **kw)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out)
+
+
+def test_attention_in_a_cache_past_32_bit_offsets():
+    """Pages whose bytes lie beyond 2^32: the same answer as from a small cache."""
+    gdn = _gdn()
+    c = _attn_case(2, 4, 128, 64, [500, 77], [1, 130], 61, nan_past=False)
+    o, lse, _ = _attn_run(c)
+    P = (1 << 32) // (2 * 64 * 128) + 64
+    big = dict(c)
+    shift = P - len(c["ks"])
+    big["table"] = [[p + shift if p >= 0 else -1 for p in row] for row in c["table"]]
+    caches = []
+    for codes, sc in ((c["kc"], c["ks"]), (c["vc"], c["vs"])):
+        b = torch.empty(P, 2, 64, 128, dtype=torch.float8_e4m3fn, device="cuda")
+        b[shift:].view(torch.uint8).copy_(codes.view(torch.uint8))
+        s = torch.ones(P, 2, device="cuda")
+        s[shift:].copy_(sc)
+        caches.append((b, s))
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    o2 = gdn.gdn_kv8_attention(c["q"].cuda(), caches[0][0], caches[1][0], caches[0][1], caches[1][1], i(big["table"]), i(c["lens"]),
+                               cu_seqlens=i(c["cu"]), max_q_len=c["max_q"])
+    assert torch.equal(o, o2)
+    # and the write, to the last page
+    slots = i([(P - 1) * 64 + 3])
+    k = c["q"][:1, :2].cuda().contiguous()
+    before = caches[0][0][P - 1].float().cpu().numpy().astype(np.float64), caches[0][1][P - 1].cpu().numpy().astype(np.float64)
+    gdn.gdn_kv8_append(k, k, caches[0][0], caches[1][0], caches[0][1], caches[1][1], slots)
+    ref = U.append(U.f64(k), before[0][None], before[1][None], [3])
+    _same_cache(caches[0][0][P - 1:], caches[0][1][P - 1:], ref)
+
+
+def test_attention_wait_that_runs_out():
+    """The testing hook: every block's first wait runs out, the status says so, and the next call is right again."""
+    gdn = _gdn()
+    c = _attn_case(2, 4, 128, 64, [300, 90], [2, 140], 71)
+    o, lse, _ = _attn_run(c)
+    gdn.testing_force_wait_expiry(True)
+    try:
+        _, _, st = _attn_run(c)
+    finally:
+        gdn.testing_force_wait_expiry(False)
+    assert st == gdn.DEV_WAIT_TIMEOUT
+    o2, lse2, st = _attn_run(c)
+    assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
