@@ -38,71 +38,17 @@
 
 #include "gdn_chunk_shared.cuh"
 #include "gdn_common.cuh"
-#include "gdn_kv8.cuh"
+#include "gdn_kv8_attn.cuh"
 #include "gdn_sm103.cuh"
 
 namespace {
 
 using namespace gdn;
+using namespace gdnkv;
 
 constexpr int kKeys = 64;       // keys a stage
 constexpr int kConsumers = 4;   // consumer warps
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnArgs : gdn_host::Kv8AttnArgs {
-  int G;  // query heads a kv head
-  float scale_log2e;
-  int split;        // keys a split (a multiple of 64)
-  int max_splits;   // splits of the longest context
-  int row_cap;      // rows of partial results that a (request, kv head) has
-  float *part_o;    // [(n HK + h) row_cap + row][max_splits][D]
-  float2 *part_ml;  // [(n HK + h) row_cap + row][max_splits]: maximum, sum
-};
-
-// What one tile of rows [row0, row0 + count) of a request works on; rows are
-// (token, head of the group), token first.
-struct Span {
-  int t0, m;   // the request's tokens
-  int L;       // its context
-  int keys;    // keys that some row of the tile sees
-  int splits;  // at least 1
-  int bits;    // status bits of what is wrong with the request
-};
-// False: there is nothing to do.
-__device__ __forceinline__ bool request_span(const AttnArgs &a, int n, int row0, int count, Span &s) {
-  s.bits = 0;
-  s.t0 = n;
-  s.m = 1;
-  if (a.cu) {
-    const int c0 = a.cu[n], c1 = a.cu[n + 1];
-    if (c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0) || c1 - c0 > a.max_q) {
-      s.bits = GDN_DEV_BAD_CU_SEQLENS;
-      return false;
-    }
-    s.t0 = c0;
-    s.m = c1 - c0;
-  }
-  if (row0 >= s.m * a.G) return false;
-  s.L = a.seq_lens[n];
-  if (s.L < 0 || s.L > a.max_seq) {
-    s.bits = GDN_DEV_BAD_SEQ_LEN;
-    return false;
-  }
-  const int last = min(row0 + count, s.m * a.G) - 1;
-  s.keys = max(0, s.L - s.m + last / a.G + 1);
-  s.splits = max(1, (s.keys + a.split - 1) / a.split);
-  return true;
-}
-
-// Four columns of a finished row: o = acc / l, and the row's logsumexp.
-__device__ __forceinline__ void store_row4(const AttnArgs &a, int tok, int head, int D, int c, float4 acc, float top, float l) {
-  const int64_t row = (int64_t)tok * a.HQ + head;
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is 0
-  *reinterpret_cast<uint2 *>(a.o + row * D + c) =
-      make_uint2(gdn::pack_bf16(acc.x * inv, acc.y * inv), gdn::pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
-}
 
 template <int D, int MT>
 struct DecodeLay {
@@ -131,7 +77,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float ex2f(float x) { return gdnc::ex2(x); }
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -160,13 +105,6 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
-// Whether any of four codes is NaN (0x7f or 0xff).
-__device__ __forceinline__ uint32_t any_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
-  const uint32_t m = any_nan(w);       // bit 7 of every NaN byte
-  return w & ~((m >> 7) * 0xffu);
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2)
     kv8_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -177,19 +115,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = blockIdx.z, h = blockIdx.y, rt = blockIdx.x / a.max_splits, sp = blockIdx.x % a.max_splits;
+  const int n = blockIdx.z, h = blockIdx.y, sp = blockIdx.x;
   // The joining kernel's blocks may come in as soon as every block here has
   // started; they wait for this grid's results.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   Span s;
-  if (!request_span(a, n, rt * 16 * MT, 16 * MT, s)) {
+  if (!request_span(a, n, 0, 16 * MT, s)) {
     if (tid == 0 && s.bits) set_status(a.dev_status, s.bits);
     return;
   }
-  if (tid == 0 && s.bits) set_status(a.dev_status, s.bits);
-  if (sp >= s.splits) return;
-  const int row0 = rt * 16 * MT, L = s.L, m = s.m;
+  if (s.m * a.G > a.row_most || sp >= s.splits) return;
+  const int L = s.L, m = s.m;
+  constexpr int row0 = 0;
   const int k_begin = sp * a.split, k_end = min(s.keys, k_begin + a.split);
   const int stages = (max(0, k_end - k_begin) + kKeys - 1) / kKeys;
 
@@ -533,14 +471,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 // splits and are added at the end.
 constexpr int kJoinThreads = 128;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const AttnArgs a, int tile_rows) {
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const AttnArgs a) {
   constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
   __shared__ float4 so[GROUPS][LANES];
   __shared__ float sl[GROUPS], sm[GROUPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = blockIdx.z, h = blockIdx.y, row = blockIdx.x;
   Span s;
-  if (!request_span(a, n, row / tile_rows * tile_rows, tile_rows, s) || row >= s.m * a.G || s.splits == 1) return;
+  if (!request_span(a, n, 0, a.row_cap, s) || s.m * a.G > a.row_most || row >= s.m * a.G || s.splits == 1) return;
   const int64_t at = (((int64_t)n * a.HK + h) * a.row_cap + row) * a.max_splits;
   const int c = threadIdx.x % LANES, gr = threadIdx.x / LANES;
   float top = -INFINITY;
@@ -586,50 +524,32 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const AttnArgs a
 }
 
 // ---------------------------------------------------------------- host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                        cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
-  }();
-  return fn;
-}
-// Map over a cache [P HK][bs][D] of bytes, box {D, keys, 1}.
-bool cache_map(CUtensorMap *mp, const void *ptr, int D, int bs, int64_t planes, int keys) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)bs, (cuuint64_t)planes};
-  const cuuint64_t str[2] = {(cuuint64_t)D, (cuuint64_t)D * (cuuint64_t)bs};
-  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)keys, 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return fn(mp, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dim, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Rows of a tile (16, 32 or 64), keys a split and splits for a call's sizes.
+// How a call's requests are worked on, from its host bounds.  Requests of up to
+// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 16,
+// 32 or 64 rows a block, the others to kv8_prefill_kernel.  A call whose bounds
+// allow more than 64 rows may mix long and short requests (a serving step that
+// prefills some and decodes others): then those of at most 16 rows (64 where
+// the group itself is larger) stay with the first kernel, where a long context
+// of few rows is split over many blocks.
 struct DecodePlan {
-  int mt, tiles, split, max_splits, row_cap;
+  int mt, split, max_splits, row_cap, row_most;
 };
 DecodePlan plan_decode(int N, int HK, int G, int max_q, int max_seq) {
-  DecodePlan p;
+  DecodePlan p{};
   const int64_t rows = (int64_t)max_q * G;
-  p.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  p.tiles = (int)((rows + 16 * p.mt - 1) / (16 * p.mt));
-  p.row_cap = 16 * p.mt * p.tiles;
+  if (rows <= 64) p.row_most = (int)rows;
+  else if (N == 1 || G > 64) p.row_most = 0;
+  else p.row_most = G <= 16 ? 16 : 64;
+  if (p.row_most == 0) return p;
+  p.mt = p.row_most <= 16 ? 1 : p.row_most <= 32 ? 2 : 4;
+  p.row_cap = 16 * p.mt;
   const int64_t keys = ((int64_t)max_seq + kKeys - 1) / kKeys * kKeys;
-  int64_t want = (152 * 2 * 6) / ((int64_t)N * HK * p.tiles);  // six blocks for each place on the GPU
-  if (p.tiles > 1 || want < 1) want = 1;
+  int64_t want = (152 * 2 * 6) / ((int64_t)N * HK);  // six blocks for each place on the GPU
+  if (want < 1) want = 1;
   int64_t split = (keys + want - 1) / want;
   split = (split + kKeys - 1) / kKeys * kKeys;
   if (split < 4 * kKeys) split = 4 * kKeys;
-  if (p.tiles == 1 && split > 2048) split = 2048;
+  if (split > 2048) split = 2048;
   p.split = (int)(split < keys ? split : keys < kKeys ? kKeys : keys);
   p.max_splits = (int)((keys + p.split - 1) / p.split);
   if (p.max_splits < 1) p.max_splits = 1;
@@ -641,11 +561,12 @@ cudaError_t launch_decode(const AttnArgs &a, const DecodePlan &p, cudaStream_t s
   using Ly = DecodeLay<D, MT>;
   CUtensorMap mk, mv;
   const int keys = a.bs < kKeys ? a.bs : kKeys;
-  if (!cache_map(&mk, a.kc, D, a.bs, (int64_t)a.P * a.HK, keys) || !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys))
+  if (!cache_map(&mk, a.kc, D, a.bs, (int64_t)a.P * a.HK, keys, true) ||
+      !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys, true))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::BYTES);
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<D, MT><<<dim3((unsigned)p.max_splits * (unsigned)p.tiles, a.HK, a.N), kThreads, Ly::BYTES, s>>>(a, mk, mv);
+  kv8_decode_kernel<D, MT><<<dim3(p.max_splits, a.HK, a.N), kThreads, Ly::BYTES, s>>>(a, mk, mv);
   if ((e = cudaGetLastError()) != cudaSuccess || p.max_splits == 1) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -656,7 +577,7 @@ cudaError_t launch_decode(const AttnArgs &a, const DecodePlan &p, cudaStream_t s
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, a, 16 * MT);
+  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, a);
 }
 
 }  // namespace
@@ -666,7 +587,7 @@ namespace gdn_host {
 size_t kv8_attn_workspace_bytes(int N, int HK, int G, int D, int max_q, int max_seq) {
   if (N <= 0 || max_q <= 0) return 0;
   const DecodePlan p = plan_decode(N, HK, G, max_q, max_seq);
-  if (p.max_splits == 1) return 0;
+  if (p.max_splits <= 1) return 0;
   return (size_t)N * HK * p.row_cap * p.max_splits * (size_t)(D + 2) * sizeof(float);
 }
 
@@ -679,8 +600,14 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs &c, cudaStream_t s) {
   a.split = p.split;
   a.max_splits = p.max_splits;
   a.row_cap = p.row_cap;
+  a.row_most = p.row_most;
+  if (a.split < 1) a.split = kKeys;
   a.part_o = static_cast<float *>(c.ws);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)c.N * c.HK * p.row_cap * p.max_splits * c.D);
+  if ((int64_t)c.max_q * a.G > p.row_most) {
+    const cudaError_t e = launch_prefill(a, p.row_most + 1, s);
+    if (e != cudaSuccess || p.row_most == 0) return e;
+  }
   if (c.D == 128) {
     if (p.mt == 1) return launch_decode<128, 1>(a, p, s);
     if (p.mt == 2) return launch_decode<128, 2>(a, p, s);

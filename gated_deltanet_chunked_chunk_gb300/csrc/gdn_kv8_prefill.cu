@@ -1,0 +1,555 @@
+// gdn_kv8_prefill.cu -- attention over the paged 8-bit cache for many rows a
+// request (prompts and their chunks), on tcgen05.  The mathematics and the
+// number formats are those of gdn_kv8_attn.cu.
+//
+// Bound: the tensor cores, 4 keys D operations for each (row, key, value) pair
+// that a row sees.  One block works on 256 rows of one (request, kv head), rows
+// being (token, head of the group) pairs, so that the head's group shares the
+// keys and values it loads: two tiles of 128 rows, whose softmaxes take turns
+// on the tensor cores' two accumulators.
+//
+// Products.  S = Q K^T takes the cache's bytes as they stand: kind::f8f6f4 with
+// Q, brought to a largest magnitude of 128 to 256 by a power of two for each
+// row, as the sum of two e4m3 numbers.  A bf16 number has 8 significant bits
+// and an e4m3 number 4, so high part and remainder are exact but for elements
+// under 2^-9 of 256.  Two products at twice the 16-bit rate cost what one f16
+// product would, and no key is converted.  O = P V is kind::f16: P in f16 from
+// tensor memory (11 bits; e4m3 would leave 4), V widened to f16 (exact) by four
+// warps, once for both tiles.
+//
+// Warps: 0-3 and 4-7 softmax of the two tiles (a thread holds one row: its 128
+// logits come from tensor memory to registers, no shuffles), 8-11 widen V, 12
+// brings pages by TMA, 13 and 14 issue the products of the two tiles.  Tensor
+// memory (512 columns): S of both tiles, P in place of its S, O of both tiles.
+// An S of the next key tile is issued right after the P V that last read its
+// columns; products of one thread execute in order, so "S is there" also says
+// that O may be touched.  O is rescaled only when the running maximum grew by
+// more than 8 (p' <= 256 is safe in f16), by the softmax warps themselves.
+#include "gdn_kv8_attn.cuh"
+
+namespace {
+
+using namespace gdn;
+using namespace gdnkv;
+
+constexpr int kTileKeys = 128;
+constexpr int kPrefThreads = 512;
+constexpr int kParSlots = 8;  // key tiles whose page constants are kept: more than can be in flight
+
+template <int D>
+struct PrefLay {
+  static constexpr int T8 = 128 * D;   // bytes of a K, V or Q-part tile
+  static constexpr int T16 = 256 * D;  // bytes of a widened V tile
+  static constexpr int NK = 3, NV = 2, NW = 2;
+  static constexpr int OFF_Q = 0;  // tile 0 high, low, tile 1 high, low
+  static constexpr int OFF_K = OFF_Q + 4 * T8;
+  static constexpr int OFF_W = OFF_K + NK * T8;
+  static constexpr int OFF_V = OFF_W + NW * T16;
+  static constexpr int OFF_PAR = OFF_V + NV * T8;  // float4 {k scale, lv, 2^-lv, 0} x 8 pages a slot
+  static constexpr int OFF_BAR = OFF_PAR + kParSlots * 128;
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NW + 10 + kParSlots;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
+  static constexpr int BYTES = OFF_MISC + 32;
+  static_assert(BYTES <= 227 * 1024, "one block an SM");
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+// K-major shared-memory descriptor of rows of D bytes as TMA swizzles them.
+template <int D> __device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFF);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>((8 * D) >> 4) << 32;  // 8 rows
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(D == 128 ? 2 : 4) << 61;  // 128-byte, 64-byte swizzle
+  return d;
+}
+constexpr uint32_t idesc_f32(int M, int N, int b_mn) {  // f16 (kind::f16) or e4m3 (kind::f8f6f4) operands, fp32 result
+  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// A (128 rows x 16 f16) from tensor memory.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Ties 32 registers to the wait before it.
+__device__ __forceinline__ void tie32(uint32_t *r) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mov.b64 z, {%5, %5}; fma.rn.f32x2 x, x, y, z; "
+      "mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+// Waits for a barrier's phase; gives up after the limit or once another warp has.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *failed, int32_t *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long from = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*failed) return false;
+    if (clock64() - from > gdnc::kWaitLimit) {
+      *failed = 1;
+      set_status(status, GDN_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrefThreads, 1)
+    kv8_prefill_kernel(const AttnArgs a, int min_rows, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using Ly = PrefLay<D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the last tokens' blocks, which see the most keys, start first
+  const int n = blockIdx.z, h = blockIdx.y, row0 = (int)(gridDim.x - 1 - blockIdx.x) * 256;
+  Span s;
+  if (!request_span(a, n, row0, 256, s)) {
+    if (tid == 0 && s.bits) set_status(a.dev_status, s.bits);
+    return;
+  }
+  const int rows = s.m * a.G, L = s.L;
+  if (rows < min_rows) return;  // the other kernel's
+  const int tiles = (s.keys + kTileKeys - 1) / kTileKeys;
+  const int low = L - s.m + row0 / a.G;  // what the first row sees last
+
+  const uint32_t bar = sb + Ly::OFF_BAR;
+  auto KF = [&](int i) { return bar + 8 * i; };
+  auto KE = [&](int i) { return bar + 8 * (Ly::NK + i); };
+  auto VF = [&](int i) { return bar + 8 * (2 * Ly::NK + i); };
+  auto VE = [&](int i) { return bar + 8 * (2 * Ly::NK + Ly::NV + i); };
+  auto WF = [&](int i) { return bar + 8 * (2 * Ly::NK + 2 * Ly::NV + i); };
+  auto WE = [&](int i) { return bar + 8 * (2 * Ly::NK + 2 * Ly::NV + Ly::NW + i); };
+  const uint32_t bx = bar + 8 * (2 * Ly::NK + 2 * Ly::NV + 2 * Ly::NW);
+  auto SF = [&](int w) { return bx + 8 * w; };
+  auto PF = [&](int w) { return bx + 16 + 8 * w; };
+  auto OD = [&](int w) { return bx + 32 + 8 * w; };
+  const uint32_t QR = bx + 48, never = bx + 56;
+  auto DR = [&](int w) { return bx + 64 + 8 * w; };
+  auto PR = [&](int i) { return bx + 80 + 8 * i; };
+  volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_MISC);
+  volatile int *nan_zone = failed + 1;
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
+  if (tid == 0) {
+    for (int i = 0; i < Ly::NK; ++i) { mbar_init(KF(i), 1); mbar_init(KE(i), 2); }
+    for (int i = 0; i < Ly::NV; ++i) { mbar_init(VF(i), 1); mbar_init(VE(i), 4); }
+    for (int i = 0; i < Ly::NW; ++i) { mbar_init(WF(i), 4); mbar_init(WE(i), 2); }
+    for (int i = 0; i < 2; ++i) { mbar_init(SF(i), 1); mbar_init(PF(i), 128); mbar_init(OD(i), 1); mbar_init(DR(i), 1); }
+    for (int i = 0; i < kParSlots; ++i) mbar_init(PR(i), 1);
+    mbar_init(QR, 256);
+    mbar_init(never, 1);
+    mbar_fence_init();
+    *failed = 0;
+    *nan_zone = 0;
+  }
+  if (warp == 13) tmem_alloc(sb + Ly::OFF_MISC + 8, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Of the block's 65536 registers (512 threads x 128) the softmax warps take
+  // 192 a thread, the other warps 64: 2 x 128 x 192 + 2 x 128 x 64 = 65536.
+  float m_ref = -INFINITY, l_sum = 0.f;
+  int issued_k = 0, issued_v = 0;  // key tiles that the producer has issued
+  const int wg = warp >> 2;
+  const int row = row0 + (wg & 1) * 128 + (tid & 127);
+  const bool on = wg < 2 && row < rows;
+  const int limit = on ? L - s.m + row / a.G : -1;
+  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+  const uint32_t S_col = tmem + lanes + (wg & 1) * 128, O_col = tmem + lanes + 256 + (wg & 1) * D;
+
+  if (wg < 2) {
+    // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    float krow;
+    {
+      // the row's query: largest magnitude, then high and low parts
+      const uint16_t *src = a.q + (int64_t)(s.t0 + row / a.G) * a.ldq + (int64_t)(h * a.G + row % a.G) * D;
+      uint4 u[D / 8];
+      float top = 0.f, bad = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        u[i] = on ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = bf16lo_f(w[e]), y = bf16hi_f(w[e]);
+          top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+          bad = fmaf(x, 0.f, fmaf(y, 0.f, bad));  // NaN once an element is not finite
+        }
+      }
+      int e2 = (int)(__float_as_uint(top) >> 23) - 127;
+      e2 = e2 < -100 ? -100 : e2 > 120 ? 120 : e2;
+      const float down = pow2(7 - e2);
+      krow = pow2(e2 - 7) * a.scale_log2e + bad;
+      const uint32_t qh = sb + Ly::OFF_Q + wg * 2 * Ly::T8, ql = qh + Ly::T8;
+      const uint32_t r = tid & 127;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 &v = u[2 * c + (e >> 1)];
+          const uint32_t w0 = (e & 1) ? v.z : v.x, w1 = (e & 1) ? v.w : v.y;
+          const float x0 = bf16lo_f(w0) * down, x1 = bf16hi_f(w0) * down, x2 = bf16lo_f(w1) * down, x3 = bf16hi_f(w1) * down;
+          const uint32_t h0 = cvt_e4m3x2(x0, x1), h1 = cvt_e4m3x2(x2, x3);
+          const float2 b0 = f16x2_f32(e4m3x2_f16x2(h0)), b1 = f16x2_f32(e4m3x2_f16x2(h1));
+          hi[e] = h0 | (h1 << 16);
+          lo[e] = cvt_e4m3x2(x0 - b0.x, x1 - b0.y) | (cvt_e4m3x2(x2 - b1.x, x3 - b1.y) << 16);
+        }
+        const uint32_t at = D == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
+        sts128(qh + at, hi[0], hi[1], hi[2], hi[3]);
+        sts128(ql + at, lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(QR);
+    }
+    bool ok = true;
+    if (a.force_expiry && !mbar_wait_bounded(never, 0, gdnc::kTestWaitLimit)) {
+      *failed = 1;
+      set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
+      ok = false;
+    }
+    for (int j = 0; j < tiles; ++j) {
+      if (ok) ok = wait_bar(PR(j % kParSlots), (j / kParSlots) & 1, failed, a.dev_status);
+      if (ok) ok = wait_bar(SF(wg), j & 1, failed, a.dev_status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      uint32_t r[128];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32_issue(S_col + 32 * i, r + 32 * i);
+      tmem_ld_wait(r);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) tie32(r + 32 * i);
+
+      const uint32_t par = sb + Ly::OFF_PAR + (j % kParSlots) * 128;
+      const int k0 = j * kTileKeys;
+      const bool masked = k0 + kTileKeys - 1 > low;
+      float c[8], b[8], iv[8], top = -INFINITY;  // constants of 16 keys each
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        const float4 f = lds_f4(par + (16 * g / a.bs) * 16);
+        c[g] = krow * f.x;
+        b[g] = f.y;
+        iv[g] = f.z;
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float t = fmaf(__uint_as_float(r[16 * g + i]), c[g], b[g]);
+            if (k0 + 16 * g + i > limit) t = -INFINITY;
+            top = fmaxf(top, t);
+            r[16 * g + i] = __float_as_uint(t);
+          }
+          c[g] = 1.f;  // t itself from here on
+          b[g] = 0.f;
+        } else {
+          float x = __uint_as_float(r[16 * g]);
+#pragma unroll
+          for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(r[16 * g + i]));
+          top = fmaxf(top, fmaf(x, c[g], b[g]));
+        }
+      }
+      float grow = 1.f;
+      if (top > m_ref + 8.f || (m_ref == -INFINITY && top > -INFINITY)) {
+        grow = ex2f(m_ref - top);
+        m_ref = top;
+        l_sum *= grow;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          tmem_ld32_issue(O_col + i, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * grow);
+          tmem_st32(O_col + i, o);
+        }
+      }
+      const float base = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        float2 sum = make_float2(0.f, 0.f);
+        const float bb = b[g] - base;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float2 t = fma2(make_float2(__uint_as_float(r[16 * g + 2 * i]), __uint_as_float(r[16 * g + 2 * i + 1])), c[g], bb);
+          t.x = ex2f(t.x);
+          t.y = ex2f(t.y);
+          sum = add2(sum, t);
+          r[8 * g + i] = pack_f16(t.x, t.y);
+        }
+        l_sum = fmaf(sum.x + sum.y, iv[g], l_sum);
+        if (g == 3) tmem_st32(S_col, r);
+      }
+      tmem_st32(S_col + 32, r + 32);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(PF(wg));
+    }
+    if (ok && tiles > 0) ok = wait_bar(OD(wg), 0, failed, a.dev_status);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (wg == 2) {
+      // ------------------------------------------------------------ widen V
+      const int ct = tid - 256;
+      for (int j = 0; j < tiles; ++j) {
+        const int iv = j % Ly::NV, iw = j % Ly::NW;
+        bool ok = wait_bar(VF(iv), (j / Ly::NV) & 1, failed, a.dev_status);
+        if (ok && j >= Ly::NW) ok = wait_bar(WE(iw), (j / Ly::NW - 1) & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t src = sb + Ly::OFF_V + iv * Ly::T8, dst = sb + Ly::OFF_W + iw * Ly::T16;
+        const int k0 = j * kTileKeys;
+        const bool zone = k0 + kTileKeys - 1 > low;
+        uint32_t seen = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int e = i * 128 + ct, key = e / (D / 16), ch = e % (D / 16);
+          uint4 u = lds128(src + key * D + ch * 16);
+          if (zone) {
+            // keys past the context, and NaN that only later rows may see: see
+            // gdn_kv8_attn.cu
+            if (k0 + key >= L) u = make_uint4(0, 0, 0, 0);
+            seen |= any_nan(u.x) | any_nan(u.y) | any_nan(u.z) | any_nan(u.w);
+            u = make_uint4(drop_nan(u.x), drop_nan(u.y), drop_nan(u.z), drop_nan(u.w));
+          }
+          const uint32_t base = dst + (ch >> 2) * 16384 + key * 128;
+          const uint32_t c0 = (((ch & 3) * 2) ^ (key & 7)) << 4, c1 = (((ch & 3) * 2 + 1) ^ (key & 7)) << 4;
+          const uint32_t x0 = e4m3x2_f16x2(u.x), x1 = e4m3x2_f16x2(u.x >> 16), x2 = e4m3x2_f16x2(u.y), x3 = e4m3x2_f16x2(u.y >> 16);
+          const uint32_t y0 = e4m3x2_f16x2(u.z), y1 = e4m3x2_f16x2(u.z >> 16), y2 = e4m3x2_f16x2(u.w), y3 = e4m3x2_f16x2(u.w >> 16);
+          // the upper 64 columns write their halves in the other order: the
+          // eight lanes of a row then meet eight different places
+          const bool sw = (ch >> 2) & 1;
+          sts128(base + (sw ? c1 : c0), sw ? y0 : x0, sw ? y1 : x1, sw ? y2 : x2, sw ? y3 : x3);
+          sts128(base + (sw ? c0 : c1), sw ? x0 : y0, sw ? x1 : y1, sw ? x2 : y2, sw ? x3 : y3);
+        }
+        if (seen) *nan_zone = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(VE(iv));
+          mbar_arrive(WF(iw));
+        }
+      }
+    } else if (warp == 12) {
+      // ----------------------------------------------------------- producer
+      const int ppt = a.bs >= kTileKeys ? 1 : kTileKeys / a.bs, box = kTileKeys / ppt;
+      int batch = -1, page = -1;
+      float ks = 0.f, lv = 0.f, iv = 1.f;
+      for (int j = 0; j < tiles; ++j) {
+        const int first = j * ppt;
+        if (first / 32 != batch) {
+          batch = first / 32;
+          const int pi = batch * 32 + lane;
+          page = -1;
+          ks = 0.f;
+          lv = -INFINITY;
+          iv = 1.f;
+          if ((int64_t)pi * a.bs < s.keys) {
+            const int32_t p = a.table[(int64_t)n * a.width + pi];
+            if (p < 0 || p >= a.P) {
+              set_status(a.dev_status, GDN_DEV_BAD_SLOT);
+            } else {
+              page = p;
+              const int64_t at = (int64_t)p * a.HK + h;
+              ks = a.ks[at];
+              const float v = a.vs[at];
+              lv = log2f(v);
+              iv = 1.f / v;
+            }
+          }
+        }
+        const int ik = j % Ly::NK, vi = j % Ly::NV;
+        bool ok = true;
+        if (j >= Ly::NK) ok = wait_bar(KE(ik), (j / Ly::NK - 1) & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int src = (first - batch * 32 + (lane & (ppt - 1))) & 31;
+        const int pg = __shfl_sync(0xffffffffu, page, src);
+        const float4 par = make_float4(__shfl_sync(0xffffffffu, ks, src), __shfl_sync(0xffffffffu, lv, src),
+                                       __shfl_sync(0xffffffffu, iv, src), 0.f);
+        if (lane < ppt) *reinterpret_cast<float4 *>(smem + Ly::OFF_PAR + (j % kParSlots) * 128 + lane * 16) = par;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(PR(j % kParSlots));
+          mbar_arrive_expect_tx(KF(ik), Ly::T8);
+        }
+        __syncwarp();
+        const int z = pg >= 0 ? pg * a.HK + h : a.P * a.HK;  // outside the tensor: zeros
+        if (lane < ppt) tma_load_3d(sb + Ly::OFF_K + ik * Ly::T8 + lane * box * D, &mk, KF(ik), 0, 0, z);
+        issued_k = j + 1;
+        if (j >= Ly::NV) ok = wait_bar(VE(vi), (j / Ly::NV - 1) & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (lane == 0) mbar_arrive_expect_tx(VF(vi), Ly::T8);
+        __syncwarp();
+        if (lane < ppt) tma_load_3d(sb + Ly::OFF_V + vi * Ly::T8 + lane * box * D, &mv, VF(vi), 0, 0, z);
+        issued_v = j + 1;
+      }
+    } else if (warp < 15) {
+      // ----------------------------------------------------------- products
+      const int w = warp - 13;
+      if (tiles > 0 && elect_one()) {
+        constexpr uint32_t id_s = idesc_f32(128, 128, 0), id_o = idesc_f32(128, D, 1);
+        const uint64_t qh = desc_rows<D>(sb + Ly::OFF_Q + w * 2 * Ly::T8), ql = desc_rows<D>(sb + Ly::OFF_Q + w * 2 * Ly::T8 + Ly::T8);
+        const uint32_t S = tmem + w * 128, O = tmem + 256 + w * D;
+        auto logits = [&](int j) {
+          const int ik = j % Ly::NK;
+          if (!wait_bar(KF(ik), (j / Ly::NK) & 1, failed, a.dev_status)) return false;
+          tc_fence_after();
+          const uint64_t kd = desc_rows<D>(sb + Ly::OFF_K + ik * Ly::T8);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) umma_f8(S, qh + 2 * kk, kd + 2 * kk, id_s, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) umma_f8(S, ql + 2 * kk, kd + 2 * kk, id_s, 1);
+          umma_commit(SF(w));
+          umma_commit(KE(ik));
+          return true;
+        };
+        bool ok = wait_bar(QR, 0, failed, a.dev_status) && logits(0);
+        for (int j = 0; ok && j < tiles; ++j) {
+          const int iw = j % Ly::NW;
+          ok = wait_bar(WF(iw), (j / Ly::NW) & 1, failed, a.dev_status) && wait_bar(PF(w), j & 1, failed, a.dev_status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = umma_desc_sw128_mn(sb + Ly::OFF_W + iw * Ly::T16, 16384);
+#pragma unroll
+          for (int kk = 0; kk < kTileKeys / 16; ++kk) umma_f16_ta(O, S + 8 * kk, vd + 128 * kk, id_o, j > 0 || kk > 0);
+          umma_commit(WE(iw));
+          if (j + 1 < tiles) ok = logits(j + 1);
+          else umma_commit(OD(w));
+        }
+        if (!ok) {  // let this warp's products finish before the block leaves
+          umma_commit(DR(w));
+          if (!mbar_wait_bounded(DR(w), 0, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  __syncthreads();
+  if (*failed) {
+    if (warp == 12 && lane == 0) {  // copies in flight
+      bool ok = true;
+      for (int i = 0; i < Ly::NK && i < issued_k; ++i)
+        ok &= mbar_wait_bounded(KF(i), ((issued_k - 1 - i) / Ly::NK) & 1, gdnc::kWaitLimit);
+      for (int i = 0; i < Ly::NV && i < issued_v; ++i)
+        ok &= mbar_wait_bounded(VF(i), ((issued_v - 1 - i) / Ly::NV) & 1, gdnc::kWaitLimit);
+      if (!ok) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
+    }
+    __syncthreads();
+    if (warp == 13) tmem_dealloc(tmem, 512);
+    return;
+  }
+  if (wg < 2) {
+    // ---------------------------------------------------------------- output
+    tc_fence_after();
+    const int tok = s.t0 + row / a.G, head = h * a.G + row % a.G;
+    const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+    uint16_t *dst = a.o + ((int64_t)tok * a.HQ + head) * D;
+    const bool zone = *nan_zone != 0;
+#pragma unroll 1
+    for (int i = 0; i < D; i += 32) {
+      uint32_t o[32];
+      if (tiles > 0) {
+        tmem_ld32_issue(O_col + i, o);
+        tmem_ld_wait(o);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = tiles > 0 && l_sum != 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+      if (zone && on) {  // NaN values in the keys of the masked zone that this row does see
+        for (int key = max(0, low + 1 - kTileKeys) / kTileKeys * kTileKeys; key <= limit; ++key) {
+          const int32_t p = a.table[(int64_t)n * a.width + key / a.bs];
+          if (p < 0 || p >= a.P) continue;
+          const uint8_t *v = a.vc + (((int64_t)p * a.HK + h) * a.bs + key % a.bs) * D + i;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if ((v[e] & 0x7f) == 0x7f) o[e] = 0x7fc00000u;
+        }
+      }
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4 *>(dst + i + e) =
+              make_uint4(pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                         pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+      }
+    }
+    if (on && a.lse) a.lse[(int64_t)tok * a.HQ + head] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs &a, int min_rows, cudaStream_t s) {
+  using Ly = PrefLay<D>;
+  CUtensorMap mk, mv;
+  const int keys = a.bs < kTileKeys ? a.bs : kTileKeys;
+  if (!cache_map(&mk, a.kc, D, a.bs, (int64_t)a.P * a.HK, keys, true) || !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys, false))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)a.max_q * a.G;
+  kv8_prefill_kernel<D><<<dim3((unsigned)((rows + 255) / 256), a.HK, a.N), kPrefThreads, Ly::BYTES, s>>>(a, min_rows, mk, mv);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace gdnkv {
+cudaError_t launch_prefill(const AttnArgs &a, int min_rows, cudaStream_t s) {
+  return a.D == 128 ? launch<128>(a, min_rows, s) : launch<64>(a, min_rows, s);
+}
+}  // namespace gdnkv
