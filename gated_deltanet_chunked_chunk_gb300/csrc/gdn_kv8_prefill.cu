@@ -19,7 +19,7 @@
 //
 // Warps: 0-3 and 4-7 softmax of the two tiles (a thread holds one row: its 128
 // logits come from tensor memory to registers, no shuffles), 8-11 widen V, 12
-// brings pages by TMA, 13 and 14 issue the products of the two tiles.  Tensor
+// brings pages by TMA, 13 issues the products.  Tensor
 // memory (512 columns): S of both tiles, P in place of its S, O of both tiles.
 // An S of the next key tile is issued right after the P V that last read its
 // columns; products of one thread execute in order, so "S is there" also says
@@ -115,6 +115,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -162,6 +167,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   if (rows < min_rows) return;  // the other kernel's
   const int tiles = (s.keys + kTileKeys - 1) / kTileKeys;
   const int low = L - s.m + row0 / a.G;  // what the first row sees last
+  const int page_bits = 31 - __clz(a.bs);
 
   const uint32_t bar = sb + Ly::OFF_BAR;
   auto KF = [&](int i) { return bar + 8 * i; };
@@ -175,18 +181,19 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   auto PF = [&](int w) { return bx + 16 + 8 * w; };
   auto OD = [&](int w) { return bx + 32 + 8 * w; };
   const uint32_t QR = bx + 48, never = bx + 56;
-  auto DR = [&](int w) { return bx + 64 + 8 * w; };
+  const uint32_t DR = bx + 64;
   auto PR = [&](int i) { return bx + 80 + 8 * i; };
   volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_MISC);
   volatile int *nan_zone = failed + 1;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
   if (tid == 0) {
-    for (int i = 0; i < Ly::NK; ++i) { mbar_init(KF(i), 1); mbar_init(KE(i), 2); }
+    for (int i = 0; i < Ly::NK; ++i) { mbar_init(KF(i), 1); mbar_init(KE(i), 1); }
     for (int i = 0; i < Ly::NV; ++i) { mbar_init(VF(i), 1); mbar_init(VE(i), 4); }
-    for (int i = 0; i < Ly::NW; ++i) { mbar_init(WF(i), 4); mbar_init(WE(i), 2); }
-    for (int i = 0; i < 2; ++i) { mbar_init(SF(i), 1); mbar_init(PF(i), 128); mbar_init(OD(i), 1); mbar_init(DR(i), 1); }
+    for (int i = 0; i < Ly::NW; ++i) { mbar_init(WF(i), 4); mbar_init(WE(i), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(SF(i), 1); mbar_init(PF(i), 128); mbar_init(OD(i), 1); }
     for (int i = 0; i < kParSlots; ++i) mbar_init(PR(i), 1);
     mbar_init(QR, 256);
+    mbar_init(DR, 1);
     mbar_init(never, 1);
     mbar_fence_init();
     *failed = 0;
@@ -279,11 +286,14 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       float c[8], b[8], iv[8], top = -INFINITY;  // constants of 16 keys each
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
-        const float4 f = lds_f4(par + (16 * g / a.bs) * 16);
+        const float4 f = lds_f4(par + ((16 * g) >> page_bits) * 16);
         c[g] = krow * f.x;
         b[g] = f.y;
         iv[g] = f.z;
-        if (masked) {
+      }
+      if (masked) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float t = fmaf(__uint_as_float(r[16 * g + i]), c[g], b[g]);
@@ -293,11 +303,17 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
           }
           c[g] = 1.f;  // t itself from here on
           b[g] = 0.f;
-        } else {
-          float x = __uint_as_float(r[16 * g]);
+        }
+      } else {
 #pragma unroll
-          for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(r[16 * g + i]));
-          top = fmaxf(top, fmaf(x, c[g], b[g]));
+        for (int g = 0; g < 8; ++g) {
+          float x[5];
+#pragma unroll
+          for (int i = 0; i < 5; ++i)
+            x[i] = max3(__uint_as_float(r[16 * g + 3 * i]), __uint_as_float(r[16 * g + 3 * i + 1]), __uint_as_float(r[16 * g + 3 * i + 2]));
+          x[0] = max3(x[0], x[1], x[2]);
+          x[3] = max3(x[3], x[4], __uint_as_float(r[16 * g + 15]));
+          top = fmaxf(top, fmaf(fmaxf(x[0], x[3]), c[g], b[g]));
         }
       }
       float grow = 1.f;
@@ -435,42 +451,54 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
         if (lane < ppt) tma_load_3d(sb + Ly::OFF_V + vi * Ly::T8 + lane * box * D, &mv, VF(vi), 0, 0, z);
         issued_v = j + 1;
       }
-    } else if (warp < 15) {
+    } else if (warp == 13) {
       // ----------------------------------------------------------- products
-      const int w = warp - 13;
+      // One thread issues for both tiles, P V and then the next S of one tile
+      // before the other's: the tensor cores work in that order, so a tile's
+      // softmax runs while they have the other tile.  (Two issuing warps share
+      // the tensor cores evenly, so that both tiles wait, and compute, at the
+      // same time: 1.05 ms against 0.80 for 4096 tokens over 16384 keys.)
       if (tiles > 0 && elect_one()) {
         constexpr uint32_t id_s = idesc_f32(128, 128, 0), id_o = idesc_f32(128, D, 1);
-        const uint64_t qh = desc_rows<D>(sb + Ly::OFF_Q + w * 2 * Ly::T8), ql = desc_rows<D>(sb + Ly::OFF_Q + w * 2 * Ly::T8 + Ly::T8);
-        const uint32_t S = tmem + w * 128, O = tmem + 256 + w * D;
-        auto logits = [&](int j) {
+        const uint64_t q0 = desc_rows<D>(sb + Ly::OFF_Q);
+        auto logits = [&](int w, int j) {
           const int ik = j % Ly::NK;
-          if (!wait_bar(KF(ik), (j / Ly::NK) & 1, failed, a.dev_status)) return false;
-          tc_fence_after();
+          if (w == 0) {
+            if (!wait_bar(KF(ik), (j / Ly::NK) & 1, failed, a.dev_status)) return false;
+            tc_fence_after();
+          }
           const uint64_t kd = desc_rows<D>(sb + Ly::OFF_K + ik * Ly::T8);
+          const uint64_t qh = q0 + w * (2 * Ly::T8 / 16), ql = qh + Ly::T8 / 16;
+          const uint32_t S = tmem + w * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) umma_f8(S, qh + 2 * kk, kd + 2 * kk, id_s, kk > 0);
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk) umma_f8(S, ql + 2 * kk, kd + 2 * kk, id_s, 1);
           umma_commit(SF(w));
-          umma_commit(KE(ik));
+          if (w == 1) umma_commit(KE(ik));
           return true;
         };
-        bool ok = wait_bar(QR, 0, failed, a.dev_status) && logits(0);
+        bool ok = wait_bar(QR, 0, failed, a.dev_status) && logits(0, 0) && logits(1, 0);
         for (int j = 0; ok && j < tiles; ++j) {
           const int iw = j % Ly::NW;
-          ok = wait_bar(WF(iw), (j / Ly::NW) & 1, failed, a.dev_status) && wait_bar(PF(w), j & 1, failed, a.dev_status);
-          if (!ok) break;
-          tc_fence_after();
           const uint64_t vd = umma_desc_sw128_mn(sb + Ly::OFF_W + iw * Ly::T16, 16384);
+          ok = wait_bar(WF(iw), (j / Ly::NW) & 1, failed, a.dev_status);
 #pragma unroll
-          for (int kk = 0; kk < kTileKeys / 16; ++kk) umma_f16_ta(O, S + 8 * kk, vd + 128 * kk, id_o, j > 0 || kk > 0);
-          umma_commit(WE(iw));
-          if (j + 1 < tiles) ok = logits(j + 1);
-          else umma_commit(OD(w));
+          for (int w = 0; w < 2; ++w) {
+            ok = ok && wait_bar(PF(w), j & 1, failed, a.dev_status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t P = tmem + w * 128, O = tmem + 256 + w * D;
+#pragma unroll
+            for (int kk = 0; kk < kTileKeys / 16; ++kk) umma_f16_ta(O, P + 8 * kk, vd + 128 * kk, id_o, j > 0 || kk > 0);
+            if (w == 1) umma_commit(WE(iw));
+            if (j + 1 < tiles) ok = logits(w, j + 1);
+            else umma_commit(OD(w));
+          }
         }
-        if (!ok) {  // let this warp's products finish before the block leaves
-          umma_commit(DR(w));
-          if (!mbar_wait_bounded(DR(w), 0, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
+        if (!ok) {  // let the products in flight finish before the block leaves
+          umma_commit(DR);
+          if (!mbar_wait_bounded(DR, 0, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
         }
       }
       __syncwarp();
