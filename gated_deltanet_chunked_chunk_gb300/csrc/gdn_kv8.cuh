@@ -43,6 +43,12 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+// Four codes as two f16x2 pairs.
+__device__ __forceinline__ void e4m3x4_f16x2(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
 __device__ __forceinline__ float2 f16x2_f32(uint32_t h) {
   float2 r;
   asm("{ .reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }" : "=f"(r.x), "=f"(r.y) : "r"(h));

@@ -10,61 +10,74 @@
 //   t_ij = log2(e) scale ks (q_i . kcode_j) + lv,   p'_ij = 2^(t_ij - m_i),
 //   O_i = sum_j p'_ij vcode_j,   l_i = sum_j p'_ij 2^-lv
 // with m_i the running maximum of t.  So p' is in [0, 1] whatever the scales
-// are, codes enter the products as they are (e4m3 is exact in f16), and
-// o = O / l, logsumexp = (m + log2 l) ln 2.  Maxima and sums are fp32, products
-// f16 with fp32 accumulation: p' rounds to 11 bits, and q, brought to a largest
-// magnitude of 1 to 2 by a power of two for each row, loses nothing (bf16 has 8
-// bits) but elements under 2^-24 of the row's largest.
+// are, codes enter the products as they are (e4m3 is exact in f16), and o = O /
+// l, logsumexp = (m + log2 l) ln 2.  Maxima, sums and accumulators are fp32.  p'
+// rounds to f16 (11 bits); q, brought to a largest magnitude of 1 to 2 by a
+// power of two for each row, loses nothing there (bf16 has 8 bits) but elements
+// under 2^-24 of the row's largest.
 //
 // Bound: HBM, 2 D bytes for each (token, kv head), read once for all the query
-// rows of the head's group.  One block works on one split (a stretch of keys)
-// of one (request, kv head); the rows of a block are (token, head of the
-// group) pairs.  A producer warp brings pages by TMA into a ring of 64-key
-// stages (128-byte swizzle, so that the fragment reads below meet no bank
-// twice), four consumer warps take stages in turn, each with a softmax of its
-// own that they join at the end; a second kernel joins splits.
-// mma.sync rather than tcgen05: a tile has 16 to 64 rows, not 128, and its
-// products take a quarter of the time that its bytes do.
+// rows of the head's group.
 //
-// Fragments.  S = Q K^T (m16n8k16): thread (g, t) = (lane / 4, lane % 4) holds
-// for key n = g 16-byte chunks t, t + 4, .. of its row; the order of d inside a
-// product is free as long as Q has the same, so no element moves.  Keys of an
-// 8-key tile are taken in the order 0 4 1 5 2 6 3 7: then the 8 lanes that read
-// shared memory together hit 8 different 16-byte places.  O = P V: the
-// accumulators of S are the A operand as they stand, and a byte permutation
-// pairs the two keys of a thread for each d.
-#include <cuda.h>
-#include <math.h>
-
-#include "gdn_chunk_shared.cuh"
-#include "gdn_common.cuh"
+// Work.  The contexts of all (request, kv head) pairs, cut into stages of 64
+// keys, form one line of stages; a team of MT warps (rows are (token, head of
+// the group) pairs, 8 NT a warp) takes a stretch of it, all teams stretches of
+// the same length, so ragged contexts balance by themselves.  A team that meets
+// a whole pair writes its output; of a pair that several teams share each writes
+// a partial result (two a team at most), and a second kernel joins them in
+// order.  A team finds its place by a prefix sum over the requests.
+// Every team has K and V tiles of its own in shared memory, 100 to 200 KB on a
+// SM: the next K tile is called (TMA, swizzled) as soon as the products with
+// the present one are done, the next V tile likewise, and other warps compute
+// meanwhile.
+//
+// Fragments (mma.sync m16n8k16, f16).  The products are taken transposed, S^T =
+// K Q^T and O^T = V^T P^T, so that keys and columns fill the 16 rows of a tile
+// and 8 query rows its 8 columns: a group of 8 heads wastes nothing, and the
+// widening of a code, which is what most instructions do, serves all of a
+// warp's rows.  (With the rows as the 16 of a tile: 1140 instructions a stage,
+// 202 us for 256 ragged contexts; an e4m3 mma.sync is taken apart into
+// conversions and f16 products on this GPU: 1630, 246 us.)  Thread (g, t) =
+// (lane / 4, lane % 4) holds for keys g and g + 8 of a tile the 16-byte chunks
+// t, t + 4, .. of their rows; the order of d inside a product is free as long as
+// Q has the same, so no byte moves.  Keys of 8 are taken in the order 0 4 1 5 2
+// 6 3 7: then the 8 lanes that read shared memory together hit 8 different
+// 16-byte places.  P's 8 x 8 blocks are transposed by movmatrix; for V^T a byte
+// permutation pairs the two keys of a thread for each d.
+// mma.sync rather than tcgen05: a tile has 8 to 64 rows, not 128, and its
+// products take less time than its bytes do.
 #include "gdn_kv8_attn.cuh"
-#include "gdn_sm103.cuh"
 
 namespace {
 
 using namespace gdn;
 using namespace gdnkv;
 
-constexpr int kKeys = 64;       // keys a stage
-constexpr int kConsumers = 4;   // consumer warps
-constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kKeys = 64;         // keys a stage
+constexpr int kSMs = 152;
+constexpr int kMinStages = 2;     // stages a team takes at least
 
-template <int D, int MT>
+// D: head size; NT: tiles of 8 rows a warp; MT: warps a team.
+template <int D, int NT, int MT>
 struct DecodeLay {
-  static constexpr int TILE = kKeys * D;        // bytes of K (or V) a stage
-  static constexpr int STAGE = 2 * TILE;
-  static constexpr int NS = D == 128 ? 6 : 10;  // stages
-  static constexpr int OFF_PAR = NS * STAGE;    // float4 {kmul, lv, 2^-lv, 0} x 4 pages a stage
-  static constexpr int OFF_BAR = OFF_PAR + NS * 64;
-  static constexpr int BYTES = OFF_BAR + (2 * NS + 1) * 8 + 16;
-  static constexpr int WM = MT;                 // warps over rows
-  static constexpr int WK = kConsumers / MT;    // warps over keys
-  // joining the warps at the end, in the ring's memory: O [WK][16 MT][D + 4] and m, l
-  static constexpr int JROW = D + 4;
-  static constexpr int JOIN = WK * 16 * MT * JROW * 4 + WK * 16 * MT * 8;
-  static_assert(JOIN <= NS * STAGE, "join fits the ring");
+  static constexpr int TILE = kKeys * D;                // bytes of a K or V tile
+  static constexpr int R = MT * (D == 128 ? 1 : 2);     // tiles of K, and of V, that a team holds
+  static constexpr int WARPS = NT == 4 ? 8 : 12;        // warps of all teams on a SM (registers: 255, 168)
+  static constexpr int TEAMS = WARPS / MT * kSMs;
+  static constexpr int ROWS = 8 * NT * MT;              // rows a team
+  static constexpr int KP = NT == 1 ? 64 : 32;          // keys a pass
+  static constexpr bool QS = NT == 4;                   // the query fragments stay in shared memory
+  static constexpr int QB = QS ? D / 16 * NT * 2 * 128 : 0;  // their bytes a warp
+  static constexpr int OFF_K = 0, OFF_V = R * TILE;
+  static constexpr int OFF_Q = 2 * R * TILE;
+  static constexpr int OFF_PAR = OFF_Q + MT * QB;       // float4 {k scale, lv, 2^-lv, 0} x 4 pages, R + 1 slots
+  static constexpr int OFF_BAR = OFF_PAR + (R + 1) * 64;
+  static constexpr int OFF_AHEAD = OFF_BAR + (2 * R + 1) * 8 + 8;
+  static constexpr int BYTES = OFF_AHEAD + 48;
+  static_assert((BYTES + 1024) * (WARPS / MT) <= 228 * 1024, "all teams of a SM fit");
 };
+// Partial rows of all teams, two results a team, of the largest variant.
+constexpr int64_t kPartRows = (int64_t)kSMs * 2 * 8 * 32;
 
 __device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -77,6 +90,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// The 8 x 8 block of f16 that the warp holds (row lane / 4, columns 2 (lane % 4),
+// + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -84,6 +104,17 @@ __device__ __forceinline__ float quad_max(float x) {
 __device__ __forceinline__ float quad_add(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+// Over the lanes of one t (the keys of a query row).
+__device__ __forceinline__ float keys_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float keys_add(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 // Byte offset of 16-byte chunk c of row r in a tile of D-byte rows as TMA
 // leaves it (128-byte swizzle for D = 128, 64-byte swizzle for D = 64).
@@ -105,262 +136,433 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, 2)
+
+// Stages of request n, 0 where this kernel has nothing to do for it; s is its
+// span.  A request whose rows see no key has one stage, which writes its zeros.
+__device__ __forceinline__ int stages_of(const AttnArgs &a, int n, Span &s) {
+  if (!request_span(a, n, 0, a.row_cap, s) || s.m * a.G > a.row_most) return 0;
+  return max(1, (s.keys + kKeys - 1) / kKeys);
+}
+// Stages that a team takes.
+__device__ __forceinline__ int64_t stretch_of(int64_t total, int teams) {
+  const int64_t per = (total + teams - 1) / teams;
+  return per < kMinStages ? kMinStages : per;
+}
+
+// Where a walk along the line of stages stands.
+struct Place {
+  int n, h;       // request, kv head
+  int stage, of;  // stage of the pair, stages that it has
+  Span s;
+};
+__device__ __forceinline__ void next_request(const AttnArgs &a, Place &p) {
+  p.stage = 0;
+  p.h = 0;
+  do {
+    ++p.n;
+    p.of = p.n < a.N ? stages_of(a, p.n, p.s) : 1;
+  } while (p.of == 0);
+}
+
+template <int D, int NT, int MT>
+__global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     kv8_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using Ly = DecodeLay<D, MT>;
-  constexpr int NCH = D / 64;  // 16-byte chunks of a key row that a thread holds
-  constexpr int KS = D / 16;   // k-steps of S
-  constexpr int NO = D / 8;    // n-tiles of O
+  using Ly = DecodeLay<D, NT, MT>;
+  constexpr int R = Ly::R;
+  constexpr int NCH = D / 64;       // 16-byte chunks of a key row that a thread holds
+  constexpr int NA = D / 16;        // tiles of 16 columns of O
+  constexpr int NK = Ly::KP / 16;   // tiles of 16 keys a pass
+  constexpr int WPK = D / 32;       // words of a value row that a thread holds
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = blockIdx.z, h = blockIdx.y, sp = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x;
   // The joining kernel's blocks may come in as soon as every block here has
   // started; they wait for this grid's results.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  Span s;
-  if (!request_span(a, n, 0, 16 * MT, s)) {
-    if (tid == 0 && s.bits) set_status(a.dev_status, s.bits);
-    return;
-  }
-  if (s.m * a.G > a.row_most || sp >= s.splits) return;
-  const int L = s.L, m = s.m;
-  constexpr int row0 = 0;
-  const int k_begin = sp * a.split, k_end = min(s.keys, k_begin + a.split);
-  const int stages = (max(0, k_end - k_begin) + kKeys - 1) / kKeys;
-
-  const uint32_t bar = sb + Ly::OFF_BAR;
-  const uint32_t never = bar + 16 * Ly::NS;
-  volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_BAR + (2 * Ly::NS + 1) * 8);
-  auto full = [&](int st) { return bar + 8 * st; };
-  auto empty = [&](int st) { return bar + 8 * (Ly::NS + st); };
-  if (tid == 0) {
-    for (int st = 0; st < Ly::NS; ++st) {
-      mbar_init(full(st), 1);
-      mbar_init(empty(st), Ly::WM);
-    }
-    mbar_init(never, 1);
+  const uint32_t bar = sb + Ly::OFF_BAR, never = bar + 16 * R;
+  volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_BAR + (2 * R + 1) * 8);
+  auto KF = [&](int i) { return bar + 8 * i; };
+  auto VF = [&](int i) { return bar + 8 * (R + i); };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * R + 1; ++i) mbar_init(bar + 8 * i, 1);
     mbar_fence_init();
     *failed = 0;
   }
-  __syncthreads();
+  if (MT > 1) __syncthreads(); else __syncwarp();
 
-  float o[NO][4];
-  float mx[2] = {-INFINITY, -INFINITY}, ls[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < NO; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-  const int g = lane >> 2, t = lane & 3;
-  const int mt = warp % Ly::WM, kg = warp / Ly::WM;
-  int issued = 0;  // stages that the producer has issued
-
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------- producer
-    const int ppt = a.bs >= kKeys ? 1 : kKeys / a.bs;  // copies a stage (of K, and of V)
-    const int box = kKeys / ppt;                       // keys a copy
-    const int pg0 = k_begin / a.bs;
-    int batch = -1, page = -1;
-    float ks = 0.f, lv = 0.f, iv = 1.f;
-    for (int it = 0; it < stages; ++it) {
-      const int st = it % Ly::NS, use = it / Ly::NS;
-      const int first = (k_begin + it * kKeys) / a.bs - pg0;
-      if (first / 32 != batch) {
-        // table entries and scales, 32 pages at a time, a page a lane.  A page
-        // that is not there counts as keys that nothing sees: logits of -inf.
-        batch = first / 32;
-        const int pi = pg0 + batch * 32 + lane;
-        page = -1;
-        ks = 0.f;
-        lv = -INFINITY;
-        iv = 1.f;
-        if ((int64_t)pi * a.bs < k_end) {
-          const int32_t p = a.table[(int64_t)n * a.width + pi];
-          if (p < 0 || p >= a.P) {
-            set_status(a.dev_status, GDN_DEV_BAD_SLOT);
-          } else {
-            page = p;
-            const int64_t at = (int64_t)p * a.HK + h;
-            ks = a.ks[at];
-            const float v = a.vs[at];
-            lv = log2f(v);
-            iv = 1.f / v;
-          }
-        }
-      }
-      if (use > 0) {  // until the stage is free, or a consumer has given up
-        const long long from = clock64();
-        while (!mbar_try_wait(empty(st), (use - 1) & 1)) {
-          if (*failed) break;
-          if (clock64() - from > gdnc::kWaitLimit) {
-            if (lane == 0) set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
-            *failed = 1;
-            break;
-          }
-        }
-      }
-      if (__any_sync(0xffffffffu, *failed)) break;
-      const int src = (first - batch * 32 + (lane & (ppt - 1))) & 31;
-      const int pg = __shfl_sync(0xffffffffu, page, src);
-      const float4 par = make_float4(__shfl_sync(0xffffffffu, ks, src), __shfl_sync(0xffffffffu, lv, src),
-                                     __shfl_sync(0xffffffffu, iv, src), 0.f);
-      if (lane < ppt) *reinterpret_cast<float4 *>(smem + Ly::OFF_PAR + st * 64 + lane * 16) = par;
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(full(st), Ly::STAGE);
-      __syncwarp();
-      if (lane < ppt) {
-        // pages that are not there lie outside the tensor: TMA fills in zeros
-        const int z = pg >= 0 ? pg * a.HK + h : a.P * a.HK;
-        const int y = (k_begin + it * kKeys) % a.bs;
-        const uint32_t dst = sb + st * Ly::STAGE + lane * box * D;
-        tma_load_3d(dst, &mk, full(st), 0, y, z);
-        tma_load_3d(dst + Ly::TILE, &mv, full(st), 0, y, z);
-      }
-      issued = it + 1;
+  // ------------------------------------------------- this team's stretch
+  // Lane l sums the stages of requests [l seg, (l + 1) seg); the last team
+  // also writes every request's place on the line for the joining kernel.
+  Place at{};
+  int left;  // stages of this team still to do
+  {
+    Span s;
+    const int seg = (a.N + 31) / 32;
+    int64_t mine = 0;
+    int bits = 0;
+    for (int n = lane * seg; n < min(a.N, (lane + 1) * seg); ++n) {
+      mine += (int64_t)stages_of(a, n, s) * a.HK;
+      bits |= s.bits;
     }
-  } else {
-    // ------------------------------------------------------------ consumers
-    // Queries: row g and row g + 8 of this warp's 16; thread t holds d =
-    // 16 (t + 4 i) + 0..15, k-step 4 i + w taking 4 w + {0, 1 | 2, 3} of them.
-    uint32_t qf[KS][4];
-    float krow[2];
-    int limit[2];
+    if (bits && team == 0 && warp == 0) set_status(a.dev_status, bits);
+    int64_t incl = mine;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = row0 + 16 * mt + g + 8 * r;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    const int64_t per = stretch_of(total, Ly::TEAMS), start = per * team;
+    if (team == Ly::TEAMS - 1 && warp == 0) {
+      int64_t run = incl - mine;
+      for (int n = lane * seg; n < min(a.N, (lane + 1) * seg); ++n) {
+        a.place[n] = run;
+        run += (int64_t)stages_of(a, n, s) * a.HK;
+      }
+      if (lane == 0) a.place[a.N] = total;
+    }
+    if (start >= total) return;
+    left = (int)min(per, total - start);
+    const int owner = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;  // the lane whose requests hold the start
+    int64_t run = __shfl_sync(0xffffffffu, incl - mine, owner);
+    for (int base = owner * seg;; base += 32) {
+      const int n = base + lane;
+      const int64_t c = n < a.N ? (int64_t)stages_of(a, n, s) * a.HK : 0;
+      int64_t sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run + sum > start);
+      if (past) {
+        const int l = __ffs((int)past) - 1;
+        at.n = base + l;
+        const int64_t in = start - (run + __shfl_sync(0xffffffffu, sum - c, l));
+        at.of = stages_of(a, at.n, at.s);
+        at.h = (int)(in / at.of);
+        at.stage = (int)(in - (int64_t)at.h * at.of);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+
+  // -------------------------------------------------------------- calling
+  // Warp 0 runs R stages ahead of the products: `ahead` is its place, `to_call`
+  // the stages it has still to call.  Table entries and scales are read 32
+  // pages at a time, a page a lane.  A page that is not there counts as keys
+  // that nothing sees (logits of -inf) and reads zeros.
+  // The place is kept in shared memory: the products need the registers.
+  Place &ahead = *reinterpret_cast<Place *>(smem + Ly::OFF_AHEAD);
+  static_assert(sizeof(Place) <= 48, "room for the place");
+  int to_call = left;
+  int called = 0, called_k = 0;  // stages called so far; their K tiles
+  int batch = -1, page = -1;
+  float ks = 0.f, lv = 0.f, iv = 1.f;
+  int zc = 0, yc = 0;  // the called stage's coordinates
+  const int ppt = a.bs >= kKeys ? 1 : kKeys / a.bs;  // copies a tile
+  const int box = kKeys / ppt;                       // keys a copy
+  const int page_bits = 31 - __clz(a.bs);
+  auto call_k = [&]() {
+    if (to_call == 0 || *failed) return;
+    const int stage = ahead.stage, head = ahead.h;
+    const int first = (stage * kKeys) >> page_bits;
+    if (first / 32 != batch) {
+      batch = first / 32;
+      const int pi = batch * 32 + lane;
+      page = -1;
+      ks = 0.f;
+      lv = -INFINITY;
+      iv = 1.f;
+      if (((int64_t)pi << page_bits) < ahead.s.keys) {
+        const int32_t p = a.table[(int64_t)ahead.n * a.width + pi];
+        if (p < 0 || p >= a.P) {
+          set_status(a.dev_status, GDN_DEV_BAD_SLOT);
+        } else {
+          page = p;
+          const int64_t i = (int64_t)p * a.HK + head;
+          ks = a.ks[i];
+          const float v = a.vs[i];
+          lv = log2f(v);
+          iv = 1.f / v;
+        }
+      }
+    }
+    const int src = (first - batch * 32 + (lane & (ppt - 1))) & 31;
+    const int pg = __shfl_sync(0xffffffffu, page, src);
+    const float4 par = make_float4(__shfl_sync(0xffffffffu, ks, src), __shfl_sync(0xffffffffu, lv, src),
+                                   __shfl_sync(0xffffffffu, iv, src), 0.f);
+    zc = pg >= 0 ? pg * a.HK + head : a.P * a.HK;  // outside the tensor: TMA fills in zeros
+    yc = (stage * kKeys) & (a.bs - 1);
+    const int slot = called % R;
+    if (lane < ppt) *reinterpret_cast<float4 *>(smem + Ly::OFF_PAR + (called % (R + 1)) * 64 + lane * 16) = par;
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(KF(slot), Ly::TILE);
+    __syncwarp();
+    if (lane < ppt) tma_load_3d(sb + Ly::OFF_K + slot * Ly::TILE + lane * box * D, &mk, KF(slot), 0, yc, zc);
+    ++called_k;
+    // on to the next stage
+    if (stage + 1 < ahead.of) {
+      __syncwarp();
+      if (lane == 0) ahead.stage = stage + 1;
+    } else {
+      Place p = ahead;
+      p.stage = 0;
+      batch = -1;
+      if (++p.h == a.HK && to_call > 1) next_request(a, p);
+      __syncwarp();
+      if (lane == 0) ahead = p;
+    }
+    __syncwarp();
+  };
+  auto call_v = [&]() {  // the V tile of the stage that call_k has just called
+    if (to_call == 0 || *failed) return;
+    const int slot = called % R;
+    if (lane == 0) mbar_arrive_expect_tx(VF(slot), Ly::TILE);
+    __syncwarp();
+    if (lane < ppt) tma_load_3d(sb + Ly::OFF_V + slot * Ly::TILE + lane * box * D, &mv, VF(slot), 0, yc, zc);
+    ++called;
+    --to_call;
+  };
+  if (warp == 0) {
+    if (lane == 0) ahead = at;
+    __syncwarp();
+    for (int i = 0; i < R; ++i) {
+      call_k();
+      call_v();
+    }
+  }
+
+  const int g = lane >> 2, t = lane & 3;
+  const int kperm = (g >> 1) | ((g & 1) << 2);  // row of key g of 8
+  const uint32_t sel0 = (g & 1) ? 0x1504u : 0x5140u, sel1 = (g & 1) ? 0x3726u : 0x7362u;
+  const int va = t + 4 * (g & 1), vb = t + 4 * ((g & 1) ^ 1);
+  const uint32_t qs = sb + Ly::OFF_Q + warp * Ly::QB + lane * 16;
+  int done = 0;  // stages that the products have used
+
+  while (left > 0) {
+    // ---------------------------------------------- one pair's stretch
+    const Span s = at.s;
+    const int h = at.h, L = s.L, m = s.m;
+    const bool from_start = at.stage == 0, to_end = left >= at.of - at.stage;
+    const int count = to_end ? at.of - at.stage : left;
+    const int row0 = 8 * NT * warp;  // this warp's first row
+    // Queries: row row0 + 8 nt + g; thread t holds d = 16 (t + 4 i) + 0..15,
+    // k-step 4 i + w taking 4 w + {0, 1 | 2, 3} of them.
+    uint32_t qf[Ly::QS ? 1 : 4 * NCH][NT][2];
+    float krow[NT][2];  // of rows row0 + 8 nt + 2 t + e
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + 8 * nt + g;
       const bool on = row < m * a.G;
-      limit[r] = on ? L - m + row / a.G : -1;
-      float x[NCH][16], top = 0.f, bad = 0.f;
+      uint4 u[2 * NCH];
+      float top = 0.f, bad = 0.f;
       const uint16_t *src = a.q + (int64_t)(s.t0 + row / a.G) * a.ldq + (int64_t)(h * a.G + row % a.G) * D;
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
+      for (int i = 0; i < 2 * NCH; ++i) {
+        u[i] = on ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * (t + 4 * (i >> 1))) + (i & 1)) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint4 u = on ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * (t + 4 * i)) + v) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[i][8 * v + 2 * e] = bf16lo_f(w[e]);
-            x[i][8 * v + 2 * e + 1] = bf16hi_f(w[e]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          top = fmaxf(top, fabsf(x[i][e]));
-          bad = fmaf(x[i][e], 0.f, bad);  // NaN once an element is not finite
+        for (int e = 0; e < 4; ++e) {
+          const float x = bf16lo_f(w[e]), y = bf16hi_f(w[e]);
+          top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
+          bad = fmaf(x, 0.f, fmaf(y, 0.f, bad));  // NaN once an element is not finite
         }
       }
       top = quad_max(top);
       bad = quad_add(bad);
       int e2 = (int)(__float_as_uint(top) >> 23) - 127;
       e2 = e2 < -100 ? -100 : e2 > 120 ? 120 : e2;
-      const float down = gdnkv::pow2(-e2);
-      krow[r] = gdnkv::pow2(e2) * a.scale_log2e + bad;
+      const float down = pow2(-e2), kr = pow2(e2) * a.scale_log2e + bad;
+      krow[nt][0] = __shfl_sync(0xffffffffu, kr, 8 * t);
+      krow[nt][1] = __shfl_sync(0xffffffffu, kr, 8 * t + 4);
 #pragma unroll
-      for (int i = 0; i < NCH; ++i)
+      for (int i = 0; i < 2 * NCH; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t f[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          qf[4 * i + w][r] = pack_f16(x[i][4 * w] * down, x[i][4 * w + 1] * down);
-          qf[4 * i + w][r + 2] = pack_f16(x[i][4 * w + 2] * down, x[i][4 * w + 3] * down);
+        for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16lo_f(w[e]) * down, bf16hi_f(w[e]) * down);
+        if (Ly::QS) {  // k-steps 2 i and 2 i + 1 of this row tile: [k-step pair][row tile][lane] of 16 bytes
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (i * NT + nt) * 512), "r"(f[0]), "r"(f[1]), "r"(f[2]),
+                       "r"(f[3])
+                       : "memory");
+        } else {
+          qf[Ly::QS ? 0 : 2 * i][nt][0] = f[0];
+          qf[Ly::QS ? 0 : 2 * i][nt][1] = f[1];
+          qf[Ly::QS ? 0 : 2 * i + 1][nt][0] = f[2];
+          qf[Ly::QS ? 0 : 2 * i + 1][nt][1] = f[3];
         }
-    }
-    const int low = L - m + (row0 + 16 * mt) / a.G;  // what the tile's first row sees last
-    const int kperm = (g >> 1) | ((g & 1) << 2);     // row of key n = g in an 8-key tile
-    const uint32_t sel0 = (g & 1) ? 0x1504u : 0x5140u, sel1 = (g & 1) ? 0x3726u : 0x7362u;
-    const int va = t + 4 * (g & 1), vb = t + 4 * ((g & 1) ^ 1);
-
-    for (int it = kg; it < stages; it += Ly::WK) {
-      const int st = it % Ly::NS, use = it / Ly::NS;
-      bool ok = true;
-      if (a.force_expiry) ok = mbar_wait_bounded(never, 0, gdnc::kTestWaitLimit);
-      if (ok) ok = mbar_wait_bounded(full(st), use & 1, gdnc::kWaitLimit);
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
-        *failed = 1;
-        break;
       }
-      const uint32_t kt = sb + st * Ly::STAGE, vt = kt + Ly::TILE, par = sb + Ly::OFF_PAR + st * 64;
-      const int k0 = k_begin + it * kKeys;
-
-      float p[kKeys / 8][4];
+    }
+    const int low = L - m + row0 / a.G;  // what this warp's first row sees last
+    // O^T: tile x, row tile nt: columns 2 NA.. of this thread g are d = NA g .. ;
+    // o[x][nt][e + 2 f] is d = 2 NA g + 2 x + f (NA = D / 16) of row 2 t + e.
+    float o[NA][NT][4];
+    float mx[NT][2], ls[NT][2];
 #pragma unroll
-      for (int j = 0; j < kKeys / 8; ++j) {
-        p[j][0] = p[j][1] = p[j][2] = p[j][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) {
+      mx[nt][0] = mx[nt][1] = -INFINITY;
+      ls[nt][0] = ls[nt][1] = 0.f;
+#pragma unroll
+      for (int x = 0; x < NA; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][nt][e] = 0.f;
+    }
+
+    for (int it = 0; it < count; ++it, ++done) {
+      const int slot = done % R, phase = (done / R) & 1;
+      const int k0 = (at.stage + it) * kKeys;
+      if (!*failed) {
+        bool ok = true;
+        if (a.force_expiry) ok = mbar_wait_bounded(never, 0, gdnc::kTestWaitLimit);
+        if (ok) ok = mbar_wait_bounded(KF(slot), phase, gdnc::kWaitLimit);
+        if (!ok) {
+          set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
+          *failed = 1;
+        }
+      }
+      const uint32_t kt = sb + Ly::OFF_K + slot * Ly::TILE, vt = sb + Ly::OFF_V + slot * Ly::TILE;
+      const uint32_t par = sb + Ly::OFF_PAR + (done % (R + 1)) * 64;
+      const bool masked = k0 + kKeys - 1 > low;
+      uint32_t nan_seen = 0;
+#pragma unroll 1
+      for (int pass = 0; pass < kKeys / Ly::KP; ++pass) {
+        const int kp = pass * Ly::KP;
+        float p[NK][NT][4];
+#pragma unroll
+        for (int x = 0; x < NK; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) p[x][nt][0] = p[x][nt][1] = p[x][nt][2] = p[x][nt][3] = 0.f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-          const uint4 u = lds128(kt + tile_at<D>(8 * j + kperm, t + 4 * i));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint32_t kw[NK][2][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma_f16(p[j], qf[4 * i + e], gdnkv::e4m3x2_f16x2(w[e]), gdnkv::e4m3x2_f16x2(w[e] >> 16));
-        }
-      }
-      const bool masked = k0 + kKeys - 1 > low;
-      float top[2] = {-INFINITY, -INFINITY}, iv[kKeys / 16];
+          for (int x = 0; x < NK; ++x)
 #pragma unroll
-      for (int jj = 0; jj < kKeys / 16; ++jj) {  // a page holds 16 keys at least
-        const float4 f = lds_f4(par + (a.bs >= kKeys ? 0 : 16 * jj / a.bs) * 16);
-        iv[jj] = f.z;
-        const float c0 = krow[0] * f.x, c1 = krow[1] * f.x;
-#pragma unroll
-        for (int jx = 0; jx < 2; ++jx) {
-          const int j = 2 * jj + jx;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            p[j][e] = fmaf(p[j][e], c0, f.y);
-            p[j][2 + e] = fmaf(p[j][2 + e], c1, f.y);
-            if (masked) {
-              const int key = k0 + 8 * j + t + 4 * e;
-              if (key > limit[0]) p[j][e] = -INFINITY;
-              if (key > limit[1]) p[j][2 + e] = -INFINITY;
+            for (int r = 0; r < 2; ++r) {
+              const uint4 u = lds128(kt + tile_at<D>(kp + 16 * x + 8 * r + kperm, t + 4 * i));
+              kw[x][r][0] = u.x; kw[x][r][1] = u.y; kw[x][r][2] = u.z; kw[x][r][3] = u.w;
             }
-            top[0] = fmaxf(top[0], p[j][e]);
-            top[1] = fmaxf(top[1], p[j][2 + e]);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t q2[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (Ly::QS) {
+                const uint2 u = lds64(qs + ((2 * i + (w >> 1)) * NT + nt) * 512 + (w & 1) * 8);
+                q2[nt][0] = u.x;
+                q2[nt][1] = u.y;
+              } else {
+                q2[nt][0] = qf[Ly::QS ? 0 : 4 * i + w][nt][0];
+                q2[nt][1] = qf[Ly::QS ? 0 : 4 * i + w][nt][1];
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < NK; ++x) {
+              uint32_t f[4];
+              e4m3x4_f16x2(kw[x][0][w], f[0], f[2]);
+              e4m3x4_f16x2(kw[x][1][w], f[1], f[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(p[x][nt], f, q2[nt][0], q2[nt][1]);
+            }
           }
         }
-      }
-      float base[2], down[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float now = fmaxf(mx[r], quad_max(top[r]));
-        base[r] = now == -INFINITY ? 0.f : now;
-        down[r] = ex2f(mx[r] - base[r]);
-        mx[r] = now;
-        ls[r] *= down[r];
-      }
-#pragma unroll
-      for (int j = 0; j < kKeys / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[j][e] = ex2f(p[j][e] - base[e >> 1]);
-          ls[e >> 1] = fmaf(p[j][e], iv[j >> 1], ls[e >> 1]);
+        if (pass == kKeys / Ly::KP - 1) {
+          if (MT > 1) __syncthreads(); else __syncwarp();  // the K tile is free
+          if (warp == 0) call_k();
         }
-      if (__any_sync(0xffffffffu, down[0] != 1.f || down[1] != 1.f)) {
+
+        float top[NT][2], iv_of[NK];
 #pragma unroll
-        for (int i = 0; i < NO; ++i)
+        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][e] *= down[e >> 1];
-      }
-      uint32_t nan_seen = 0;
+        for (int x = 0; x < NK; ++x) {  // a page holds 16 keys at least
+          const float4 f = lds_f4(par + ((a.bs >= kKeys ? 0 : kp + 16 * x) >> page_bits) * 16);
+          iv_of[x] = f.z;
 #pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk) {
-        const uint32_t pa[4] = {pack_f16(p[2 * kk][0], p[2 * kk][1]), pack_f16(p[2 * kk][2], p[2 * kk][3]),
-                                pack_f16(p[2 * kk + 1][0], p[2 * kk + 1][1]), pack_f16(p[2 * kk + 1][2], p[2 * kk + 1][3])};
-        uint32_t wa[2][D / 32], wb[2][D / 32];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int jx = 0; jx < 2; ++jx) {
-          const int j = 2 * kk + jx;
-          if (D == 128) {
-            const uint4 u = lds128(vt + tile_at<D>(8 * j + va, g)), w = lds128(vt + tile_at<D>(8 * j + vb, g));
-            wa[jx][0] = u.x; wa[jx][1] = u.y; wa[jx][D / 64] = u.z; wa[jx][D / 32 - 1] = u.w;
-            wb[jx][0] = w.x; wb[jx][1] = w.y; wb[jx][D / 64] = w.z; wb[jx][D / 32 - 1] = w.w;
-          } else {
-            const uint2 u = lds64(vt + tile_at<D>(8 * j + va, g >> 1) + 8 * (g & 1));
-            const uint2 w = lds64(vt + tile_at<D>(8 * j + vb, g >> 1) + 8 * (g & 1));
-            wa[jx][0] = u.x; wa[jx][1] = u.y;
-            wb[jx][0] = w.x; wb[jx][1] = w.y;
+            for (int e = 0; e < 2; ++e) {
+              const float c = krow[nt][e] * f.x;
+              p[x][nt][e] = fmaf(p[x][nt][e], c, f.y);
+              p[x][nt][2 + e] = fmaf(p[x][nt][2 + e], c, f.y);
+            }
+        }
+        if (masked) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int row = row0 + 8 * nt + 2 * t + e;
+              const int limit = row < m * a.G ? L - m + row / a.G : -1;
+#pragma unroll
+              for (int x = 0; x < NK; ++x) {
+                if (k0 + kp + 16 * x + kperm > limit) p[x][nt][e] = -INFINITY;
+                if (k0 + kp + 16 * x + 8 + kperm > limit) p[x][nt][2 + e] = -INFINITY;
+              }
+            }
+        }
+        float base[NT][2], down[NT][2];
+        bool moved = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x0 = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < NK; ++x) x0 = fmaxf(x0, fmaxf(p[x][nt][e], p[x][nt][2 + e]));
+            const float now = fmaxf(mx[nt][e], keys_max(x0));
+            base[nt][e] = now == -INFINITY ? 0.f : now;
+            down[nt][e] = ex2f(mx[nt][e] - base[nt][e]);
+            moved |= now != mx[nt][e];
+            mx[nt][e] = now;
+          }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            ls[nt][0] *= down[nt][0];
+            ls[nt][1] *= down[nt][1];
+#pragma unroll
+            for (int x = 0; x < NA; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[x][nt][e] *= down[nt][e & 1];
+          }
+        }
+        uint32_t pb[NK][NT][2];
+#pragma unroll
+        for (int x = 0; x < NK; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[x][nt][e] = ex2f(p[x][nt][e] - base[nt][e & 1]);
+            ls[nt][0] = fmaf(p[x][nt][0] + p[x][nt][2], iv_of[x], ls[nt][0]);
+            ls[nt][1] = fmaf(p[x][nt][1] + p[x][nt][3], iv_of[x], ls[nt][1]);
+            pb[x][nt][0] = transpose8(pack_f16(p[x][nt][0], p[x][nt][1]));
+            pb[x][nt][1] = transpose8(pack_f16(p[x][nt][2], p[x][nt][3]));
+          }
+
+        if (pass == 0 && !*failed && !mbar_wait_bounded(VF(slot), phase, gdnc::kWaitLimit)) {
+          set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
+          *failed = 1;
+        }
+#pragma unroll
+        for (int x = 0; x < NK; ++x) {
+          uint32_t wa[2][WPK], wb[2][WPK];  // keys of 8: this thread's two, WPK words of each
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int j = kp + 16 * x + 8 * r;
+            if (D == 128) {
+              const uint4 u = lds128(vt + tile_at<D>(j + va, g)), w = lds128(vt + tile_at<D>(j + vb, g));
+              wa[r][0] = u.x; wa[r][1] = u.y; wa[r][WPK / 2] = u.z; wa[r][WPK - 1] = u.w;
+              wb[r][0] = w.x; wb[r][1] = w.y; wb[r][WPK / 2] = w.z; wb[r][WPK - 1] = w.w;
+            } else {
+              const uint2 u = lds64(vt + tile_at<D>(j + va, g >> 1) + 8 * (g & 1));
+              const uint2 w = lds64(vt + tile_at<D>(j + vb, g >> 1) + 8 * (g & 1));
+              wa[r][0] = u.x; wa[r][1] = u.y;
+              wb[r][0] = w.x; wb[r][1] = w.y;
+            }
           }
           if (masked) {
             // Keys past the context hold whatever the page held before, and a
@@ -368,254 +570,247 @@ __global__ void __launch_bounds__(kThreads, 2)
             // 0 x NaN is not.  Such codes become 0; NaN that a row does see is
             // put back below.
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-              if (k0 + 8 * j + va >= L) wa[jx][x] = 0;
-              if (k0 + 8 * j + vb >= L) wb[jx][x] = 0;
-              nan_seen |= any_nan(wa[jx][x]) | any_nan(wb[jx][x]);
-              wa[jx][x] = drop_nan(wa[jx][x]);
-              wb[jx][x] = drop_nan(wb[jx][x]);
+            for (int r = 0; r < 2; ++r) {
+              const int j = k0 + kp + 16 * x + 8 * r;
+#pragma unroll
+              for (int y = 0; y < WPK; ++y) {
+                if (j + va >= L) wa[r][y] = 0;
+                if (j + vb >= L) wb[r][y] = 0;
+                nan_seen |= any_nan(wa[r][y]) | any_nan(wb[r][y]);
+                wa[r][y] = drop_nan(wa[r][y]);
+                wb[r][y] = drop_nan(wb[r][y]);
+              }
             }
           }
-        }
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          const uint32_t l0 = __byte_perm(wa[0][x], wb[0][x], sel0), l1 = __byte_perm(wa[0][x], wb[0][x], sel1);
-          const uint32_t h0 = __byte_perm(wa[1][x], wb[1][x], sel0), h1 = __byte_perm(wa[1][x], wb[1][x], sel1);
-          mma_f16(o[4 * x], pa, gdnkv::e4m3x2_f16x2(l0), gdnkv::e4m3x2_f16x2(h0));
-          mma_f16(o[4 * x + 1], pa, gdnkv::e4m3x2_f16x2(l0 >> 16), gdnkv::e4m3x2_f16x2(h0 >> 16));
-          mma_f16(o[4 * x + 2], pa, gdnkv::e4m3x2_f16x2(l1), gdnkv::e4m3x2_f16x2(h1));
-          mma_f16(o[4 * x + 3], pa, gdnkv::e4m3x2_f16x2(l1 >> 16), gdnkv::e4m3x2_f16x2(h1 >> 16));
+          for (int y = 0; y < WPK; ++y) {
+            uint32_t f[4];
+            e4m3x4_f16x2(__byte_perm(wa[0][y], wb[0][y], sel0), f[0], f[1]);
+            e4m3x4_f16x2(__byte_perm(wa[1][y], wb[1][y], sel0), f[2], f[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * y][nt], f, pb[x][nt][0], pb[x][nt][1]);
+            e4m3x4_f16x2(__byte_perm(wa[0][y], wb[0][y], sel1), f[0], f[1]);
+            e4m3x4_f16x2(__byte_perm(wa[1][y], wb[1][y], sel1), f[2], f[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * y + 1][nt], f, pb[x][nt][0], pb[x][nt][1]);
+          }
         }
       }
       if (masked && __any_sync(0xffffffffu, nan_seen != 0)) {
-        const unsigned char *vs = smem + st * Ly::STAGE + Ly::TILE;
+        const unsigned char *v = smem + Ly::OFF_V + slot * Ly::TILE;
+#pragma unroll 1
         for (int key = 0; key < kKeys && k0 + key < L; ++key)
 #pragma unroll
-          for (int i = 0; i < NO; ++i)
+          for (int x = 0; x < 2 * NA; ++x) {
+            const int d = 2 * NA * g + x;
+            if ((v[tile_at<D>(key, d >> 4) + (d & 15)] & 0x7f) != 0x7f) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int d = (2 * t + e) * (D / 8) + i;
-              if ((vs[tile_at<D>(key, d >> 4) + (d & 15)] & 0x7f) != 0x7f) continue;
-              if (k0 + key <= limit[0]) o[i][e] = NAN;
-              if (k0 + key <= limit[1]) o[i][2 + e] = NAN;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (k0 + key <= L - m + (row0 + 8 * nt + 2 * t + e) / a.G) o[x >> 1][nt][e + 2 * (x & 1)] = NAN;
+          }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(st));
+      if (MT > 1) __syncthreads(); else __syncwarp();  // the V tile is free
+      if (warp == 0) call_v();
     }
+
+    // ------------------------------------------------ the stretch's result
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float l = keys_add(ls[nt][e]);
+        const int row = row0 + 8 * nt + 2 * t + e;
+        if (row >= m * a.G || *failed) continue;
+        if (from_start && to_end) {
+          const int64_t out = (int64_t)(s.t0 + row / a.G) * a.HQ + h * a.G + row % a.G;
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing is 0
+#pragma unroll
+          for (int x = 0; x < NA; x += 4)
+            *reinterpret_cast<uint4 *>(a.o + out * D + 2 * NA * g + 2 * x) =
+                make_uint4(pack_bf16(o[x][nt][e] * inv, o[x][nt][e + 2] * inv), pack_bf16(o[x + 1][nt][e] * inv, o[x + 1][nt][e + 2] * inv),
+                           pack_bf16(o[x + 2][nt][e] * inv, o[x + 2][nt][e + 2] * inv),
+                           pack_bf16(o[x + 3][nt][e] * inv, o[x + 3][nt][e + 2] * inv));
+          if (a.lse && g == 0) a.lse[out] = l == 0.f ? -INFINITY : (mx[nt][e] + log2f(l)) * kLn2;
+        } else {
+          // the pair began before this team's stretch: slot 0, else slot 1
+          const int64_t part = ((int64_t)team * 2 + (from_start ? 1 : 0)) * a.row_cap + row;
+#pragma unroll
+          for (int x = 0; x < NA; x += 2)
+            *reinterpret_cast<float4 *>(a.part_o + part * D + 2 * NA * g + 2 * x) =
+                make_float4(o[x][nt][e], o[x][nt][e + 2], o[x + 1][nt][e], o[x + 1][nt][e + 2]);
+          if (g == 0) a.part_ml[part] = make_float2(mx[nt][e], l);
+        }
+      }
+    left -= count;
+    at.stage = 0;
+    if (left > 0 && ++at.h == a.HK) next_request(a, at);
   }
 
-  __syncthreads();
-  if (*failed) {
-    // A wait ran out: write nothing, and stay until this block's copies are in.
-    if (warp == kConsumers && lane == 0) {
-      for (int st = 0; st < Ly::NS && st < issued; ++st) {
-        const int last = (issued - 1 - st) / Ly::NS;
-        if (!mbar_wait_bounded(full(st), last & 1, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
-      }
-    }
-    return;
+  if (MT > 1) __syncthreads();
+  if (*failed && warp == 0 && lane == 0) {
+    // A wait ran out, nothing was written since; stay until the copies are in.
+    bool ok = true;
+    for (int i = 0; i < R && i < called_k; ++i) ok &= mbar_wait_bounded(KF(i), ((called_k - 1 - i) / R) & 1, gdnc::kWaitLimit);
+    for (int i = 0; i < R && i < called; ++i) ok &= mbar_wait_bounded(VF(i), ((called - 1 - i) / R) & 1, gdnc::kWaitLimit);
+    if (!ok) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
   }
+}
 
-  // Join the warps over keys.
-  float *js = reinterpret_cast<float *>(smem);
-  float2 *jml = reinterpret_cast<float2 *>(smem + Ly::WK * 16 * MT * Ly::JROW * 4);
-  if (warp < kConsumers) {
+// Joins the partial results of a pair's rows, in order.  WIDE: block x of a pair
+// takes row x, each of its four warps a quarter of the pieces (calls with few
+// pairs, which are cut into many pieces each); else rows 4 x .. 4 x + 3, a warp
+// each.  A lane reads the maximum and sum of one piece, 32 at a time; D / 4
+// lanes hold four columns each.  Latency counts here: three dependent reads.
+template <int D, bool WIDE>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int teams) {
+  constexpr int LANES = D / 4;
+  __shared__ float4 so[WIDE ? 4 : 1][LANES];
+  __shared__ float2 sml[4];
+  const int n = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = WIDE ? blockIdx.x : 4 * blockIdx.x + warp;
+  Span s;
+  const int of = stages_of(a, n, s);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (of == 0 || row >= s.m * a.G) return;
+  const int64_t per = stretch_of(a.place[a.N], teams);
+  const int64_t from = a.place[n] + (int64_t)h * of, first = from / per, last = (from + of - 1) / per;
+  const int pieces = (int)(last - first) + 1;
+  if (pieces == 1) return;
+  const int share = WIDE ? (pieces + 3) / 4 : pieces;
+  const int i0 = WIDE ? warp * share : 0, i1 = min(pieces, i0 + share);
+  const int c = lane % LANES;
+  // piece 0 is its team's slot 1, the others their teams' slot 0
+  auto at = [&](int i) { return ((first + i) * 2 + (i == 0 ? 1 : 0)) * a.row_cap + row; };
+  float top = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b = i0; b < i1; b += 32) {
+    const int cnt = min(32, i1 - b);
+    const float2 ml = lane < cnt ? a.part_ml[at(b + lane)] : make_float2(-INFINITY, 0.f);
+    float now = ml.x;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      ls[r] = quad_add(ls[r]);
-      const int row = kg * 16 * MT + 16 * mt + g + 8 * r;
-      if (t == 0) jml[row] = make_float2(mx[r], ls[r]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < NO; i += 4)
-          *reinterpret_cast<float4 *>(js + row * Ly::JROW + (2 * t + e) * (D / 8) + i) =
-              make_float4(o[i][2 * r + e], o[i + 1][2 * r + e], o[i + 2][2 * r + e], o[i + 3][2 * r + e]);
+    for (int o = 16; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+    now = fmaxf(now, top);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float w = ex2f(ml.x - base), old = ex2f(top - base);
+    top = now;
+    l = fmaf(l, old, warp_sum(w * ml.y));
+    acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll 8
+    for (int i = 0; i < cnt; ++i) {
+      const float4 v = *reinterpret_cast<const float4 *>(a.part_o + at(b + i) * D + 4 * c);
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      acc.x = fmaf(wi, v.x, acc.x);
+      acc.y = fmaf(wi, v.y, acc.y);
+      acc.z = fmaf(wi, v.z, acc.z);
+      acc.w = fmaf(wi, v.w, acc.w);
     }
   }
-  __syncthreads();
-  const int mine = min(16 * MT, m * a.G - row0);
-  for (int e = tid; e < mine * (D / 4); e += kThreads) {
-    const int r = e / (D / 4), c = (e - r * (D / 4)) * 4;
-    float top = -INFINITY;
+  if (WIDE) {
+    if (lane < LANES) so[warp][c] = acc;
+    if (lane == 0) sml[warp] = make_float2(top, l);
+    __syncthreads();
+    if (warp != 0) return;
+    top = -INFINITY;
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < Ly::WK; ++k) top = fmaxf(top, jml[k * 16 * MT + r].x);
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, sml[i].x);
     const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < Ly::WK; ++k) {
-      const float2 ml = jml[k * 16 * MT + r];
-      const float w = ex2f(ml.x - base);
-      const float4 v = *reinterpret_cast<const float4 *>(js + (k * 16 * MT + r) * Ly::JROW + c);
-      l = fmaf(w, ml.y, l);
+    for (int i = 0; i < 4; ++i) {
+      const float w = ex2f(sml[i].x - base);
+      const float4 v = so[WIDE ? i : 0][c];
+      l = fmaf(w, sml[i].y, l);
       acc.x = fmaf(w, v.x, acc.x);
       acc.y = fmaf(w, v.y, acc.y);
       acc.z = fmaf(w, v.z, acc.z);
       acc.w = fmaf(w, v.w, acc.w);
     }
-    const int row = row0 + r;
-    if (s.splits == 1) {
-      store_row4(a, s.t0 + row / a.G, h * a.G + row % a.G, D, c, acc, top, l);
-    } else {
-      const int64_t at = (((int64_t)n * a.HK + h) * a.row_cap + row) * a.max_splits + sp;
-      *reinterpret_cast<float4 *>(a.part_o + at * D + c) = acc;
-      if (c == 0) a.part_ml[at] = make_float2(top, l);
-    }
   }
-}
-
-// Joins the splits of a row, in order: one block a (request, kv head, row).
-// D / 4 lanes hold four columns each; the block's other threads take further
-// splits and are added at the end.
-constexpr int kJoinThreads = 128;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const AttnArgs a) {
-  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
-  __shared__ float4 so[GROUPS][LANES];
-  __shared__ float sl[GROUPS], sm[GROUPS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n = blockIdx.z, h = blockIdx.y, row = blockIdx.x;
-  Span s;
-  if (!request_span(a, n, 0, a.row_cap, s) || s.m * a.G > a.row_most || row >= s.m * a.G || s.splits == 1) return;
-  const int64_t at = (((int64_t)n * a.HK + h) * a.row_cap + row) * a.max_splits;
-  const int c = threadIdx.x % LANES, gr = threadIdx.x / LANES;
-  float top = -INFINITY;
-  for (int i = gr; i < s.splits; i += GROUPS) top = fmaxf(top, a.part_ml[at + i].x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = gr; i < s.splits; i += GROUPS) {
-    const float2 ml = a.part_ml[at + i];
-    const float4 v = *reinterpret_cast<const float4 *>(a.part_o + (at + i) * D + 4 * c);
-    const float w = ex2f(ml.x - base);
-    l = fmaf(w, ml.y, l);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  so[gr][c] = acc;
-  if (c == 0) {
-    sl[gr] = l;
-    sm[gr] = top;
-  }
-  __syncthreads();
-  if (gr != 0) return;
-  float best = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < GROUPS; ++k) best = fmaxf(best, sm[k]);
-  const float b2 = best == -INFINITY ? 0.f : best;
-  l = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int k = 0; k < GROUPS; ++k) {
-    const float w = ex2f(sm[k] - b2);
-    const float4 v = so[k][c];
-    l = fmaf(w, sl[k], l);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  store_row4(a, s.t0 + row / a.G, h * a.G + row % a.G, D, 4 * c, acc, best, l);
+  if (lane < LANES) store_row4(a, s.t0 + row / a.G, h * a.G + row % a.G, D, 4 * c, acc, top, l);
 }
 
 // ---------------------------------------------------------------- host side
 // How a call's requests are worked on, from its host bounds.  Requests of up to
-// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 16,
-// 32 or 64 rows a block, the others to kv8_prefill_kernel.  A call whose bounds
+// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 8, 16,
+// 32 or 64 rows a team, the others to kv8_prefill_kernel.  A call whose bounds
 // allow more than 64 rows may mix long and short requests (a serving step that
 // prefills some and decodes others): then those of at most 16 rows (64 where
 // the group itself is larger) stay with the first kernel, where a long context
-// of few rows is split over many blocks.
+// of few rows is split over many teams.
 struct DecodePlan {
-  int mt, split, max_splits, row_cap, row_most;
+  int row_cap, row_most;
 };
-DecodePlan plan_decode(int N, int HK, int G, int max_q, int max_seq) {
+DecodePlan plan_decode(int N, int G, int max_q) {
   DecodePlan p{};
   const int64_t rows = (int64_t)max_q * G;
   if (rows <= 64) p.row_most = (int)rows;
   else if (N == 1 || G > 64) p.row_most = 0;
   else p.row_most = G <= 16 ? 16 : 64;
-  if (p.row_most == 0) return p;
-  p.mt = p.row_most <= 16 ? 1 : p.row_most <= 32 ? 2 : 4;
-  p.row_cap = 16 * p.mt;
-  const int64_t keys = ((int64_t)max_seq + kKeys - 1) / kKeys * kKeys;
-  int64_t want = (152 * 2 * 6) / ((int64_t)N * HK);  // six blocks for each place on the GPU
-  if (want < 1) want = 1;
-  int64_t split = (keys + want - 1) / want;
-  split = (split + kKeys - 1) / kKeys * kKeys;
-  if (split < 4 * kKeys) split = 4 * kKeys;
-  if (split > 2048) split = 2048;
-  p.split = (int)(split < keys ? split : keys < kKeys ? kKeys : keys);
-  p.max_splits = (int)((keys + p.split - 1) / p.split);
-  if (p.max_splits < 1) p.max_splits = 1;
+  p.row_cap = p.row_most <= 8 ? 8 : p.row_most <= 16 ? 16 : p.row_most <= 32 ? 32 : 64;
   return p;
 }
 
-template <int D, int MT>
-cudaError_t launch_decode(const AttnArgs &a, const DecodePlan &p, cudaStream_t s) {
-  using Ly = DecodeLay<D, MT>;
+template <int D, int NT, int MT>
+cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
+  using Ly = DecodeLay<D, NT, MT>;
+  static_assert((int64_t)Ly::TEAMS * 2 * Ly::ROWS <= kPartRows, "partial results");
   CUtensorMap mk, mv;
   const int keys = a.bs < kKeys ? a.bs : kKeys;
   if (!cache_map(&mk, a.kc, D, a.bs, (int64_t)a.P * a.HK, keys, true) ||
       !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys, true))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<D, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::BYTES);
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<D, MT><<<dim3(p.max_splits, a.HK, a.N), kThreads, Ly::BYTES, s>>>(a, mk, mv);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.max_splits == 1) return e;
+  kv8_decode_kernel<D, NT, MT><<<Ly::TEAMS, 32 * MT, Ly::BYTES, s>>>(a, mk, mv);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.row_cap, a.HK, a.N);
-  cfg.blockDim = dim3(kJoinThreads);
+  const bool wide = (int64_t)a.N * a.HK * 8 < Ly::TEAMS;  // eight pieces a pair, or more
+  cfg.gridDim = dim3(wide ? a.row_most : (a.row_most + 3) / 4, a.HK, a.N);
+  cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, true>, a, (int)Ly::TEAMS)
+              : cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, false>, a, (int)Ly::TEAMS);
+}
+template <int D> cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
+  if (a.row_cap == 8) return launch_decode<D, 1, 1>(a, s);
+  if (a.row_cap == 16) return launch_decode<D, 2, 1>(a, s);
+  if (a.row_cap == 32) return launch_decode<D, 4, 1>(a, s);
+  return launch_decode<D, 4, 2>(a, s);
 }
 
 }  // namespace
 
 namespace gdn_host {
 
-size_t kv8_attn_workspace_bytes(int N, int HK, int G, int D, int max_q, int max_seq) {
-  if (N <= 0 || max_q <= 0) return 0;
-  const DecodePlan p = plan_decode(N, HK, G, max_q, max_seq);
-  if (p.max_splits <= 1) return 0;
-  return (size_t)N * HK * p.row_cap * p.max_splits * (size_t)(D + 2) * sizeof(float);
+size_t kv8_attn_workspace_bytes(int N, int G, int D, int max_q) {
+  if (N <= 0 || max_q <= 0 || plan_decode(N, G, max_q).row_most == 0) return 0;
+  return (size_t)kPartRows * (size_t)(D + 2) * sizeof(float) + ((size_t)N + 1) * sizeof(int64_t);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs &c, cudaStream_t s) {
-  const DecodePlan p = plan_decode(c.N, c.HK, c.HQ / c.HK, c.max_q, c.max_seq);
   AttnArgs a{};
   static_cast<Kv8AttnArgs &>(a) = c;
   a.G = c.HQ / c.HK;
+  const DecodePlan p = plan_decode(c.N, a.G, c.max_q);
   a.scale_log2e = c.scale * gdnc::kLog2e;
-  a.split = p.split;
-  a.max_splits = p.max_splits;
   a.row_cap = p.row_cap;
   a.row_most = p.row_most;
-  if (a.split < 1) a.split = kKeys;
   a.part_o = static_cast<float *>(c.ws);
-  a.part_ml = reinterpret_cast<float2 *>(a.part_o + (size_t)c.N * c.HK * p.row_cap * p.max_splits * c.D);
+  a.part_ml = reinterpret_cast<float2 *>(a.part_o + kPartRows * c.D);
+  a.place = reinterpret_cast<int64_t *>(a.part_ml + kPartRows);
   if ((int64_t)c.max_q * a.G > p.row_most) {
     const cudaError_t e = launch_prefill(a, p.row_most + 1, s);
     if (e != cudaSuccess || p.row_most == 0) return e;
   }
-  if (c.D == 128) {
-    if (p.mt == 1) return launch_decode<128, 1>(a, p, s);
-    if (p.mt == 2) return launch_decode<128, 2>(a, p, s);
-    return launch_decode<128, 4>(a, p, s);
-  }
-  if (p.mt == 1) return launch_decode<64, 1>(a, p, s);
-  if (p.mt == 2) return launch_decode<64, 2>(a, p, s);
-  return launch_decode<64, 4>(a, p, s);
+  return c.D == 128 ? launch_rows<128>(a, s) : launch_rows<64>(a, s);
 }
 
 }  // namespace gdn_host

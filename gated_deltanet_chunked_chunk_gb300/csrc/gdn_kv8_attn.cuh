@@ -27,12 +27,11 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
 struct AttnArgs : gdn_host::Kv8AttnArgs {
   int G;  // query heads a kv head
   float scale_log2e;
-  int split;        // keys a split (a multiple of 64)
-  int max_splits;   // splits of the longest context
-  int row_cap;      // rows of partial results that a (request, kv head) has
-  int row_most;     // requests with more rows are the other kernel's
-  float *part_o;    // [(n HK + h) row_cap + row][max_splits][D]
-  float2 *part_ml;  // [(n HK + h) row_cap + row][max_splits]: maximum, sum
+  int row_cap;      // rows of a team of the decode kernel (8, 16, 32 or 64)
+  int row_most;     // requests with more rows are the prefill kernel's
+  float *part_o;    // [team][2][row_cap][D] partial results
+  float2 *part_ml;  // [team][2][row_cap]: maximum, sum
+  int64_t *place;   // [N + 1] where a request's stages begin on the line of all
 };
 
 // What one tile of rows [row0, row0 + count) of a request works on; rows are
@@ -41,7 +40,6 @@ struct Span {
   int t0, m;   // the request's tokens
   int L;       // its context
   int keys;    // keys that some row of the tile sees
-  int splits;  // at least 1
   int bits;    // status bits of what is wrong with the request
 };
 // False: there is nothing to do.
@@ -66,7 +64,6 @@ __device__ __forceinline__ bool request_span(const AttnArgs &a, int n, int row0,
   }
   const int last = min(row0 + count, s.m * a.G) - 1;
   s.keys = max(0, s.L - s.m + last / a.G + 1);
-  s.splits = max(1, (s.keys + a.split - 1) / a.split);
   return true;
 }
 

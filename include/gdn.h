@@ -616,7 +616,10 @@ size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int
  * a context of seq_lens[n] tokens, the new ones last; its token i of m sees the
  * places 0 .. seq_lens[n] - m + i.
  *     o = softmax(scale q K^T) V,  lse = log sum exp(scale q K^T)
- * A token that sees nothing has o = 0 and lse = -inf.
+ * A token that sees nothing has o = 0 and lse = -inf.  Two calls with the same
+ * arguments agree bit for bit; where a context is cut between blocks depends on
+ * the lengths of the whole batch, so in another batch a request's last bits can
+ * differ.
  *   q             : bf16 [T, HQ, D], ldq elements between tokens; query head h
  *                   reads kv head h / (HQ / HK)
  *   block_table   : int32 [N, width]; a needed entry outside [0, P) sets
