@@ -1,8 +1,10 @@
 """Build libgdn.so for sm_103a with nvcc (no cmake, no torch extension machinery).
 
 Every ``csrc/*.cu`` file is compiled to an object in parallel, then linked into
-``_build/libgdn.so`` next to this file.  Rebuilds only when a source or header
-is newer than the library.
+``_build/libgdn.so`` next to this file; ``csrc/gdn_torch.cpp``, the PyTorch
+binding of the operators around the recurrence, becomes ``_build/_gdn_torch.so``,
+linked to it.  Rebuilds only when a source or header is newer than the library,
+or the binding was built for another PyTorch.
 """
 from __future__ import annotations
 
@@ -10,6 +12,8 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +21,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
+BINDING = os.path.join(BUILD, "_gdn_torch.so")
+STAMP = os.path.join(BUILD, "_gdn_torch.for")  # the interpreter and PyTorch that BINDING was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", os.path.join(ROOT, "include")]
@@ -34,15 +40,35 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
 
 
+def _built_for() -> str:
+    import torch
+    return f"{sys.version} {torch.__version__} {torch.__file__}"
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not all(os.path.exists(p) for p in (LIB, BINDING, STAMP)):
         return False
-    t = os.path.getmtime(LIB)
+    with open(STAMP) as f:
+        if f.read() != _built_for():
+            return False
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _binding_command(obj: str):
+    """g++ command that compiles gdn_torch.cpp against the running interpreter's PyTorch."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+            "-c", os.path.join(CSRC, "gdn_torch.cpp"), "-o", obj]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -63,19 +89,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    binding_obj = os.path.join(BUILD, "gdn_torch.o")
+
+    def compile_binding():
+        r = subprocess.run(_binding_command(binding_obj), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on gdn_torch.cpp:\n{r.stdout}\n{r.stderr}")
+        return r.stderr
+
+    with ThreadPoolExecutor(max_workers=min(16, len(srcs) + 1)) as ex:
+        binding = ex.submit(compile_binding)
         for msg in ex.map(compile_one, zip(srcs, objs)):
             if verbose and msg:
                 print(msg)
+        msg = binding.result()
+        if verbose and msg:
+            print(msg)
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, binding_obj, "-L", BUILD, "-lgdn", "-L", libs, "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    with open(STAMP, "w") as f:
+        f.write(_built_for())
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))

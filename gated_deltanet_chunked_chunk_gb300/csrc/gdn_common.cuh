@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdn.h"
 
 #define GDN_CHUNK 64
@@ -141,6 +143,31 @@ struct ChunkBwdArgs {
 };
 size_t chunk_bwd_workspace_bytes(int B, int T, int H, int HV, int K, int V, int N, int varlen);
 cudaError_t launch_chunk_bwd(const ChunkBwdArgs &a, cudaStream_t s);
+// SMs of the current device, and leave for a kernel to use `bytes` of dynamic
+// shared memory, each asked of the runtime once a device (a query costs as
+// much as a small launch's checks).  `done`: a static of the caller, a bit a device.
+inline int sm_count() {
+  static std::atomic<int> count[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  int n = count[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = 152;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    count[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+template <class F> cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 // Norms, rotary positions and the paged 8-bit cache (gdn_norm.cu, gdn_rope.cu,
 // gdn_paged.cu, gdn_kv8_attn.cu).  Row r of z starts at (r / z_group) z_stride +
 // (r % z_group) D elements; act: 0 none, 1 SiLU, 2 sigmoid.

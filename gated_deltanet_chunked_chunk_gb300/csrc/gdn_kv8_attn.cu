@@ -762,7 +762,8 @@ cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
   if (!cache_map(&mk, a.kc, D, a.bs, (int64_t)a.P * a.HK, keys, true) ||
       !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys, true))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<D, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = gdn_host::allow_smem(kv8_decode_kernel<D, NT, MT>, Ly::BYTES, done);
   if (e != cudaSuccess) return e;
   kv8_decode_kernel<D, NT, MT><<<Ly::TEAMS, 32 * MT, Ly::BYTES, s>>>(a, mk, mv);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

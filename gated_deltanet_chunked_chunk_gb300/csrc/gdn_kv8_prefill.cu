@@ -567,7 +567,8 @@ cudaError_t launch(const AttnArgs &a, int min_rows, cudaStream_t s) {
   const int keys = a.bs < kTileKeys ? a.bs : kTileKeys;
   if (!cache_map(&mk, a.kc, D, a.bs, (int64_t)a.P * a.HK, keys, true) || !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys, false))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::BYTES);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = gdn_host::allow_smem(kv8_prefill_kernel<D>, Ly::BYTES, done);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.max_q * a.G;
   kv8_prefill_kernel<D><<<dim3((unsigned)((rows + 255) / 256), a.HK, a.N), kPrefThreads, Ly::BYTES, s>>>(a, min_rows, mk, mv);

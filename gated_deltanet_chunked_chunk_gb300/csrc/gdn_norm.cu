@@ -399,13 +399,6 @@ void launch_act(const NormArgs &a, int act, int blocks, cudaStream_t s) {
   else launch_one<BWD, L, NV, THREADS, ACT_SIGMOID>(a, blocks, s);
 }
 
-int sm_count() {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 // Lanes a row, vectors a lane and threads a block for a width; L = 0: the plain loop.
 struct Plan { int L, NV, threads, rows; };
 Plan plan_of(int D, bool aligned) {

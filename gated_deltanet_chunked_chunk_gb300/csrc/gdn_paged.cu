@@ -286,9 +286,7 @@ cudaError_t launch_paged_plan(const int32_t *cached, const int32_t *cu, int N, i
 cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ldv, uint8_t *kc, uint8_t *vc,
                               float *ks, float *vs, const int32_t *slots, int64_t T, int P, int HK, int D, int bs,
                               int32_t *dev_status, cudaStream_t s) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   AppendArgs a{{k, v}, {ldk, ldv}, {kc, vc}, {ks, vs}, slots, T, P, HK, D, bs, 1, dev_status};
   int64_t window = T * 2 * HK / ((int64_t)sms * 48);  // about 48 warps an SM
   a.window = (int)(window < 1 ? 1 : window > bs ? bs : window);

@@ -164,9 +164,7 @@ namespace gdn_host {
 cudaError_t launch_rope(const uint16_t *q, const uint16_t *k, const int32_t *pos, const float *inv_freq, int64_t T, int HQ,
                         int HK, int D, int rot, int interleaved, int inverse, float factor, int64_t ldq, int64_t ldk,
                         uint16_t *qo, uint16_t *ko, cudaStream_t s) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   RopeArgs a{q, k, qo, ko, ldq, ldk, pos, inv_freq, T, HQ, HK, D, rot, inverse, interleaved, factor, 1};
   // Tokens a block: 16 once the grid fills the SMs several times over, fewer
   // below that; the tile's angles (rot / 2 pairs of 8 bytes a token) stay
