@@ -290,7 +290,7 @@ int gdn_norm_gate(const uint16_t *x, const uint16_t *residual, const uint16_t *z
   if (z && z_rows < 0) return GDN_EINVAL;
   if (rows == 0) return GDN_OK;
   if (!x || !weight || !y) return GDN_EINVAL;
-  if (z_rows == 0) { z_rows = rows; z_stride = 0; }
+  if (z_rows == 0) z_stride = 0;
   return cuda_status(gdn_host::launch_norm_fwd(x, residual, z, weight, res_scale, eps, activation, rows, D, z_rows, z_stride,
                                                y, h, static_cast<cudaStream_t>(stream)));
 }
@@ -310,7 +310,7 @@ int gdn_norm_gate_bwd(const uint16_t *dy, const uint16_t *h, const uint16_t *z, 
   const size_t need = gdn_host::norm_bwd_workspace_bytes(rows, D);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
   if (!aligned16({workspace})) return GDN_EINVAL;
-  if (z_rows == 0) { z_rows = rows > 0 ? rows : 1; z_stride = 0; }
+  if (z_rows == 0) z_stride = 0;
   return cuda_status(gdn_host::launch_norm_bwd(dy, h, z, dh, weight, res_scale, eps, activation, rows, D, z_rows, z_stride,
                                                dx, dresidual, dz, dweight, workspace, static_cast<cudaStream_t>(stream)));
 }
@@ -348,6 +348,7 @@ int gdn_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ld
                    int page_size, int32_t *dev_status, void *stream) {
   if (T < 0 || P <= 0 || HK <= 0 || D <= 0 || page_size <= 0) return GDN_EINVAL;
   if (ldk < (int64_t)HK * D || ldv < (int64_t)HK * D || (int64_t)P * page_size > 2147483647LL) return GDN_EINVAL;
+  if (HK > 32767) return GDN_EUNSUPPORTED;  // heads index the grid's y dimension
   if (T == 0) return GDN_OK;
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !slot_mapping) return GDN_EINVAL;
   return cuda_status(gdn_host::launch_kv8_append(k, v, ldk, ldv, k_cache, v_cache, k_scale, v_scale, slot_mapping, T, P, HK,

@@ -63,6 +63,36 @@ __device__ __forceinline__ float softplus_fast(float x) {
 }
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
+// Two fp32 numbers and operations on both.
+struct f2 {
+  float x, y;
+};
+__device__ __forceinline__ f2 f2_of(float lo, float hi) { return f2{lo, hi}; }
+__device__ __forceinline__ float2 f2_get(f2 a) { return make_float2(a.x, a.y); }
+__device__ __forceinline__ f2 f2_both(float x) { return f2{x, x}; }
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) { return f2{a.x * b.x, a.y * b.y}; }
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) { return f2{a.x + b.x, a.y + b.y}; }
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) { return f2{fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
+// From and to the bits of two bf16.
+__device__ __forceinline__ f2 f2_bf16(uint32_t u) { return f2_of(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t f2_to_bf16(f2 a) {
+  const float2 x = f2_get(a);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+  return r;
+}
+// sigmoid of both: 1 / (1 + 2^(-z log2 e)) with the hardware's 2^x and 1/x.
+__device__ __forceinline__ f2 f2_sigmoid(f2 z) {
+  const float2 t = f2_get(f2_mul(z, f2_both(-1.4426950408889634f)));
+  float a, b;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(t.y));
+  const float2 e = f2_get(f2_add(f2_of(a, b), f2_both(1.f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(e.y));
+  return f2_of(a, b);
+}
+
 __device__ __forceinline__ void set_status(int32_t *st, int bits) {
   if (st) atomicOr(st, bits);
 }

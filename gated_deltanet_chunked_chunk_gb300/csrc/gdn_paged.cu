@@ -30,7 +30,6 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
     int32_t *slots, int32_t *positions, int32_t *num_free_out, int32_t *dev_status) {
   __shared__ int32_t s_start[kPlan], s_cached[kPlan], s_before[kPlan], s_end[kPlan];
   __shared__ int32_t s_warp[32];
-  __shared__ int32_t s_lo, s_hi;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int32_t tok = (int32_t)min((int64_t)blockIdx.x * kPlan + tid, (int64_t)T);
   int left = *num_free;
@@ -117,156 +116,222 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
 
 // ----------------------------------------------------------------- append
 // A run is a stretch of consecutive new tokens that go to consecutive places
-// of one page.  One warp writes a run of one head of K or V: it forms the
-// largest magnitude, the exponent e of the page's new scale 2^e, moves the
-// codes that were there before to that scale, and writes the new ones.
+// of one page.  For a run of one head of K or V: the largest magnitude, the
+// exponent e of the page's new scale 2^e, the codes that were there before moved
+// to that scale, the new ones written.
 //
 // The scale is a power of two because then x 2^-e is exact, the only rounding
 // is the one to the 8-bit format, and a page whose scale grows keeps its older
 // codes' bits as long as they stay normal numbers of the format.
 //
 // Bound: HBM for a prefill (2 bytes read, 1 written an element), latency for a
-// decode step.  A warp takes the runs that begin in a window of `window`
-// tokens: one token where there are few, a page's worth where there are many,
-// so that a long prefill has one run a warp.
+// decode step.  Runs are found with ballots over 32 slots.  Where tokens are
+// many (windows of a page's length), a block of four warps takes the runs that
+// begin in a window and keeps a run's values in registers between the maximum
+// and the rounding (reading them twice: 104 us for 65536 tokens of 4 heads,
+// against 39, 5.1 TB/s).  Where they are few, a warp takes the run of one token.
 struct AppendArgs {
-  const uint16_t *x[2];
-  int64_t ld[2];
-  uint8_t *cache[2];
-  float *scale[2];
+  const uint16_t *k, *v;
+  int64_t ldk, ldv;
+  uint8_t *kc, *vc;
+  float *ks, *vs;
   const int32_t *slots;
   int64_t T;
   int P, HK, D, bs, window;
+  int page_bits;  // log2(bs), or -1
   int32_t *dev_status;
 };
+__device__ __forceinline__ int page_of(const AppendArgs &a, int32_t slot) { return a.page_bits >= 0 ? slot >> a.page_bits : slot / a.bs; }
+__device__ __forceinline__ int place_of(const AppendArgs &a, int32_t slot) {
+  return a.page_bits >= 0 ? slot & (a.bs - 1) : slot % a.bs;
+}
 
-// Place of token t, or -1 (PAD, or a slot outside the cache).
+// Place of token t, or -1 (PAD, a slot outside the cache, no token).
 __device__ __forceinline__ int32_t slot_of(const AppendArgs &a, int64_t t, int &bits) {
+  if (t < 0 || t >= a.T) return -1;
   const int32_t s = a.slots[t];
-  if (s >= 0 && s / a.bs < a.P) return s;
+  if (s >= 0 && page_of(a, s) < a.P) return s;
   if (s != -1) bits |= GDN_DEV_BAD_SLOT;
   return -1;
-}
-__device__ __forceinline__ bool follows(const AppendArgs &a, int32_t prev, int32_t s) {
-  return prev >= 0 && s == prev + 1 && s % a.bs != 0;
 }
 __device__ __forceinline__ float finite_abs(float x) {
   x = fabsf(x);
   return x <= 3.402823466e38f ? x : 0.f;  // infinities and NaN do not set a scale
 }
+// Largest finite magnitude of two bf16, given their bits.
+__device__ __forceinline__ float amax2(uint32_t u) {
+  return fmaxf(finite_abs(__uint_as_float(u << 16)), finite_abs(__uint_as_float(u & 0xffff0000u)));
+}
+__device__ __forceinline__ uint32_t codes2(uint32_t u, float inv) {
+  const float2 x = gdn::f2_get(gdn::f2_mul(gdn::f2_bf16(u), gdn::f2_both(inv)));
+  return gdnkv::cvt_e4m3x2(x.x, x.y);
+}
 
-template <bool VEC>
-__device__ void write_run(const AppendArgs &a, int kv, int h, int64_t t0, int n, int32_t slot) {
-  const int lane = threadIdx.x & 31;
-  const int page = slot / a.bs, off = slot - page * a.bs;
-  const uint16_t *x = a.x[kv] + t0 * a.ld[kv] + (int64_t)h * a.D;
-  uint8_t *codes = a.cache[kv] + ((int64_t)page * a.HK + h) * (int64_t)a.bs * a.D;
-  float *scale = a.scale[kv] + (int64_t)page * a.HK + h;
-  const int vpr = a.D / 8;
+// WARPS warps write a run of n tokens from t0 to places from `slot` on.  NV > 0:
+// a thread holds up to NV units of 16 elements (NV * 32 * WARPS units hold a
+// page; D / 16 divides 32 WARPS); NV = 0: values read twice, in units of 16 with
+// VEC, else element by element (any D and alignment).
+template <int WARPS, int NV, bool VEC>
+__device__ __forceinline__ void write_run(const AppendArgs &a, int kv, int h, int64_t t0, int n, int32_t slot, float *sh) {
+  constexpr int TH = 32 * WARPS;
+  const int tid = WARPS > 1 ? (int)threadIdx.x : (int)(threadIdx.x & 31);
+  const int page = page_of(a, slot), off = place_of(a, slot);
+  const int64_t ld = kv ? a.ldv : a.ldk;
+  const uint16_t *x = (kv ? a.v : a.k) + t0 * ld + (int64_t)h * a.D;
+  uint8_t *codes = (kv ? a.vc : a.kc) + ((int64_t)page * a.HK + h) * (int64_t)a.bs * a.D;
+  float *scale = (kv ? a.vs : a.ks) + (int64_t)page * a.HK + h;
+  const float before = off > 0 ? *scale : 0.f;
+  uint8_t *dst = codes + (int64_t)off * a.D;
   float amax = 0.f;
-  if (VEC) {
-    for (int e = lane; e < n * vpr; e += 32) {
-      const int r = e / vpr, c = e - r * vpr;
-      const uint4 v = *reinterpret_cast<const uint4 *>(x + (int64_t)r * a.ld[kv] + c * 8);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint4 v[NV > 0 ? NV : 1][2];
+  const int upr = a.D / 16;  // units a row
+  const int units = n * upr;
+  if (NV > 0) {
+    const int r0 = tid / upr, c = (tid - r0 * upr) * 16, dr = TH / upr;
+    const uint16_t *src = x + (int64_t)r0 * ld + c;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        amax = fmaxf(amax, finite_abs(__uint_as_float(u[j] << 16)));
-        amax = fmaxf(amax, finite_abs(__uint_as_float(u[j] & 0xffff0000u)));
+    for (int j = 0; j < NV; ++j) {
+      const bool on = tid + j * TH < units;
+      const uint4 *p = reinterpret_cast<const uint4 *>(src + (int64_t)j * dr * ld);
+      v[j][0] = on ? __ldcs(p) : make_uint4(0, 0, 0, 0);
+      v[j][1] = on ? __ldcs(p + 1) : make_uint4(0, 0, 0, 0);
+    }
+    // maxima of the magnitudes' bits, two at a time
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        top = __vmaxu2(top, __vmaxu2(v[j][k].x & 0x7fff7fffu, v[j][k].y & 0x7fff7fffu));
+        top = __vmaxu2(top, __vmaxu2(v[j][k].z & 0x7fff7fffu, v[j][k].w & 0x7fff7fffu));
       }
+    if ((top & 0xffffu) < 0x7f80u && (top >> 16) < 0x7f80u) {
+      amax = amax2(top);
+    } else {  // an infinity or NaN among them
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          amax = fmaxf(amax, fmaxf(fmaxf(amax2(v[j][k].x), amax2(v[j][k].y)), fmaxf(amax2(v[j][k].z), amax2(v[j][k].w))));
+    }
+  } else if (VEC) {
+    for (int e = tid; e < units; e += TH) {
+      const int r = e / upr, c = (e - r * upr) * 16;
+      const uint4 *p = reinterpret_cast<const uint4 *>(x + (int64_t)r * ld + c);
+      const uint4 u = p[0], w = p[1];
+      amax = fmaxf(amax, fmaxf(fmaxf(amax2(u.x), amax2(u.y)), fmaxf(amax2(u.z), amax2(u.w))));
+      amax = fmaxf(amax, fmaxf(fmaxf(amax2(w.x), amax2(w.y)), fmaxf(amax2(w.z), amax2(w.w))));
     }
   } else {
-    for (int e = lane; e < n * a.D; e += 32) {
+    for (int e = tid; e < n * a.D; e += TH) {
       const int r = e / a.D, c = e - r * a.D;
-      amax = fmaxf(amax, finite_abs(gdn::bf2f(x[(int64_t)r * a.ld[kv] + c])));
+      amax = fmaxf(amax, finite_abs(gdn::bf2f(x[(int64_t)r * ld + c])));
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (WARPS > 1) {
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) amax = fmaxf(amax, sh[i]);
+    __syncthreads();
+  }
   int e = gdnkv::scale_exponent(amax);
   if (off > 0) {
-    const int old = gdnkv::exponent_of(*scale);
+    const int old = gdnkv::exponent_of(before);
     if (old >= e) {
       e = old;
     } else {
       // older codes move to the larger scale, rounded to the format again
       const float f = gdnkv::pow2(max(old - e, -126));
-      const int words = off * a.D / 4;
       if (a.D % 4 == 0) {
         uint32_t *p = reinterpret_cast<uint32_t *>(codes);
-        for (int i = lane; i < words; i += 32) p[i] = gdnkv::rescale4(p[i], f);
+        for (int i = tid; i < off * a.D / 4; i += TH) p[i] = gdnkv::rescale4(p[i], f);
       } else {
-        for (int i = lane; i < off * a.D; i += 32) codes[i] = (uint8_t)gdnkv::rescale4(codes[i], f);
+        for (int i = tid; i < off * a.D; i += TH) codes[i] = (uint8_t)gdnkv::rescale4(codes[i], f);
       }
     }
   }
   const float inv = gdnkv::pow2(-e);
-  uint8_t *dst = codes + (int64_t)off * a.D;
-  if (VEC) {
-    for (int i = lane; i < n * vpr; i += 32) {
-      const int r = i / vpr, c = i - r * vpr;
-      const uint4 v = *reinterpret_cast<const uint4 *>(x + (int64_t)r * a.ld[kv] + c * 8);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[2];
+  if (NV > 0) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t lo = gdnkv::cvt_e4m3x2(__uint_as_float(u[2 * j] << 16) * inv, __uint_as_float(u[2 * j] & 0xffff0000u) * inv);
-        const uint32_t hi =
-            gdnkv::cvt_e4m3x2(__uint_as_float(u[2 * j + 1] << 16) * inv, __uint_as_float(u[2 * j + 1] & 0xffff0000u) * inv);
-        o[j] = lo | (hi << 16);
+    for (int j = 0; j < NV; ++j) {
+      if (tid + j * TH >= units) break;
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        o[2 * k] = codes2(v[j][k].x, inv) | (codes2(v[j][k].y, inv) << 16);
+        o[2 * k + 1] = codes2(v[j][k].z, inv) | (codes2(v[j][k].w, inv) << 16);
       }
-      *reinterpret_cast<uint2 *>(dst + (int64_t)i * 8) = make_uint2(o[0], o[1]);
+      *reinterpret_cast<uint4 *>(dst + (int64_t)(tid + j * TH) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else if (VEC) {
+    for (int e = tid; e < units; e += TH) {
+      const int r = e / upr, c = (e - r * upr) * 16;
+      const uint4 *p = reinterpret_cast<const uint4 *>(x + (int64_t)r * ld + c);
+      const uint4 u = p[0], w = p[1];
+      *reinterpret_cast<uint4 *>(dst + (int64_t)e * 16) =
+          make_uint4(codes2(u.x, inv) | (codes2(u.y, inv) << 16), codes2(u.z, inv) | (codes2(u.w, inv) << 16),
+                     codes2(w.x, inv) | (codes2(w.y, inv) << 16), codes2(w.z, inv) | (codes2(w.w, inv) << 16));
     }
   } else {
-    for (int i = lane; i < n * a.D; i += 32) {
+    for (int i = tid; i < n * a.D; i += TH) {
       const int r = i / a.D, c = i - r * a.D;
-      dst[i] = (uint8_t)gdnkv::cvt_e4m3x2(gdn::bf2f(x[(int64_t)r * a.ld[kv] + c]) * inv, 0.f);
+      dst[i] = (uint8_t)gdnkv::cvt_e4m3x2(gdn::bf2f(x[(int64_t)r * ld + c]) * inv, 0.f);
     }
   }
-  __syncwarp();
-  if (lane == 0) *scale = gdnkv::pow2(e);
+  if (tid == 0) *scale = gdnkv::pow2(e);
 }
 
-template <bool VEC>
-__global__ void __launch_bounds__(256) kv8_append_kernel(const AppendArgs a) {
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+// One head of K or V and one window of tokens a group of WARPS warps; a warp of
+// a wider group finds the runs for itself, all alike.  Short runs (a large
+// decode step's) go to the warps in turn, long ones to all of them.
+template <int WARPS, int NV, bool VEC>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) kv8_append_kernel(const AppendArgs a) {
+  __shared__ float sh[WARPS];
+  const int64_t unit = WARPS == 1 ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const int lane = threadIdx.x & 31;
-  const int per = 2 * a.HK;
-  const int64_t win = unit / per;
-  const int64_t t0 = win * a.window;
+  const int64_t t0 = unit * a.window, t1 = min(t0 + a.window, a.T);
   if (t0 >= a.T) return;
-  const int kv = (int)(unit % per) & 1, h = (int)(unit % per) >> 1;
-  const int64_t t1 = min(t0 + a.window, a.T);
-  int bits = 0;
-  for (int64_t t = t0; t < t1;) {
-    const int32_t s = slot_of(a, t, bits);
-    if (s < 0) {
-      ++t;
-      continue;
-    }
-    if (t > 0) {
-      int ignore = 0;
-      if (follows(a, slot_of(a, t - 1, ignore), s)) {  // an earlier token leads this run
-        ++t;
-        continue;
+  const int kv = blockIdx.y & 1, h = blockIdx.y >> 1;
+  int bits = 0, ignore = 0, short_runs = 0;
+  for (int64_t base = t0; base < t1; base += 32) {
+    const int64_t t = base + lane;
+    const int32_t s = slot_of(a, t, t < t1 ? bits : ignore);
+    int32_t prev = __shfl_up_sync(0xffffffffu, s, 1);
+    if (lane == 0) prev = slot_of(a, t - 1, ignore);
+    const bool follows = s >= 0 && prev >= 0 && s == prev + 1 && place_of(a, s) != 0;
+    const uint32_t cont = __ballot_sync(0xffffffffu, follows);
+    uint32_t lead = __ballot_sync(0xffffffffu, t < t1 && s >= 0 && !follows);
+    while (lead) {
+      const int p = __ffs((int)lead) - 1;
+      lead &= lead - 1;
+      const int32_t slot = __shfl_sync(0xffffffffu, s, p);
+      // tokens p + 1 .. that follow; a run that reaches the last of the 32 may go on
+      const uint32_t stop = ~(p == 31 ? 0u : cont >> (p + 1)) ;
+      int n = 1 + min(31 - p, __ffs((int)stop) - 1);
+      if (p + n == 32) {
+        for (;;) {
+          const int32_t more = slot_of(a, base + p + n + lane, ignore);
+          const bool ok = more == slot + n + lane && place_of(a, slot) + n + lane < a.bs;
+          const uint32_t m = ~__ballot_sync(0xffffffffu, ok);
+          n += m ? __ffs((int)m) - 1 : 32;
+          if (m) break;
+        }
+      }
+      if (WARPS > 1 && n * a.D <= 512) {
+        if (short_runs++ % WARPS == (int)(threadIdx.x >> 5)) write_run<1, 0, VEC>(a, kv, h, base + p, n, slot, sh);
+      } else {
+        write_run<WARPS, NV, VEC>(a, kv, h, base + p, n, slot, sh);
       }
     }
-    // the run's length: 32 tokens at a time
-    int n = 1;
-    const int most = a.bs - s % a.bs;
-    while (n < most) {
-      int ignore = 0;
-      const int64_t tt = t + n + lane;
-      const bool ok = n + lane < most && tt < a.T && slot_of(a, tt, ignore) == s + n + lane;
-      const uint32_t m = __ballot_sync(0xffffffffu, ok);
-      const int k = m == 0xffffffffu ? 32 : __ffs((int)~m) - 1;
-      n += k;
-      if (k < 32) break;
-    }
-    write_run<VEC>(a, kv, h, t, n, s);
-    t += n;
   }
-  if (bits && lane == 0) set_status(a.dev_status, bits);
+  if (bits && (WARPS == 1 || threadIdx.x < 32)) set_status(a.dev_status, bits);
+}
+
+template <int NV> void launch_windows(const AppendArgs &a, int64_t units, cudaStream_t s) {
+  kv8_append_kernel<4, NV, true><<<dim3((unsigned)units, 2 * a.HK), 128, 0, s>>>(a);
 }
 
 }  // namespace
@@ -287,18 +352,30 @@ cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk,
                               float *ks, float *vs, const int32_t *slots, int64_t T, int P, int HK, int D, int bs,
                               int32_t *dev_status, cudaStream_t s) {
   const int sms = sm_count();
-  AppendArgs a{{k, v}, {ldk, ldv}, {kc, vc}, {ks, vs}, slots, T, P, HK, D, bs, 1, dev_status};
-  int64_t window = T * 2 * HK / ((int64_t)sms * 48);  // about 48 warps an SM
-  a.window = (int)(window < 1 ? 1 : window > bs ? bs : window);
-  const int64_t units = (T + a.window - 1) / a.window * 2 * HK;
-  const int64_t blocks = (units + 7) / 8;
+  AppendArgs a{k, v, ldk, ldv, kc, vc, ks, vs, slots, T, P, HK, D, bs, 1, -1, dev_status};
+  for (int i = 0; i < 31; ++i)
+    if (bs == 1 << i) a.page_bits = i;
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(kc) |
+                         reinterpret_cast<uintptr_t>(vc);
+  // 16-byte accesses, and threads that keep their column from row to row
+  const bool vec = !(bits & 15) && (D == 16 || D == 32 || D == 64 || D == 128 || D == 256 || D == 512) && ldk % 8 == 0 && ldv % 8 == 0;
+  // Windows of a page's length once the tokens would fill every SM with blocks
+  // four times over and a thread can hold its share of a page; else a token each.
+  const int held = (bs * (D / 16) + 127) / 128;  // units a thread
+  const bool wide = vec && held <= 8 && bs >= 8 && (T + bs - 1) / bs * 2 * HK >= 4 * (int64_t)sms;
+  if (wide) a.window = bs;
+  const int64_t units = (T + a.window - 1) / a.window, blocks = wide ? units : (units + 7) / 8;
   if (blocks > 2147483647LL) return cudaErrorInvalidValue;
-  const uintptr_t in = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
-  const uintptr_t out = reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc);
-  if (!(in & 15) && !(out & 7) && D % 8 == 0 && ldk % 8 == 0 && ldv % 8 == 0)
-    kv8_append_kernel<true><<<(int)blocks, 256, 0, s>>>(a);
-  else
-    kv8_append_kernel<false><<<(int)blocks, 256, 0, s>>>(a);
+  if (wide) {
+    if (held <= 1) launch_windows<1>(a, units, s);
+    else if (held <= 2) launch_windows<2>(a, units, s);
+    else if (held <= 4) launch_windows<4>(a, units, s);
+    else launch_windows<8>(a, units, s);
+  } else if (vec) {
+    kv8_append_kernel<1, 0, true><<<dim3((unsigned)blocks, 2 * HK), 256, 0, s>>>(a);
+  } else {
+    kv8_append_kernel<1, 0, false><<<dim3((unsigned)blocks, 2 * HK), 256, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -78,7 +78,7 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
 // Places in a head: rotated ones first (a pair of vectors each in the half
 // layout, a vector each when interleaved), then the vectors that pass.
 template <bool INTER>
-__global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int places, int rows_at_once) {
+__global__ void __launch_bounds__(256, 8) rope_vec_kernel(const RopeArgs a, int places, int rows_at_once) {
   extern __shared__ float2 cs[];
   const int64_t t0 = (int64_t)blockIdx.x * a.tile;
   const int n = (int)(a.T - t0 < a.tile ? a.T - t0 : a.tile);
@@ -90,43 +90,68 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int pla
   if (r0 >= rows_at_once) return;
   int t = r0 / H, h = r0 - t * H;
   const int dt = rows_at_once / H, dh = rows_at_once - dt * H;
-  for (; t < n; t += dt, h += dh) {
-    if (h >= H) {
-      h -= H;
-      if (++t >= n) break;
+  const bool pass = u >= turned;  // this thread's place is not turned
+  const int e0 = pass ? a.rot + (u - turned) * 8 : u * 8, e1 = e0 + half;
+  // Two (token, head) rows a trip, both loads issued before either is used:
+  // eight blocks of 32 registers a thread on a SM measured 191 us for 65536 x 36
+  // heads of 128, one row a trip 206, three (more registers) 207.
+  constexpr int U = 2;
+  while (t < n) {
+    const uint16_t *in[U];
+    uint16_t *out[U];
+    int tt[U];
+    uint4 v0[U], v1[U];
+    bool on[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      on[i] = t < n;
+      tt[i] = t;
+      const int64_t tok = t0 + t;
+      const bool isq = h < a.HQ;
+      in[i] = isq ? a.q + tok * a.ldq + (int64_t)h * a.D : a.k + tok * a.ldk + (int64_t)(h - a.HQ) * a.D;
+      out[i] = isq ? a.qo + (tok * a.HQ + h) * a.D : a.ko + (tok * a.HK + h - a.HQ) * a.D;
+      if (on[i]) {
+        if (!pass || in[i] != out[i]) v0[i] = __ldcs(reinterpret_cast<const uint4 *>(in[i] + e0));
+        if (!INTER && !pass) v1[i] = __ldcs(reinterpret_cast<const uint4 *>(in[i] + e1));
+      }
+      t += dt;
+      h += dh;
+      if (h >= H) {
+        h -= H;
+        ++t;
+      }
     }
-    const bool isq = h < a.HQ;
-    const uint16_t *in = isq ? a.q + (t0 + t) * a.ldq + (int64_t)h * a.D : a.k + (t0 + t) * a.ldk + (int64_t)(h - a.HQ) * a.D;
-    uint16_t *out = isq ? a.qo + ((t0 + t) * a.HQ + h) * a.D : a.ko + ((t0 + t) * a.HK + h - a.HQ) * a.D;
-    if (u >= turned) {
-      const int e = a.rot + (u - turned) * 8;
-      if (in != out) __stcs(reinterpret_cast<uint4 *>(out + e), __ldcs(reinterpret_cast<const uint4 *>(in + e)));
-      continue;
-    }
-    if (INTER) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (!on[i]) continue;
+      if (pass) {
+        if (in[i] != out[i]) __stcs(reinterpret_cast<uint4 *>(out[i] + e0), v0[i]);
+        continue;
+      }
       float x[8], y[8];
-      unpack8(__ldcs(reinterpret_cast<const uint4 *>(in + u * 8)), x);
-      const float2 *c = cs + t * half + u * 4;
+      unpack8(v0[i], x);
+      if (INTER) {
+        const float2 *c = cs + tt[i] * half + u * 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 w = c[j];
-        y[2 * j] = x[2 * j] * w.x - x[2 * j + 1] * w.y;
-        y[2 * j + 1] = x[2 * j] * w.y + x[2 * j + 1] * w.x;
-      }
-      __stcs(reinterpret_cast<uint4 *>(out + u * 8), pack8(y));
-    } else {
-      float x[8], z[8], y[8], v[8];
-      unpack8(__ldcs(reinterpret_cast<const uint4 *>(in + u * 8)), x);
-      unpack8(__ldcs(reinterpret_cast<const uint4 *>(in + half + u * 8)), z);
-      const float2 *c = cs + t * half + u * 8;
+        for (int j = 0; j < 4; ++j) {
+          const float2 w = c[j];
+          y[2 * j] = x[2 * j] * w.x - x[2 * j + 1] * w.y;
+          y[2 * j + 1] = x[2 * j] * w.y + x[2 * j + 1] * w.x;
+        }
+        __stcs(reinterpret_cast<uint4 *>(out[i] + e0), pack8(y));
+      } else {
+        float z[8], v[8];
+        unpack8(v1[i], z);
+        const float2 *c = cs + tt[i] * half + u * 8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 w = c[j];
-        y[j] = x[j] * w.x - z[j] * w.y;
-        v[j] = x[j] * w.y + z[j] * w.x;
+        for (int j = 0; j < 8; ++j) {
+          const float2 w = c[j];
+          y[j] = x[j] * w.x - z[j] * w.y;
+          v[j] = x[j] * w.y + z[j] * w.x;
+        }
+        __stcs(reinterpret_cast<uint4 *>(out[i] + e0), pack8(y));
+        __stcs(reinterpret_cast<uint4 *>(out[i] + e1), pack8(v));
       }
-      __stcs(reinterpret_cast<uint4 *>(out + u * 8), pack8(y));
-      __stcs(reinterpret_cast<uint4 *>(out + half + u * 8), pack8(v));
     }
   }
 }
@@ -166,12 +191,12 @@ cudaError_t launch_rope(const uint16_t *q, const uint16_t *k, const int32_t *pos
                         uint16_t *qo, uint16_t *ko, cudaStream_t s) {
   const int sms = sm_count();
   RopeArgs a{q, k, qo, ko, ldq, ldk, pos, inv_freq, T, HQ, HK, D, rot, inverse, interleaved, factor, 1};
-  // Tokens a block: 16 once the grid fills the SMs several times over, fewer
-  // below that; the tile's angles (rot / 2 pairs of 8 bytes a token) stay
+  // Tokens a block: 8 once the grid fills the SMs several times over (16: 200
+  // against 191 us), fewer below that; the tile's angles (rot / 2 pairs of 8 bytes a token) stay
   // within 32 KB.
   int64_t tile = T / ((int64_t)sms * 8);
   const int64_t most = (32 << 10) / ((int64_t)(rot / 2) * 8 + 1);
-  if (tile > 16) tile = 16;
+  if (tile > 8) tile = 8;
   if (tile > most) tile = most;
   if (tile < 1) tile = 1;
   if ((T + tile - 1) / tile > 2147483647LL) return cudaErrorInvalidValue;
