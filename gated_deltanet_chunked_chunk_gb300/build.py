@@ -115,7 +115,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, binding_obj, "-L", BUILD, "-lgdn", "-L", libs, "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_cpu",
+           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

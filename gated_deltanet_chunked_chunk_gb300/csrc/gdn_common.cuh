@@ -63,6 +63,15 @@ __device__ __forceinline__ float softplus_fast(float x) {
 }
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
+// Programmatic dependent launch.  A kernel launched with launch_dependent()
+// below may have its blocks in place while the kernel before it on the stream
+// still runs; grid_wait() waits until that kernel is done and its writes are
+// visible, and every thread calls it before it touches global memory (also where
+// it then has nothing to do: a grid that ended early would let the next one pass
+// the one before).  grid_release() lets such a successor's blocks come in.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Two fp32 numbers and operations on both.
 struct f2 {
   float x, y;
@@ -197,6 +206,22 @@ template <class F> cudaError_t allow_smem(F *kernel, int bytes, std::atomic<uint
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+// A launch whose blocks may come in before the stream's last kernel is done; the
+// kernel begins with gdn::grid_wait().
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A &&...args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 // Norms, rotary positions and the paged 8-bit cache (gdn_norm.cu, gdn_rope.cu,
 // gdn_paged.cu, gdn_kv8_attn.cu).  Row r of z starts at (r / z_group) z_stride +

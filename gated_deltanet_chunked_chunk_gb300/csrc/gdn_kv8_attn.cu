@@ -176,9 +176,6 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x;
-  // The joining kernel's blocks may come in as soon as every block here has
-  // started; they wait for this grid's results.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const uint32_t bar = sb + Ly::OFF_BAR, never = bar + 16 * R;
   volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_BAR + (2 * R + 1) * 8);
@@ -190,13 +187,44 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     *failed = 0;
   }
   if (MT > 1) __syncthreads(); else __syncwarp();
+  grid_wait();
+  // Only now: the joining kernel reads lengths and offsets before its own wait.
+  grid_release();
 
   // ------------------------------------------------- this team's stretch
-  // Lane l sums the stages of requests [l seg, (l + 1) seg); the last team
-  // also writes every request's place on the line for the joining kernel.
+  // Up to 32 requests, a lane each; else lane l sums the stages of requests
+  // [l seg, (l + 1) seg) and the requests of the lane that holds the start are
+  // looked at again.  The last team also writes every request's place on the
+  // line for the joining kernel, which forms the places of few requests itself.
   Place at{};
   int left;  // stages of this team still to do
-  {
+  if (a.N <= 32) {
+    Span s{};
+    const int of = lane < a.N ? stages_of(a, lane, s) : 0;
+    if (s.bits && team == 0 && warp == 0) set_status(a.dev_status, s.bits);
+    // below 2^31: 32 contexts of up to 2^25 stages would be 2^36 keys
+    const uint32_t mine = (uint32_t)of * (uint32_t)a.HK;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t per = (uint32_t)stretch_of(total, Ly::TEAMS), start = per * (uint32_t)team;
+    if (start >= total) return;
+    left = (int)min(per, total - start);
+    const int n = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;
+    at.n = n;
+    at.of = __shfl_sync(0xffffffffu, of, n);
+    at.s.t0 = __shfl_sync(0xffffffffu, s.t0, n);
+    at.s.m = __shfl_sync(0xffffffffu, s.m, n);
+    at.s.L = __shfl_sync(0xffffffffu, s.L, n);
+    at.s.keys = __shfl_sync(0xffffffffu, s.keys, n);
+    const uint32_t in = start - (__shfl_sync(0xffffffffu, incl, n) - (uint32_t)at.of * (uint32_t)a.HK);
+    at.h = (int)(in / (uint32_t)at.of);
+    at.stage = (int)(in - (uint32_t)at.h * (uint32_t)at.of);
+  } else {
     Span s;
     const int seg = (a.N + 31) / 32;
     int64_t mine = 0;
@@ -224,7 +252,7 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     }
     if (start >= total) return;
     left = (int)min(per, total - start);
-    const int owner = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;  // the lane whose requests hold the start
+    const int owner = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;
     int64_t run = __shfl_sync(0xffffffffu, incl - mine, owner);
     for (int base = owner * seg;; base += 32) {
       const int n = base + lane;
@@ -255,6 +283,22 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
   // pages at a time, a page a lane.  A page that is not there counts as keys
   // that nothing sees (logits of -inf) and reads zeros.
   // The place is kept in shared memory: the products need the registers.
+  // The first pair's queries are read meanwhile.
+  const int g = lane >> 2, t = lane & 3;
+  const int row0 = 8 * NT * warp;  // this warp's first row
+  uint4 qraw[NT][2 * NCH];
+  auto read_q = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + 8 * nt + g;
+      const uint16_t *src = a.q + (int64_t)(at.s.t0 + row / a.G) * a.ldq + (int64_t)(at.h * a.G + row % a.G) * D;
+#pragma unroll
+      for (int i = 0; i < 2 * NCH; ++i)
+        qraw[nt][i] = row < at.s.m * a.G ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * (t + 4 * (i >> 1))) + (i & 1))
+                                         : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (NT == 1) read_q();
   Place &ahead = *reinterpret_cast<Place *>(smem + Ly::OFF_AHEAD);
   static_assert(sizeof(Place) <= 48, "room for the place");
   int to_call = left;
@@ -269,40 +313,46 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     if (to_call == 0 || *failed) return;
     const int stage = ahead.stage, head = ahead.h;
     const int first = (stage * kKeys) >> page_bits;
-    if (first / 32 != batch) {
+    const bool fresh = first / 32 != batch;
+    float vs = 0.f;
+    if (fresh) {
       batch = first / 32;
       const int pi = batch * 32 + lane;
       page = -1;
-      ks = 0.f;
-      lv = -INFINITY;
-      iv = 1.f;
       if (((int64_t)pi << page_bits) < ahead.s.keys) {
-        const int32_t p = a.table[(int64_t)ahead.n * a.width + pi];
-        if (p < 0 || p >= a.P) {
+        page = a.table[(int64_t)ahead.n * a.width + pi];
+        if (page < 0 || page >= a.P) {
           set_status(a.dev_status, GDN_DEV_BAD_SLOT);
-        } else {
-          page = p;
-          const int64_t i = (int64_t)p * a.HK + head;
-          ks = a.ks[i];
-          const float v = a.vs[i];
-          lv = log2f(v);
-          iv = 1.f / v;
+          page = -1;
         }
+      }
+      ks = 0.f;
+      if (page >= 0) {
+        const int64_t i = (int64_t)page * a.HK + head;
+        ks = a.ks[i];
+        vs = a.vs[i];
       }
     }
     const int src = (first - batch * 32 + (lane & (ppt - 1))) & 31;
     const int pg = __shfl_sync(0xffffffffu, page, src);
-    const float4 par = make_float4(__shfl_sync(0xffffffffu, ks, src), __shfl_sync(0xffffffffu, lv, src),
-                                   __shfl_sync(0xffffffffu, iv, src), 0.f);
     zc = pg >= 0 ? pg * a.HK + head : a.P * a.HK;  // outside the tensor: TMA fills in zeros
     yc = (stage * kKeys) & (a.bs - 1);
+    // The tile is called before the scales are looked at, whose reads are on
+    // their way too; the arrival, which makes the constants visible, comes last.
     const int slot = called % R;
-    if (lane < ppt) *reinterpret_cast<float4 *>(smem + Ly::OFF_PAR + (called % (R + 1)) * 64 + lane * 16) = par;
-    __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(KF(slot), Ly::TILE);
+    if (lane == 0) mbar_expect_tx(KF(slot), Ly::TILE);
     __syncwarp();
     if (lane < ppt) tma_load_3d(sb + Ly::OFF_K + slot * Ly::TILE + lane * box * D, &mk, KF(slot), 0, yc, zc);
     ++called_k;
+    if (fresh) {  // a page that is not there: -inf
+      lv = log2f(vs);
+      iv = vs > 0.f ? 1.f / vs : 1.f;
+    }
+    const float4 par = make_float4(__shfl_sync(0xffffffffu, ks, src), __shfl_sync(0xffffffffu, lv, src),
+                                   __shfl_sync(0xffffffffu, iv, src), 0.f);
+    if (lane < ppt) *reinterpret_cast<float4 *>(smem + Ly::OFF_PAR + (called % (R + 1)) * 64 + lane * 16) = par;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(KF(slot));
     // on to the next stage
     if (stage + 1 < ahead.of) {
       __syncwarp();
@@ -335,7 +385,6 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     }
   }
 
-  const int g = lane >> 2, t = lane & 3;
   const int kperm = (g >> 1) | ((g & 1) << 2);  // row of key g of 8
   const uint32_t sel0 = (g & 1) ? 0x1504u : 0x5140u, sel1 = (g & 1) ? 0x3726u : 0x7362u;
   const int va = t + 4 * (g & 1), vb = t + 4 * ((g & 1) ^ 1);
@@ -348,21 +397,17 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     const int h = at.h, L = s.L, m = s.m;
     const bool from_start = at.stage == 0, to_end = left >= at.of - at.stage;
     const int count = to_end ? at.of - at.stage : left;
-    const int row0 = 8 * NT * warp;  // this warp's first row
     // Queries: row row0 + 8 nt + g; thread t holds d = 16 (t + 4 i) + 0..15,
     // k-step 4 i + w taking 4 w + {0, 1 | 2, 3} of them.
     uint32_t qf[Ly::QS ? 1 : 4 * NCH][NT][2];
     float krow[NT][2];  // of rows row0 + 8 nt + 2 t + e
+    if (NT > 1 || done > 0) read_q();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + 8 * nt + g;
-      const bool on = row < m * a.G;
-      uint4 u[2 * NCH];
+      const uint4 *u = qraw[nt];
       float top = 0.f, bad = 0.f;
-      const uint16_t *src = a.q + (int64_t)(s.t0 + row / a.G) * a.ldq + (int64_t)(h * a.G + row % a.G) * D;
 #pragma unroll
       for (int i = 0; i < 2 * NCH; ++i) {
-        u[i] = on ? __ldg(reinterpret_cast<const uint4 *>(src + 16 * (t + 4 * (i >> 1))) + (i & 1)) : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -670,12 +715,35 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int tea
   __shared__ float2 sml[4];
   const int n = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = WIDE ? blockIdx.x : 4 * blockIdx.x + warp;
+  // A dependent launch that the decode kernel, which has waited for what came
+  // before, lets in: lengths and offsets may be read before the wait.
+  grid_release();
   Span s;
   const int of = stages_of(a, n, s);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The request's place on the line: from the decode kernel, or, where the
+  // requests are few, formed here while that kernel still runs.
+  int64_t total = 0, place = 0;
+  if (a.N <= 32) {
+    Span other;
+    for (int i = lane; i < a.N; i += 32) {
+      const int64_t c = (int64_t)stages_of(a, i, other) * a.HK;
+      total += c;
+      if (i < n) place += c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      place += __shfl_xor_sync(0xffffffffu, place, o);
+    }
+  }
+  grid_wait();
   if (of == 0 || row >= s.m * a.G) return;
-  const int64_t per = stretch_of(a.place[a.N], teams);
-  const int64_t from = a.place[n] + (int64_t)h * of, first = from / per, last = (from + of - 1) / per;
+  if (a.N > 32) {
+    total = a.place[a.N];
+    place = a.place[n];
+  }
+  const int64_t per = stretch_of(total, teams);
+  const int64_t from = place + (int64_t)h * of, first = from / per, last = (from + of - 1) / per;
   const int pieces = (int)(last - first) + 1;
   if (pieces == 1) return;
   const int share = WIDE ? (pieces + 3) / 4 : pieces;
@@ -765,20 +833,12 @@ cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = gdn_host::allow_smem(kv8_decode_kernel<D, NT, MT>, Ly::BYTES, done);
   if (e != cudaSuccess) return e;
-  kv8_decode_kernel<D, NT, MT><<<Ly::TEAMS, 32 * MT, Ly::BYTES, s>>>(a, mk, mv);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
+  if ((e = gdn_host::launch_dependent(kv8_decode_kernel<D, NT, MT>, dim3(Ly::TEAMS), 32 * MT, Ly::BYTES, s, a, mk, mv)) != cudaSuccess)
+    return e;
   const bool wide = (int64_t)a.N * a.HK * 8 < Ly::TEAMS;  // eight pieces a pair, or more
-  cfg.gridDim = dim3(wide ? a.row_most : (a.row_most + 3) / 4, a.HK, a.N);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, true>, a, (int)Ly::TEAMS)
-              : cudaLaunchKernelEx(&cfg, kv8_join_kernel<D, false>, a, (int)Ly::TEAMS);
+  const dim3 grid(wide ? a.row_most : (a.row_most + 3) / 4, a.HK, a.N);
+  return wide ? gdn_host::launch_dependent(kv8_join_kernel<D, true>, grid, 128, 0, s, a, (int)Ly::TEAMS)
+              : gdn_host::launch_dependent(kv8_join_kernel<D, false>, grid, 128, 0, s, a, (int)Ly::TEAMS);
 }
 template <int D> cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
   if (a.row_cap == 8) return launch_decode<D, 1, 1>(a, s);

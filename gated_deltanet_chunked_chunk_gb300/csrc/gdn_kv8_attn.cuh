@@ -47,6 +47,7 @@ __device__ __forceinline__ bool request_span(const AttnArgs &a, int n, int row0,
   s.bits = 0;
   s.t0 = n;
   s.m = 1;
+  s.L = a.seq_lens[n];
   if (a.cu) {
     const int c0 = a.cu[n], c1 = a.cu[n + 1];
     if (c0 < 0 || c1 < c0 || c1 > a.T || (n == 0 && c0 != 0) || c1 - c0 > a.max_q) {
@@ -57,7 +58,6 @@ __device__ __forceinline__ bool request_span(const AttnArgs &a, int n, int row0,
     s.m = c1 - c0;
   }
   if (row0 >= s.m * a.G) return false;
-  s.L = a.seq_lens[n];
   if (s.L < 0 || s.L > a.max_seq) {
     s.bits = GDN_DEV_BAD_SEQ_LEN;
     return false;

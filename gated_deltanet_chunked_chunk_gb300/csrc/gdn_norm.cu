@@ -126,6 +126,8 @@ template <int L, int NV, int THREADS, int ACT, bool RES>
 __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
   using S = Shape<L, NV, THREADS>;
   __shared__ float sh[2][32];
+  grid_release();
+  grid_wait();
   int turn = 0;
   const int l = S::kBlock ? (int)threadIdx.x : (int)(threadIdx.x % L);
   const int nvec = a.D / 8;
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(THREADS, (NV == 1 && L <= 32) ? 4 : 1) norm_bw
   constexpr int kTensors = 2 + (ACT != ACT_NONE ? 1 : 0) + (RES ? 1 : 0);
   extern __shared__ uint4 ring[];  // [kAhead][kTensors][NV][THREADS], then the blocks' sums
   __shared__ float sh[2][32];
+  grid_wait();
   int turn = 0;
   const int l = S::kBlock ? (int)threadIdx.x : (int)(threadIdx.x % L);
   const int nvec = a.D / 8;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, (NV == 1 && L <= 32) ? 4 : 1) norm_bw
     }
   }
   // the kernel that adds the partial rows may come in; it waits for this grid
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   float *part = a.part + (int64_t)blockIdx.x * a.D;
   if (S::kBlock) {
 #pragma unroll
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__
   __shared__ float sh[32][33];
   const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + c;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   float v = 0.f;
   if (e < D) {
 #pragma unroll 8
@@ -439,16 +442,14 @@ cudaError_t launch_bwd(const NormArgs &a, int blocks, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = gdn_host::allow_smem(norm_bwd_kernel<L, NV, THREADS, ACT, RES>, bytes, done);
   if (e != cudaSuccess) return e;
-  norm_bwd_kernel<L, NV, THREADS, ACT, RES><<<blocks, THREADS, bytes, s>>>(a);
-  return cudaGetLastError();
+  return gdn_host::launch_dependent(norm_bwd_kernel<L, NV, THREADS, ACT, RES>, dim3(blocks), THREADS, bytes, s, a);
 }
 template <bool BWD, int L, int NV, int THREADS, int ACT>
 cudaError_t launch_one(const NormArgs &a, int blocks, cudaStream_t s) {
   const bool res = BWD ? a.dh != nullptr : a.res != nullptr;
   if (BWD) return res ? launch_bwd<L, NV, THREADS, ACT, true>(a, blocks, s) : launch_bwd<L, NV, THREADS, ACT, false>(a, blocks, s);
-  if (res) norm_fwd_kernel<L, NV, THREADS, ACT, true><<<blocks, THREADS, 0, s>>>(a);
-  else norm_fwd_kernel<L, NV, THREADS, ACT, false><<<blocks, THREADS, 0, s>>>(a);
-  return cudaGetLastError();
+  return res ? gdn_host::launch_dependent(norm_fwd_kernel<L, NV, THREADS, ACT, true>, dim3(blocks), THREADS, 0, s, a)
+             : gdn_host::launch_dependent(norm_fwd_kernel<L, NV, THREADS, ACT, false>, dim3(blocks), THREADS, 0, s, a);
 }
 template <bool BWD, int L, int NV, int THREADS>
 cudaError_t launch_act(const NormArgs &a, int act, int blocks, cudaStream_t s) {
@@ -527,16 +528,7 @@ cudaError_t launch_norm_bwd(const uint16_t *dy, const uint16_t *h, const uint16_
     const cudaError_t e = dispatch<true>(a, act, p, blocks, s);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((D + 31) / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_dw_kernel, static_cast<const float *>(a.part), blocks, D, dw);
+  return launch_dependent(norm_dw_kernel, dim3((D + 31) / 32), 1024, 0, s, static_cast<const float *>(a.part), blocks, D, dw);
 }
 
 }  // namespace gdn_host

@@ -26,11 +26,17 @@ constexpr int kPlan = 1024;
 
 __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
     const int32_t *__restrict__ cached, const int32_t *__restrict__ cu, int N, int32_t T, int32_t *table, int width,
-    const int32_t *__restrict__ free_pages, int F, const int32_t *__restrict__ num_free, int bs, int32_t *seq_lens,
-    int32_t *slots, int32_t *positions, int32_t *num_free_out, int32_t *dev_status) {
+    const int32_t *__restrict__ free_pages, int F, const int32_t *__restrict__ num_free, int bs, int page_bits,
+    int32_t *seq_lens, int32_t *slots, int32_t *positions, int32_t *num_free_out, int32_t *dev_status) {
   __shared__ int32_t s_start[kPlan], s_cached[kPlan], s_before[kPlan], s_end[kPlan];
   __shared__ int32_t s_warp[32];
+  gdn::grid_release();
+  gdn::grid_wait();
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  auto pages_of = [&](uint32_t tokens) {  // below 2^31 tokens
+    const uint32_t x = tokens + (uint32_t)bs - 1;
+    return page_bits >= 0 ? x >> page_bits : x / (uint32_t)bs;
+  };
   const int32_t tok = (int32_t)min((int64_t)blockIdx.x * kPlan + tid, (int64_t)T);
   int left = *num_free;
   left = left < 0 ? 0 : left > F ? F : left;
@@ -48,13 +54,14 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
         a = b = 0;
         c = c < 0 ? 0 : c;
       }
-      const int64_t total = (int64_t)c + b - a;
-      int64_t have = ((int64_t)c + bs - 1) / bs, need = (total + bs - 1) / bs;
-      if (need > width) {
+      const uint32_t total = (uint32_t)c + (uint32_t)(b - a);  // below 2^31, as checked
+      const uint32_t have = pages_of(c);
+      uint32_t need = pages_of(total);
+      if (need > (uint32_t)width) {
         bits |= GDN_DEV_NO_PAGE;
-        need = width;
+        need = (uint32_t)width;
       }
-      want = (int32_t)(need > have ? need - have : 0);
+      want = need > have ? (int32_t)(need - have) : 0;
       if (blockIdx.x == 0) seq_lens[n] = (int32_t)total;
     }
     // inclusive scan of want over the block
@@ -69,12 +76,14 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
     s_end[tid] = b;
     s_cached[tid] = c;
     __syncthreads();
-    int32_t add = 0, all = 0;
-    for (int i = 0; i < 32; ++i) {
-      const int32_t v = s_warp[i];
-      if (i < w) add += v;
-      all += v;
+    int32_t sums = s_warp[lane];  // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, sums, o);
+      if (lane >= o) sums += y;
     }
+    const int32_t all = __shfl_sync(0xffffffffu, sums, 31);
+    const int32_t add = w == 0 ? 0 : __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
     s_before[tid] = base + add + x - want;
     __syncthreads();
     if (tok < T && tok >= s_start[0] && slot < 0) {
@@ -86,8 +95,8 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
       }
       if (s_start[lo] <= tok && tok < s_end[lo]) {
         pos = s_cached[lo] + (tok - s_start[lo]);
-        const int pg = pos / bs, off = pos - pg * bs;
-        const int have = (int)(((int64_t)s_cached[lo] + bs - 1) / bs);
+        const int pg = (int)(page_bits >= 0 ? (uint32_t)pos >> page_bits : (uint32_t)pos / (uint32_t)bs), off = pos - pg * bs;
+        const int have = (int)pages_of(s_cached[lo]);
         int32_t page = -1;
         if (pg < width) {
           int32_t *entry = table + (int64_t)(n0 + lo) * width + pg;
@@ -290,6 +299,8 @@ __device__ __forceinline__ void write_run(const AppendArgs &a, int kv, int h, in
 template <int WARPS, int NV, bool VEC>
 __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) kv8_append_kernel(const AppendArgs a) {
   __shared__ float sh[WARPS];
+  gdn::grid_release();
+  gdn::grid_wait();
   const int64_t unit = WARPS == 1 ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const int lane = threadIdx.x & 31;
   const int64_t t0 = unit * a.window, t1 = min(t0 + a.window, a.T);
@@ -330,8 +341,16 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) kv8_append_kern
   if (bits && (WARPS == 1 || threadIdx.x < 32)) set_status(a.dev_status, bits);
 }
 
-template <int NV> void launch_windows(const AppendArgs &a, int64_t units, cudaStream_t s) {
-  kv8_append_kernel<4, NV, true><<<dim3((unsigned)units, 2 * a.HK), 128, 0, s>>>(a);
+template <int WARPS, int NV, bool VEC> cudaError_t launch_append(const AppendArgs &a, int64_t blocks, cudaStream_t s) {
+  return gdn_host::launch_dependent(kv8_append_kernel<WARPS, NV, VEC>, dim3((unsigned)blocks, 2 * a.HK), WARPS == 1 ? 256 : 32 * WARPS, 0,
+                                    s, a);
+}
+
+// log2(x) where x is a power of two, else -1.
+int bits_of(int x) {
+  for (int i = 0; i < 31; ++i)
+    if (x == 1 << i) return i;
+  return -1;
 }
 
 }  // namespace
@@ -343,18 +362,15 @@ cudaError_t launch_paged_plan(const int32_t *cached, const int32_t *cu, int N, i
                               int32_t *slots, int32_t *positions, int32_t *num_free_out, int32_t *dev_status,
                               cudaStream_t s) {
   const int blocks = T > 0 ? (T + kPlan - 1) / kPlan : 1;
-  paged_plan_kernel<<<blocks, kPlan, 0, s>>>(cached, cu, N, T, table, width, free_pages, F, num_free, bs, seq_lens, slots,
-                                             positions, num_free_out, dev_status);
-  return cudaGetLastError();
+  return launch_dependent(paged_plan_kernel, dim3(blocks), kPlan, 0, s, cached, cu, N, T, table, width, free_pages, F, num_free, bs,
+                          bits_of(bs), seq_lens, slots, positions, num_free_out, dev_status);
 }
 
 cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ldv, uint8_t *kc, uint8_t *vc,
                               float *ks, float *vs, const int32_t *slots, int64_t T, int P, int HK, int D, int bs,
                               int32_t *dev_status, cudaStream_t s) {
   const int sms = sm_count();
-  AppendArgs a{k, v, ldk, ldv, kc, vc, ks, vs, slots, T, P, HK, D, bs, 1, -1, dev_status};
-  for (int i = 0; i < 31; ++i)
-    if (bs == 1 << i) a.page_bits = i;
+  AppendArgs a{k, v, ldk, ldv, kc, vc, ks, vs, slots, T, P, HK, D, bs, 1, bits_of(bs), dev_status};
   const uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | reinterpret_cast<uintptr_t>(kc) |
                          reinterpret_cast<uintptr_t>(vc);
   // 16-byte accesses, and threads that keep their column from row to row
@@ -366,17 +382,11 @@ cudaError_t launch_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk,
   if (wide) a.window = bs;
   const int64_t units = (T + a.window - 1) / a.window, blocks = wide ? units : (units + 7) / 8;
   if (blocks > 2147483647LL) return cudaErrorInvalidValue;
-  if (wide) {
-    if (held <= 1) launch_windows<1>(a, units, s);
-    else if (held <= 2) launch_windows<2>(a, units, s);
-    else if (held <= 4) launch_windows<4>(a, units, s);
-    else launch_windows<8>(a, units, s);
-  } else if (vec) {
-    kv8_append_kernel<1, 0, true><<<dim3((unsigned)blocks, 2 * HK), 256, 0, s>>>(a);
-  } else {
-    kv8_append_kernel<1, 0, false><<<dim3((unsigned)blocks, 2 * HK), 256, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  if (!wide) return vec ? launch_append<1, 0, true>(a, blocks, s) : launch_append<1, 0, false>(a, blocks, s);
+  if (held <= 1) return launch_append<4, 1, true>(a, blocks, s);
+  if (held <= 2) return launch_append<4, 2, true>(a, blocks, s);
+  if (held <= 4) return launch_append<4, 4, true>(a, blocks, s);
+  return launch_append<4, 8, true>(a, blocks, s);
 }
 
 }  // namespace gdn_host

@@ -79,6 +79,8 @@ __device__ __forceinline__ uint4 pack8(const float *f) {
 // layout, a vector each when interleaved), then the vectors that pass.
 template <bool INTER>
 __global__ void __launch_bounds__(256, 8) rope_vec_kernel(const RopeArgs a, int places, int rows_at_once) {
+  gdn::grid_release();
+  gdn::grid_wait();
   extern __shared__ float2 cs[];
   const int64_t t0 = (int64_t)blockIdx.x * a.tile;
   const int n = (int)(a.T - t0 < a.tile ? a.T - t0 : a.tile);
@@ -208,11 +210,10 @@ cudaError_t launch_rope(const uint16_t *q, const uint16_t *k, const int32_t *pos
   const bool vec = !(bits & 15) && D % 8 == 0 && rot % (interleaved ? 8 : 16) == 0 && ldq % 8 == 0 && ldk % 8 == 0;
   const int places = vec ? (interleaved ? D / 8 : D / 8 - rot / 16) : 0;
   if (vec && places <= 256) {
-    if (interleaved) rope_vec_kernel<true><<<grid, 256, smem, s>>>(a, places, 256 / places);
-    else rope_vec_kernel<false><<<grid, 256, smem, s>>>(a, places, 256 / places);
-  } else {
-    rope_any_kernel<<<grid, 256, smem, s>>>(a);
+    return interleaved ? launch_dependent(rope_vec_kernel<true>, dim3(grid), 256, smem, s, a, places, 256 / places)
+                       : launch_dependent(rope_vec_kernel<false>, dim3(grid), 256, smem, s, a, places, 256 / places);
   }
+  rope_any_kernel<<<grid, 256, smem, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -125,7 +126,7 @@ const uint16_t *bf(const Tensor &t) { return ptr<const uint16_t>(t); }
 uint16_t *bf_out(const Tensor &t) { return ptr<uint16_t>(t); }
 void *stream_of(const at::Device &d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
 Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, const at::Device &dev) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+  return Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
 }
 
 struct Status {
