@@ -851,9 +851,18 @@ template <int D> cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
 
 namespace gdn_host {
 
+namespace {
+// Bytes of the decode kernel's part of the workspace, a multiple of 16.
+size_t decode_workspace(int N, int D) {
+  const size_t bytes = (size_t)kPartRows * (size_t)(D + 2) * sizeof(float) + ((size_t)N + 1) * sizeof(int64_t);
+  return (bytes + 15) / 16 * 16;
+}
+}  // namespace
+
 size_t kv8_attn_workspace_bytes(int N, int G, int D, int max_q) {
-  if (N <= 0 || max_q <= 0 || plan_decode(N, G, max_q).row_most == 0) return 0;
-  return (size_t)kPartRows * (size_t)(D + 2) * sizeof(float) + ((size_t)N + 1) * sizeof(int64_t);
+  if (N <= 0 || max_q <= 0) return 0;
+  const int most = plan_decode(N, G, max_q).row_most;
+  return (most > 0 ? decode_workspace(N, D) : 0) + ((int64_t)max_q * G > most ? gdnkv::prefill_workspace(D) : 0);
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs &c, cudaStream_t s) {
@@ -864,11 +873,16 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs &c, cudaStream_t s) {
   a.scale_log2e = c.scale * gdnc::kLog2e;
   a.row_cap = p.row_cap;
   a.row_most = p.row_most;
-  a.part_o = static_cast<float *>(c.ws);
-  a.part_ml = reinterpret_cast<float2 *>(a.part_o + kPartRows * c.D);
-  a.place = reinterpret_cast<int64_t *>(a.part_ml + kPartRows);
+  unsigned char *ws = static_cast<unsigned char *>(c.ws);
+  if (p.row_most > 0) {
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + kPartRows * c.D);
+    a.place = reinterpret_cast<int64_t *>(a.part_ml + kPartRows);
+    ws += decode_workspace(c.N, c.D);
+  }
   if ((int64_t)c.max_q * a.G > p.row_most) {
-    const cudaError_t e = launch_prefill(a, p.row_most + 1, s);
+    gdnkv::prefill_place(a, ws);
+    const cudaError_t e = gdnkv::launch_prefill(a, p.row_most + 1, s);
     if (e != cudaSuccess || p.row_most == 0) return e;
   }
   return c.D == 128 ? launch_rows<128>(a, s) : launch_rows<64>(a, s);

@@ -32,6 +32,9 @@ struct AttnArgs : gdn_host::Kv8AttnArgs {
   float *part_o;    // [team][2][row_cap][D] partial results
   float2 *part_ml;  // [team][2][row_cap]: maximum, sum
   int64_t *place;   // [N + 1] where a request's stages begin on the line of all
+  float *tile_o;    // the prefill kernel's partial results: [slot][256][D]
+  float2 *tile_ml;  // [slot][256]: maximum, sum
+  int4 *owners;     // [slot] request, head, tile and pieces of the item that begins there
 };
 
 // What one tile of rows [row0, row0 + count) of a request works on; rows are
@@ -107,5 +110,8 @@ inline bool cache_map(CUtensorMap *mp, const void *ptr, int D, int bs, int64_t p
 
 // Attention of the requests that have at least min_rows rows (gdn_kv8_prefill.cu).
 cudaError_t launch_prefill(const AttnArgs &a, int min_rows, cudaStream_t s);
+// Bytes of workspace that it needs, and their place.
+size_t prefill_workspace(int D);
+void prefill_place(AttnArgs &a, void *ws);
 
 }  // namespace gdnkv

@@ -25,6 +25,22 @@
 // columns; products of one thread execute in order, so "S is there" also says
 // that O may be touched.  O is rescaled only when the running maximum grew by
 // more than 8 (p' <= 256 is safe in f16), by the softmax warps themselves.
+//
+// The last items, where they do not come out even with the SMs, are cut along
+// their keys (find_job).  4096 tokens over 16384 keys, 32 heads of 128, 4 kv
+// heads: 512 items on 152 SMs, 747 us (1.29 PFLOP/s, 68 % of a 16-bit library
+// product) against 838 with the last 56 items whole; 512 tokens over 16384: 145 us,
+// two pieces an item.  A key tile takes 3600 cycles, of which the tensor cores
+// work 2176: a softmax thread's chain from "S is there" to "P is there" (load,
+// maximum, exponentials, store: 2000) is longer than the other tile's products
+// that hide it.  Two threads a row (1200 us: with 64 logits each their registers
+// spill), blocks that stay and take a stretch of all items' key tiles (822 us:
+// what that adds to the loop costs more than the even end gains) and reading the
+// logits twice (1490 us) were slower.
+#include <limits.h>
+
+#include <algorithm>
+
 #include "gdn_kv8_attn.cuh"
 
 namespace {
@@ -34,6 +50,9 @@ using namespace gdnkv;
 
 constexpr int kTileKeys = 128;
 constexpr int kPrefThreads = 512;
+constexpr int kItemRows = 256;
+constexpr int kSlots = 152;     // partial results, one for each SM
+constexpr int kPieceTiles = 8;  // key tiles that a piece of an item has at least
 constexpr int kParSlots = 8;  // key tiles whose page constants are kept: more than can be in flight
 
 template <int D>
@@ -49,7 +68,7 @@ struct PrefLay {
   static constexpr int OFF_BAR = OFF_PAR + kParSlots * 128;
   static constexpr int BARS = 2 * NK + 2 * NV + 2 * NW + 10 + kParSlots;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
-  static constexpr int BYTES = OFF_MISC + 32;
+  static constexpr int BYTES = OFF_MISC + 32 + 17 * 8 + 48;
   static_assert(BYTES <= 227 * 1024, "one block an SM");
 };
 
@@ -88,6 +107,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
       "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
       "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  tmem_ld_wait8(r);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Ties 32 registers to the wait before it.
@@ -149,24 +179,121 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+// An item is 256 rows of one (request, kv head).  Those of a call stand in one
+// order: requests, in each the last rows (which see the most keys) first, heads.
+// Where the items do not come out even with the SMs, the last ones are cut along
+// their keys, each into as many pieces as leave no SM without one; a small
+// kernel joins the pieces.
+struct Job {
+  int n, h, tile;     // tile: of 256 rows
+  int piece, pieces;  // pieces 0: nothing to do
+  int slot;           // where a piece's result goes
+};
+__device__ __forceinline__ int item_tiles(const AttnArgs &a, int n, int min_rows, bool report) {
+  Span s;
+  const bool some = n < a.N && request_span(a, n, 0, 1, s);
+  if (n < a.N && report && s.bits) set_status(a.dev_status, s.bits);
+  return some && s.m * a.G >= min_rows ? (s.m * a.G + kItemRows - 1) / kItemRows : 0;
+}
+// This block's job, found by all its threads.  sums: 17 numbers of shared memory.
+__device__ __forceinline__ Job find_job(const AttnArgs &a, int min_rows, int sms, int64_t *sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (a.N + kPrefThreads - 1) / kPrefThreads, n0 = tid * each;
+  const bool report = blockIdx.x == 0;
+  int64_t mine = 0;
+  for (int i = 0; i < each; ++i) mine += (int64_t)a.HK * item_tiles(a, n0 + i, min_rows, report);
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sums[warp] = upto;
+  int *found = reinterpret_cast<int *>(sums + kPrefThreads / 32);  // the request, its items before this one
+  if (tid == 0) *found = -1;
+  __syncthreads();
+  int64_t total = 0, before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < kPrefThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  // (more than the host's bound only where cu_seqlens is no such array)
+  const int all = (int)min(total, (int64_t)gridDim.x - kSlots);
+  const int whole = all / sms * sms, rest = all - whole;
+  // Pieces of each of the last items, one an SM.  (Two turns of smaller pieces,
+  // 56 items in 5 pieces each, end no earlier: 780 us against 767.)
+  const int cut = rest > 0 ? min(sms, kSlots) / rest : 1;
+  const int b = blockIdx.x;
+  Job job{};
+  job.slot = b - whole;
+  int item = b;
+  job.pieces = 1;
+  if (b >= whole && cut > 1) {
+    item = whole + job.slot / cut;
+    job.piece = job.slot % cut;
+    job.pieces = cut;
+  }
+  if (item < all && item >= before && item < before + mine) {
+    int n = n0, at = (int)(item - before);
+    for (int t; at >= (t = a.HK * item_tiles(a, n, min_rows, false)); ++n) at -= t;
+    found[0] = n;
+    found[1] = at;
+  }
+  __syncthreads();
+  job.n = found[0];
+  if (job.n < 0) {
+    job.pieces = 0;
+    return job;
+  }
+  const int at = found[1];
+  job.h = at % a.HK;
+  job.tile = item_tiles(a, job.n, min_rows, false) - 1 - at / a.HK;
+  return job;
+}
+
+// What the block works on.  It stands in shared memory, and each kind of warp
+// takes what it needs: the loops need the registers.
+struct Work {
+  int n, h, row0, rows;  // rows: the request's
+  int t0, past, keys;    // past: L - m, what stands before the request's first token
+  int base, tiles;       // key tiles: the `tiles` from base on
+  int pieces, slot;
+};
+
 template <int D>
 __global__ void __launch_bounds__(kPrefThreads, 1)
-    kv8_prefill_kernel(const AttnArgs a, int min_rows, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    kv8_prefill_kernel(const AttnArgs a, int min_rows, int sms, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using Ly = PrefLay<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the last tokens' blocks, which see the most keys, start first
-  const int n = blockIdx.z, h = blockIdx.y, row0 = (int)(gridDim.x - 1 - blockIdx.x) * 256;
-  Span s;
-  if (!request_span(a, n, row0, 256, s)) {
-    if (tid == 0 && s.bits) set_status(a.dev_status, s.bits);
-    return;
+  grid_wait();
+  Job job = find_job(a, min_rows, sms, reinterpret_cast<int64_t *>(smem + Ly::OFF_MISC + 32));
+  volatile Work *work = reinterpret_cast<volatile Work *>(smem + Ly::OFF_MISC + 32 + 17 * 8);
+  {
+    const int row0 = job.tile * kItemRows;
+    Span s{};
+    if (job.pieces > 0) request_span(a, job.n, row0, kItemRows, s);  // true: find_job has found it so
+    const int all = (s.keys + kTileKeys - 1) / kTileKeys;
+    job.pieces = min(job.pieces, max(1, all / kPieceTiles));
+    if (tid == 0 && job.slot >= 0 && job.slot < kSlots)
+      a.owners[job.slot] = make_int4(job.n, job.h, job.tile, job.piece == 0 && job.pieces > 1 ? job.pieces : 0);
+    if (job.piece >= job.pieces) return;
+    if (tid == 0) {
+      work->n = job.n;
+      work->h = job.h;
+      work->row0 = row0;
+      work->rows = s.m * a.G;
+      work->t0 = s.t0;
+      work->past = s.L - s.m;
+      work->keys = s.keys;
+      work->base = (int)((int64_t)all * job.piece / job.pieces);
+      work->tiles = (int)((int64_t)all * (job.piece + 1) / job.pieces) - work->base;
+      work->pieces = job.pieces;
+      work->slot = job.slot;
+    }
   }
-  const int rows = s.m * a.G, L = s.L;
-  if (rows < min_rows) return;  // the other kernel's
-  const int tiles = (s.keys + kTileKeys - 1) / kTileKeys;
-  const int low = L - s.m + row0 / a.G;  // what the first row sees last
   const int page_bits = 31 - __clz(a.bs);
 
   const uint32_t bar = sb + Ly::OFF_BAR;
@@ -207,22 +334,25 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
 
   // Of the block's 65536 registers (512 threads x 128) the softmax warps take
   // 192 a thread, the other warps 64: 2 x 128 x 192 + 2 x 128 x 64 = 65536.
+  // (184 and 72: 767 us against 747, though ptxas then spills less.)
+  const int tiles = work->tiles;
   float m_ref = -INFINITY, l_sum = 0.f;
   int issued_k = 0, issued_v = 0;  // key tiles that the producer has issued
   const int wg = warp >> 2;
-  const int row = row0 + (wg & 1) * 128 + (tid & 127);
-  const bool on = wg < 2 && row < rows;
-  const int limit = on ? L - s.m + row / a.G : -1;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
   const uint32_t S_col = tmem + lanes + (wg & 1) * 128, O_col = tmem + lanes + 256 + (wg & 1) * D;
 
   if (wg < 2) {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int row = work->row0 + wg * 128 + (tid & 127), base = work->base;
+    const bool on = row < work->rows;
+    const int low = work->past + work->row0 / a.G;  // what the first row sees last
+    const int limit = on ? work->past + row / a.G : -1;
     float krow;
     {
       // the row's query: largest magnitude, then high and low parts
-      const uint16_t *src = a.q + (int64_t)(s.t0 + row / a.G) * a.ldq + (int64_t)(h * a.G + row % a.G) * D;
+      const uint16_t *src = a.q + (int64_t)(work->t0 + row / a.G) * a.ldq + (int64_t)(work->h * a.G + row % a.G) * D;
       uint4 u[D / 8];
       float top = 0.f, bad = 0.f;
 #pragma unroll
@@ -281,7 +411,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       for (int i = 1; i < 4; ++i) tie32(r + 32 * i);
 
       const uint32_t par = sb + Ly::OFF_PAR + (j % kParSlots) * 128;
-      const int k0 = j * kTileKeys;
+      const int k0 = (base + j) * kTileKeys;
       const bool masked = k0 + kTileKeys - 1 > low;
       float c[8], b[8], iv[8], top = -INFINITY;  // constants of 16 keys each
 #pragma unroll
@@ -324,20 +454,19 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
       }
       if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
-          tmem_ld32_issue(O_col + i, o);
-          tmem_ld_wait(o);
+        for (int i = 0; i < D; i += 8) {  // few at a time: the logits hold 128 registers
+          uint32_t o[8];
+          tmem_ld8(O_col + i, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * grow);
-          tmem_st32(O_col + i, o);
+          for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * grow);
+          tmem_st8(O_col + i, o);
         }
       }
-      const float base = m_ref == -INFINITY ? 0.f : m_ref;
+      const float ref = m_ref == -INFINITY ? 0.f : m_ref;
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         float2 sum = make_float2(0.f, 0.f);
-        const float bb = b[g] - base;
+        const float bb = b[g] - ref;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float2 t = fma2(make_float2(__uint_as_float(r[16 * g + 2 * i]), __uint_as_float(r[16 * g + 2 * i + 1])), c[g], bb);
@@ -359,14 +488,15 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (wg == 2) {
       // ------------------------------------------------------------ widen V
-      const int ct = tid - 256;
+      const int ct = tid - 256, base = work->base, past = work->past, low = past + work->row0 / a.G;
+      const int L = past + work->rows / a.G;
       for (int j = 0; j < tiles; ++j) {
         const int iv = j % Ly::NV, iw = j % Ly::NW;
         bool ok = wait_bar(VF(iv), (j / Ly::NV) & 1, failed, a.dev_status);
         if (ok && j >= Ly::NW) ok = wait_bar(WE(iw), (j / Ly::NW - 1) & 1, failed, a.dev_status);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t src = sb + Ly::OFF_V + iv * Ly::T8, dst = sb + Ly::OFF_W + iw * Ly::T16;
-        const int k0 = j * kTileKeys;
+        const int k0 = (base + j) * kTileKeys;
         const bool zone = k0 + kTileKeys - 1 > low;
         uint32_t seen = 0;
 #pragma unroll
@@ -401,10 +531,11 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
     } else if (warp == 12) {
       // ----------------------------------------------------------- producer
       const int ppt = a.bs >= kTileKeys ? 1 : kTileKeys / a.bs, box = kTileKeys / ppt;
+      const int n = work->n, h = work->h, keys = work->keys, base = work->base;
       int batch = -1, page = -1;
       float ks = 0.f, lv = 0.f, iv = 1.f;
       for (int j = 0; j < tiles; ++j) {
-        const int first = j * ppt;
+        const int first = (base + j) * ppt;
         if (first / 32 != batch) {
           batch = first / 32;
           const int pi = batch * 32 + lane;
@@ -412,7 +543,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
           ks = 0.f;
           lv = -INFINITY;
           iv = 1.f;
-          if ((int64_t)pi * a.bs < s.keys) {
+          if ((int64_t)pi * a.bs < keys) {
             const int32_t p = a.table[(int64_t)n * a.width + pi];
             if (p < 0 || p >= a.P) {
               set_status(a.dev_status, GDN_DEV_BAD_SLOT);
@@ -522,8 +653,12 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   if (wg < 2) {
     // ---------------------------------------------------------------- output
     tc_fence_after();
-    const int tok = s.t0 + row / a.G, head = h * a.G + row % a.G;
-    const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+    const int n = work->n, h = work->h, row = work->row0 + wg * 128 + (tid & 127);
+    const bool on = row < work->rows, part = work->pieces > 1;
+    const int low = work->past + work->row0 / a.G, limit = work->past + row / a.G;
+    const int tok = work->t0 + row / a.G, head = h * a.G + row % a.G;
+    const float inv = part ? 1.f : l_sum == 0.f ? 0.f : 1.f / l_sum;
+    const int64_t at = (int64_t)work->slot * kItemRows + (row - work->row0);
     uint16_t *dst = a.o + ((int64_t)tok * a.HQ + head) * D;
     const bool zone = *nan_zone != 0;
 #pragma unroll 1
@@ -545,7 +680,11 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
             if ((v[e] & 0x7f) == 0x7f) o[e] = 0x7fc00000u;
         }
       }
-      if (on) {
+      if (on && part) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<uint4 *>(a.tile_o + at * D + i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else if (on) {
 #pragma unroll
         for (int e = 0; e < 32; e += 8)
           *reinterpret_cast<uint4 *>(dst + i + e) =
@@ -553,11 +692,54 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
                          pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
       }
     }
-    if (on && a.lse) a.lse[(int64_t)tok * a.HQ + head] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
+    if (on && part) a.tile_ml[at] = make_float2(m_ref, l_sum);
+    else if (on && a.lse) a.lse[(int64_t)tok * a.HQ + head] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 13) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of the items that were cut: a warp a row, a lane four columns.
+template <int D>
+__global__ void __launch_bounds__(256) kv8_join_items_kernel(const AttnArgs a) {
+  constexpr int LANES = D / 4;
+  grid_wait();
+  const int4 w = a.owners[blockIdx.x];
+  if (w.w == 0) return;
+  Span s;
+  const int row0 = w.z * kItemRows;
+  if (!request_span(a, w.x, row0, kItemRows, s)) return;
+  const int lane = threadIdx.x & 31, c = lane % LANES, rows = min(kItemRows, s.m * a.G - row0);
+  for (int r = 8 * blockIdx.y + (threadIdx.x >> 5); r < rows; r += 8 * gridDim.y) {
+    auto at = [&](int i) { return (int64_t)(blockIdx.x + i) * kItemRows + r; };
+    float top = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < w.w; b += 32) {
+      const int cnt = min(32, w.w - b);
+      const float2 ml = lane < cnt ? a.tile_ml[at(b + lane)] : make_float2(-INFINITY, 0.f);
+      float now = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+      now = fmaxf(now, top);
+      const float ref = now == -INFINITY ? 0.f : now;
+      const float wt = ex2f(ml.x - ref), old = ex2f(top - ref);
+      top = now;
+      l = fmaf(l, old, warp_sum(wt * ml.y));
+      acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+#pragma unroll 4
+      for (int i = 0; i < cnt; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(a.tile_o + at(b + i) * D + 4 * c);
+        const float wi = __shfl_sync(0xffffffffu, wt, i);
+        acc.x = fmaf(wi, v.x, acc.x);
+        acc.y = fmaf(wi, v.y, acc.y);
+        acc.z = fmaf(wi, v.z, acc.z);
+        acc.w = fmaf(wi, v.w, acc.w);
+      }
+    }
+    const int row = row0 + r;
+    if (lane < LANES) store_row4(a, s.t0 + row / a.G, w.y * a.G + row % a.G, D, 4 * c, acc, top, l);
+  }
 }
 
 template <int D>
@@ -570,9 +752,13 @@ cudaError_t launch(const AttnArgs &a, int min_rows, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = gdn_host::allow_smem(kv8_prefill_kernel<D>, Ly::BYTES, done);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.max_q * a.G;
-  kv8_prefill_kernel<D><<<dim3((unsigned)((rows + 255) / 256), a.HK, a.N), kPrefThreads, Ly::BYTES, s>>>(a, min_rows, mk, mv);
-  return cudaGetLastError();
+  // no more items than this, and a slot's block for each SM
+  const int64_t rows = (int64_t)a.T * a.G, most = a.HK * (rows / kItemRows + std::min<int64_t>(a.N, rows / min_rows));
+  if (most > INT_MAX - kSlots) return cudaErrorInvalidConfiguration;
+  e = gdn_host::launch_dependent(kv8_prefill_kernel<D>, dim3((unsigned)most + kSlots), kPrefThreads, Ly::BYTES, s, a, min_rows,
+                                 gdn_host::sm_count(), mk, mv);
+  if (e != cudaSuccess) return e;
+  return gdn_host::launch_dependent(kv8_join_items_kernel<D>, dim3(kSlots, 8), 256, 0, s, a);
 }
 
 }  // namespace
@@ -580,5 +766,13 @@ cudaError_t launch(const AttnArgs &a, int min_rows, cudaStream_t s) {
 namespace gdnkv {
 cudaError_t launch_prefill(const AttnArgs &a, int min_rows, cudaStream_t s) {
   return a.D == 128 ? launch<128>(a, min_rows, s) : launch<64>(a, min_rows, s);
+}
+size_t prefill_workspace(int D) {
+  return (size_t)kSlots * (kItemRows * (size_t)(D + 2) * sizeof(float) + sizeof(int4));
+}
+void prefill_place(AttnArgs &a, void *ws) {
+  a.tile_o = static_cast<float *>(ws);
+  a.tile_ml = reinterpret_cast<float2 *>(a.tile_o + (size_t)kSlots * kItemRows * a.D);
+  a.owners = reinterpret_cast<int4 *>(a.tile_ml + (size_t)kSlots * kItemRows);
 }
 }  // namespace gdnkv

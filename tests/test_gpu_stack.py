@@ -598,3 +598,53 @@ def test_attention_wait_that_runs_out():
     assert st == gdn.DEV_WAIT_TIMEOUT
     o2, lse2, st = _attn_run(c)
     assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("HK,G,D,bs,lens,news", [
+    (1, 8, 128, 64, [5000], [70]), (2, 4, 64, 16, [2300, 1, 2100], [65, 1, 129]), (4, 2, 128, 32, [3000, 40, 0, 2049], [33, 300, 5, 200]),
+    (1, 1, 128, 128, [4100], [300]), (2, 8, 128, 64, [6000, 2500, 90], [1, 40, 70])])
+def test_attention_of_many_tokens_over_long_contexts(HK, G, D, bs, lens, news):
+    """Contexts long enough, and rows few enough, for tiles of rows to be cut along their keys; short requests and
+    ones of a single token in the same call."""
+    c = _attn_case(HK, G, D, bs, lens, news, sum(lens) + D + 2)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+    o3, lse3, _ = _attn_run(c)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+def test_attention_nan_in_a_cut_tile():
+    """NaN values that only the last rows of a cut tile see, and a NaN key in the middle that all rows see."""
+    for where in ("value", "key"):
+        c = _attn_case(1, 8, 128, 64, [4000], [70], 5)
+        at = 3996 if where == "value" else 1000
+        c["vc" if where == "value" else "kc"].view(torch.uint8)[c["table"][0][at // 64], 0, at % 64, 5] = 0x7f
+        o, lse, st = _attn_run(c)
+        assert st == 0
+        if where == "value":
+            _attn_check(c, o, lse)
+            assert torch.isnan(o[-4:, :, 5]).all() and not torch.isnan(o[:-4]).any()
+        else:
+            assert torch.isnan(o).all()
+
+
+@pytest.mark.parametrize("N,hi,most", [(70, 900, 1), (600, 40, 1), (600, 60, 9), (40, 300, 33)])
+def test_attention_of_many_requests(N, hi, most):
+    """More requests than a warp, or a block, has threads; tokens from none to `most`."""
+    rng = np.random.RandomState(N + most)
+    news = [1] * N if most == 1 else [int(x) for x in rng.randint(0, most + 1, N)]
+    lens = [int(m + x) for m, x in zip(news, rng.randint(0, hi, N))]
+    c = _attn_case(1, 2 if most < 33 else 8, 64, 16, lens, news, N + hi)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+
+
+def test_attention_offsets_that_go_back_are_reported():
+    """cu_seqlens that count the same tokens again and again: a status, no access out of place."""
+    gdn = _gdn()
+    c = _attn_case(2, 8, 128, 64, [300] * 9, [20] * 9, 3)
+    c["cu"], c["max_q"] = [0, 180, 0, 180, 0, 180, 0, 180, 0, 180], 180
+    _, _, st = _attn_run(c)
+    assert st & gdn.DEV_BAD_CU_SEQLENS
