@@ -157,13 +157,14 @@ class _Rotary(torch.autograd.Function):
     def backward(ctx, dq, dk):
         positions, inv_freq = ctx.saved_tensors
         interleaved, factor = ctx.args
-        dq, dk = gdn_rope(dq.to(torch.bfloat16).contiguous(), dk.to(torch.bfloat16).contiguous(), positions, inv_freq, interleaved=interleaved,
+        dk = None if dk is None else dk.to(torch.bfloat16).contiguous()
+        dq, dk = gdn_rope(dq.to(torch.bfloat16).contiguous(), dk, positions, inv_freq, interleaved=interleaved,
                           attention_factor=factor, inverse=True)
         return dq, dk, None, None, None, None
 
 
 def rotary_embedding(q, k, positions, inv_freq, interleaved: bool = False, attention_factor: float = 1.0):
-    """Differentiable gdn_rope of q and k."""
+    """Differentiable gdn_rope of q and k (k may be None)."""
     return _Rotary.apply(q, k, positions, inv_freq, interleaved, attention_factor)
 
 

@@ -635,7 +635,9 @@ size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int
  *   o             : bf16 [T, HQ, D];  lse: fp32 [T, HQ] or NULL
  * D 64 or 128, page_size 16, 32, 64 or 128 (else GDN_EUNSUPPORTED, as for N >
  * 65535 or HK > 65535); HQ % HK == 0.  q, the caches, o and the workspace must
- * start on a 16-byte boundary and ldq be a multiple of 8 (else GDN_EINVAL).
+ * start on a 16-byte boundary and ldq be a multiple of 8 (else GDN_EINVAL);
+ * GDN_EWORKSPACE for a small workspace.  Two launches where requests have up to
+ * 64 rows (tokens x HQ / HK) or one request has more, four where a call may mix both.
  */
 int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, const uint8_t *v_cache,
                       const float *k_scale, const float *v_scale, const int32_t *block_table, int width,

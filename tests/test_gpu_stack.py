@@ -648,3 +648,58 @@ def test_attention_offsets_that_go_back_are_reported():
     c["cu"], c["max_q"] = [0, 180, 0, 180, 0, 180, 0, 180, 0, 180], 180
     _, _, st = _attn_run(c)
     assert st & gdn.DEV_BAD_CU_SEQLENS
+
+
+def test_rotary_embedding_of_queries_alone():
+    gdn = _gdn()
+    inv, _ = gdn.rope_frequencies(32, device="cuda")
+    q = torch.randn(5, 2, 64, generator=_gen(4)).to(BF).cuda().requires_grad_(True)
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    out, none = gdn.rotary_embedding(q, None, pos, inv)
+    assert none is None
+    dy = torch.randn(5, 2, 64, generator=_gen(5)).to(BF).cuda()
+    (dq,) = torch.autograd.grad(out, q, dy)
+    assert torch.equal(dq, gdn.gdn_rope(dy, None, pos, inv, inverse=True)[0])
+
+
+def test_refusals_of_types_shapes_and_layouts():
+    """Checks of the Python entries on device tensors; nothing is launched."""
+    gdn = _gdn()
+    x, w = torch.zeros(3, 2, 64, dtype=BF, device="cuda"), torch.ones(64, device="cuda")
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    f8 = lambda *s: torch.zeros(*s, dtype=torch.float8_e4m3fn, device="cuda")
+    one = torch.ones(4, 2, device="cuda")
+    cache = (f8(4, 2, 16, 64), f8(4, 2, 16, 64), one, one)
+    table, lens, fr = i(0, 1, 2).view(3, 1), i(1, 1, 1), torch.ones(32, device="cuda")
+    wrong = [
+        (TypeError, lambda: gdn.gdn_norm_gate(x.float(), w)),
+        (TypeError, lambda: gdn.gdn_norm_gate(x, w.to(BF))),
+        (ValueError, lambda: gdn.gdn_norm_gate(x, w[:63])),
+        (ValueError, lambda: gdn.gdn_norm_gate(x, w, z=x[:2])),
+        (ValueError, lambda: gdn.gdn_norm_gate(x, w, residual=x[:, :1])),
+        (ValueError, lambda: gdn.gdn_norm_gate(x.transpose(0, 1), w)),
+        (ValueError, lambda: gdn.gdn_norm_gate_bwd(x, x[:2], w)),
+        (TypeError, lambda: gdn.gdn_rope(x, x, torch.zeros(3, device="cuda"), fr)),
+        (ValueError, lambda: gdn.gdn_rope(x, x, i(0, 1), fr)),
+        (ValueError, lambda: gdn.gdn_rope(x, x[:2], i(0, 1, 2), fr)),
+        (gdn.GDNError, lambda: gdn.gdn_rope(x, x, i(0, 1, 2), torch.ones(33, device="cuda"))),
+        (TypeError, lambda: gdn.gdn_paged_plan(i(0).long(), i(0, 1), i(0).view(1, 1), i(0), i(1), 16, 1)),
+        (ValueError, lambda: gdn.gdn_paged_plan(i(0), i(0, 1, 2), i(0).view(1, 1), i(0), i(1), 16, 1)),
+        (TypeError, lambda: gdn.gdn_kv8_append(x, x, *cache, i(0, 1, 2).long())),
+        (TypeError, lambda: gdn.gdn_kv8_append(x, x, cache[0].view(torch.uint8), *cache[1:], i(0, 1, 2))),
+        (ValueError, lambda: gdn.gdn_kv8_append(x, x[:2], *cache, i(0, 1, 2))),
+        (ValueError, lambda: gdn.gdn_kv8_append(x, x, *cache[:3], one[:3], i(0, 1, 2))),
+        (TypeError, lambda: gdn.gdn_kv8_attention(x.half(), *cache, table, lens)),
+        (ValueError, lambda: gdn.gdn_kv8_attention(x, *cache, table[:2], lens)),
+        (ValueError, lambda: gdn.gdn_kv8_attention(x[..., :32], *cache, table, lens)),
+        (gdn.GDNError, lambda: gdn.gdn_kv8_attention(x, *cache, table, lens, max_seq_len=17)),
+        (gdn.GDNError, lambda: gdn.gdn_kv8_attention(x, *cache, table, lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))),
+    ]
+    for n, (error, call) in enumerate(wrong):
+        try:
+            call()
+        except error:
+            continue
+        except Exception as e:
+            raise AssertionError(f"refusal {n}: {type(e).__name__} {e} instead of {error.__name__}")
+        raise AssertionError(f"refusal {n}: accepted")
