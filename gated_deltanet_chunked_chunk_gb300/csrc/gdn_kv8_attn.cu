@@ -44,8 +44,10 @@
 // 6 3 7: then the 8 lanes that read shared memory together hit 8 different
 // 16-byte places.  P's 8 x 8 blocks are transposed by movmatrix; for V^T a byte
 // permutation pairs the two keys of a thread for each d.
-// mma.sync rather than tcgen05: a tile has 8 to 64 rows, not 128, and its
-// products take less time than its bytes do.
+// mma.sync rather than tcgen05: up to 16 rows the products take less time than
+// their bytes do.  17 to 32 rows, where they do not, are gdn_kv8_rows.cu's; 33 to
+// 64 (a range between that kernel and the prefill's, which is 13 % faster for
+// them over 131072 keys and 35 % slower over 4096) are two warps a team here.
 #include "gdn_kv8_attn.cuh"
 
 namespace {
@@ -54,8 +56,6 @@ using namespace gdn;
 using namespace gdnkv;
 
 constexpr int kKeys = 64;         // keys a stage
-constexpr int kSMs = 152;
-constexpr int kMinStages = 2;     // stages a team takes at least
 
 // D: head size; NT: tiles of 8 rows a warp; MT: warps a team.
 template <int D, int NT, int MT>
@@ -84,11 +84,6 @@ __device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 // The 8 x 8 block of f16 that the warp holds (row lane / 4, columns 2 (lane % 4),
 // + 1), transposed.
@@ -121,49 +116,11 @@ __device__ __forceinline__ float keys_add(float x) {
 template <int D> __device__ __forceinline__ uint32_t tile_at(uint32_t r, uint32_t c) {
   return D == 128 ? r * 128u + ((c ^ (r & 7u)) << 4) : r * 64u + ((c ^ ((r >> 1) & 3u)) << 4);
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
-}
-
-// Stages of request n, 0 where this kernel has nothing to do for it; s is its
-// span.  A request whose rows see no key has one stage, which writes its zeros.
-__device__ __forceinline__ int stages_of(const AttnArgs &a, int n, Span &s) {
-  if (!request_span(a, n, 0, a.row_cap, s) || s.m * a.G > a.row_most) return 0;
-  return max(1, (s.keys + kKeys - 1) / kKeys);
-}
-// Stages that a team takes.
-__device__ __forceinline__ int64_t stretch_of(int64_t total, int teams) {
-  const int64_t per = (total + teams - 1) / teams;
-  return per < kMinStages ? kMinStages : per;
-}
-
-// Where a walk along the line of stages stands.
-struct Place {
-  int n, h;       // request, kv head
-  int stage, of;  // stage of the pair, stages that it has
-  Span s;
-};
-__device__ __forceinline__ void next_request(const AttnArgs &a, Place &p) {
-  p.stage = 0;
-  p.h = 0;
-  do {
-    ++p.n;
-    p.of = p.n < a.N ? stages_of(a, p.n, p.s) : 1;
-  } while (p.of == 0);
-}
-
 template <int D, int NT, int MT>
 __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     kv8_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -191,91 +148,10 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
   // Only now: the joining kernel reads lengths and offsets before its own wait.
   grid_release();
 
-  // ------------------------------------------------- this team's stretch
-  // Up to 32 requests, a lane each; else lane l sums the stages of requests
-  // [l seg, (l + 1) seg) and the requests of the lane that holds the start are
-  // looked at again.  The last team also writes every request's place on the
-  // line for the joining kernel, which forms the places of few requests itself.
   Place at{};
-  int left;  // stages of this team still to do
-  if (a.N <= 32) {
-    Span s{};
-    const int of = lane < a.N ? stages_of(a, lane, s) : 0;
-    if (s.bits && team == 0 && warp == 0) set_status(a.dev_status, s.bits);
-    // below 2^31: 32 contexts of up to 2^25 stages would be 2^36 keys
-    const uint32_t mine = (uint32_t)of * (uint32_t)a.HK;
-    uint32_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
-    const uint32_t per = (uint32_t)stretch_of(total, Ly::TEAMS), start = per * (uint32_t)team;
-    if (start >= total) return;
-    left = (int)min(per, total - start);
-    const int n = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;
-    at.n = n;
-    at.of = __shfl_sync(0xffffffffu, of, n);
-    at.s.t0 = __shfl_sync(0xffffffffu, s.t0, n);
-    at.s.m = __shfl_sync(0xffffffffu, s.m, n);
-    at.s.L = __shfl_sync(0xffffffffu, s.L, n);
-    at.s.keys = __shfl_sync(0xffffffffu, s.keys, n);
-    const uint32_t in = start - (__shfl_sync(0xffffffffu, incl, n) - (uint32_t)at.of * (uint32_t)a.HK);
-    at.h = (int)(in / (uint32_t)at.of);
-    at.stage = (int)(in - (uint32_t)at.h * (uint32_t)at.of);
-  } else {
-    Span s;
-    const int seg = (a.N + 31) / 32;
-    int64_t mine = 0;
-    int bits = 0;
-    for (int n = lane * seg; n < min(a.N, (lane + 1) * seg); ++n) {
-      mine += (int64_t)stages_of(a, n, s) * a.HK;
-      bits |= s.bits;
-    }
-    if (bits && team == 0 && warp == 0) set_status(a.dev_status, bits);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
-    const int64_t per = stretch_of(total, Ly::TEAMS), start = per * team;
-    if (team == Ly::TEAMS - 1 && warp == 0) {
-      int64_t run = incl - mine;
-      for (int n = lane * seg; n < min(a.N, (lane + 1) * seg); ++n) {
-        a.place[n] = run;
-        run += (int64_t)stages_of(a, n, s) * a.HK;
-      }
-      if (lane == 0) a.place[a.N] = total;
-    }
-    if (start >= total) return;
-    left = (int)min(per, total - start);
-    const int owner = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;
-    int64_t run = __shfl_sync(0xffffffffu, incl - mine, owner);
-    for (int base = owner * seg;; base += 32) {
-      const int n = base + lane;
-      const int64_t c = n < a.N ? (int64_t)stages_of(a, n, s) * a.HK : 0;
-      int64_t sum = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, run + sum > start);
-      if (past) {
-        const int l = __ffs((int)past) - 1;
-        at.n = base + l;
-        const int64_t in = start - (run + __shfl_sync(0xffffffffu, sum - c, l));
-        at.of = stages_of(a, at.n, at.s);
-        at.h = (int)(in / at.of);
-        at.stage = (int)(in - (int64_t)at.h * at.of);
-        break;
-      }
-      run += __shfl_sync(0xffffffffu, sum, 31);
-    }
-  }
+  const int left_all = find_place(a, team, Ly::TEAMS, warp == 0, at);
+  if (left_all == 0) return;
+  int left = left_all;  // stages of this team still to do
 
   // -------------------------------------------------------------- calling
   // Warp 0 runs R stages ahead of the products: `ahead` is its place, `to_call`
@@ -802,8 +678,9 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int tea
 
 // ---------------------------------------------------------------- host side
 // How a call's requests are worked on, from its host bounds.  Requests of up to
-// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 8, 16,
-// 32 or 64 rows a team, the others to kv8_prefill_kernel.  A call whose bounds
+// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 8, 16 or
+// 64 rows a team, or, where 17 to 32 is the most, to kv8_rows_kernel (stages of 128
+// keys there), the others to kv8_prefill_kernel.  A call whose bounds
 // allow more than 64 rows may mix long and short requests (a serving step that
 // prefills some and decodes others): then those of at most 16 rows (64 where
 // the group itself is larger) stay with the first kernel, where a long context
@@ -821,6 +698,13 @@ DecodePlan plan_decode(int N, int G, int max_q) {
   return p;
 }
 
+template <int D>
+cudaError_t launch_join(const AttnArgs &a, int teams, cudaStream_t s) {
+  const bool wide = (int64_t)a.N * a.HK * 8 < teams;  // eight pieces a pair, or more
+  const dim3 grid(wide ? a.row_most : (a.row_most + 3) / 4, a.HK, a.N);
+  return wide ? gdn_host::launch_dependent(kv8_join_kernel<D, true>, grid, 128, 0, s, a, teams)
+              : gdn_host::launch_dependent(kv8_join_kernel<D, false>, grid, 128, 0, s, a, teams);
+}
 template <int D, int NT, int MT>
 cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
   using Ly = DecodeLay<D, NT, MT>;
@@ -835,15 +719,15 @@ cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if ((e = gdn_host::launch_dependent(kv8_decode_kernel<D, NT, MT>, dim3(Ly::TEAMS), 32 * MT, Ly::BYTES, s, a, mk, mv)) != cudaSuccess)
     return e;
-  const bool wide = (int64_t)a.N * a.HK * 8 < Ly::TEAMS;  // eight pieces a pair, or more
-  const dim3 grid(wide ? a.row_most : (a.row_most + 3) / 4, a.HK, a.N);
-  return wide ? gdn_host::launch_dependent(kv8_join_kernel<D, true>, grid, 128, 0, s, a, (int)Ly::TEAMS)
-              : gdn_host::launch_dependent(kv8_join_kernel<D, false>, grid, 128, 0, s, a, (int)Ly::TEAMS);
+  return launch_join<D>(a, Ly::TEAMS, s);
 }
 template <int D> cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
   if (a.row_cap == 8) return launch_decode<D, 1, 1>(a, s);
   if (a.row_cap == 16) return launch_decode<D, 2, 1>(a, s);
-  if (a.row_cap == 32) return launch_decode<D, 4, 1>(a, s);
+  if (a.row_cap == 32) {
+    const cudaError_t e = launch_kv8_rows(a, s);
+    return e != cudaSuccess ? e : launch_join<D>(a, kSMs, s);
+  }
   return launch_decode<D, 4, 2>(a, s);
 }
 
@@ -873,6 +757,7 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs &c, cudaStream_t s) {
   a.scale_log2e = c.scale * gdnc::kLog2e;
   a.row_cap = p.row_cap;
   a.row_most = p.row_most;
+  a.stage_bits = p.row_cap == 32 ? 7 : 6;
   unsigned char *ws = static_cast<unsigned char *>(c.ws);
   if (p.row_most > 0) {
     a.part_o = reinterpret_cast<float *>(ws);

@@ -13,6 +13,8 @@
 
 namespace gdnkv {
 
+using gdn::set_status;
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2f(float x) { return gdnc::ex2(x); }
@@ -27,7 +29,8 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
 struct AttnArgs : gdn_host::Kv8AttnArgs {
   int G;  // query heads a kv head
   float scale_log2e;
-  int row_cap;      // rows of a team of the decode kernel (8, 16, 32 or 64)
+  int row_cap;      // rows of a team of the kernels for few rows (8, 16, 32 or 64)
+  int stage_bits;   // log2 of the keys of their stages
   int row_most;     // requests with more rows are the prefill kernel's
   float *part_o;    // [team][2][row_cap][D] partial results
   float2 *part_ml;  // [team][2][row_cap]: maximum, sum
@@ -79,6 +82,143 @@ __device__ __forceinline__ void store_row4(const AttnArgs &a, int tok, int head,
   if (a.lse && c == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
+// ------------------------------------------------------- the line of stages
+constexpr int kSMs = 152;
+constexpr int kMinStages = 2;  // stages a team takes at least
+
+// Stages of request n, 0 where the kernels for few rows have nothing to do for
+// it; s is its span.  A request whose rows see no key has one stage, which writes its zeros.
+__device__ __forceinline__ int stages_of(const AttnArgs &a, int n, Span &s) {
+  if (!request_span(a, n, 0, a.row_cap, s) || s.m * a.G > a.row_most) return 0;
+  return max(1, (s.keys + (1 << a.stage_bits) - 1) >> a.stage_bits);
+}
+// Stages that a team takes.
+__device__ __forceinline__ int64_t stretch_of(int64_t total, int teams) {
+  const int64_t per = (total + teams - 1) / teams;
+  return per < kMinStages ? kMinStages : per;
+}
+
+// Where a walk along the line of stages stands.
+struct Place {
+  int n, h;       // request, kv head
+  int stage, of;  // stage of the pair, stages that it has
+  Span s;
+};
+__device__ __forceinline__ void next_request(const AttnArgs &a, Place &p) {
+  p.stage = 0;
+  p.h = 0;
+  do {
+    ++p.n;
+    p.of = p.n < a.N ? stages_of(a, p.n, p.s) : 1;
+  } while (p.of == 0);
+}
+// A team's stretch of the line, found by a warp: where it begins; returns its
+// stages (0: none).  `first` for one warp of each team.
+__device__ __forceinline__ int find_place(const AttnArgs &a, int team, int teams, bool first, Place &at) {
+  const int lane = threadIdx.x & 31;
+  int left;
+  // Up to 32 requests, a lane each; else lane l sums the stages of requests
+  // [l seg, (l + 1) seg) and the requests of the lane that holds the start are
+  // looked at again.  The last team also writes every request's place on the
+  // line for the joining kernel, which forms the places of few requests itself.
+  if (a.N <= 32) {
+    Span s{};
+    const int of = lane < a.N ? stages_of(a, lane, s) : 0;
+    if (s.bits && team == 0 && first) set_status(a.dev_status, s.bits);
+    // below 2^31: 32 contexts of up to 2^25 stages would be 2^36 keys
+    const uint32_t mine = (uint32_t)of * (uint32_t)a.HK;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t per = (uint32_t)stretch_of(total, teams), start = per * (uint32_t)team;
+    if (start >= total) return 0;
+    left = (int)min(per, total - start);
+    const int n = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;
+    at.n = n;
+    at.of = __shfl_sync(0xffffffffu, of, n);
+    at.s.t0 = __shfl_sync(0xffffffffu, s.t0, n);
+    at.s.m = __shfl_sync(0xffffffffu, s.m, n);
+    at.s.L = __shfl_sync(0xffffffffu, s.L, n);
+    at.s.keys = __shfl_sync(0xffffffffu, s.keys, n);
+    const uint32_t in = start - (__shfl_sync(0xffffffffu, incl, n) - (uint32_t)at.of * (uint32_t)a.HK);
+    at.h = (int)(in / (uint32_t)at.of);
+    at.stage = (int)(in - (uint32_t)at.h * (uint32_t)at.of);
+  } else {
+    Span s;
+    const int seg = (a.N + 31) / 32;
+    int64_t mine = 0;
+    int bits = 0;
+    for (int n = lane * seg; n < min(a.N, (lane + 1) * seg); ++n) {
+      mine += (int64_t)stages_of(a, n, s) * a.HK;
+      bits |= s.bits;
+    }
+    if (bits && team == 0 && first) set_status(a.dev_status, bits);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31);
+    const int64_t per = stretch_of(total, teams), start = per * team;
+    if (team == teams - 1 && first) {
+      int64_t run = incl - mine;
+      for (int n = lane * seg; n < min(a.N, (lane + 1) * seg); ++n) {
+        a.place[n] = run;
+        run += (int64_t)stages_of(a, n, s) * a.HK;
+      }
+      if (lane == 0) a.place[a.N] = total;
+    }
+    if (start >= total) return 0;
+    left = (int)min(per, total - start);
+    const int owner = __ffs((int)__ballot_sync(0xffffffffu, incl > start)) - 1;
+    int64_t run = __shfl_sync(0xffffffffu, incl - mine, owner);
+    for (int base = owner * seg;; base += 32) {
+      const int n = base + lane;
+      const int64_t c = n < a.N ? (int64_t)stages_of(a, n, s) * a.HK : 0;
+      int64_t sum = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run + sum > start);
+      if (past) {
+        const int l = __ffs((int)past) - 1;
+        at.n = base + l;
+        const int64_t in = start - (run + __shfl_sync(0xffffffffu, sum - c, l));
+        at.of = stages_of(a, at.n, at.s);
+        at.h = (int)(in / at.of);
+        at.stage = (int)(in - (int64_t)at.h * at.of);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  return left;
+}
+
+// ------------------------------------------------------------------ helpers
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
 // ---------------------------------------------------------------- host side
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -110,7 +250,10 @@ inline bool cache_map(CUtensorMap *mp, const void *ptr, int D, int bs, int64_t p
 
 // Attention of the requests that have at least min_rows rows (gdn_kv8_prefill.cu).
 cudaError_t launch_prefill(const AttnArgs &a, int min_rows, cudaStream_t s);
-// Bytes of workspace that it needs, and their place.
+// Attention of the requests of up to 32 rows, stages of 128 keys; partial results
+// as the decode kernel's, kSMs teams (gdn_kv8_rows.cu).
+cudaError_t launch_kv8_rows(const AttnArgs &a, cudaStream_t s);
+// Bytes of workspace that the prefill kernel needs, and their place.
 size_t prefill_workspace(int D);
 void prefill_place(AttnArgs &a, void *ws);
 

@@ -4,6 +4,8 @@ Tolerances, from the roundings: a bf16 output is one rounding of an fp32 result,
 off by some 2^-21 of the terms that were added, so 2^-8 of the value plus 2^-18 of the largest term.  fp32 sums over
 rows: 2^-19 of the sum of magnitudes.  Attention: p is rounded to 11 bits (2^-12 each, at most 2^-11 of
 sum p |v| with the fp32 errors of the logits) and o to bf16.  Codes, scales and whole numbers: equal."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -612,6 +614,67 @@ def test_attention_of_many_tokens_over_long_contexts(HK, G, D, bs, lens, news):
     _attn_check(c, o, lse)
     o3, lse3, _ = _attn_run(c)
     assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+@pytest.mark.parametrize("HK,G,D,bs,lens,news", [
+    (1, 8, 128, 64, [4], [4]), (2, 8, 128, 64, [127, 128, 129, 0, 260, 3], [4, 3, 4, 2, 0, 4]), (1, 32, 64, 16, [1, 1000], [1, 1]),
+    (2, 8, 64, 32, [5000, 4], [4, 4]), (1, 6, 128, 128, [3000, 2, 640, 1281], [5, 4, 1, 5]), (4, 8, 128, 16, [7000], [4]),
+    (1, 20, 128, 64, [300] * 3, [1, 1, 1])])
+def test_attention_of_drafts(HK, G, D, bs, lens, news):
+    """17 to 32 rows a kv head: contexts of one tile, of many, cut between blocks, empty ones."""
+    c = _attn_case(HK, G, D, bs, lens, news, sum(lens) + D + 3)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+    o3, lse3, _ = _attn_run(c)
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+def test_attention_of_many_drafts_with_nan():
+    """More pairs than blocks, contexts of a tile or two, NaN past every context and one value that only the last token
+    of request 7 sees."""
+    rng = np.random.RandomState(9)
+    news = [int(x) for x in rng.randint(0, 5, 90)]
+    news[7] = 4
+    lens = [int(m + x) for m, x in zip(news, rng.randint(0, 300, 90))]
+    c = _attn_case(2, 8, 128, 32, lens, news, 22)
+    at = lens[7] - 1
+    c["vc"].view(torch.uint8)[c["table"][7][at // 32], 1, at % 32, 100] = 0x7f
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+    assert int(torch.isnan(o).sum()) == 8
+
+
+def test_attention_of_drafts_whose_weights_are_tiny():
+    """One key far above 20000 others, whose weights of 2^-14 add up to more than its own."""
+    c = _attn_case(1, 8, 128, 64, [20000], [4], 33, spread=0.0)
+    c["kc"].view(torch.uint8).zero_()
+    q = torch.zeros_like(c["q"].float())
+    q[..., 0] = 1.0
+    c["q"] = q.to(BF)
+    page, place = c["table"][0][100 // 64], 100 % 64
+    one = torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    c["kc"].view(torch.uint8)[page, 0, place, 0] = one
+    scale = 14.0 / math.log2(math.e) / float(c["ks"][page, 0])
+    o, lse, st = _attn_run(c, scale=scale)
+    assert st == 0
+    _attn_check(c, o, lse, scale=scale)
+
+
+def test_attention_of_drafts_wait_that_runs_out():
+    """The testing hook on this path: a status, and the next call is right again."""
+    gdn = _gdn()
+    c = _attn_case(2, 8, 128, 64, [300, 900], [4, 3], 72)
+    o, lse, _ = _attn_run(c)
+    gdn.testing_force_wait_expiry(True)
+    try:
+        _, _, st = _attn_run(c)
+    finally:
+        gdn.testing_force_wait_expiry(False)
+    assert st == gdn.DEV_WAIT_TIMEOUT
+    o2, lse2, st = _attn_run(c)
+    assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_attention_nan_in_a_cut_tile():
