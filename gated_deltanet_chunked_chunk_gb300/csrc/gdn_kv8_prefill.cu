@@ -27,16 +27,20 @@
 // more than 8 (p' <= 256 is safe in f16), by the softmax warps themselves.
 //
 // The last items, where they do not come out even with the SMs, are cut along
-// their keys (find_job).  4096 tokens over 16384 keys, 32 heads of 128, 4 kv
-// heads: 512 items on 152 SMs, 747 us (1.29 PFLOP/s, 68 % of a 16-bit library
-// product) against 838 with the last 56 items whole; 512 tokens over 16384: 145 us,
-// two pieces an item.  A key tile takes 3600 cycles, of which the tensor cores
-// work 2176: a softmax thread's chain from "S is there" to "P is there" (load,
-// maximum, exponentials, store: 2000) is longer than the other tile's products
-// that hide it.  Two threads a row (1200 us: with 64 logits each their registers
-// spill), blocks that stay and take a stretch of all items' key tiles (822 us:
-// what that adds to the loop costs more than the even end gains) and reading the
-// logits twice (1490 us) were slower.
+// their keys (find_work).  4096 tokens over 16384 keys, 32 heads of 128, 4 kv
+// heads: 512 items on 152 SMs, 714 us (1.35 PFLOP/s, 71 % of a 16-bit library
+// product), about 90 us less than with the last 56 items whole; 512 tokens over
+// 16384: 139 us, two pieces an item.  What a block works on stands in shared memory,
+// as every register that the loops spill costs (740 us with 70 bytes more of
+// them).  A key tile takes 3500 cycles, of which the tensor cores work 2176: a
+// softmax thread's chain from "S is there" to "P is there" (load, maximum,
+// exponentials, store: 2000) is longer than the other tile's products that hide
+// it; P V begins when the first half of P is there (747 us without).  Two threads a
+// row (1200 us: with 64 logits each their registers spill), blocks that stay and
+// take a stretch of all items' key tiles (822 us: what that adds to the loop costs
+// more than the even end gains) and reading the logits twice (1490 us) were
+// slower.  A block's own start and end (its item, queries, the result: 28000
+// cycles) are what short prompts pay.
 #include <limits.h>
 
 #include <algorithm>
@@ -51,7 +55,7 @@ using namespace gdnkv;
 constexpr int kTileKeys = 128;
 constexpr int kPrefThreads = 512;
 constexpr int kItemRows = 256;
-constexpr int kSlots = 152;     // partial results, one for each SM
+constexpr int kSlots = kSMs;    // partial results, one for each SM
 constexpr int kPieceTiles = 8;  // key tiles that a piece of an item has at least
 constexpr int kParSlots = 8;  // key tiles whose page constants are kept: more than can be in flight
 
@@ -66,10 +70,19 @@ struct PrefLay {
   static constexpr int OFF_V = OFF_W + NW * T16;
   static constexpr int OFF_PAR = OFF_V + NV * T8;  // float4 {k scale, lv, 2^-lv, 0} x 8 pages a slot
   static constexpr int OFF_BAR = OFF_PAR + kParSlots * 128;
-  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NW + 10 + kParSlots;
+  static constexpr int BARS = 2 * NK + 2 * NV + 2 * NW + 12 + kParSlots;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
-  static constexpr int BYTES = OFF_MISC + 32 + 17 * 8 + 48;
+  static constexpr int BYTES = OFF_MISC + 32 + 16 * 8 + 48;
   static_assert(BYTES <= 227 * 1024, "one block an SM");
+};
+
+// What a block works on.  It stands in shared memory, and each kind of warp
+// takes what it needs: the loops need the registers.
+struct Work {
+  int n, h, row0, rows;  // rows: the request's
+  int t0, past, keys;    // past: L - m, what stands before the request's first token
+  int base, tiles;       // key tiles: the `tiles` from base on
+  int pieces, slot;      // pieces the item has, 0: nothing to do; where this one's result goes
 };
 
 // An item is 256 rows of one (request, kv head).  Those of a call stand in one
@@ -77,19 +90,14 @@ struct PrefLay {
 // Where the items do not come out even with the SMs, the last ones are cut along
 // their keys, each into as many pieces as leave no SM without one; a small
 // kernel joins the pieces.
-struct Job {
-  int n, h, tile;     // tile: of 256 rows
-  int piece, pieces;  // pieces 0: nothing to do
-  int slot;           // where a piece's result goes
-};
 __device__ __forceinline__ int item_tiles(const AttnArgs &a, int n, int min_rows, bool report) {
   Span s;
   const bool some = n < a.N && request_span(a, n, 0, 1, s);
   if (n < a.N && report && s.bits) set_status(a.dev_status, s.bits);
   return some && s.m * a.G >= min_rows ? (s.m * a.G + kItemRows - 1) / kItemRows : 0;
 }
-// This block's job, found by all its threads.  sums: 17 numbers of shared memory.
-__device__ __forceinline__ Job find_job(const AttnArgs &a, int min_rows, int sms, int64_t *sums) {
+// Finds this block's work, by all its threads.  sums: 16 numbers of shared memory.
+__device__ __forceinline__ void find_work(const AttnArgs &a, int min_rows, int sms, int64_t *sums, volatile Work *work) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (a.N + kPrefThreads - 1) / kPrefThreads, n0 = tid * each;
   const bool report = blockIdx.x == 0;
@@ -102,8 +110,7 @@ __device__ __forceinline__ Job find_job(const AttnArgs &a, int min_rows, int sms
     if (lane >= o) upto += x;
   }
   if (lane == 31) sums[warp] = upto;
-  int *found = reinterpret_cast<int *>(sums + kPrefThreads / 32);  // the request, its items before this one
-  if (tid == 0) *found = -1;
+  if (tid == 0) work->pieces = 0;
   __syncthreads();
   int64_t total = 0, before = upto - mine;
 #pragma unroll
@@ -115,44 +122,42 @@ __device__ __forceinline__ Job find_job(const AttnArgs &a, int min_rows, int sms
   const int all = (int)min(total, (int64_t)gridDim.x - kSlots);
   const int whole = all / sms * sms, rest = all - whole;
   // Pieces of each of the last items, one an SM.  (Two turns of smaller pieces,
-  // 56 items in 5 pieces each, end no earlier: 780 us against 767.)
+  // 56 items in 5 pieces each, ended later: 780 us where this took 767.)
   const int cut = rest > 0 ? min(sms, kSlots) / rest : 1;
-  const int b = blockIdx.x;
-  Job job{};
-  job.slot = b - whole;
-  int item = b;
-  job.pieces = 1;
-  if (b >= whole && cut > 1) {
-    item = whole + job.slot / cut;
-    job.piece = job.slot % cut;
-    job.pieces = cut;
+  const int slot = (int)blockIdx.x - whole;
+  int item = blockIdx.x, piece = 0, pieces = 1;
+  if (slot >= 0 && cut > 1) {
+    item = whole + slot / cut;
+    piece = slot % cut;
+    pieces = cut;
   }
   if (item < all && item >= before && item < before + mine) {
-    int n = n0, at = (int)(item - before);
-    for (int t; at >= (t = a.HK * item_tiles(a, n, min_rows, false)); ++n) at -= t;
-    found[0] = n;
-    found[1] = at;
+    int n = n0, at = (int)(item - before), tiles;
+    for (int t; at >= (t = a.HK * (tiles = item_tiles(a, n, min_rows, false))); ++n) at -= t;
+    const int h = at % a.HK, tile = tiles - 1 - at / a.HK;
+    Span s;
+    request_span(a, n, tile * kItemRows, kItemRows, s);  // true: it has tiles
+    const int keys = (s.keys + kTileKeys - 1) / kTileKeys;
+    pieces = min(pieces, max(1, keys / kPieceTiles));
+    if (piece < pieces) {
+      work->n = n;
+      work->h = h;
+      work->row0 = tile * kItemRows;
+      work->rows = s.m * a.G;
+      work->t0 = s.t0;
+      work->past = s.L - s.m;
+      work->keys = s.keys;
+      work->base = (int)((int64_t)keys * piece / pieces);
+      work->tiles = (int)((int64_t)keys * (piece + 1) / pieces) - work->base;
+      work->slot = slot;
+      work->pieces = pieces;
+    }
+    if (slot >= 0 && slot < kSlots) a.owners[slot] = make_int4(n, h, tile, piece == 0 && pieces > 1 ? pieces : 0);
+  } else if (tid == 0 && item >= all && slot >= 0 && slot < kSlots) {
+    a.owners[slot] = make_int4(0, 0, 0, 0);
   }
   __syncthreads();
-  job.n = found[0];
-  if (job.n < 0) {
-    job.pieces = 0;
-    return job;
-  }
-  const int at = found[1];
-  job.h = at % a.HK;
-  job.tile = item_tiles(a, job.n, min_rows, false) - 1 - at / a.HK;
-  return job;
 }
-
-// What the block works on.  It stands in shared memory, and each kind of warp
-// takes what it needs: the loops need the registers.
-struct Work {
-  int n, h, row0, rows;  // rows: the request's
-  int t0, past, keys;    // past: L - m, what stands before the request's first token
-  int base, tiles;       // key tiles: the `tiles` from base on
-  int pieces, slot;
-};
 
 template <int D>
 __global__ void __launch_bounds__(kPrefThreads, 1)
@@ -162,31 +167,9 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_wait();
-  Job job = find_job(a, min_rows, sms, reinterpret_cast<int64_t *>(smem + Ly::OFF_MISC + 32));
-  volatile Work *work = reinterpret_cast<volatile Work *>(smem + Ly::OFF_MISC + 32 + 17 * 8);
-  {
-    const int row0 = job.tile * kItemRows;
-    Span s{};
-    if (job.pieces > 0) request_span(a, job.n, row0, kItemRows, s);  // true: find_job has found it so
-    const int all = (s.keys + kTileKeys - 1) / kTileKeys;
-    job.pieces = min(job.pieces, max(1, all / kPieceTiles));
-    if (tid == 0 && job.slot >= 0 && job.slot < kSlots)
-      a.owners[job.slot] = make_int4(job.n, job.h, job.tile, job.piece == 0 && job.pieces > 1 ? job.pieces : 0);
-    if (job.piece >= job.pieces) return;
-    if (tid == 0) {
-      work->n = job.n;
-      work->h = job.h;
-      work->row0 = row0;
-      work->rows = s.m * a.G;
-      work->t0 = s.t0;
-      work->past = s.L - s.m;
-      work->keys = s.keys;
-      work->base = (int)((int64_t)all * job.piece / job.pieces);
-      work->tiles = (int)((int64_t)all * (job.piece + 1) / job.pieces) - work->base;
-      work->pieces = job.pieces;
-      work->slot = job.slot;
-    }
-  }
+  volatile Work *work = reinterpret_cast<volatile Work *>(smem + Ly::OFF_MISC + 32 + 16 * 8);
+  find_work(a, min_rows, sms, reinterpret_cast<int64_t *>(smem + Ly::OFF_MISC + 32), work);
+  if (work->pieces == 0) return;
   const int page_bits = 31 - __clz(a.bs);
 
   const uint32_t bar = sb + Ly::OFF_BAR;
@@ -202,7 +185,8 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   auto OD = [&](int w) { return bx + 32 + 8 * w; };
   const uint32_t QR = bx + 48, never = bx + 56;
   const uint32_t DR = bx + 64;
-  auto PR = [&](int i) { return bx + 80 + 8 * i; };
+  auto PH = [&](int w) { return bx + 72 + 8 * w; };
+  auto PR = [&](int i) { return bx + 88 + 8 * i; };
   volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_MISC);
   volatile int *nan_zone = failed + 1;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
@@ -210,7 +194,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
     for (int i = 0; i < Ly::NK; ++i) { mbar_init(KF(i), 1); mbar_init(KE(i), 1); }
     for (int i = 0; i < Ly::NV; ++i) { mbar_init(VF(i), 1); mbar_init(VE(i), 4); }
     for (int i = 0; i < Ly::NW; ++i) { mbar_init(WF(i), 4); mbar_init(WE(i), 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(SF(i), 1); mbar_init(PF(i), 128); mbar_init(OD(i), 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(SF(i), 1); mbar_init(PF(i), 128); mbar_init(PH(i), 128); mbar_init(OD(i), 1); }
     for (int i = 0; i < kParSlots; ++i) mbar_init(PR(i), 1);
     mbar_init(QR, 256);
     mbar_init(DR, 1);
@@ -226,8 +210,8 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   // Of the block's 65536 registers (512 threads x 128) the softmax warps take
-  // 192 a thread, the other warps 64: 2 x 128 x 192 + 2 x 128 x 64 = 65536.
-  // (184 and 72: 767 us against 747, though ptxas then spills less.)
+  // 184 a thread, the other warps 72: 2 x 128 x 184 + 2 x 128 x 72 = 65536.  (200
+  // and 56: 727 us against 714.)
   const int tiles = work->tiles;
   float m_ref = -INFINITY, l_sum = 0.f;
   int issued_k = 0, issued_v = 0;  // key tiles that the producer has issued
@@ -237,7 +221,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
 
   if (wg < 2) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int row = work->row0 + wg * 128 + (tid & 127), base = work->base;
     const bool on = row < work->rows;
     const int low = work->past + work->row0 / a.G;  // what the first row sees last
@@ -369,7 +353,12 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
           r[8 * g + i] = pack_f16(t.x, t.y);
         }
         l_sum = fmaf(sum.x + sum.y, iv[g], l_sum);
-        if (g == 3) tmem_st32(S_col, r);
+        if (g == 3) {  // the first keys' products may begin
+          tmem_st32(S_col, r);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(PH(wg));
+        }
       }
       tmem_st32(S_col + 32, r + 32);
       tmem_st_wait();
@@ -378,7 +367,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
     }
     if (ok && tiles > 0) ok = wait_bar(OD(wg), 0, failed, a.dev_status);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (wg == 2) {
       // ------------------------------------------------------------ widen V
       const int ct = tid - 256, base = work->base, past = work->past, low = past + work->row0 / a.G;
@@ -509,12 +498,17 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
           ok = wait_bar(WF(iw), (j / Ly::NW) & 1, failed, a.dev_status);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            ok = ok && wait_bar(PF(w), j & 1, failed, a.dev_status);
+            ok = ok && wait_bar(PH(w), j & 1, failed, a.dev_status);
             if (!ok) break;
             tc_fence_after();
             const uint32_t P = tmem + w * 128, O = tmem + 256 + w * D;
 #pragma unroll
-            for (int kk = 0; kk < kTileKeys / 16; ++kk) umma_f16_ta(O, P + 8 * kk, vd + 128 * kk, id_o, j > 0 || kk > 0);
+            for (int kk = 0; kk < kTileKeys / 32; ++kk) umma_f16_ta(O, P + 8 * kk, vd + 128 * kk, id_o, j > 0 || kk > 0);
+            ok = wait_bar(PF(w), j & 1, failed, a.dev_status);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = kTileKeys / 32; kk < kTileKeys / 16; ++kk) umma_f16_ta(O, P + 8 * kk, vd + 128 * kk, id_o, 1);
             if (w == 1) umma_commit(WE(iw));
             if (j + 1 < tiles) ok = logits(w, j + 1);
             else umma_commit(OD(w));
