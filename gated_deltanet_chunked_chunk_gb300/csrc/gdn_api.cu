@@ -357,7 +357,7 @@ int gdn_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ld
 
 size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int max_q_len, int max_seq_len) {
   if (N <= 0 || T <= 0 || HK <= 0 || HQ <= 0 || HQ % HK || !head_dim_ok(D) || max_q_len <= 0 || max_seq_len < 0) return 0;
-  return gdn_host::kv8_attn_workspace_bytes(N, HQ / HK, D, max_q_len < T ? max_q_len : T);
+  return gdn_host::kv8_attn_workspace_bytes(N, T, HQ / HK, D, max_q_len < T ? max_q_len : T);
 }
 
 int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, const uint8_t *v_cache,
@@ -378,7 +378,7 @@ int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, co
   if (!aligned16({q, k_cache, v_cache, o, workspace})) return GDN_EINVAL;
   const int max_q = max_q_len < T ? max_q_len : T;
   if ((int64_t)P * HK > 2147483646LL || (int64_t)max_q * (HQ / HK) > (1 << 30)) return GDN_EUNSUPPORTED;
-  const size_t need = gdn_host::kv8_attn_workspace_bytes(N, HQ / HK, D, max_q);
+  const size_t need = gdn_host::kv8_attn_workspace_bytes(N, T, HQ / HK, D, max_q);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
   if (!(scale > 0.f)) scale = 1.f / sqrtf((float)D);  // also catches NaN
   gdn_host::Kv8AttnArgs a{};

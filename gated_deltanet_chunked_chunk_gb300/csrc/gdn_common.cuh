@@ -259,6 +259,6 @@ struct Kv8AttnArgs {
   int32_t *dev_status;
   int force_expiry;  // testing hook: the first bounded wait of every block runs out
 };
-size_t kv8_attn_workspace_bytes(int N, int G, int D, int max_q);
+size_t kv8_attn_workspace_bytes(int N, int T, int G, int D, int max_q);
 cudaError_t launch_kv8_attn(const Kv8AttnArgs &a, cudaStream_t s);
 }  // namespace gdn_host

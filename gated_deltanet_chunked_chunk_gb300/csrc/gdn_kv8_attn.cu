@@ -688,12 +688,15 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int tea
 struct DecodePlan {
   int row_cap, row_most;
 };
-DecodePlan plan_decode(int N, int G, int max_q) {
+DecodePlan plan_decode(int N, int T, int G, int max_q) {
   DecodePlan p{};
   const int64_t rows = (int64_t)max_q * G;
   if (rows <= 64) p.row_most = (int)rows;
   else if (N == 1 || G > 64) p.row_most = 0;
   else p.row_most = G <= 16 ? 16 : 64;
+  // T tokens of N requests, none with more than max_q: where even the shortest
+  // possible one has more rows than that, the first kernel is not launched.
+  if (rows > 64 && (T - (N - 1) * (int64_t)max_q) * G > p.row_most) p.row_most = 0;
   p.row_cap = p.row_most <= 8 ? 8 : p.row_most <= 16 ? 16 : p.row_most <= 32 ? 32 : 64;
   return p;
 }
@@ -743,9 +746,9 @@ size_t decode_workspace(int N, int D) {
 }
 }  // namespace
 
-size_t kv8_attn_workspace_bytes(int N, int G, int D, int max_q) {
+size_t kv8_attn_workspace_bytes(int N, int T, int G, int D, int max_q) {
   if (N <= 0 || max_q <= 0) return 0;
-  const int most = plan_decode(N, G, max_q).row_most;
+  const int most = plan_decode(N, T, G, max_q).row_most;
   return (most > 0 ? decode_workspace(N, D) : 0) + ((int64_t)max_q * G > most ? gdnkv::prefill_workspace(D) : 0);
 }
 
@@ -753,7 +756,7 @@ cudaError_t launch_kv8_attn(const Kv8AttnArgs &c, cudaStream_t s) {
   AttnArgs a{};
   static_cast<Kv8AttnArgs &>(a) = c;
   a.G = c.HQ / c.HK;
-  const DecodePlan p = plan_decode(c.N, a.G, c.max_q);
+  const DecodePlan p = plan_decode(c.N, c.T, a.G, c.max_q);
   a.scale_log2e = c.scale * gdnc::kLog2e;
   a.row_cap = p.row_cap;
   a.row_most = p.row_most;

@@ -677,6 +677,20 @@ def test_attention_of_drafts_wait_that_runs_out():
     assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("lens,news", [([300, 200, 150], [100, 100, 100]), ([300, 200, 150], [100, 100, 3]),
+                                       ([300, 200, 150], [100, 100, 2]), ([90, 200], [70, 1])])
+def test_attention_of_prompts_whose_shortest_is_known(lens, news):
+    """Tokens and bounds that do, or do not, rule out requests of few rows."""
+    c = _attn_case(2, 8, 64, 32, lens, news, 61)
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o, lse)
+    c["max_q"] += 40  # a looser bound: the same answer from other launches
+    o2, lse2, st = _attn_run(c)
+    assert st == 0
+    _attn_check(c, o2, lse2)
+
+
 def test_attention_nan_in_a_cut_tile():
     """NaN values that only the last rows of a cut tile see, and a NaN key in the middle that all rows see."""
     for where in ("value", "key"):
