@@ -20,8 +20,8 @@
 // rows of the head's group.
 //
 // Work.  The contexts of all (request, kv head) pairs, cut into stages of 64
-// keys, form one line of stages; a team of MT warps (rows are (token, head of
-// the group) pairs, 8 NT a warp) takes a stretch of it, all teams stretches of
+// keys, form one line of stages; a team, one warp (rows are (token, head of
+// the group) pairs, 8 NT of them), takes a stretch of it, all teams stretches of
 // the same length, so ragged contexts balance by themselves.  A team that meets
 // a whole pair writes its output; of a pair that several teams share each writes
 // a partial result (two a team at most), and a second kernel joins them in
@@ -45,9 +45,9 @@
 // 16-byte places.  P's 8 x 8 blocks are transposed by movmatrix; for V^T a byte
 // permutation pairs the two keys of a thread for each d.
 // mma.sync rather than tcgen05: up to 16 rows the products take less time than
-// their bytes do.  17 to 32 rows, where they do not, are gdn_kv8_rows.cu's; 33 to
-// 64 (a range between that kernel and the prefill's, which is 13 % faster for
-// them over 131072 keys and 35 % slower over 4096) are two warps a team here.
+// their bytes do.  17 to 32 rows, where they do not, are gdn_kv8_rows.cu's, more are
+// gdn_kv8_prefill.cu's (40 rows: two warps a team took 270 us
+// where that takes 209 for 4 requests of 131072 keys, and 22 against 27 for one of 4096).
 #include "gdn_kv8_attn.cuh"
 
 namespace {
@@ -57,27 +57,24 @@ using namespace gdnkv;
 
 constexpr int kKeys = 64;         // keys a stage
 
-// D: head size; NT: tiles of 8 rows a warp; MT: warps a team.
-template <int D, int NT, int MT>
+// D: head size; NT: tiles of 8 rows a team.
+template <int D, int NT>
 struct DecodeLay {
   static constexpr int TILE = kKeys * D;                // bytes of a K or V tile
-  static constexpr int R = MT * (D == 128 ? 1 : 2);     // tiles of K, and of V, that a team holds
-  static constexpr int WARPS = NT == 4 ? 8 : 12;        // warps of all teams on a SM (registers: 255, 168)
-  static constexpr int TEAMS = WARPS / MT * kSMs;
-  static constexpr int ROWS = 8 * NT * MT;              // rows a team
+  static constexpr int R = D == 128 ? 1 : 2;            // tiles of K, and of V, that a team holds
+  static constexpr int PER_SM = 12;                     // teams on a SM (168 registers a thread)
+  static constexpr int TEAMS = PER_SM * kSMs;
+  static constexpr int ROWS = 8 * NT;                   // rows a team
   static constexpr int KP = NT == 1 ? 64 : 32;          // keys a pass
-  static constexpr bool QS = NT == 4;                   // the query fragments stay in shared memory
-  static constexpr int QB = QS ? D / 16 * NT * 2 * 128 : 0;  // their bytes a warp
   static constexpr int OFF_K = 0, OFF_V = R * TILE;
-  static constexpr int OFF_Q = 2 * R * TILE;
-  static constexpr int OFF_PAR = OFF_Q + MT * QB;       // float4 {k scale, lv, 2^-lv, 0} x 4 pages, R + 1 slots
+  static constexpr int OFF_PAR = 2 * R * TILE;          // float4 {k scale, lv, 2^-lv, 0} x 4 pages, R + 1 slots
   static constexpr int OFF_BAR = OFF_PAR + (R + 1) * 64;
   static constexpr int OFF_AHEAD = OFF_BAR + (2 * R + 1) * 8 + 8;
   static constexpr int BYTES = OFF_AHEAD + 48;
-  static_assert((BYTES + 1024) * (WARPS / MT) <= 228 * 1024, "all teams of a SM fit");
+  static_assert((BYTES + 1024) * PER_SM <= 228 * 1024, "all teams of a SM fit");
 };
 // Partial rows of all teams, two results a team, of the largest variant.
-constexpr int64_t kPartRows = (int64_t)kSMs * 2 * 8 * 32;
+constexpr int64_t kPartRows = (int64_t)kSMs * 2 * 12 * 16;
 
 __device__ __forceinline__ void mma_f16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -121,10 +118,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-template <int D, int NT, int MT>
-__global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
+template <int D, int NT>
+__global__ void __launch_bounds__(32, DecodeLay<D, NT>::PER_SM)
     kv8_decode_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using Ly = DecodeLay<D, NT, MT>;
+  using Ly = DecodeLay<D, NT>;
   constexpr int R = Ly::R;
   constexpr int NCH = D / 64;       // 16-byte chunks of a key row that a thread holds
   constexpr int NA = D / 16;        // tiles of 16 columns of O
@@ -132,7 +129,7 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
   constexpr int WPK = D / 32;       // words of a value row that a thread holds
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = blockIdx.x;
+  const int lane = threadIdx.x, team = blockIdx.x;
 
   const uint32_t bar = sb + Ly::OFF_BAR, never = bar + 16 * R;
   volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_BAR + (2 * R + 1) * 8);
@@ -143,13 +140,13 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     mbar_fence_init();
     *failed = 0;
   }
-  if (MT > 1) __syncthreads(); else __syncwarp();
+  __syncwarp();
   grid_wait();
   // Only now: the joining kernel reads lengths and offsets before its own wait.
   grid_release();
 
   Place at{};
-  const int left_all = find_place(a, team, Ly::TEAMS, warp == 0, at);
+  const int left_all = find_place(a, team, Ly::TEAMS, true, at);
   if (left_all == 0) return;
   int left = left_all;  // stages of this team still to do
 
@@ -161,12 +158,11 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
   // The place is kept in shared memory: the products need the registers.
   // The first pair's queries are read meanwhile.
   const int g = lane >> 2, t = lane & 3;
-  const int row0 = 8 * NT * warp;  // this warp's first row
   uint4 qraw[NT][2 * NCH];
   auto read_q = [&]() {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + 8 * nt + g;
+      const int row = 8 * nt + g;
       const uint16_t *src = a.q + (int64_t)(at.s.t0 + row / a.G) * a.ldq + (int64_t)(at.h * a.G + row % a.G) * D;
 #pragma unroll
       for (int i = 0; i < 2 * NCH; ++i)
@@ -252,19 +248,16 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     ++called;
     --to_call;
   };
-  if (warp == 0) {
-    if (lane == 0) ahead = at;
-    __syncwarp();
-    for (int i = 0; i < R; ++i) {
-      call_k();
-      call_v();
-    }
+  if (lane == 0) ahead = at;
+  __syncwarp();
+  for (int i = 0; i < R; ++i) {
+    call_k();
+    call_v();
   }
 
   const int kperm = (g >> 1) | ((g & 1) << 2);  // row of key g of 8
   const uint32_t sel0 = (g & 1) ? 0x1504u : 0x5140u, sel1 = (g & 1) ? 0x3726u : 0x7362u;
   const int va = t + 4 * (g & 1), vb = t + 4 * ((g & 1) ^ 1);
-  const uint32_t qs = sb + Ly::OFF_Q + warp * Ly::QB + lane * 16;
   int done = 0;  // stages that the products have used
 
   while (left > 0) {
@@ -273,10 +266,10 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     const int h = at.h, L = s.L, m = s.m;
     const bool from_start = at.stage == 0, to_end = left >= at.of - at.stage;
     const int count = to_end ? at.of - at.stage : left;
-    // Queries: row row0 + 8 nt + g; thread t holds d = 16 (t + 4 i) + 0..15,
+    // Queries: row 8 nt + g; thread t holds d = 16 (t + 4 i) + 0..15,
     // k-step 4 i + w taking 4 w + {0, 1 | 2, 3} of them.
-    uint32_t qf[Ly::QS ? 1 : 4 * NCH][NT][2];
-    float krow[NT][2];  // of rows row0 + 8 nt + 2 t + e
+    uint32_t qf[4 * NCH][NT][2];
+    float krow[NT][2];  // of rows 8 nt + 2 t + e
     if (NT > 1 || done > 0) read_q();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -305,19 +298,13 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
         uint32_t f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16lo_f(w[e]) * down, bf16hi_f(w[e]) * down);
-        if (Ly::QS) {  // k-steps 2 i and 2 i + 1 of this row tile: [k-step pair][row tile][lane] of 16 bytes
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (i * NT + nt) * 512), "r"(f[0]), "r"(f[1]), "r"(f[2]),
-                       "r"(f[3])
-                       : "memory");
-        } else {
-          qf[Ly::QS ? 0 : 2 * i][nt][0] = f[0];
-          qf[Ly::QS ? 0 : 2 * i][nt][1] = f[1];
-          qf[Ly::QS ? 0 : 2 * i + 1][nt][0] = f[2];
-          qf[Ly::QS ? 0 : 2 * i + 1][nt][1] = f[3];
-        }
+        qf[2 * i][nt][0] = f[0];
+        qf[2 * i][nt][1] = f[1];
+        qf[2 * i + 1][nt][0] = f[2];
+        qf[2 * i + 1][nt][1] = f[3];
       }
     }
-    const int low = L - m + row0 / a.G;  // what this warp's first row sees last
+    const int low = L - m;  // what the first row sees last
     // O^T: tile x, row tile nt: columns 2 NA.. of this thread g are d = NA g .. ;
     // o[x][nt][e + 2 f] is d = 2 NA g + 2 x + f (NA = D / 16) of row 2 t + e.
     float o[NA][NT][4];
@@ -368,31 +355,19 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
             }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            uint32_t q2[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (Ly::QS) {
-                const uint2 u = lds64(qs + ((2 * i + (w >> 1)) * NT + nt) * 512 + (w & 1) * 8);
-                q2[nt][0] = u.x;
-                q2[nt][1] = u.y;
-              } else {
-                q2[nt][0] = qf[Ly::QS ? 0 : 4 * i + w][nt][0];
-                q2[nt][1] = qf[Ly::QS ? 0 : 4 * i + w][nt][1];
-              }
-            }
 #pragma unroll
             for (int x = 0; x < NK; ++x) {
               uint32_t f[4];
               e4m3x4_f16x2(kw[x][0][w], f[0], f[2]);
               e4m3x4_f16x2(kw[x][1][w], f[1], f[3]);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(p[x][nt], f, q2[nt][0], q2[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_f16(p[x][nt], f, qf[4 * i + w][nt][0], qf[4 * i + w][nt][1]);
             }
           }
         }
         if (pass == kKeys / Ly::KP - 1) {
-          if (MT > 1) __syncthreads(); else __syncwarp();  // the K tile is free
-          if (warp == 0) call_k();
+          __syncwarp();  // the K tile is free
+          call_k();
         }
 
         float top[NT][2], iv_of[NK];
@@ -416,7 +391,7 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int row = row0 + 8 * nt + 2 * t + e;
+              const int row = 8 * nt + 2 * t + e;
               const int limit = row < m * a.G ? L - m + row / a.G : -1;
 #pragma unroll
               for (int x = 0; x < NK; ++x) {
@@ -529,11 +504,11 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (k0 + key <= L - m + (row0 + 8 * nt + 2 * t + e) / a.G) o[x >> 1][nt][e + 2 * (x & 1)] = NAN;
+                if (k0 + key <= L - m + (8 * nt + 2 * t + e) / a.G) o[x >> 1][nt][e + 2 * (x & 1)] = NAN;
           }
       }
-      if (MT > 1) __syncthreads(); else __syncwarp();  // the V tile is free
-      if (warp == 0) call_v();
+      __syncwarp();  // the V tile is free
+      call_v();
     }
 
     // ------------------------------------------------ the stretch's result
@@ -542,7 +517,7 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float l = keys_add(ls[nt][e]);
-        const int row = row0 + 8 * nt + 2 * t + e;
+        const int row = 8 * nt + 2 * t + e;
         if (row >= m * a.G || *failed) continue;
         if (from_start && to_end) {
           const int64_t out = (int64_t)(s.t0 + row / a.G) * a.HQ + h * a.G + row % a.G;
@@ -569,8 +544,7 @@ __global__ void __launch_bounds__(32 * MT, DecodeLay<D, NT, MT>::WARPS / MT)
     if (left > 0 && ++at.h == a.HK) next_request(a, at);
   }
 
-  if (MT > 1) __syncthreads();
-  if (*failed && warp == 0 && lane == 0) {
+  if (*failed && lane == 0) {
     // A wait ran out, nothing was written since; stay until the copies are in.
     bool ok = true;
     for (int i = 0; i < R && i < called_k; ++i) ok &= mbar_wait_bounded(KF(i), ((called_k - 1 - i) / R) & 1, gdnc::kWaitLimit);
@@ -678,26 +652,26 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int tea
 
 // ---------------------------------------------------------------- host side
 // How a call's requests are worked on, from its host bounds.  Requests of up to
-// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 8, 16 or
-// 64 rows a team, or, where 17 to 32 is the most, to kv8_rows_kernel (stages of 128
-// keys there), the others to kv8_prefill_kernel.  A call whose bounds
-// allow more than 64 rows may mix long and short requests (a serving step that
-// prefills some and decodes others): then those of at most 16 rows (64 where
-// the group itself is larger) stay with the first kernel, where a long context
-// of few rows is split over many teams.
+// row_most rows (tokens x heads of a group) go to kv8_decode_kernel, with 8 or 16
+// rows a team, or, where 17 to 32 is the most, to kv8_rows_kernel (stages of 128
+// keys there), the others to kv8_prefill_kernel.  A call whose bounds allow more
+// than 32 rows may mix long and short requests (a serving step that prefills some
+// and decodes others): then those of at most 16 rows (32 where the group itself
+// is larger than 16) stay with the first kernels, where a long context of few rows
+// is split over many teams.
 struct DecodePlan {
   int row_cap, row_most;
 };
 DecodePlan plan_decode(int N, int T, int G, int max_q) {
   DecodePlan p{};
   const int64_t rows = (int64_t)max_q * G;
-  if (rows <= 64) p.row_most = (int)rows;
-  else if (N == 1 || G > 64) p.row_most = 0;
-  else p.row_most = G <= 16 ? 16 : 64;
+  if (rows <= 32) p.row_most = (int)rows;
+  else if (N == 1 || G > 32) p.row_most = 0;
+  else p.row_most = G <= 16 ? 16 : 32;
   // T tokens of N requests, none with more than max_q: where even the shortest
   // possible one has more rows than that, the first kernel is not launched.
-  if (rows > 64 && (T - (N - 1) * (int64_t)max_q) * G > p.row_most) p.row_most = 0;
-  p.row_cap = p.row_most <= 8 ? 8 : p.row_most <= 16 ? 16 : p.row_most <= 32 ? 32 : 64;
+  if (rows > 32 && (T - (N - 1) * (int64_t)max_q) * G > p.row_most) p.row_most = 0;
+  p.row_cap = p.row_most <= 8 ? 8 : p.row_most <= 16 ? 16 : 32;
   return p;
 }
 
@@ -708,9 +682,9 @@ cudaError_t launch_join(const AttnArgs &a, int teams, cudaStream_t s) {
   return wide ? gdn_host::launch_dependent(kv8_join_kernel<D, true>, grid, 128, 0, s, a, teams)
               : gdn_host::launch_dependent(kv8_join_kernel<D, false>, grid, 128, 0, s, a, teams);
 }
-template <int D, int NT, int MT>
+template <int D, int NT>
 cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
-  using Ly = DecodeLay<D, NT, MT>;
+  using Ly = DecodeLay<D, NT>;
   static_assert((int64_t)Ly::TEAMS * 2 * Ly::ROWS <= kPartRows, "partial results");
   CUtensorMap mk, mv;
   const int keys = a.bs < kKeys ? a.bs : kKeys;
@@ -718,20 +692,17 @@ cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
       !cache_map(&mv, a.vc, D, a.bs, (int64_t)a.P * a.HK, keys, true))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = gdn_host::allow_smem(kv8_decode_kernel<D, NT, MT>, Ly::BYTES, done);
+  cudaError_t e = gdn_host::allow_smem(kv8_decode_kernel<D, NT>, Ly::BYTES, done);
   if (e != cudaSuccess) return e;
-  if ((e = gdn_host::launch_dependent(kv8_decode_kernel<D, NT, MT>, dim3(Ly::TEAMS), 32 * MT, Ly::BYTES, s, a, mk, mv)) != cudaSuccess)
+  if ((e = gdn_host::launch_dependent(kv8_decode_kernel<D, NT>, dim3(Ly::TEAMS), 32, Ly::BYTES, s, a, mk, mv)) != cudaSuccess)
     return e;
   return launch_join<D>(a, Ly::TEAMS, s);
 }
 template <int D> cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
-  if (a.row_cap == 8) return launch_decode<D, 1, 1>(a, s);
-  if (a.row_cap == 16) return launch_decode<D, 2, 1>(a, s);
-  if (a.row_cap == 32) {
-    const cudaError_t e = launch_kv8_rows(a, s);
-    return e != cudaSuccess ? e : launch_join<D>(a, kSMs, s);
-  }
-  return launch_decode<D, 4, 2>(a, s);
+  if (a.row_cap == 8) return launch_decode<D, 1>(a, s);
+  if (a.row_cap == 16) return launch_decode<D, 2>(a, s);
+  const cudaError_t e = launch_kv8_rows(a, s);
+  return e != cudaSuccess ? e : launch_join<D>(a, kSMs, s);
 }
 
 }  // namespace

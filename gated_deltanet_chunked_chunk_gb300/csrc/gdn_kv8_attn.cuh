@@ -29,7 +29,7 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {
 struct AttnArgs : gdn_host::Kv8AttnArgs {
   int G;  // query heads a kv head
   float scale_log2e;
-  int row_cap;      // rows of a team of the kernels for few rows (8, 16, 32 or 64)
+  int row_cap;      // rows of a team of the kernels for few rows (8, 16 or 32)
   int stage_bits;   // log2 of the keys of their stages
   int row_most;     // requests with more rows are the prefill kernel's
   float *part_o;    // [team][2][row_cap][D] partial results

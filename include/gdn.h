@@ -639,7 +639,7 @@ size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int
  * 65535 or HK > 65535); HQ % HK == 0.  q, the caches, o and the workspace must
  * start on a 16-byte boundary and ldq be a multiple of 8 (else GDN_EINVAL);
  * GDN_EWORKSPACE for a small workspace.  Two launches where requests have up to
- * 64 rows (tokens x HQ / HK) or all have more (which T, N and max_q_len must say),
+ * 32 rows (tokens x HQ / HK) or all have more (which T, N and max_q_len must say),
  * four where a call may mix both.
  */
 int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, const uint8_t *v_cache,
