@@ -553,16 +553,17 @@ __global__ void __launch_bounds__(32, DecodeLay<D, NT>::PER_SM)
   }
 }
 
-// Joins the partial results of a pair's rows, in order.  WIDE: block x of a pair
-// takes row x, each of its four warps a quarter of the pieces (calls with few
+// Joins the partial results of a pair's rows, in order.  W > 1: block x of a pair
+// takes row x, each of its W warps a share of the pieces (calls with few
 // pairs, which are cut into many pieces each); else rows 4 x .. 4 x + 3, a warp
 // each.  A lane reads the maximum and sum of one piece, 32 at a time; D / 4
 // lanes hold four columns each.  Latency counts here: three dependent reads.
-template <int D, bool WIDE>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int teams) {
+template <int D, int W>
+__global__ void __launch_bounds__(W > 1 ? 32 * W : 128) kv8_join_kernel(const AttnArgs a, int teams) {
   constexpr int LANES = D / 4;
-  __shared__ float4 so[WIDE ? 4 : 1][LANES];
-  __shared__ float2 sml[4];
+  constexpr bool WIDE = W > 1;
+  __shared__ float4 so[W][LANES];
+  __shared__ float2 sml[W];
   const int n = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = WIDE ? blockIdx.x : 4 * blockIdx.x + warp;
   // A dependent launch that the decode kernel, which has waited for what came
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int tea
   const int64_t from = place + (int64_t)h * of, first = from / per, last = (from + of - 1) / per;
   const int pieces = (int)(last - first) + 1;
   if (pieces == 1) return;
-  const int share = WIDE ? (pieces + 3) / 4 : pieces;
+  const int share = (pieces + W - 1) / W;
   const int i0 = WIDE ? warp * share : 0, i1 = min(pieces, i0 + share);
   const int c = lane % LANES;
   // piece 0 is its team's slot 1, the others their teams' slot 0
@@ -634,12 +635,12 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttnArgs a, int tea
     l = 0.f;
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, sml[i].x);
+    for (int i = 0; i < W; ++i) top = fmaxf(top, sml[i].x);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
       const float w = ex2f(sml[i].x - base);
-      const float4 v = so[WIDE ? i : 0][c];
+      const float4 v = so[i][c];
       l = fmaf(w, sml[i].y, l);
       acc.x = fmaf(w, v.x, acc.x);
       acc.y = fmaf(w, v.y, acc.y);
@@ -677,10 +678,14 @@ DecodePlan plan_decode(int N, int T, int G, int max_q) {
 
 template <int D>
 cudaError_t launch_join(const AttnArgs &a, int teams, cudaStream_t s) {
-  const bool wide = (int64_t)a.N * a.HK * 8 < teams;  // eight pieces a pair, or more
+  // Eight pieces a pair, or more; 64 or more take 16 warps (one context of 131072
+  // keys, 456 pieces: 36 us against 55; with 28 pieces 59 against 51).
+  const int64_t pairs = (int64_t)a.N * a.HK;
+  const bool wide = pairs * 8 < teams;
   const dim3 grid(wide ? a.row_most : (a.row_most + 3) / 4, a.HK, a.N);
-  return wide ? gdn_host::launch_dependent(kv8_join_kernel<D, true>, grid, 128, 0, s, a, teams)
-              : gdn_host::launch_dependent(kv8_join_kernel<D, false>, grid, 128, 0, s, a, teams);
+  if (pairs * 64 < teams) return gdn_host::launch_dependent(kv8_join_kernel<D, 16>, grid, 512, 0, s, a, teams);
+  if (wide) return gdn_host::launch_dependent(kv8_join_kernel<D, 4>, grid, 128, 0, s, a, teams);
+  return gdn_host::launch_dependent(kv8_join_kernel<D, 1>, grid, 128, 0, s, a, teams);
 }
 template <int D, int NT>
 cudaError_t launch_decode(const AttnArgs &a, cudaStream_t s) {
