@@ -254,7 +254,7 @@ __device__ __forceinline__ void write_run(const AppendArgs &a, int kv, int h, in
     } else {
       // older codes move to the larger scale, rounded to the format again
       const float f = gdnkv::pow2(max(old - e, -126));
-      if (a.D % 4 == 0) {
+      if (a.D % 4 == 0 && (reinterpret_cast<uintptr_t>(codes) & 3) == 0) {  // four at once where their address allows
         uint32_t *p = reinterpret_cast<uint32_t *>(codes);
         for (int i = tid; i < off * a.D / 4; i += TH) p[i] = gdnkv::rescale4(p[i], f);
       } else {

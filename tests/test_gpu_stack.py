@@ -780,3 +780,26 @@ def test_refusals_of_types_shapes_and_layouts():
         except Exception as e:
             raise AssertionError(f"refusal {n}: {type(e).__name__} {e} instead of {error.__name__}")
         raise AssertionError(f"refusal {n}: accepted")
+
+
+# ----------------------------------------------------- append: addresses, scales, runs
+@pytest.mark.parametrize("start", [1, 2, 3, 4])
+def test_append_to_a_cache_at_any_byte(start):
+    """Caches that begin `start` bytes into their storage, pages whose older codes move to a larger scale."""
+    gdn, g = _gdn(), _gen(80 + start)
+    bs, D, H, P = 16, 64, 2, 3
+    kc, ks = U.make_cache(P, H, bs, D, g)
+    x = (300 * torch.randn(4, H, D, generator=g)).to(BF)
+    slots = [0 * bs + 7, 0 * bs + 8, 2 * bs + 3, 1 * bs]
+    held = [torch.zeros(kc.numel() + 8, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+    dev = [b[start:start + kc.numel()].view(P, H, bs, D) for b in held]
+    for d in dev:
+        d.view(torch.uint8).copy_(kc.view(torch.uint8))
+    scales = [ks.cuda(), ks.clone().cuda()]
+    gdn.gdn_kv8_append(x.cuda(), x.cuda(), *dev, *scales, torch.tensor(slots, dtype=torch.int32, device="cuda"))
+    ref = U.append(U.f64(x), U.f64(kc.float()), U.f64(ks), slots)
+    assert (ref[1][0] > U.f64(ks)[0]).all()  # the scale did grow
+    for d, sc, b in zip(dev, scales, held):
+        _same_cache(d, sc, ref)
+        edge = b.view(torch.uint8)
+        assert not edge[:start].any() and not edge[start + kc.numel():].any()
