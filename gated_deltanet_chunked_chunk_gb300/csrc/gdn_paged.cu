@@ -42,16 +42,20 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
   left = left < 0 ? 0 : left > F ? F : left;
   int32_t slot = -1, pos = 0, base = 0;
   int bits = 0;
+  bool found = false;
   for (int n0 = 0; n0 < N; n0 += kPlan) {
     const int n = n0 + tid, cnt = min(kPlan, N - n0);
     int32_t a = 0, b = 0, c = 0, want = 0;
+    bool broken = false;
     if (n < N) {
       a = cu[n];
       b = cu[n + 1];
       c = cached[n];
-      if (a < 0 || b < a || b > T || c < 0 || (n == 0 && a != 0) || (int64_t)c + b - a > 2147483647LL) {
+      broken = a < 0 || b < a || b > T || (n == 0 && a != 0);
+      if (broken) a = b = 0;
+      if (broken || c < 0 || (int64_t)c + b - a > 2147483647LL) {
         bits |= GDN_DEV_BAD_CU_SEQLENS;
-        a = b = 0;
+        b = a;
         c = c < 0 ? 0 : c;
       }
       const uint32_t total = (uint32_t)c + (uint32_t)(b - a);  // below 2^31, as checked
@@ -75,7 +79,7 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
     s_start[tid] = a;
     s_end[tid] = b;
     s_cached[tid] = c;
-    __syncthreads();
+    const bool ordered = !__syncthreads_or(broken);
     int32_t sums = s_warp[lane];  // every warp scans the warps' sums
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -86,14 +90,19 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
     const int32_t add = w == 0 ? 0 : __shfl_sync(0xffffffffu, sums, (w + 31) & 31);
     s_before[tid] = base + add + x - want;
     __syncthreads();
-    if (tok < T && tok >= s_start[0] && slot < 0) {
+    if (tok < T && !found) {
       // the last request of these that starts at or before the token and is not empty
       int lo = 0, hi = cnt - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_start[mid] <= tok) lo = mid; else hi = mid - 1;
+      if (ordered) {
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (s_start[mid] <= tok) lo = mid; else hi = mid - 1;
+        }
+      } else {
+        for (lo = hi; lo > 0 && !(s_start[lo] <= tok && tok < s_end[lo]);) --lo;
       }
       if (s_start[lo] <= tok && tok < s_end[lo]) {
+        found = true;
         pos = s_cached[lo] + (tok - s_start[lo]);
         const int pg = (int)(page_bits >= 0 ? (uint32_t)pos >> page_bits : (uint32_t)pos / (uint32_t)bs), off = pos - pg * bs;
         const int have = (int)pages_of(s_cached[lo]);

@@ -571,8 +571,9 @@ int gdn_rope(const uint16_t *q, const uint16_t *k, const int32_t *positions, con
  *   num_free_out  : int32 [1]   pages left; another address than num_free
  * No input but the table is written, so a call can be repeated.  Too few free
  * pages, or a row too short: table entry and slots -1, GDN_DEV_NO_PAGE.  Offsets
- * that break the rules and negative lengths: GDN_DEV_BAD_CU_SEQLENS, the
- * request counts as having no new tokens.  Slots must fit int32 (caller's
+ * that break the rules, negative lengths and sums past int32:
+ * GDN_DEV_BAD_CU_SEQLENS, the request counts as having no new tokens, the
+ * others get theirs.  Slots must fit int32 (caller's
  * pages x page_size < 2^31).  N = 0 writes num_free_out and T slots of -1.
  * One launch.
  */

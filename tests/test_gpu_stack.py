@@ -803,3 +803,60 @@ def test_append_to_a_cache_at_any_byte(start):
         _same_cache(d, sc, ref)
         edge = b.view(torch.uint8)
         assert not edge[:start].any() and not edge[start + kc.numel():].any()
+
+
+# ------------------------------------------------------------- plan: bad requests
+def _plan_around(cached, cu, T, bad, bs, seed):
+    """A batch some of whose requests are bad: the others' pages, slots and positions are those of the batch in which
+    the bad ones have no new tokens, whose own slots are -1."""
+    gdn, r, N = _gdn(), np.random.RandomState(seed), len(cached)
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    news = [0 if n in bad else cu[n + 1] - cu[n] for n in range(N)]
+    held = [0 if n in bad else c for n, c in enumerate(cached)]
+    width = max(1, max(-(-(c + m) // bs) for c, m in zip(held, news)))
+    ids = r.permutation(N * width + 3).tolist()
+    table = [[ids.pop() if p < -(-held[n] // bs) else -1 for p in range(width)] for n in range(N)]
+    start = np.concatenate([[0], np.cumsum(news)]).astype(int).tolist()
+    rt, rl, rs, rp, left, missing = U.plan(held, start, table, ids, len(ids), bs, start[-1])
+    assert not missing
+    slots, pos = [-1] * T, [0] * T
+    for n in range(N):
+        for k in range(news[n]):
+            slots[cu[n] + k], pos[cu[n] + k] = rs[start[n] + k], rp[start[n] + k]
+    lens = [max(cached[n], 0) if n in bad else rl[n] for n in range(N)]
+    t, st = i(table), i([0])
+    got = gdn.gdn_paged_plan(i(cached), i(cu), t, i(ids), i([len(ids)]), bs, T, dev_status=st)
+    assert int(st) & gdn.DEV_BAD_CU_SEQLENS
+    for a, b in zip(got, (lens, slots, pos, [left])):
+        assert a.cpu().tolist() == b
+    assert t.cpu().tolist() == rt
+
+
+@pytest.mark.parametrize("cached,cu,T,bad", [
+    ([0, -1, 0], [0, 4, 8, 12], 12, {1}), ([0, 9, -3], [0, 5, 8, 12], 12, {2}), ([-7, 2], [0, 3, 9], 9, {0}),
+    ([5, 2147483647, 3], [0, 4, 8, 12], 12, {1}),        # cached + new past int32
+    ([0, 0, 0, 6], [0, 4, -7, 4, 8], 8, {1, 2}),         # a negative offset between good ones
+    ([3, 1, 0, 0], [0, 4, 99, 4, 8], 8, {1, 2}),         # one past all tokens
+    ([0, 5, 0], [3, 6, 8, 11], 11, {0})])                # the first offset is not 0
+def test_plan_bad_requests_leave_the_others_alone(cached, cu, T, bad):
+    _plan_around(cached, cu, T, bad, 4, len(cu))
+
+
+@pytest.mark.parametrize("what", ["length", "offset"])
+def test_plan_bad_requests_among_many(what):
+    """Bad requests in the first, the middle and the last of three stretches of 1024 requests."""
+    r = np.random.RandomState(5)
+    N = 2500
+    cached, cu = r.randint(0, 40, N).tolist(), np.concatenate([[0], np.cumsum(r.randint(0, 4, N))]).astype(int).tolist()
+    T = cu[-1]
+    at = [1, 500, 1023, 1024, 1700, 2499] if what == "length" else [3, 1500]
+    bad = set()
+    for n in at:
+        if what == "length":
+            cached[n] = -1 - n
+            bad.add(n)
+        else:
+            cu[n] = -n
+            bad |= {n - 1, n}
+    _plan_around(cached, cu, T, bad, 16, 6)
+
