@@ -58,7 +58,7 @@ def gdn_norm_gate(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torc
                   y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None
                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """RMS norm with a gate and a scaled residual over the last dimension: h = residual + res_scale x (x alone without
-    one), y = h / sqrt(mean(h^2) + eps) * weight * act(z).
+    one, whatever res_scale is), y = h / sqrt(mean(h^2) + eps) * weight * act(z).
 
     x, residual bf16 [..., D]; weight fp32 [D]; z bf16 of x's shape, dense or with a longer stride between its tokens
     (a slice of a projection); activation 'silu' or 'sigmoid' (used where z is given).  Returns (y, h), h None
@@ -71,7 +71,8 @@ def gdn_norm_gate_bwd(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, z
                       workspace: Optional[torch.Tensor] = None):
     """Gradients of gdn_norm_gate: dy, h (what was normed) bf16 [..., D], dh the gradient that reaches h from its other
     uses (None without a residual).  Returns (dx, dresidual, dz, dweight): bf16 but the fp32 dweight [D]; dresidual
-    None without dh, dz None without z."""
+    None without dh, dz None without z.  dx is res_scale times the gradient of h whether dh is there or not; the form
+    without a residual, whose forward does not use res_scale, has its gradient with res_scale = 1."""
     return (_c or _load()).norm_gate_bwd(dy, h, weight, z, dh, _act_of(activation, "gdn_norm_gate_bwd"), eps, res_scale,
                                          workspace)
 
@@ -81,7 +82,8 @@ class _NormGate(torch.autograd.Function):
     def forward(ctx, x, weight, residual, z, activation, eps, res_scale):
         y, h = gdn_norm_gate(x, weight, residual=residual, z=z, activation=activation, eps=eps, res_scale=res_scale)
         ctx.save_for_backward(x if h is None else h, weight, z)
-        ctx.args = (activation, eps, res_scale, residual is not None)
+        # the forward scales x only where a residual is added to it
+        ctx.args = (activation, eps, 1.0 if residual is None else res_scale, residual is not None)
         return y if h is None else (y, h)
 
     @staticmethod

@@ -490,7 +490,7 @@ int gdn_conv_decode_pack(const uint16_t *mixed_qkv, uint16_t *conv_state, int P,
 /*
  * gdn_norm_gate -- RMS norm with a gate and a scaled residual, before or after
  * a block.  For every row of D elements:
- *     h = x                       (residual == NULL)
+ *     h = x                       (residual == NULL; res_scale is not used)
  *     h = residual + res_scale x  (stored to h, rounded to bf16; the norm uses
  *                                  the value before that rounding)
  *     y = h / sqrt(mean(h^2) + eps) * weight * act(z)
@@ -522,7 +522,8 @@ size_t gdn_norm_gate_bwd_workspace_size(int64_t rows, int D);
  *   dh             : bf16 [rows, D], the gradient that reaches h from its other
  *                    uses, or NULL (none; dresidual must then be NULL too)
  *   dx, dresidual  : bf16 [rows, D]; dx = res_scale dH and dresidual = dH, with
- *                    dH the gradient of h (dresidual NULL when dh is)
+ *                    dH the gradient of h (dresidual NULL when dh is).  The form
+ *                    without a residual (h = x) has its gradient with res_scale 1
  *   dz             : bf16 [rows, D], dense; required with a gate, else NULL
  *   dweight        : fp32 [D]
  *   workspace      : gdn_norm_gate_bwd_workspace_size() bytes, 16-byte aligned

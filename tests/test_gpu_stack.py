@@ -860,3 +860,23 @@ def test_plan_bad_requests_among_many(what):
             bad |= {n - 1, n}
     _plan_around(cached, cu, T, bad, 16, 6)
 
+
+# ---------------------------------------------------------- norm: its autograd entry
+def test_norm_gate_autograd_without_a_residual_ignores_its_scale():
+    """The forward without a residual does not use res_scale, and neither does its gradient."""
+    gdn, g = _gdn(), _gen(12)
+    x, z, dy = (torch.randn(7, 96, generator=g).to(BF) for _ in range(3))
+    w = 1 + 0.1 * torch.randn(96, generator=g)
+    leaves = [t.cuda().requires_grad_() for t in (x, w, z)]
+    y, h = gdn.norm_gate(leaves[0], leaves[1], z=leaves[2], res_scale=0.5)
+    assert h is None
+    _close_bf16(y, U.norm_fwd(U.f64(x), U.f64(w), None, U.f64(z), res_scale=0.5)[0], what="y")
+    dx, dw, dz = torch.autograd.grad(y, leaves, dy.cuda())
+    h64 = U.f64(x)
+    rx, _, rz, rw = U.norm_bwd(U.f64(dy), h64, U.f64(w), U.f64(z))
+    rstd = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + 1e-6)
+    _close_bf16(dx, rx, 2.0 ** -18 * rstd * np.abs(U.f64(dy)).max(-1, keepdims=True) * 4, what="dx")
+    _close_bf16(dz, rz, 2.0 ** -18 * np.abs(U.f64(dy) * h64 * rstd), what="dz")
+    mags = np.abs(U.f64(dy) * h64 * rstd * U.act(U.f64(z), "silu")[0]).sum(0)
+    assert (np.abs(U.f64(dw) - rw) <= 2.0 ** -19 * mags + 1e-30).all()
+
