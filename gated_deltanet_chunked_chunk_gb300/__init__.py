@@ -20,6 +20,7 @@ import threading
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 __all__ = ["gdn_gating", "gdn_chunk_fwd", "gdn_recurrent_decode", "chunk_fwd_workspace_size", "chunk_fwd_kernel_launches",
            "gdn_chunk_fwd_noalloc", "NOALLOC_SCRATCH_BYTES", "gdn_causal_conv1d_fwd",
@@ -678,6 +679,7 @@ class _ChunkGatedDeltaRule(torch.autograd.Function):
         return o, ht
 
     @staticmethod
+    @once_differentiable  # gdn_chunk_bwd has no gradient of its own: a second derivative is an error
     def backward(ctx, do, dht=None):
         q, k, v, g, beta, h0, cu = ctx.saved_tensors
         do = do.to(torch.bfloat16).contiguous()
@@ -698,7 +700,7 @@ def chunk_gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     qwen3.5", Usage section 1).  Returns (o, final_state) (final_state None
     unless ``output_final_state``); autograd runs gdn_chunk_bwd and yields
     gradients for q, k, v (in their bf16 dtype), g, beta and initial_state
-    (fp32)."""
+    (fp32), once: a second derivative raises."""
     out = _ChunkGatedDeltaRule.apply(q, k, v, g, beta, initial_state, scale, output_final_state, cu_seqlens,
                                      use_qk_l2norm_in_kernel, num_seqs)
     if isinstance(out, tuple):

@@ -13,6 +13,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import GDNError, lib_path, load_library
 
@@ -87,6 +88,7 @@ class _NormGate(torch.autograd.Function):
         return y if h is None else (y, h)
 
     @staticmethod
+    @once_differentiable  # the gradient kernels have no gradient of their own: a second derivative is an error
     def backward(ctx, dy, dh=None):
         h, weight, z = ctx.saved_tensors
         activation, eps, res_scale, has_res = ctx.args
@@ -98,7 +100,7 @@ class _NormGate(torch.autograd.Function):
 
 
 def norm_gate(x, weight, residual=None, z=None, activation="silu", eps: float = 1e-6, res_scale: float = 1.0):
-    """Differentiable gdn_norm_gate: returns (y, h), h None without a residual; gradients for x, weight, residual, z."""
+    """Differentiable (once) gdn_norm_gate: returns (y, h), h None without a residual; gradients for x, weight, residual, z."""
     out = _NormGate.apply(x, weight, residual, z, activation, eps, res_scale)
     return out if isinstance(out, tuple) else (out, None)
 
@@ -156,6 +158,7 @@ class _Rotary(torch.autograd.Function):
         return gdn_rope(q, k, positions, inv_freq, interleaved=interleaved, attention_factor=attention_factor)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         positions, inv_freq = ctx.saved_tensors
         interleaved, factor = ctx.args
@@ -166,7 +169,7 @@ class _Rotary(torch.autograd.Function):
 
 
 def rotary_embedding(q, k, positions, inv_freq, interleaved: bool = False, attention_factor: float = 1.0):
-    """Differentiable gdn_rope of q and k (k may be None)."""
+    """Differentiable (once) gdn_rope of q and k (k may be None)."""
     return _Rotary.apply(q, k, positions, inv_freq, interleaved, attention_factor)
 
 

@@ -880,3 +880,28 @@ def test_norm_gate_autograd_without_a_residual_ignores_its_scale():
     mags = np.abs(U.f64(dy) * h64 * rstd * U.act(U.f64(z), "silu")[0]).sum(0)
     assert (np.abs(U.f64(dw) - rw) <= 2.0 ** -19 * mags + 1e-30).all()
 
+
+# ------------------------------------------------------------- second derivatives
+@pytest.mark.parametrize("entry", ["norm_gate", "rotary_embedding", "chunk_gated_delta_rule"])
+def test_second_derivatives_are_refused(entry):
+    """The gradients come from kernels that have none of their own: with another differentiable path beside them the
+    second derivative would miss a term, so it raises.  First derivatives with create_graph stay what they are."""
+    gdn, g = _gdn(), _gen(13)
+    x = torch.randn(1, 8, 2, 64, generator=g).to(BF).cuda().requires_grad_()
+    if entry == "norm_gate":
+        w = torch.ones(64, device="cuda")
+        call = lambda: gdn.norm_gate(x, w)[0]
+    elif entry == "rotary_embedding":
+        inv, _ = gdn.rope_frequencies(64, device="cuda")
+        pos = torch.arange(8, dtype=torch.int32, device="cuda")
+        call = lambda: gdn.rotary_embedding(x[0], None, pos, inv)[0]
+    else:
+        gates = torch.rand(1, 8, 2, generator=g).cuda()
+        k = torch.randn(1, 8, 2, 64, generator=g).to(BF).cuda()
+        call = lambda: gdn.chunk_gated_delta_rule(x, k, k, -gates, gates, output_final_state=False)[0]
+    (plain,) = torch.autograd.grad(call().float().square().sum(), x)
+    (dx,) = torch.autograd.grad(call().float().square().sum(), x, create_graph=True)
+    assert torch.equal(dx, plain)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (dx.float().square().sum() + x.float().square().sum()).backward()
+
