@@ -23,10 +23,12 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return e < kExpMin ? kExpMin : e;
 }
-// Exponent of a scale that an append wrote (a power of two).
-__device__ __forceinline__ int exponent_of(float scale) {
-  const int e = (int)((__float_as_uint(scale) >> 23) & 0xffu) - 127;
-  return e < kExpMin ? kExpMin : e > 120 ? 120 : e;
+// Least exponent e, -60 to 126, with 2^e not below a scale; for those that an append
+// wrote (powers of two) the scale is 2^e.
+__device__ __forceinline__ int exponent_over(float scale) {
+  const uint32_t u = __float_as_uint(scale) & 0x7fffffffu;
+  const int e = (int)(u >> 23) - 127 + ((u & 0x7fffffu) ? 1 : 0);
+  return e < kExpMin ? kExpMin : e > 126 ? 126 : e;
 }
 
 // Two numbers rounded to e4m3 (to nearest, ties to even; beyond 448, and

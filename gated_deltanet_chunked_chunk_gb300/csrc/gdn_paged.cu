@@ -257,12 +257,12 @@ __device__ __forceinline__ void write_run(const AppendArgs &a, int kv, int h, in
   }
   int e = gdnkv::scale_exponent(amax);
   if (off > 0) {
-    const int old = gdnkv::exponent_of(before);
-    if (old >= e) {
-      e = old;
-    } else {
-      // older codes move to the larger scale, rounded to the format again
-      const float f = gdnkv::pow2(max(old - e, -126));
+    // The page's scale does not fall.  Older codes move to the new one, rounded to
+    // the format again, where it is another: a larger power of two, or the page came
+    // with a scale that is none.
+    e = max(e, gdnkv::exponent_over(before));
+    const float f = before * gdnkv::pow2(-e);  // in [0, 1]; up to 4 where 2^126 is the most that e can be
+    if (f != 1.f) {
       if (a.D % 4 == 0 && (reinterpret_cast<uintptr_t>(codes) & 3) == 0) {  // four at once where their address allows
         uint32_t *p = reinterpret_cast<uint32_t *>(codes);
         for (int i = tid; i < off * a.D / 4; i += TH) p[i] = gdnkv::rescale4(p[i], f);

@@ -585,13 +585,15 @@ int gdn_paged_plan(const int32_t *cached_lens, const int32_t *cu_seqlens, int N,
 /*
  * The paged 8-bit cache.  k_cache, v_cache: e4m3 codes [P, HK, page_size, D];
  * k_scale, v_scale: fp32 [P, HK]; value = code * scale.  gdn_kv8_append writes
- * scales that are powers of two; the attention takes any positive ones.
+ * scales that are powers of two and moves a page that came with another one to
+ * such a scale; the attention takes any positive finite ones.
  *
  * gdn_kv8_append -- the write of new keys and values.  For each page and head
  * that a call writes to:
  *     e     = the least exponent >= -60 with every finite new |x| <= 448 2^e, and,
- *             where the page holds earlier tokens, not below its present one
- *     codes = earlier codes 2^(e_before - e), new x 2^-e, rounded to e4m3 (to
+ *             where the page holds earlier tokens, 2^e not below its present scale
+ *             (e is at most 126)
+ *     codes = earlier codes (scale before) 2^-e, new x 2^-e, rounded to e4m3 (to
  *             nearest, ties to even; infinities become +-448, NaN stays NaN)
  *     scale = 2^e
  * A write to place 0 begins the page anew: what it held does not count.

@@ -905,3 +905,35 @@ def test_second_derivatives_are_refused(entry):
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (dx.float().square().sum() + x.float().square().sum()).backward()
 
+
+@pytest.mark.parametrize("D,bs", [(64, 16), (10, 5)])
+def test_append_to_pages_whose_scale_is_no_power_of_two(D, bs):
+    """Pages from elsewhere: their older tokens keep their values, rounded once to the page's new scale, whether that
+    scale comes from the old one (small new tokens) or from the new tokens (large ones)."""
+    gdn, g = _gdn(), _gen(90 + D)
+    # few significant bits, so that a code times such a scale is exact in fp32
+    before = torch.tensor([0.75, 1.25, 1.9375 * 2.0 ** -30, 1.5 * 2.0 ** -70, 2.0 ** -100, 3.0, 2.0 ** 122, 0.0, 0.25])
+    P = len(before)
+    codes = (60 * torch.randn(P, 1, bs, D, generator=g)).to(torch.float8_e4m3fn)
+    ks = before[:, None].clone()
+    x = torch.randn(2 * P, 1, D, generator=g)
+    x[1::2] *= 3000.0
+    for n, rows in enumerate((x[::2].to(BF), x[1::2].to(BF))):
+        off = 2 + n
+        slots = [p * bs + off for p in range(P)]
+        dev = [codes.cuda(), codes.clone().cuda(), ks.cuda(), ks.clone().cuda()]
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        gdn.gdn_kv8_append(rows.cuda(), rows.cuda(), *dev, torch.tensor(slots, dtype=torch.int32, device="cuda"), dev_status=st)
+        assert int(st) == 0
+        rc, rs = U.f64(codes.float()), U.f64(ks)
+        for p in range(P):
+            s = float(before[p])
+            m, e = math.frexp(s)
+            over = U.EXP_MIN if s == 0 else max(U.EXP_MIN, e - 1 if m == 0.5 else e)
+            e = max(over, U.least_exponent(float(rows[p].float().abs().max())))
+            rc[p, 0, :off] = U.to_e4m3(rc[p, 0, :off] * s * 2.0 ** -e)
+            rc[p, 0, off] = U.to_e4m3(U.f64(rows[p, 0]) * 2.0 ** -e)
+            rs[p, 0] = 2.0 ** e
+        for d, sc in ((dev[0], dev[2]), (dev[1], dev[3])):
+            _same_cache(d, sc, (rc, rs))
+
