@@ -286,9 +286,9 @@ int gdn_norm_gate(const uint16_t *x, const uint16_t *residual, const uint16_t *z
                   float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride, uint16_t *y,
                   uint16_t *h, void *stream) {
   if (rows < 0 || D <= 0 || activation < 0 || activation > 2 || !(eps >= 0.f)) return GDN_EINVAL;
+  if (rows == 0) return GDN_OK;  // before the pointers: those of empty tensors are null
   if ((activation != 0) != (z != nullptr) || (residual != nullptr) != (h != nullptr)) return GDN_EINVAL;
   if (z && z_rows < 0) return GDN_EINVAL;
-  if (rows == 0) return GDN_OK;
   if (!x || !weight || !y) return GDN_EINVAL;
   if (z_rows == 0) z_stride = 0;
   return cuda_status(gdn_host::launch_norm_fwd(x, residual, z, weight, res_scale, eps, activation, rows, D, z_rows, z_stride,
@@ -304,9 +304,11 @@ int gdn_norm_gate_bwd(const uint16_t *dy, const uint16_t *h, const uint16_t *z, 
                       uint16_t *dx, uint16_t *dresidual, uint16_t *dz, float *dweight, void *workspace,
                       size_t workspace_bytes, void *stream) {
   if (rows < 0 || D <= 0 || activation < 0 || activation > 2 || !(eps >= 0.f)) return GDN_EINVAL;
-  if ((activation != 0) != (dz != nullptr) || (dh != nullptr) != (dresidual != nullptr) || !dweight) return GDN_EINVAL;
-  if (z && z_rows < 0) return GDN_EINVAL;
-  if (rows > 0 && ((activation != 0) != (z != nullptr) || !dy || !h || !weight || !dx)) return GDN_EINVAL;
+  if (!dweight) return GDN_EINVAL;
+  if (rows > 0) {  // the pointers of empty tensors are null
+    if ((activation != 0) != (z != nullptr) || (activation != 0) != (dz != nullptr)) return GDN_EINVAL;
+    if ((dh != nullptr) != (dresidual != nullptr) || !dy || !h || !weight || !dx || (z && z_rows < 0)) return GDN_EINVAL;
+  }
   const size_t need = gdn_host::norm_bwd_workspace_bytes(rows, D);
   if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
   if (!aligned16({workspace})) return GDN_EINVAL;

@@ -937,3 +937,15 @@ def test_append_to_pages_whose_scale_is_no_power_of_two(D, bs):
         for d, sc in ((dev[0], dev[2]), (dev[1], dev[3])):
             _same_cache(d, sc, (rc, rs))
 
+
+@pytest.mark.parametrize("kind", ["silu", "sigmoid"])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_gate_and_gradients_of_an_empty_batch(kind, res):
+    gdn = _gdn()
+    e, w = torch.empty(0, 2, 64, dtype=BF, device="cuda"), torch.ones(64, device="cuda")
+    leaves = [t.clone().requires_grad_() for t in (e, w, e)] + ([e.clone().requires_grad_()] if res else [])
+    y, h = gdn.norm_gate(leaves[0], leaves[1], z=leaves[2], residual=leaves[3] if res else None, activation=kind)
+    assert y.shape == e.shape and (h.shape == e.shape if res else h is None)
+    grads = torch.autograd.grad([y, h] if res else y, leaves, [e, e] if res else e)
+    assert [g.shape for g in grads] == [t.shape for t in leaves] and (grads[1] == 0).all()
+

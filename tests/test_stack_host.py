@@ -46,6 +46,12 @@ def test_norm_gate_without_rows(lib):
     assert _norm(lib, rows=0, x=None, weight=None, y=None) == gdn.GDN_OK
 
 
+@pytest.mark.parametrize("kw", [dict(activation=1), dict(activation=2, residual=None, h=None), dict(residual=F), dict(h=F)])
+def test_norm_gate_of_an_empty_batch(lib, kw):
+    """Empty tensors have null pointers: a call without rows does nothing, whatever it would do with some."""
+    assert _norm(lib, rows=0, x=None, y=None, **kw) == gdn.GDN_OK
+
+
 NORM_B = ("dy h z dh weight res_scale eps activation rows D z_rows z_stride dx dresidual dz dweight workspace workspace_bytes "
           "stream")
 
