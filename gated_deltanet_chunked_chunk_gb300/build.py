@@ -49,12 +49,17 @@ def _built_for() -> str:
     return f"{sys.version} {torch.__version__} {torch.__file__}"
 
 
-def up_to_date() -> bool:
-    if not all(os.path.exists(p) for p in (LIB, BINDING, STAMP)):
+def binding_fits() -> bool:
+    """Whether the binding was built for the running interpreter and PyTorch."""
+    if not os.path.exists(STAMP):
         return False
     with open(STAMP) as f:
-        if f.read() != _built_for():
-            return False
+        return f.read() == _built_for()
+
+
+def up_to_date() -> bool:
+    if not (os.path.exists(LIB) and os.path.exists(BINDING) and binding_fits()):
+        return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
@@ -120,9 +125,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(STAMP):  # from here on it is another binding's
+        os.remove(STAMP)
     os.replace(tmp, BINDING)
-    with open(STAMP, "w") as f:
+    with open(tmp, "w") as f:
         f.write(_built_for())
+    os.replace(tmp, STAMP)
     return LIB
 
 

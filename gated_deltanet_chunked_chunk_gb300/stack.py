@@ -31,12 +31,17 @@ _c = None
 
 
 def _load():
-    """The compiled binding (built by ``build.py``); raises if it is missing."""
+    """The compiled binding (built by ``build.py``); raises if it is missing or was built for another interpreter or
+    PyTorch, whose tensors it would misread."""
     global _c
+    from . import build
     load_library()
     path = os.path.join(os.path.dirname(lib_path()), "_gdn_torch.so")
     if not os.path.exists(path):
         raise RuntimeError(f"_gdn_torch.so not found at {path}; build it first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')")
+    if not build.binding_fits():
+        raise RuntimeError(f"{path} was built for another interpreter or PyTorch than the running one; build it again "
                            "(python -c 'import __graft_entry__ as g; g.build()')")
     loader = importlib.machinery.ExtensionFileLoader(__package__ + "._gdn_torch", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(loader.name, path, loader=loader))

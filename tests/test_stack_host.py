@@ -214,6 +214,19 @@ def test_python_entries_refuse_what_is_no_tensor_and_unknown_names(lib):
         gdn.gdn_norm_gate_bwd(x, x, torch.ones(64), activation=7)
 
 
+@pytest.mark.parametrize("stamp", ["another interpreter and PyTorch", None])
+def test_binding_built_for_another_pytorch_is_refused(lib, tmp_path, monkeypatch, stamp):
+    from gated_deltanet_chunked_chunk_gb300 import stack
+    assert stack._load() is not None
+    if stamp is not None:
+        (tmp_path / "for").write_text(stamp)
+    monkeypatch.setattr(gbuild, "STAMP", str(tmp_path / "for"))
+    assert not gbuild.up_to_date()
+    monkeypatch.setattr(stack, "_c", None)
+    with pytest.raises(RuntimeError, match="build it again"):
+        gdn.gdn_norm_gate(torch.zeros(3, 64, dtype=BF), torch.ones(64))
+
+
 # --------------------------------------------------------- rotary frequencies
 def test_rope_frequencies_formulas():
     inv, att = gdn.rope_frequencies(128, 10000.0)
