@@ -113,12 +113,12 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
             page = *entry;
           } else {
             const int32_t at = left - 1 - (s_before[lo] + pg - have);
-            if (at >= 0) page = free_pages[at];
-            else bits |= GDN_DEV_NO_PAGE;
+            if (at >= 0) page = max(free_pages[at], -1);
             if (off == 0) *entry = page;
           }
         }
         if (page >= 0) slot = page * bs + off;
+        else bits |= GDN_DEV_NO_PAGE;
       }
     }
     base += all;

@@ -63,7 +63,8 @@ enum gdn_device_status_bits {
                                  of that block may still have been written after
                                  it exited; treat the context as suspect */
   GDN_DEV_NO_PAGE = 16,       /* gdn_paged_plan: the free list, or a table row, is too
-                                 short; the tokens left out have slot -1 */
+                                 short, or an entry that is needed is negative; the
+                                 tokens left out have slot -1 */
   GDN_DEV_BAD_SEQ_LEN = 32    /* a context length < 0 or > max_seq_len (request skipped) */
 };
 
@@ -571,7 +572,9 @@ int gdn_rope(const uint16_t *q, const uint16_t *k, const int32_t *positions, con
  *   positions     : int32 [T]   place in the request's context (0 without a request)
  *   num_free_out  : int32 [1]   pages left; another address than num_free
  * No input but the table is written, so a call can be repeated.  Too few free
- * pages, or a row too short: table entry and slots -1, GDN_DEV_NO_PAGE.  Offsets
+ * pages, or a row too short: table entry and slots -1, GDN_DEV_NO_PAGE; the same
+ * bit where a new token's place is on a page that the request keeps and whose
+ * entry is negative (a step before was short of it).  Offsets
  * that break the rules, negative lengths and sums past int32:
  * GDN_DEV_BAD_CU_SEQLENS, the request counts as having no new tokens, the
  * others get theirs.  Slots must fit int32 (caller's

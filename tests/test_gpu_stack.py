@@ -949,3 +949,17 @@ def test_norm_gate_and_gradients_of_an_empty_batch(kind, res):
     grads = torch.autograd.grad([y, h] if res else y, leaves, [e, e] if res else e)
     assert [g.shape for g in grads] == [t.shape for t in leaves] and (grads[1] == 0).all()
 
+
+def test_plan_reports_tokens_on_a_page_that_an_earlier_step_did_not_get():
+    """A step that runs out of pages says so, and so does the next one, whose tokens fall on the missing page."""
+    gdn = _gdn()
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    t, st = i([[-1, -1], [4, -1]]), i([0])
+    cu = i([0, 3, 4])
+    lens, slots, pos, left = gdn.gdn_paged_plan(i([0, 1]), cu, t, i([9]), i([0]), 16, 4, dev_status=st)
+    assert int(st) == gdn.DEV_NO_PAGE and slots.tolist() == [-1, -1, -1, 4 * 16 + 1]
+    st.zero_()
+    lens, slots, pos, left = gdn.gdn_paged_plan(lens, cu, t, i([9]), i([1]), 16, 4, dev_status=st)
+    assert int(st) == gdn.DEV_NO_PAGE and slots.tolist() == [-1, -1, -1, 4 * 16 + 2] and pos.tolist() == [3, 4, 5, 2]
+    assert t.tolist() == [[-1, -1], [4, -1]] and left.tolist() == [1]
+
