@@ -351,6 +351,7 @@ int gdn_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ld
   if (T < 0 || P <= 0 || HK <= 0 || D <= 0 || page_size <= 0) return GDN_EINVAL;
   if (ldk < (int64_t)HK * D || ldv < (int64_t)HK * D || (int64_t)P * page_size > 2147483647LL) return GDN_EINVAL;
   if (HK > 32767) return GDN_EUNSUPPORTED;  // heads index the grid's y dimension
+  if ((int64_t)page_size * D > 2147483647LL) return GDN_EUNSUPPORTED;  // places in a page are 32-bit
   if (T == 0) return GDN_OK;
   if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !slot_mapping) return GDN_EINVAL;
   return cuda_status(gdn_host::launch_kv8_append(k, v, ldk, ldv, k_cache, v_cache, k_scale, v_scale, slot_mapping, T, P, HK,

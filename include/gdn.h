@@ -607,7 +607,7 @@ int gdn_paged_plan(const int32_t *cached_lens, const int32_t *cu_seqlens, int N,
  *                   the order of their places, and must not belong to two runs.
  * Codes past a page's last token are left as they were.  T = 0 is a no-op.  One
  * launch.  GDN_EINVAL: null pointers, sizes <= 0, strides below a token's width;
- * GDN_EUNSUPPORTED: HK > 32767.
+ * GDN_EUNSUPPORTED: HK > 32767, page_size x D past int32.
  */
 int gdn_kv8_append(const uint16_t *k, const uint16_t *v, int64_t ldk, int64_t ldv, uint8_t *k_cache, uint8_t *v_cache,
                    float *k_scale, float *v_scale, const int32_t *slot_mapping, int64_t T, int P, int HK, int D,

@@ -137,6 +137,11 @@ def test_kv8_append_limits(lib):
     assert _append(lib, T=0, k=None, v=None) == gdn.GDN_OK
 
 
+def test_kv8_append_page_past_32_bits(lib):
+    """A page's values of one head are counted in 32 bits (nothing is launched: the call is refused)."""
+    assert _append(lib, P=1, HK=1, page_size=1 << 20, D=4096, ldk=4096, ldv=4096) == gdn.GDN_EUNSUPPORTED
+
+
 ATTN = ("q ldq k_cache v_cache k_scale v_scale block_table width seq_lens cu_seqlens N T P HQ HK D page_size max_q_len "
         "max_seq_len scale o lse workspace workspace_bytes dev_status stream")
 
