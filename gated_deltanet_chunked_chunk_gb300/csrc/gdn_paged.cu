@@ -172,6 +172,17 @@ __device__ __forceinline__ int32_t slot_of(const AppendArgs &a, int64_t t, int &
   if (s != -1) bits |= GDN_DEV_BAD_SLOT;
   return -1;
 }
+// For every lane's token t, whose place is s: the place of the last token before it
+// that has one, of those up to 32 before the warp's first; -1: none has.
+__device__ __forceinline__ int32_t last_before(const AppendArgs &a, int64_t t, int32_t s) {
+  const int lane = threadIdx.x & 31;
+  int ignore = 0;
+  const int32_t behind = slot_of(a, t - 32, ignore);
+  const uint32_t here = __ballot_sync(0xffffffffu, s >= 0) & ((1u << lane) - 1), there = __ballot_sync(0xffffffffu, behind >= 0);
+  const int32_t near = __shfl_sync(0xffffffffu, s, here ? 31 - __clz((int)here) : 0);
+  const int32_t far = __shfl_sync(0xffffffffu, behind, there ? 31 - __clz((int)there) : 0);
+  return here ? near : far;
+}
 __device__ __forceinline__ float finite_abs(float x) {
   x = fabsf(x);
   return x <= 3.402823466e38f ? x : 0.f;  // infinities and NaN do not set a scale
@@ -306,7 +317,7 @@ __device__ __forceinline__ void write_run(const AppendArgs &a, int kv, int h, in
 // a wider group finds the runs for itself, all alike.  Short runs (a large
 // decode step's) go to the warps in turn, long ones to all of them.
 template <int WARPS, int NV, bool VEC>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) kv8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS, NV == 8 ? 5 : 0) kv8_append_kernel(const AppendArgs a) {
   __shared__ float sh[WARPS];
   gdn::grid_release();
   gdn::grid_wait();
@@ -321,9 +332,20 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) kv8_append_kern
     const int32_t s = slot_of(a, t, t < t1 ? bits : ignore);
     int32_t prev = __shfl_up_sync(0xffffffffu, s, 1);
     if (lane == 0) prev = slot_of(a, t - 1, ignore);
-    const bool follows = s >= 0 && prev >= 0 && s == prev + 1 && place_of(a, s) != 0;
+    const bool same = s >= 0 && prev >= 0 && page_of(a, prev) == page_of(a, s), follows = same && s == prev + 1;
     const uint32_t cont = __ballot_sync(0xffffffffu, follows);
-    uint32_t lead = __ballot_sync(0xffffffffu, t < t1 && s >= 0 && !follows);
+    bool begins = t < t1 && s >= 0 && !follows;
+    // A second run of a page would race with the first for its scale: where the last
+    // token with a place is that page's, it is left out and reported.  That token is
+    // mostly the one before; behind skipped ones it is looked for, 32 places back.
+    if (__any_sync(0xffffffffu, begins && (same || (prev < 0 && t > 0)))) {
+      const int32_t last = last_before(a, t, s);
+      if (begins && last >= 0 && page_of(a, last) == page_of(a, s)) {
+        begins = false;
+        bits |= GDN_DEV_BAD_SLOT;
+      }
+    }
+    uint32_t lead = __ballot_sync(0xffffffffu, begins);
     while (lead) {
       const int p = __ffs((int)lead) - 1;
       lead &= lead - 1;

@@ -604,7 +604,11 @@ int gdn_paged_plan(const int32_t *cached_lens, const int32_t *cu_seqlens, int N,
  *   slot_mapping  : int32 [T] as gdn_paged_plan writes it; -1 skips the token,
  *                   others outside [0, P page_size) set GDN_DEV_BAD_SLOT and are
  *                   skipped.  The tokens of one page must be consecutive and in
- *                   the order of their places, and must not belong to two runs.
+ *                   the order of their places, and must not belong to two runs: a
+ *                   skipped token, a hole or a repeated place within them begins
+ *                   a second one.  That run is not written and sets
+ *                   GDN_DEV_BAD_SLOT where only skipped tokens, 31 at most, stand
+ *                   between the two; otherwise the page's result is undefined.
  * Codes past a page's last token are left as they were.  T = 0 is a no-op.  One
  * launch.  GDN_EINVAL: null pointers, sizes <= 0, strides below a token's width;
  * GDN_EUNSUPPORTED: HK > 32767, page_size x D past int32.

@@ -963,3 +963,28 @@ def test_plan_reports_tokens_on_a_page_that_an_earlier_step_did_not_get():
     assert int(st) == gdn.DEV_NO_PAGE and slots.tolist() == [-1, -1, -1, 4 * 16 + 2] and pos.tolist() == [3, 4, 5, 2]
     assert t.tolist() == [[-1, -1], [4, -1]] and left.tolist() == [1]
 
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("places", [[3, -1, 4], [3, 3], [4, 3], [15, 0], [3] + 31 * [-1] + [4], [3, 5], [3, -1, 4, 5, -1, 6]])
+def test_append_leaves_out_a_second_run_of_a_page(places, many):
+    """A rejected token in the middle of a draft, a hole, a repeated place: the first run is written, the rest is left out
+    and reported; other pages get theirs.  `many`: enough tokens for blocks of four warps."""
+    gdn, g = _gdn(), _gen(len(places))
+    bs, D, H, lead = 16, 64, 8 if many else 2, 900 if many else 2
+    P = -(-lead // bs) + 3
+    slots = list(range(lead)) + [(P - 2) * bs + p if p >= 0 else -1 for p in places] + [(P - 1) * bs + 7, (P - 1) * bs + 8]
+    first = 1
+    while first < len(places) and places[first] == places[0] + first and places[first]:
+        first += 1
+    kept = list(slots)
+    kept[lead + first:lead + len(places)] = [-1] * (len(places) - first)
+    kc, ks = U.make_cache(P, H, bs, D, g)
+    x = (3 * torch.randn(len(slots), H, D, generator=g)).to(BF)
+    dev = [t.cuda() for t in (kc, kc.clone(), ks, ks.clone())]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_kv8_append(x.cuda(), x.cuda(), *dev, torch.tensor(slots, dtype=torch.int32, device="cuda"), dev_status=st)
+    assert int(st) == gdn.DEV_BAD_SLOT
+    ref = U.append(U.f64(x), U.f64(kc.float()), U.f64(ks), kept)
+    _same_cache(dev[0], dev[2], ref)
+    _same_cache(dev[1], dev[3], ref)
+
