@@ -9,12 +9,13 @@
 // the exponent: with lv = log2(v scale) the kernel forms
 //   t_ij = log2(e) scale ks (q_i . kcode_j) + lv,   p'_ij = 2^(t_ij - m_i),
 //   O_i = sum_j p'_ij vcode_j,   l_i = sum_j p'_ij 2^-lv
-// with m_i the running maximum of t.  So p' is in [0, 1] whatever the scales
-// are, codes enter the products as they are (e4m3 is exact in f16), and o = O /
-// l, logsumexp = (m + log2 l) ln 2.  Maxima, sums and accumulators are fp32.  p'
-// rounds to f16 (11 bits); q, brought to a largest magnitude of 1 to 2 by a
-// power of two for each row, loses nothing there (bf16 has 8 bits) but elements
-// under 2^-24 of the row's largest.
+// with m_i the running maximum of t less 13.  So p' is at most 2^13 whatever the
+// scales are, codes enter the products as they are (e4m3 is exact in f16), and o =
+// O / l, logsumexp = (m + log2 l) ln 2.  Maxima, sums and accumulators are fp32.
+// p' rounds to f16: 11 bits down to 2^-27 of the row's largest weight, steps of
+// 2^-37 of it below that (p' of at most 1 would lose all weights under 2^-25).  q,
+// brought to a largest magnitude of 1 to 2 by a power of two for each row, loses
+// nothing there (bf16 has 8 bits) but elements under 2^-24 of the row's largest.
 //
 // Bound: HBM, 2 D bytes for each (token, kv head), read once for all the query
 // rows of the head's group.
@@ -56,6 +57,7 @@ using namespace gdn;
 using namespace gdnkv;
 
 constexpr int kKeys = 64;         // keys a stage
+constexpr float kLift = 13.f;     // exponent of a row's largest weight
 
 // D: head size; NT: tiles of 8 rows a team.
 template <int D, int NT>
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(32, DecodeLay<D, NT>::PER_SM)
             float x0 = -INFINITY;
 #pragma unroll
             for (int x = 0; x < NK; ++x) x0 = fmaxf(x0, fmaxf(p[x][nt][e], p[x][nt][2 + e]));
-            const float now = fmaxf(mx[nt][e], keys_max(x0));
+            const float now = fmaxf(mx[nt][e], reference_of(keys_max(x0), kLift));
             base[nt][e] = now == -INFINITY ? 0.f : now;
             down[nt][e] = ex2f(mx[nt][e] - base[nt][e]);
             moved |= now != mx[nt][e];

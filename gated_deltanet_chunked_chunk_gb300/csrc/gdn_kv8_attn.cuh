@@ -19,6 +19,15 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2f(float x) { return gdnc::ex2(x); }
 
+// What a row's exponents are taken against when `top` is the largest of them: `lift`
+// below it, so that its weight is 2^lift and one of f16 still has a bit at 2^-24.
+// `lift` is at most 15 (2^16 is past f16), and exponents so large that their difference
+// rounds to more have top itself.
+__device__ __forceinline__ float reference_of(float top, float lift) {
+  const float r = top - lift;
+  return top - r > 15.f ? top : r;
+}
+
 // Whether any of four codes is NaN (0x7f or 0xff).
 __device__ __forceinline__ uint32_t any_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t drop_nan(uint32_t w) {

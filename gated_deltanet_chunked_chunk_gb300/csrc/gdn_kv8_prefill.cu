@@ -23,8 +23,9 @@
 // memory (512 columns): S of both tiles, P in place of its S, O of both tiles.
 // An S of the next key tile is issued right after the P V that last read its
 // columns; products of one thread execute in order, so "S is there" also says
-// that O may be touched.  O is rescaled only when the running maximum grew by
-// more than 8 (p' <= 256 is safe in f16), by the softmax warps themselves.
+// that O may be touched.  A row's reference is taken 11 under its maximum, so that f16
+// holds weights down to 2^-35 of the largest, and O is rescaled, by the softmax warps
+// themselves, only when an exponent is more than 15 above it (p' <= 2^15 is safe in f16).
 //
 // The last items, where they do not come out even with the SMs, are cut along
 // their keys (find_work).  4096 tokens over 16384 keys, 32 heads of 128, 4 kv
@@ -57,6 +58,7 @@ constexpr int kPrefThreads = 512;
 constexpr int kItemRows = 256;
 constexpr int kSlots = kSMs;    // partial results, one for each SM
 constexpr int kPieceTiles = 8;  // key tiles that a piece of an item has at least
+constexpr float kLift = 11.f, kMost = 15.f;  // exponents of a new maximum, and the largest
 constexpr int kParSlots = 8;  // key tiles whose page constants are kept: more than can be in flight
 
 template <int D>
@@ -324,9 +326,10 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
         }
       }
       float grow = 1.f;
-      if (top > m_ref + 8.f || (m_ref == -INFINITY && top > -INFINITY)) {
-        grow = ex2f(m_ref - top);
-        m_ref = top;
+      if (top - m_ref > kMost) {  // (of -inf both, NaN: no)
+        const float now = reference_of(top, kLift);
+        grow = ex2f(m_ref - now);
+        m_ref = now;
         l_sum *= grow;
       }
       if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {

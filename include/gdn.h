@@ -632,8 +632,9 @@ size_t gdn_kv8_attention_workspace_size(int N, int T, int HQ, int HK, int D, int
  * arguments agree bit for bit; where a context is cut between blocks depends on
  * the lengths of the whole batch, so in another batch a request's last bits can
  * differ.  A row's weights (softmax weight x page scale of the value) enter the
- * products with 11 bits, those under 2^-14 of the largest with the absolute
- * precision 2^-25 of it; sums and maxima are fp32.
+ * products with 11 bits, those under 2^-18 of the largest with the absolute
+ * precision 2^-29 of it (2^-36 but for calls of 17 to 32 rows a request); sums and
+ * maxima are fp32.
  *   q             : bf16 [T, HQ, D], ldq elements between tokens; query head h
  *                   reads kv head h / (HQ / HK)
  *   block_table   : int32 [N, width]; a needed entry outside [0, P) sets

@@ -988,3 +988,34 @@ def test_append_leaves_out_a_second_run_of_a_page(places, many):
     _same_cache(dev[0], dev[2], ref)
     _same_cache(dev[1], dev[3], ref)
 
+
+# --------------------------------------------------------- attention: far weights
+@pytest.mark.parametrize("G,D,N,news,ctx", [(8, 128, 700, 1, 3000), (16, 64, 700, 1, 3000), (8, 128, 1, 70, 3000), (8, 64, 1, 70, 3000),
+                                            (8, 128, 160, 4, 3000)])
+@pytest.mark.parametrize("bits", [20.0, 25.1, 28.0])
+def test_attention_of_a_key_far_above_all_others(G, D, N, news, ctx, bits):
+    """A key at the context's beginning whose weight is 2^bits of the others' and whose value is 0: the result is the
+    others' mean times their mass.  700 requests (of the same pages), so that a team has many stages of one context.
+    Beside the bound of the other tests a weight may be off by 2^-36 of the largest (17 to 32 rows a request: 2^-29)."""
+    c = _attn_case(1, G, D, 64, [ctx], [news], 5, spread=0.0)
+    c["kc"].view(torch.uint8).zero_()
+    c["vc"].view(torch.uint8).bitwise_and_(0x7f)  # values of one sign, which do not cancel
+    q = torch.zeros_like(c["q"].float())
+    q[..., 0] = 1.0
+    c["q"] = q.to(BF)
+    page = c["table"][0][0]
+    c["kc"].view(torch.uint8)[page, 0, 20, 0] = torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    c["vc"].view(torch.uint8)[page, 0, 20] = 0
+    scale = bits / math.log2(math.e) / float(c["ks"][page, 0])
+    args = [U.f64(c[k].float() if k in ("kc", "vc") else c[k]) for k in ("q", "kc", "vc", "ks", "vs")]
+    ref, rl, mag = U.attention(*args, c["table"], c["lens"], c["cu"], scale)
+    v = np.concatenate([args[2][p, 0] * args[4][p, 0] for p in c["table"][0][:-(-ctx // 64)]])[:ctx]
+    c["table"], c["lens"], c["q"] = c["table"] * N, c["lens"] * N, c["q"].repeat(N, 1, 1)
+    c["cu"] = [news * n for n in range(N + 1)]
+    o, lse, st = _attn_run(c, scale=scale)
+    assert st == 0
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + 2.0 ** (-29 if 16 < news * G <= 32 else -36) * np.abs(v).sum(0)
+    off = np.abs(U.f64(o).reshape(N, *ref.shape) - ref)
+    assert (off <= tol).all(), f"worst {(off / np.abs(ref)).max():.3f} of the value"
+    assert (np.abs(U.f64(lse).reshape(N, *rl.shape) - rl) <= 2.0 ** -17 * (1 + np.abs(rl))).all()
+
