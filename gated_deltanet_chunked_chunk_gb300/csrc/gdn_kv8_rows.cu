@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_bar_sync(1 + wg, 128);
           if ((warp & 3) == 0) {
             const float top = fmaxf(fmaxf(tops[lane], tops[kRows + lane]), fmaxf(tops[2 * kRows + lane], tops[3 * kRows + lane]));
-            const float old = -ref[lane], now = fmaxf(old, top - kLift);
+            const float old = -ref[lane], now = fmaxf(old, reference_of(top, kLift));
             res[lane] = ex2f(old - now);
             ref[lane] = -now;
           }

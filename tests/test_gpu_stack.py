@@ -1019,3 +1019,21 @@ def test_attention_of_a_key_far_above_all_others(G, D, N, news, ctx, bits):
     assert (off <= tol).all(), f"worst {(off / np.abs(ref)).max():.3f} of the value"
     assert (np.abs(U.f64(lse).reshape(N, *rl.shape) - rl) <= 2.0 ** -17 * (1 + np.abs(rl))).all()
 
+
+@pytest.mark.parametrize("news", [1, 2, 4, 70])
+@pytest.mark.parametrize("top", [1.5 * 2 ** 20, 1.1 * 2 ** 26, 1.6 * 2 ** 26, 1.3 * 2 ** 27, 1.9 * 2 ** 27, 1.2 * 2 ** 28])
+def test_attention_of_very_large_logits(news, top):
+    """Exponents (base 2) whose fp32 steps are as wide as f16 is high: one key has all the weight, nothing overflows."""
+    c = _attn_case(1, 8, 128, 64, [700], [news], 6, spread=0.0)
+    c["kc"].view(torch.uint8).zero_()
+    q = torch.zeros_like(c["q"].float())
+    q[..., 0] = 1.0
+    c["q"] = q.to(BF)
+    for key, val in ((5, 0.75), (300, 1.0), (620, 0.875)):
+        c["kc"].view(torch.uint8)[c["table"][0][key // 64], 0, key % 64, 0] = torch.tensor(val).to(torch.float8_e4m3fn).view(torch.uint8)
+    c["ks"][:] = 1.0
+    scale = float(np.float32(top / math.log2(math.e)))
+    o, lse, st = _attn_run(c, scale=scale)
+    assert st == 0
+    _attn_check(c, o, lse, scale=scale)
+
