@@ -24,6 +24,7 @@ namespace {
 using at::Tensor;
 
 PyObject *g_error = nullptr;  // GDNError(function, status)
+PyObject *g_memory_error = nullptr;  // torch.OutOfMemoryError
 
 struct Refused {  // a Python exception to raise
   PyObject *type;
@@ -166,7 +167,9 @@ template <PyObject *(*F)(Args &)> PyObject *entry(PyObject *, PyObject *const *v
     } else if (!PyErr_Occurred()) {
       PyErr_Format(PyExc_RuntimeError, "%s: status %d", s.fn, s.code);
     }
-  } catch (const std::exception &e) {  // an allocation that failed, say
+  } catch (const c10::OutOfMemoryError &e) {  // torch.OutOfMemoryError, as from torch's own calls
+    PyErr_SetString(g_memory_error ? g_memory_error : PyExc_RuntimeError, e.what_without_backtrace());
+  } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
@@ -397,17 +400,19 @@ PyObject *kv8_attention(Args &a) {
   return wrap(o);
 }
 
-PyObject *set_error(Args &a) {
-  PyObject *o = a.next();
-  Py_INCREF(o);
-  Py_XDECREF(g_error);
-  g_error = o;
+PyObject *set_errors(Args &a) {  // the exceptions that this module raises beside Python's own
+  for (PyObject **at : {&g_error, &g_memory_error}) {
+    PyObject *o = a.next();
+    Py_INCREF(o);
+    Py_XDECREF(*at);
+    *at = o;
+  }
   Py_RETURN_NONE;
 }
 
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(norm_gate),  ENTRY(norm_gate_bwd), ENTRY(rope),      ENTRY(paged_plan),
-                           ENTRY(kv8_append), ENTRY(kv8_attention), ENTRY(set_error), {nullptr, nullptr, 0, nullptr}};
+                           ENTRY(kv8_append), ENTRY(kv8_attention), ENTRY(set_errors), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_gdn_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -2,7 +2,8 @@
 attention that reads it.  Same manner as the rest of the binding: arguments are checked, outputs allocated, raw
 pointers and the current stream passed to libgdn (``include/gdn.h``); here that is done by the compiled module
 ``_gdn_torch`` (``csrc/gdn_torch.cpp``), since a decode step's calls take less time on the GPU than the same checks do
-in Python.  TypeError: a wrong type; ValueError: a wrong device, shape or layout; GDNError: what the library refuses."""
+in Python.  TypeError: a wrong type; ValueError: a wrong device, shape or layout; GDNError: what the library refuses;
+torch.OutOfMemoryError: an output or a workspace that does not fit."""
 from __future__ import annotations
 
 import functools
@@ -46,7 +47,7 @@ def _load():
     loader = importlib.machinery.ExtensionFileLoader(__package__ + "._gdn_torch", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(loader.name, path, loader=loader))
     loader.exec_module(module)
-    module.set_error(GDNError)
+    module.set_errors(GDNError, torch.OutOfMemoryError)
     _c = module
     return module
 

@@ -1037,3 +1037,23 @@ def test_attention_of_very_large_logits(news, top):
     assert st == 0
     _attn_check(c, o, lse, scale=scale)
 
+
+def test_outputs_that_do_not_fit_raise_the_out_of_memory_error():
+    """The error that a program catches to free its caches and try again (the process' share of the memory is made
+    small for the call; nothing is allocated)."""
+    gdn = _gdn()
+    T = 1 << 16
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # before q too, which would take a part of a larger block and leave the rest free
+    inv, _ = gdn.rope_frequencies(64, device="cuda")
+    q, pos = torch.zeros(T, 8, 64, dtype=BF, device="cuda"), torch.zeros(T, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(torch.cuda.memory_reserved() / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            gdn.gdn_rope(q, None, pos, inv)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(gdn.gdn_rope(q, None, pos, inv)[0], q)
+
