@@ -11,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -94,8 +95,11 @@ struct Args {
   }
 };
 
-void on_gpu(const Tensor &t, const char *name) {
+// Makes the tensor's device the current one for the call: launches, and what the
+// library asks of its device, go by that.
+c10::cuda::CUDAGuard on_gpu(const Tensor &t, const char *name) {
   if (!t.is_cuda()) value_error(std::string(name) + " must be on a CUDA device, got " + t.device().str());
+  return c10::cuda::CUDAGuard(t.device());
 }
 void kind(const Tensor &t, const char *name, at::ScalarType dtype, const at::Device &dev) {
   if (t.scalar_type() != dtype)
@@ -208,7 +212,7 @@ PyObject *norm_gate(Args &a) {
   const int act = a.int32("activation");
   const float eps = a.real("eps"), rs = a.real("res_scale");
   Tensor y = a.maybe("y"), h = a.maybe("h");
-  on_gpu(x, "x");
+  const auto device = on_gpu(x, "x");
   need(x, "x", at::kBFloat16, x.device(), -1);
   const int D = width_of(x, w, fn);
   const Gate g = gate_of(z, x, act, fn);
@@ -233,7 +237,7 @@ PyObject *norm_gate_bwd(Args &a) {
   const int act = a.int32("activation");
   const float eps = a.real("eps"), rs = a.real("res_scale");
   Tensor ws = a.maybe("workspace");
-  on_gpu(h, "h");
+  const auto device = on_gpu(h, "h");
   need(h, "h", at::kBFloat16, h.device(), -1);
   like(dy, "dy", h, fn);
   const int D = width_of(h, w, fn);
@@ -260,7 +264,7 @@ PyObject *rope(Args &a) {
   const int inter = a.int32("interleaved"), inverse = a.int32("inverse");
   const float f = a.real("attention_factor");
   Tensor qo = a.maybe("q_out"), ko = a.maybe("k_out");
-  on_gpu(q, "q");
+  const auto device = on_gpu(q, "q");
   const at::Device dev = q.device();
   const int64_t ldq = token_stride(q, "q", dev), T = q.size(0), D = q.size(2);
   int64_t ldk = 0, HK = 0;
@@ -298,7 +302,7 @@ PyObject *paged_plan(Args &a) {
   const Tensor &fp = a.tensor("free_pages"), &nf = a.tensor("num_free");
   const int bs = a.int32("page_size"), T = a.int32("num_tokens");
   const Tensor &st = a.maybe("dev_status");
-  on_gpu(cached, "cached_lens");
+  const auto device = on_gpu(cached, "cached_lens");
   const at::Device dev = cached.device();
   need(cached, "cached_lens", at::kInt, dev, 1);
   need(cu, "cu_seqlens", at::kInt, dev, 1);
@@ -337,7 +341,7 @@ PyObject *kv8_append(Args &a) {
   const char *fn = "gdn_kv8_append";
   const Tensor &k = a.tensor("k"), &v = a.tensor("v"), &kc = a.tensor("k_cache"), &vc = a.tensor("v_cache");
   const Tensor &ks = a.tensor("k_scale"), &vs = a.tensor("v_scale"), &slots = a.tensor("slot_mapping"), &st = a.maybe("dev_status");
-  on_gpu(k, "k");
+  const auto device = on_gpu(k, "k");
   const at::Device dev = k.device();
   const int64_t ldk = token_stride(k, "k", dev), ldv = token_stride(v, "v", dev);
   const Cache c = cache_of(kc, vc, ks, vs, dev, fn);
@@ -361,7 +365,7 @@ PyObject *kv8_attention(Args &a) {
   const Tensor &lse = a.maybe("lse");
   Tensor ws = a.maybe("workspace");
   const Tensor &st = a.maybe("dev_status");
-  on_gpu(q, "q");
+  const auto device = on_gpu(q, "q");
   const at::Device dev = q.device();
   const int64_t ldq = token_stride(q, "q", dev), T = q.size(0), HQ = q.size(1), D = q.size(2);
   const Cache c = cache_of(kc, vc, ks, vs, dev, fn);

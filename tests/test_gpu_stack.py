@@ -1057,3 +1057,14 @@ def test_outputs_that_do_not_fit_raise_the_out_of_memory_error():
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.equal(gdn.gdn_rope(q, None, pos, inv)[0], q)
 
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_calls_go_to_the_tensors_device():
+    """Tensors of a device that is not the current one: the call runs there."""
+    gdn = _gdn()
+    x, w = torch.randn(9, 128, generator=_gen(3)).to(BF), torch.ones(128)
+    here = gdn.gdn_norm_gate(x.to("cuda:0"), w.to("cuda:0"))[0]
+    assert torch.cuda.current_device() == 0
+    there = gdn.gdn_norm_gate(x.to("cuda:1"), w.to("cuda:1"))[0]
+    assert torch.cuda.current_device() == 0 and there.device.index == 1 and torch.equal(here.cpu(), there.cpu())
+
