@@ -190,9 +190,22 @@ Gate gate_of(const Tensor &z, const Tensor &x, int act, const char *fn) {
   kind(z, "z", at::kBFloat16, x.device());
   if (z.sizes() != x.sizes()) value_error(std::string(fn) + ": z must have the shape of x, " + shape_text(x));
   if (z.is_contiguous()) return {act, 0, 0};
-  if (z.dim() == 3 && z.stride(2) == 1 && z.stride(1) == z.size(2)) return {act, z.size(1), z.stride(0)};
-  if (z.dim() == 2 && z.stride(1) == 1) return {act, 1, z.stride(0)};
-  value_error(std::string(fn) + ": z must be dense, or [tokens, heads, D] / [rows, D] with a longer stride between tokens");
+  // From the last dimension on: those that lie densely make a group (the heads of a
+  // token), those before them one walk from group to group.
+  int64_t i = z.dim() - 1, dense = 1, rows = 1;
+  for (; i >= 0 && (z.size(i) == 1 || z.stride(i) == dense); --i) {
+    if (i < z.dim() - 1) rows *= z.size(i);
+    dense *= z.size(i);
+  }
+  const int64_t stride = i >= 0 ? z.stride(i) : dense;
+  int64_t next = stride;
+  bool even = i < z.dim() - 1;
+  for (; i >= 0; --i) {
+    even = even && (z.size(i) == 1 || z.stride(i) == next);
+    next *= z.size(i);
+  }
+  if (!even) value_error(std::string(fn) + ": z must be dense, or [.., heads, D] / [.., D] with one longer stride between its tokens");
+  return {act, rows, stride};
 }
 void like(const Tensor &t, const char *name, const Tensor &x, const char *fn) {
   need(t, name, at::kBFloat16, x.device(), -1);

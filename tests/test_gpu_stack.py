@@ -1068,3 +1068,28 @@ def test_calls_go_to_the_tensors_device():
     there = gdn.gdn_norm_gate(x.to("cuda:1"), w.to("cuda:1"))[0]
     assert torch.cuda.current_device() == 0 and there.device.index == 1 and torch.equal(here.cpu(), there.cpu())
 
+
+@pytest.mark.parametrize("lead,heads", [((3, 5), (4,)), ((3, 5), ()), ((2, 3, 4), (2,)), ((1, 7), (1,)), ((6,), (2, 3))])
+def test_norm_gate_of_a_packed_projection_with_a_batch(lead, heads):
+    """A gate that is a slice of a projection [.., tokens, width], whatever dimensions stand before the tokens."""
+    gdn, g = _gdn(), _gen(41)
+    D, H = 64, math.prod(heads)
+    wide = torch.randn(*lead, 2 * H * D + 8, generator=g).to(BF).cuda()
+    z = wide[..., H * D:2 * H * D].unflatten(-1, (*heads, D))
+    assert not z.is_contiguous() or math.prod(lead) == 1
+    x, dy = (torch.randn(*lead, *heads, D, generator=g).to(BF).cuda() for _ in range(2))
+    w = 1 + torch.rand(D, generator=g).cuda()
+    a, b = gdn.gdn_norm_gate(x, w, z=z)[0], gdn.gdn_norm_gate(x, w, z=z.contiguous())[0]
+    assert torch.equal(a, b)
+    a, b = gdn.gdn_norm_gate_bwd(dy, x, w, z=z), gdn.gdn_norm_gate_bwd(dy, x, w, z=z.contiguous())
+    assert all(torch.equal(p, q) for p, q in zip(a, b) if p is not None)
+
+
+def test_norm_gate_refuses_gates_whose_tokens_are_not_evenly_apart():
+    gdn = _gdn()
+    w, x = torch.ones(64, device="cuda"), torch.zeros(3, 5, 2, 64, dtype=BF, device="cuda")
+    wide = torch.zeros(3, 7, 4, 128, dtype=BF, device="cuda")
+    for z in (wide[:, :5, :2, :64], wide[:, :5, :2, ::2]):
+        with pytest.raises(ValueError, match="longer stride"):
+            gdn.gdn_norm_gate(x, w, z=z)
+
