@@ -1093,3 +1093,45 @@ def test_norm_gate_refuses_gates_whose_tokens_are_not_evenly_apart():
         with pytest.raises(ValueError, match="longer stride"):
             gdn.gdn_norm_gate(x, w, z=z)
 
+
+
+# --------------------------------------- append: blocks of four warps, one for a page's length of tokens
+def _many_runs(bs, T, r):
+    """Slots of ragged requests on pages of their own, skipped tokens between some, T tokens or a few more; and pages."""
+    slots, pages = [], 0
+    while len(slots) < T:
+        if r.rand() < 0.2:
+            slots += [-1] * int(r.randint(1, 6))
+        off = int(r.randint(0, bs))
+        m = int(r.choice([1, 2, 3, int(r.randint(1, bs + 1)), int(r.randint(1, 4 * bs))]))
+        slots += range(pages * bs + off, pages * bs + off + m)
+        pages += -(-(off + m) // bs)
+    names = r.permutation(pages)
+    return [-1 if s < 0 else int(names[s // bs]) * bs + s % bs for s in slots], pages
+
+
+@pytest.mark.parametrize("HK,D,bs", [(8, 128, 16), (8, 64, 16), (8, 128, 32), (8, 64, 64), (4, 128, 64), (8, 128, 48), (8, 64, 128),
+                                     (8, 128, 128), (4, 512, 8), (16, 32, 128), (16, 16, 64), (4, 256, 16)])
+def test_append_of_many_tokens(HK, D, bs):
+    """Enough tokens for the kernel that long prompts take, with each number of values that its threads hold: runs that
+    begin anywhere in a page, cross the blocks' stretches, or are short; older codes that move; values that are not finite."""
+    gdn, g, r = _gdn(), _gen(HK + D + bs), np.random.RandomState(HK + D + bs)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    slots, P = _many_runs(bs, bs * -(-4 * sms // (2 * HK)) + 5, r)
+    T = len(slots)
+    assert -(-T // bs) * 2 * HK >= 4 * sms
+    kc, ks = U.make_cache(P, HK, bs, D, g)
+    vc, vs = U.make_cache(P, HK, bs, D, g)
+    wide = torch.randn(T, 2 * HK * D, generator=g) * torch.exp(2 * torch.randn(T, 1, generator=g))
+    for bad in (math.inf, -math.inf, math.nan):
+        wide.view(-1)[torch.randint(0, wide.numel(), (20,), generator=g)] = bad
+    wide = wide.to(BF)
+    k, v = (wide[:, i * HK * D:(i + 1) * HK * D].view(T, HK, D) for i in range(2))
+    wd = wide.cuda()
+    kd, vd = (wd[:, i * HK * D:(i + 1) * HK * D].view(T, HK, D) for i in range(2))
+    dev = [t.cuda() for t in (kc, vc, ks, vs)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_kv8_append(kd, vd, *dev, torch.tensor(slots, dtype=torch.int32, device="cuda"), dev_status=st)
+    assert int(st) == 0
+    _same_cache(dev[0], dev[2], U.append(U.f64(k), U.f64(kc.float()), U.f64(ks), slots))
+    _same_cache(dev[1], dev[3], U.append(U.f64(v), U.f64(vc.float()), U.f64(vs), slots))
