@@ -1135,3 +1135,54 @@ def test_append_of_many_tokens(HK, D, bs):
     assert int(st) == 0
     _same_cache(dev[0], dev[2], U.append(U.f64(k), U.f64(kc.float()), U.f64(ks), slots))
     _same_cache(dev[1], dev[3], U.append(U.f64(v), U.f64(vc.float()), U.f64(vs), slots))
+
+
+# ------------------------------------------- norms: more rows than the blocks take in one turn
+def _act64(z, kind):
+    s = 1.0 / (1.0 + (-z).exp())
+    return (z * s, s * (1.0 + z * (1.0 - s))) if kind == "silu" else (s, s * (1.0 - s))
+
+
+@pytest.mark.parametrize("rows,D", [(100003, 64), (50021, 128), (30011, 256), (25013, 512), (25013, 1024), (3001, 2048), (3001, 4096),
+                                    (1517, 8192), (1517, 16384), (3001, 130), (2999, 1001)])
+@pytest.mark.parametrize("kind,res", [(None, False), ("silu", True), ("sigmoid", False)])
+def test_norm_gate_and_gradients_of_many_rows(rows, D, kind, res):
+    """Every kernel in several turns, the last one not full: a turn is 38912 rows of 64 forward, and down to 608 rows of
+    16384 (backward 19456, and 152).  The formulas in 64 bits by torch.  Tolerances as above; the weight's gradient is
+    a chain of at most 128 additions (turns, row groups of a block, blocks): 2^-17 of the magnitudes."""
+    gdn = _gdn()
+    gen = torch.Generator(device="cuda").manual_seed(rows + D)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    x, dy, s = (2 * rnd(rows, D)).to(BF), rnd(rows, D).to(BF), 0.5 if res else 1.0
+    w = 1 + 0.1 * rnd(D)
+    z = rnd(rows, D).to(BF) if kind else None
+    r, dh = (rnd(rows, D).to(BF), rnd(rows, D).to(BF)) if res else (None, None)
+
+    def close(got, ref, extra, what):
+        off = (got.double() - ref).abs() - (2.0 ** -8 * ref.abs() + extra + 1e-37)
+        assert float(off.max()) <= 0, f"{what}: {int((off > 0).sum())} of {off.numel()}"
+
+    y, h = gdn.gdn_norm_gate(x, w, residual=r, z=z, activation=kind, res_scale=s)
+    h64 = x.double() if r is None else r.double() + s * x.double()
+    f, d = (1.0, None) if kind is None else _act64(z.double(), kind)
+    close(y, h64 / (h64.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.double() * f, 0.0, "y")
+    if res:
+        close(h, h64, 2.0 ** -18 * float(h64.abs().max()), "h")
+    hb = x if h is None else h
+    grads = gdn.gdn_norm_gate_bwd(dy, hb, w, z=z, dh=dh, activation=kind, res_scale=s)
+    again = gdn.gdn_norm_gate_bwd(dy, hb, w, z=z, dh=dh, activation=kind, res_scale=s)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again) if a is not None)
+    dx, dres, dz, dw = grads
+    h64 = hb.double()
+    rstd = 1.0 / (h64.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    n = h64 * rstd
+    u = dy.double() * f
+    p = u * w.double()
+    dH = rstd * (p - n * (p * n).mean(-1, keepdim=True)) + (0.0 if dh is None else dh.double())
+    terms = 2.0 ** -18 * (rstd * dy.double().abs().amax(-1, keepdim=True) * 4 + (2.0 if res else 0.0))
+    close(dx, s * dH, terms, "dx")
+    if res:
+        close(dres, dH, terms, "dresidual")
+    if kind:
+        close(dz, dy.double() * n * w.double() * d, 2.0 ** -18 * (dy.double() * n).abs(), "dz")
+    assert ((dw.double() - (u * n).sum(0)).abs() <= 2.0 ** -17 * (u * n).abs().sum(0)).all()
