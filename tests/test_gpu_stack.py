@@ -1186,3 +1186,44 @@ def test_norm_gate_and_gradients_of_many_rows(rows, D, kind, res):
     if kind:
         close(dz, dy.double() * n * w.double() * d, 2.0 ** -18 * (dy.double() * n).abs(), "dz")
     assert ((dw.double() - (u * n).sum(0)).abs() <= 2.0 ** -17 * (u * n).abs().sum(0)).all()
+
+
+# ---------------------------------- attention: more tiles of rows than SMs, so whole ones come before those cut
+def _attn64(c, scale):
+    """o, lse and sum_j p_ij |v_j| in 64 bits by torch, one product a (request, kv head)."""
+    HK, G, D, bs = c["HK"], c["G"], c["D"], c["bs"]
+    q, ks, vs = (c[k].cuda().double() for k in ("q", "ks", "vs"))
+    o, mag, lse = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    for n, L in enumerate(c["lens"]):
+        t0, t1 = c["cu"][n], c["cu"][n + 1]
+        m = t1 - t0
+        pages = torch.tensor(c["table"][n][:-(-L // bs)], device="cuda")
+        seen = torch.arange(L, device="cuda") <= torch.arange(L - m, L, device="cuda").repeat_interleave(G)[:, None]
+        for h in range(HK):
+            K, V = ((codes.cuda().float().double()[pages, h] * s[pages, h][:, None, None]).reshape(-1, D)[:L]
+                    for codes, s in ((c["kc"], ks), (c["vc"], vs)))
+            s = (q[t0:t1, h * G:(h + 1) * G].reshape(m * G, D) @ K.T * scale).masked_fill(~seen, -math.inf)
+            lse[t0:t1, h * G:(h + 1) * G] = s.logsumexp(-1).view(m, G)
+            p = s.sub_(s.logsumexp(-1, keepdim=True)).exp_()
+            o[t0:t1, h * G:(h + 1) * G] = (p @ V).view(m, G, D)
+            mag[t0:t1, h * G:(h + 1) * G] = (p @ V.abs()).view(m, G, D)
+    return o, lse, mag
+
+
+@pytest.mark.parametrize("HK,G,D,bs,lens,news,most", [
+    (2, 8, 128, 64, [2500, 5000], [2450, 300], 152),               # 174 tiles: 152 whole, 22 in 5 pieces
+    (4, 4, 64, 16, [3000, 2100, 4200], [3000, 2000, 200], 304),     # 332: two turns whole, 28 in 4 pieces
+    (1, 8, 64, 128, [4864], [4864], 152),                           # one tile an SM, none left
+    (1, 8, 128, 32, [8064, 3], [8064, 3], 152)])                    # 253: 101 left, too many to cut
+def test_attention_of_more_tiles_of_rows_than_sms(HK, G, D, bs, lens, news, most):
+    c = _attn_case(HK, G, D, bs, lens, news, sum(lens) + D, nan_past=False)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert HK * sum(-(-m * G // 256) for m in news) >= most
+    o, lse, st = _attn_run(c)
+    assert st == 0
+    ro, rl, mag = _attn64(c, D ** -0.5)
+    off = (o.double() - ro).abs() - (2.0 ** -8 * ro.abs() + 2.0 ** -10 * mag + 1e-37)
+    assert float(off.max()) <= 0, f"{int((off > 0).sum())} of {off.numel()}"
+    assert ((lse.double() - rl).abs() <= 2.0 ** -17 * (1 + rl.abs())).all()
+    again, lse2, _ = _attn_run(c)
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
