@@ -29,14 +29,15 @@
 //
 // The last items, where they do not come out even with the SMs, are cut along
 // their keys (find_work).  4096 tokens over 16384 keys, 32 heads of 128, 4 kv
-// heads: 512 items on 152 SMs, 714 us (1.35 PFLOP/s, 71 % of a 16-bit library
-// product), about 90 us less than with the last 56 items whole; 512 tokens over
-// 16384: 139 us, two pieces an item.  What a block works on stands in shared memory,
-// as every register that the loops spill costs (740 us with 70 bytes more of
-// them).  A key tile takes 3500 cycles, of which the tensor cores work 2176: a
-// softmax thread's chain from "S is there" to "P is there" (load, maximum,
-// exponentials, store: 2000) is longer than the other tile's products that hide
-// it; P V begins when the first half of P is there (747 us without).  Two threads a
+// heads: 512 items on 152 SMs, 727 us (1.32 PFLOP/s, 70 % of a 16-bit library
+// product) on new inputs each time; on the same ones 682 us, and 787 with the last 56
+// items whole; 512 tokens over 16384: 130 us, two pieces an item (whole 232).  What a
+// block works on stands in shared memory, as every register that the loops spill
+// costs (70 bytes more of them: 25 us).  A key tile takes 3500 cycles, of which the
+// tensor cores work 2176: S of a tile's next keys waits for its P V, as P stands in
+// S's columns, and that for a softmax thread's chain from "S is there" to "P is
+// there" (load, maximum, exponentials, store: 2000), longer than the other tile's
+// products that hide it; P V begins when the first half of P is there (7 us).  Two threads a
 // row (1200 us: with 64 logits each their registers spill), blocks that stay and
 // take a stretch of all items' key tiles (822 us: what that adds to the loop costs
 // more than the even end gains) and reading the logits twice (1490 us) were
@@ -124,7 +125,7 @@ __device__ __forceinline__ void find_work(const AttnArgs &a, int min_rows, int s
   const int all = (int)min(total, (int64_t)gridDim.x - kSlots);
   const int whole = all / sms * sms, rest = all - whole;
   // Pieces of each of the last items, one an SM.  (Two turns of smaller pieces,
-  // 56 items in 5 pieces each, ended later: 780 us where this took 767.)
+  // 56 items in 5 pieces each, ended 13 us later.)
   const int cut = rest > 0 ? min(sms, kSlots) / rest : 1;
   const int slot = (int)blockIdx.x - whole;
   int item = blockIdx.x, piece = 0, pieces = 1;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kPrefThreads, 1)
 
   // Of the block's 65536 registers (512 threads x 128) the softmax warps take
   // 184 a thread, the other warps 72: 2 x 128 x 184 + 2 x 128 x 72 = 65536.  (200
-  // and 56: 727 us against 714.)
+  // and 56: 694 us against 682, as above.)
   const int tiles = work->tiles;
   float m_ref = -INFINITY, l_sum = 0.f;
   int issued_k = 0, issued_v = 0;  // key tiles that the producer has issued

@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
 
 // A row's vectors come through a ring in shared memory by asynchronous copies,
 // kAhead rows ahead; a thread copies and reads places of its own only, so no
-// barrier is needed.  262144 rows of 128 with a SiLU gate: 60.2 us for both
-// kernels (5.6 TB/s); loads to registers 70, three rows ahead 60.9.
+// barrier is needed.  262144 rows of 128 with a SiLU gate: 56.4 us for both
+// kernels (5.95 TB/s), three rows ahead 57.6; loads to registers took 10 us more.
 template <int NV> struct Ahead { static constexpr int kRows = NV <= 2 ? 2 : 1; };
 __device__ __forceinline__ void copy16(void *dst, const uint16_t *src, bool on) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));

@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kPlan) paged_plan_kernel(
 // many (windows of a page's length), a block of four warps takes the runs that
 // begin in a window and keeps a run's values in registers between the maximum
 // and the rounding (reading them twice: 104 us for 65536 tokens of 4 heads,
-// against 39, 5.1 TB/s).  Where they are few, a warp takes the run of one token.
+// against 38, 5.2 TB/s).  Where they are few, a warp takes the run, if any, that
+// begins with its token, and reads the values twice.
 struct AppendArgs {
   const uint16_t *k, *v;
   int64_t ldk, ldv;

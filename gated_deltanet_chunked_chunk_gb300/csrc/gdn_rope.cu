@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(256, 8) rope_vec_kernel(const RopeArgs a, int 
   const bool pass = u >= turned;  // this thread's place is not turned
   const int e0 = pass ? a.rot + (u - turned) * 8 : u * 8, e1 = e0 + half;
   // Two (token, head) rows a trip, both loads issued before either is used:
-  // eight blocks of 32 registers a thread on a SM measured 191 us for 65536 x 36
-  // heads of 128, one row a trip 206, three (more registers) 207.
+  // eight blocks of 32 registers a thread on a SM measured 184 us for 65536 x 36
+  // heads of 128, one row a trip 198, three (more registers) 199.
   constexpr int U = 2;
   while (t < n) {
     const uint16_t *in[U];
@@ -193,8 +193,8 @@ cudaError_t launch_rope(const uint16_t *q, const uint16_t *k, const int32_t *pos
                         uint16_t *qo, uint16_t *ko, cudaStream_t s) {
   const int sms = sm_count();
   RopeArgs a{q, k, qo, ko, ldq, ldk, pos, inv_freq, T, HQ, HK, D, rot, inverse, interleaved, factor, 1};
-  // Tokens a block: 8 once the grid fills the SMs several times over (16: 200
-  // against 191 us), fewer below that; the tile's angles (rot / 2 pairs of 8 bytes a token) stay
+  // Tokens a block: 8 once the grid fills the SMs several times over (16: 193
+  // against 184 us), fewer below that; the tile's angles (rot / 2 pairs of 8 bytes a token) stay
   // within 32 KB.
   int64_t tile = T / ((int64_t)sms * 8);
   const int64_t most = (32 << 10) / ((int64_t)(rot / 2) * 8 + 1);
