@@ -589,7 +589,8 @@ int gdn_paged_plan(const int32_t *cached_lens, const int32_t *cu_seqlens, int N,
  * The paged 8-bit cache.  k_cache, v_cache: e4m3 codes [P, HK, page_size, D];
  * k_scale, v_scale: fp32 [P, HK]; value = code * scale.  gdn_kv8_append writes
  * scales that are powers of two and moves a page that came with another one to
- * such a scale; the attention takes any positive finite ones.
+ * such a scale; the attention takes any finite ones from 2^-90 on (sums of weights
+ * over a value's scale stay within fp32 for 2^20 keys and more).
  *
  * gdn_kv8_append -- the write of new keys and values.  For each page and head
  * that a call writes to:

@@ -1227,3 +1227,15 @@ def test_attention_of_more_tiles_of_rows_than_sms(HK, G, D, bs, lens, news, most
     assert ((lse.double() - rl).abs() <= 2.0 ** -17 * (1 + rl.abs())).all()
     again, lse2, _ = _attn_run(c)
     assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("news", [1, 2, 4, 70])
+def test_attention_scales_at_the_ends_of_their_range(news):
+    """Values in pages of scale 2^-90, and of 2^100, alone: neither the sum of the weights nor the result overflows."""
+    for e in (-90, 100):
+        c = _attn_case(1, 8, 128, 64, [3000], [news], 7)
+        c["vs"] = torch.full_like(c["vs"], 2.0 ** e)
+        o, lse, st = _attn_run(c)
+        assert st == 0 and torch.isfinite(o).all()
+        _attn_check(c, o, lse)
+
