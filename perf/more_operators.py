@@ -376,7 +376,7 @@ def work(case):
 def _to8(x):
     """x rounded to the 8-bit format's values: three bits after the leading one, steps of 2^-9 below 2^-6, ties to even."""
     exp = torch.frexp(x)[1].clamp(min=-5)
-    step = torch.ldexp(torch.ones_like(x), exp - 4)
+    step = ((exp.long() - 4 + 1023) << 52).view(torch.float64)  # 2^(exp - 4) from its bits: a power on the GPU may be off by one
     return (torch.round(x / step) * step).clamp(-448.0, 448.0)
 
 
