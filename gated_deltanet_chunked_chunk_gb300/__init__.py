@@ -31,7 +31,8 @@ __all__ = ["gdn_gating", "gdn_chunk_fwd", "gdn_recurrent_decode", "chunk_fwd_wor
            "DEV_BAD_SLOT", "DEV_WAIT_TIMEOUT", "DEV_DRAIN_TIMEOUT", "EXPORTED_SYMBOLS",
            "testing_force_wait_expiry", "DEV_NO_PAGE", "DEV_BAD_SEQ_LEN",
            "gdn_norm_gate", "gdn_norm_gate_bwd", "norm_gate", "gdn_rope", "rotary_embedding", "rope_frequencies",
-           "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention", "kv8_attention_workspace_size"]
+           "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention", "kv8_attention_workspace_size",
+           "gdn_attention_fwd", "gdn_attention_bwd", "attention", "attention_bwd_workspace_size"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libgdn.so")
@@ -51,7 +52,8 @@ EXPORTED_SYMBOLS = ("gdn_status_string", "gdn_version", "gdn_gating", "gdn_chunk
                     "gdn_chunk_bwd", "gdn_chunk_fwd_gated", "gdn_testing_force_wait_expiry",
                     "gdn_causal_conv1d_update_spec",
                     "gdn_norm_gate", "gdn_norm_gate_bwd_workspace_size", "gdn_norm_gate_bwd", "gdn_rope",
-                    "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention_workspace_size", "gdn_kv8_attention")
+                    "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention_workspace_size", "gdn_kv8_attention",
+                    "gdn_attention_fwd", "gdn_attention_bwd_workspace_size", "gdn_attention_bwd")
 
 #: Size of the fixed scratch buffer behind gdn_chunk_fwd_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -137,6 +139,12 @@ def load_library():
         lib.gdn_kv8_attention_workspace_size.restype = SZ
         lib.gdn_kv8_attention.argtypes = [P, I64, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P, P]
         lib.gdn_kv8_attention.restype = I
+        lib.gdn_attention_fwd.argtypes = [P, I64, P, I64, P, I64, P, P, I, I, I, I, I, I, I, F, P, P, P, P]
+        lib.gdn_attention_fwd.restype = I
+        lib.gdn_attention_bwd_workspace_size.argtypes = [I, I, I, I, I, I]
+        lib.gdn_attention_bwd_workspace_size.restype = SZ
+        lib.gdn_attention_bwd.argtypes = [P, P, I64, P, I64, P, I64, P, P, P, P, I, I, I, I, I, I, I, F, P, P, P, P, SZ, P, P]
+        lib.gdn_attention_bwd.restype = I
         _lib = lib
         return lib
 
@@ -711,3 +719,4 @@ def chunk_gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
 # Norms, rotary positions and the paged 8-bit cache (after the helpers above, which they use).
 from .stack import (gdn_kv8_append, gdn_kv8_attention, gdn_norm_gate, gdn_norm_gate_bwd, gdn_paged_plan,  # noqa: E402
                     gdn_rope, kv8_attention_workspace_size, norm_gate, rope_frequencies, rotary_embedding)
+from .train import attention, attention_bwd_workspace_size, gdn_attention_bwd, gdn_attention_fwd  # noqa: E402

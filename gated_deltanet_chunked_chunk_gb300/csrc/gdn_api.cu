@@ -394,4 +394,62 @@ int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, co
   return cuda_status(gdn_host::launch_kv8_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Checks that both directions of training attention share.
+static int attention_args(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                          const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int N, int Tq, int Tk, int HQ, int HK, int D,
+                          int causal, float scale, int32_t *dev_status, gdn_host::TrainAttnArgs &a) {
+  if (N < 0 || Tq < 0 || Tk < 0 || HQ <= 0 || HK <= 0 || D <= 0 || HQ % HK || (causal != 0 && causal != 1)) return GDN_EINVAL;
+  if (!cu_seqlens && (N != 1 || cu_seqlens_k)) return GDN_EINVAL;
+  if (cu_seqlens && !cu_seqlens_k && Tq != Tk) return GDN_EINVAL;
+  if (!head_dim_ok(D)) return GDN_EUNSUPPORTED;
+  if (N > 65535 || HQ > 65535) return GDN_EUNSUPPORTED;
+  if ((Tq > 0 && !q) || (Tk > 0 && (!k || !v))) return GDN_EINVAL;
+  if (ldq < (int64_t)HQ * D || ldk < (int64_t)HK * D || ldv < (int64_t)HK * D || ldq % 8 || ldk % 8 || ldv % 8) return GDN_EINVAL;
+  if (ldq >= (1LL << 38) || ldk >= (1LL << 38) || ldv >= (1LL << 38)) return GDN_EUNSUPPORTED;
+  if (!aligned16({q, k, v})) return GDN_EINVAL;
+  if (!(scale > 0.f)) scale = 1.f / sqrtf((float)D);  // also catches NaN
+  a.q = q; a.k = k; a.v = v; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv;
+  a.cu = cu_seqlens; a.cu_k = cu_seqlens_k; a.N = N; a.Tq = Tq; a.Tk = Tk; a.HQ = HQ; a.HK = HK; a.D = D;
+  a.causal = causal; a.scale = scale; a.dev_status = dev_status;
+  a.force_expiry = g_force_wait_expiry.load();
+  return GDN_OK;
+}
+
+int gdn_attention_fwd(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                      const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int N, int Tq, int Tk, int HQ, int HK, int D,
+                      int causal, float scale, uint16_t *o, float *lse, int32_t *dev_status, void *stream) {
+  gdn_host::TrainAttnArgs a{};
+  const int rc = attention_args(q, ldq, k, ldk, v, ldv, cu_seqlens, cu_seqlens_k, N, Tq, Tk, HQ, HK, D, causal, scale, dev_status, a);
+  if (rc != GDN_OK) return rc;
+  if (Tq == 0) return GDN_OK;
+  if (!o || !lse || !aligned16({o})) return GDN_EINVAL;
+  a.o = o; a.lse = lse;
+  if (!bind_context()) return GDN_ECUDA;
+  return cuda_status(gdn_host::launch_attn_fwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, int D) {
+  if (N < 0 || N > 65535 || Tq < 0 || Tk < 0 || HK <= 0 || HQ <= 0 || HQ > 65535 || HQ % HK || !head_dim_ok(D)) return 0;
+  return gdn_host::attn_bwd_workspace_bytes(N, Tq, Tk, HQ, HK, D);
+}
+
+int gdn_attention_bwd(const uint16_t *dout, const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
+                      int64_t ldv, const uint16_t *o, const float *lse, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                      int N, int Tq, int Tk, int HQ, int HK, int D, int causal, float scale, uint16_t *dq, uint16_t *dk,
+                      uint16_t *dv, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream) {
+  gdn_host::TrainAttnArgs a{};
+  const int rc = attention_args(q, ldq, k, ldk, v, ldv, cu_seqlens, cu_seqlens_k, N, Tq, Tk, HQ, HK, D, causal, scale, dev_status, a);
+  if (rc != GDN_OK) return rc;
+  if (Tq == 0 && Tk == 0) return GDN_OK;
+  if (Tq > 0 && (!dout || !o || !lse || !dq)) return GDN_EINVAL;
+  if (Tk > 0 && (!dk || !dv)) return GDN_EINVAL;
+  if (!aligned16({dout, o, dq, dk, dv, workspace})) return GDN_EINVAL;
+  const size_t need = gdn_host::attn_bwd_workspace_bytes(N, Tq, Tk, HQ, HK, D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
+  a.dout = dout; a.o = const_cast<uint16_t *>(o); a.lse = const_cast<float *>(lse);
+  a.dq = dq; a.dk = dk; a.dv = dv; a.ws = workspace;
+  if (!bind_context()) return GDN_ECUDA;
+  return cuda_status(gdn_host::launch_attn_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

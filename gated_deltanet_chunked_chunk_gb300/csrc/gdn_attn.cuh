@@ -1,0 +1,183 @@
+// gdn_attn.cuh -- what the kernels of training attention (gdn_attn_fwd.cu,
+// gdn_attn_bwd.cu) share: arguments, which rows a block works on, tensor maps.
+//
+// Packed sequences: sequence n has the rows [cu[n], cu[n + 1]) of q and the keys
+// [cu_k[n], cu_k[n + 1]) of k and v.  Rows and keys behind the last sequence count
+// as one more sequence that sees nothing, so that every row of an output is written
+// (zeros there).
+//
+// Blocks find their rows from the offsets on the device.  Sequence n gets the slots
+// from floor(cu[n] / R) + n on, R rows each: with a = R A + r and b = R B + s,
+// ceil((b - a) / R) <= B - A + 1, so no two sequences share a slot, and the slots
+// of all sequences are at most T / R + N + 1, which the host knows.
+#pragma once
+
+#include "gdn_kv8_tc.cuh"
+
+namespace gdnat {
+
+using namespace gdn;
+using gdnkv::elect_one;
+using gdnkv::ex2f;
+using gdnkv::kLn2;
+using gdnkv::tmem_st32;
+using gdnkv::tmem_st_wait;
+using gdnkv::umma_f16_ta;
+using gdnkv::wait_bar;
+
+constexpr int kTile = 128;  // rows and keys of a tile
+
+struct Args : gdn_host::TrainAttnArgs {
+  int G;  // query heads a kv head
+  float scale_log2e;
+};
+
+// Slots of R rows that T rows of N sequences take at most (the rows behind the last
+// sequence among them).
+__host__ __device__ __forceinline__ int64_t slots_of(int64_t T, int N, int R) { return T / R + N + 1; }
+
+// One side's sequences: offsets, or one sequence of all rows (cu NULL).
+struct Side {
+  const int32_t *cu;
+  int N, T;
+  __device__ __forceinline__ int at(int n) const { return cu ? cu[n] : (n == 0 ? 0 : T); }
+};
+__device__ __forceinline__ Side rows_of(const Args &a) { return Side{a.cu, a.N, a.Tq}; }
+// Keys: their own offsets, else the rows'.
+__device__ __forceinline__ Side keys_of(const Args &a) { return Side{a.cu_k ? a.cu_k : a.cu, a.N, a.Tk}; }
+
+struct Run {
+  int first, count;
+};
+// The rows of sequence n (n = N: those behind the last one); false where the offsets
+// break the rules.
+__device__ __forceinline__ bool run_of(const Side &s, int n, Run &r) {
+  const int c0 = s.at(n), c1 = n == s.N ? s.T : s.at(n + 1);
+  if (c0 < 0 || c1 < c0 || c1 > s.T || (n == 0 && c0 != 0)) return false;
+  r.first = c0;
+  r.count = c1 - c0;
+  return true;
+}
+// The sequence that owns a slot, found by a warp (every lane gets it): 32 places are
+// looked at in each turn.  Offsets that are not sorted give some sequence.
+__device__ __forceinline__ int owner_of(const Side &s, int64_t slot, int R) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, span = s.N + 1;
+  while (span > 1) {
+    const int step = (span + 31) / 32, n = lo + lane * step;
+    const bool there = lane * step < span && (int64_t)(s.at(n) / R) + n <= slot;
+    const uint32_t m = __ballot_sync(0xffffffffu, there || lane == 0);
+    const int top = 31 - __clz((int)m);
+    lo += top * step;
+    span = min(step, span - top * step);
+  }
+  return lo;
+}
+
+// What the tile of a slot works on.
+struct Tile {
+  int n;           // its sequence
+  Run rows, keys;  // the sequence's
+  int row0;        // its first row in the sequence (of the slot's side)
+};
+// `by_keys`: slots of the keys' side.  False: nothing to do.
+__device__ __forceinline__ bool tile_of(const Args &a, int64_t slot, int R, bool by_keys, Tile &t) {
+  const Side rows = rows_of(a), keys = keys_of(a), mine = by_keys ? keys : rows;
+  t.n = owner_of(mine, slot, R);
+  if (!run_of(rows, t.n, t.rows) || !run_of(keys, t.n, t.keys)) return false;
+  if (t.n == a.N) (by_keys ? t.rows : t.keys).count = 0;
+  const int64_t row0 = (slot - ((int64_t)(mine.at(t.n) / R) + t.n)) * R;
+  if (row0 < 0 || row0 >= (by_keys ? t.keys : t.rows).count) return false;
+  t.row0 = (int)row0;
+  return true;
+}
+// Reports offsets that break the rules; by all threads of one block.
+__device__ __forceinline__ void check_offsets(const Args &a) {
+  const Side rows = rows_of(a), keys = keys_of(a);
+  Run r;
+  bool bad = false;
+  for (int n = threadIdx.x; n < a.N; n += blockDim.x) bad |= !run_of(rows, n, r) || !run_of(keys, n, r);
+  if (bad) set_status(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
+}
+
+// A 128-row tile of D bf16 in shared memory: D / 64 blocks of 128 rows x 128 bytes,
+// 128-byte swizzle, as TMA brings them.
+template <int D> __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar, int head, int row) {
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kTile * 128, map, bar, c * 64, head, row);
+}
+template <int D> constexpr int tile_bytes() { return kTile * D * 2; }
+// Zeros the rows [from, 128) of a tile in shared memory (a warp).
+template <int D> __device__ __forceinline__ void zero_rows(uint32_t tile, int from) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    for (int i = from * 8 + lane; i < kTile * 8; i += 32) gdnkv::sts128(tile + c * kTile * 128 + i * 16, 0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Products of 128 x 128 x D (or 128 x D x 128) by one thread.
+// D[128 x 128] = A B^T, both rows of D in shared memory.
+template <int D> __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = umma_idesc_bf16(128, 128);
+  const uint64_t da = umma_desc_sw128(a), db = umma_desc_sw128(b);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint32_t at = (k / 4) * (kTile * 128 / 16) + (k % 4) * 2;
+    umma_bf16(d, da + at, db + at, id, k > 0);
+  }
+}
+// D[128 x D] (+)= A B: A 128 x 128 bf16 in tensor memory, its columns 0-63 packed at a
+// and 64-127 at a + 64 (over the halves of the fp32 tile they came from); B 128 rows of
+// D in shared memory.
+template <int D> __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t id = umma_idesc_bf16(128, D, 0, 1);
+  const uint64_t db = umma_desc_sw128_mn(b, kTile * 128);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) umma_f16_ta(d, a + (k / 4) * 64 + (k % 4) * 8, db + k * 128, id, add || k > 0);
+}
+
+// a b + c, a b and a - b of two numbers each.
+__device__ __forceinline__ float2 fma2v(float2 a, float b, float2 c) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mov.b64 z, {%5, %6}; fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair(const uint32_t *r, int i) {
+  return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
+// 64 columns of a row from tensor memory, without the wait.
+__device__ __forceinline__ void load64(uint32_t taddr, uint32_t *r) {
+  tmem_ld32_issue(taddr, r);
+  tmem_ld32_issue(taddr + 32, r + 32);
+}
+__device__ __forceinline__ void wait64(uint32_t *r) {
+  tmem_ld_wait(r);
+  gdnkv::tie32(r + 32);
+}
+
+// ---------------------------------------------------------------- host side
+// Map over [T][heads][D] bf16 with ld elements between tokens, box of 128 rows of 64
+// elements of one head.
+inline bool rows_map(CUtensorMap *m, const void *ptr, int D, int heads, int64_t T, int64_t ld) {
+  gdnkv::EncodeTiledFn fn = gdnkv::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, 1, kTile}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dim, str, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace gdnat

@@ -261,4 +261,23 @@ struct Kv8AttnArgs {
 };
 size_t kv8_attn_workspace_bytes(int N, int T, int G, int D, int max_q);
 cudaError_t launch_kv8_attn(const Kv8AttnArgs &a, cudaStream_t s);
+// Attention of packed sequences for training (gdn_attn_fwd.cu, gdn_attn_bwd.cu).
+struct TrainAttnArgs {
+  const uint16_t *q, *k, *v;
+  int64_t ldq, ldk, ldv;  // token strides in elements
+  const int32_t *cu, *cu_k;
+  int N, Tq, Tk, HQ, HK, D, causal;
+  float scale;
+  uint16_t *o;
+  float *lse;
+  // backward (o and lse are inputs)
+  const uint16_t *dout;
+  uint16_t *dq, *dk, *dv;
+  void *ws;
+  int32_t *dev_status;
+  int force_expiry;  // testing hook: the first bounded wait of every block runs out
+};
+cudaError_t launch_attn_fwd(const TrainAttnArgs &a, cudaStream_t s);
+size_t attn_bwd_workspace_bytes(int N, int Tq, int Tk, int HQ, int HK, int D);
+cudaError_t launch_attn_bwd(const TrainAttnArgs &a, cudaStream_t s);
 }  // namespace gdn_host

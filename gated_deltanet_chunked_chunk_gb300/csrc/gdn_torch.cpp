@@ -417,6 +417,90 @@ PyObject *kv8_attention(Args &a) {
   return wrap(o);
 }
 
+// ---------------------------------------------------- training attention
+struct Attn {
+  int64_t ldq, ldk, ldv;
+  int N, Tq, Tk, HQ, HK, D;
+};
+Attn attention_of(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &cu, const Tensor &cu_k, const Tensor &st, const char *fn) {
+  const at::Device dev = q.device();
+  Attn s{};
+  s.ldq = token_stride(q, "q", dev);
+  s.ldk = token_stride(k, "k", dev);
+  s.ldv = token_stride(v, "v", dev);
+  if (k.sizes() != v.sizes() || k.size(2) != q.size(2))
+    value_error(std::string(fn) + ": q must be [Tq, HQ, D] and k, v [Tk, HK, D]");
+  int64_t N = 1;
+  if (cu.defined()) {
+    need(cu, "cu_seqlens", at::kInt, dev, 1);
+    if (cu.size(0) < 1) value_error(std::string(fn) + ": cu_seqlens must be [N + 1]");
+    N = cu.size(0) - 1;
+  }
+  if (cu_k.defined()) {
+    need(cu_k, "cu_seqlens_k", at::kInt, dev, 1);
+    if (!cu.defined() || cu_k.size(0) != N + 1) value_error(std::string(fn) + ": cu_seqlens_k must be [N + 1], as cu_seqlens");
+  } else if (cu.defined() && k.size(0) != q.size(0)) {
+    value_error(std::string(fn) + ": keys of other lengths than the rows' need cu_seqlens_k");
+  }
+  if (st.defined()) need(st, "dev_status", at::kInt, dev, 1);
+  s.N = fits32(N, "N");
+  s.Tq = fits32(q.size(0), "Tq");
+  s.Tk = fits32(k.size(0), "Tk");
+  s.HQ = fits32(q.size(1), "HQ");
+  s.HK = fits32(k.size(1), "HK");
+  s.D = fits32(q.size(2), "D");
+  return s;
+}
+
+PyObject *attention_fwd(Args &a) {
+  const char *fn = "gdn_attention_fwd";
+  const Tensor &q = a.tensor("q"), &k = a.tensor("k"), &v = a.tensor("v"), &cu = a.maybe("cu_seqlens"), &cu_k = a.maybe("cu_seqlens_k");
+  const int causal = a.int32("causal");
+  const float scale = a.real("scale");
+  Tensor o = a.maybe("o"), lse = a.maybe("lse");
+  const Tensor &st = a.maybe("dev_status");
+  const auto device = on_gpu(q, "q");
+  const at::Device dev = q.device();
+  const Attn s = attention_of(q, k, v, cu, cu_k, st, fn);
+  if (o.defined()) like(o, "o", q, fn);
+  else o = empty(q.sizes(), at::kBFloat16, dev);
+  if (lse.defined()) {
+    need(lse, "lse", at::kFloat, dev, 2);
+    if (lse.size(0) != s.Tq || lse.size(1) != s.HQ) value_error("gdn_attention_fwd: lse must be [Tq, HQ]");
+  } else {
+    lse = empty({s.Tq, s.HQ}, at::kFloat, dev);
+  }
+  done(fn, gdn_attention_fwd(bf(q), s.ldq, bf(k), s.ldk, bf(v), s.ldv, ptr<const int32_t>(cu), ptr<const int32_t>(cu_k), s.N, s.Tq,
+                             s.Tk, s.HQ, s.HK, s.D, causal, scale, bf_out(o), ptr<float>(lse), ptr<int32_t>(st), stream_of(dev)));
+  const Tensor out[2] = {o, lse};
+  return tuple_of(out);
+}
+
+PyObject *attention_bwd(Args &a) {
+  const char *fn = "gdn_attention_bwd";
+  const Tensor &dout = a.tensor("do"), &q = a.tensor("q"), &k = a.tensor("k"), &v = a.tensor("v"), &o = a.tensor("o"), &lse = a.tensor("lse");
+  const Tensor &cu = a.maybe("cu_seqlens"), &cu_k = a.maybe("cu_seqlens_k");
+  const int causal = a.int32("causal");
+  const float scale = a.real("scale");
+  Tensor ws = a.maybe("workspace");
+  const Tensor &st = a.maybe("dev_status");
+  const auto device = on_gpu(q, "q");
+  const at::Device dev = q.device();
+  const Attn s = attention_of(q, k, v, cu, cu_k, st, fn);
+  like(dout, "do", q, fn);
+  like(o, "o", q, fn);
+  need(lse, "lse", at::kFloat, dev, 2);
+  if (lse.size(0) != s.Tq || lse.size(1) != s.HQ) value_error("gdn_attention_bwd: lse must be [Tq, HQ]");
+  const Tensor dq = empty(q.sizes(), at::kBFloat16, dev), dk = empty(k.sizes(), at::kBFloat16, dev), dv = empty(v.sizes(), at::kBFloat16, dev);
+  if (ws.defined()) need(ws, "workspace", at::kByte, dev, 1);
+  else ws = empty({(int64_t)gdn_attention_bwd_workspace_size(s.N, s.Tq, s.Tk, s.HQ, s.HK, s.D)}, at::kByte, dev);
+  done(fn, gdn_attention_bwd(bf(dout), bf(q), s.ldq, bf(k), s.ldk, bf(v), s.ldv, bf(o), ptr<const float>(lse), ptr<const int32_t>(cu),
+                             ptr<const int32_t>(cu_k), s.N, s.Tq, s.Tk, s.HQ, s.HK, s.D, causal, scale, bf_out(dq), bf_out(dk),
+                             bf_out(dv), ptr<void>(ws), (size_t)ws.numel(), ptr<int32_t>(st), stream_of(dev)));
+  const Tensor out[3] = {dq, dk, dv};
+  return tuple_of(out);
+}
+
 PyObject *set_errors(Args &a) {  // the exceptions that this module raises beside Python's own
   for (PyObject **at : {&g_error, &g_memory_error}) {
     PyObject *o = a.next();
@@ -429,7 +513,8 @@ PyObject *set_errors(Args &a) {  // the exceptions that this module raises besid
 
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(norm_gate),  ENTRY(norm_gate_bwd), ENTRY(rope),      ENTRY(paged_plan),
-                           ENTRY(kv8_append), ENTRY(kv8_attention), ENTRY(set_errors), {nullptr, nullptr, 0, nullptr}};
+                           ENTRY(kv8_append), ENTRY(kv8_attention), ENTRY(attention_fwd), ENTRY(attention_bwd),
+                           ENTRY(set_errors), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_gdn_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,65 @@
+"""A training step's attention: the forward over packed sequences, and its gradients.  Same manner as ``stack.py``: the
+compiled module ``_gdn_torch`` checks the tensors, allocates outputs and passes raw pointers and the current stream to
+libgdn (``include/gdn.h``)."""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import load_library, stack
+
+__all__ = ["gdn_attention_fwd", "gdn_attention_bwd", "attention", "attention_bwd_workspace_size"]
+
+
+def gdn_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                      cu_seqlens_k: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
+                      o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      dev_status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Softmax attention of packed sequences: see include/gdn.h.
+
+    q bf16 [Tq, HQ, D], k, v bf16 [Tk, HK, D] (any token stride that is a multiple of 8), HQ a multiple of HK, D 64 or
+    128; cu_seqlens int32 [N + 1] (None: one sequence), cu_seqlens_k the keys' offsets where they are others (then the
+    last row of a sequence sees all of its keys under ``causal``).  Returns (o bf16 [Tq, HQ, D], lse fp32 [Tq, HQ])."""
+    return (stack._c or stack._load()).attention_fwd(q, k, v, cu_seqlens, cu_seqlens_k, 1 if causal else 0,
+                                                     -1.0 if scale is None else scale, o, lse, dev_status)
+
+
+def attention_bwd_workspace_size(N, Tq, Tk, HQ, HK, D) -> int:
+    """Bytes of workspace that gdn_attention_bwd needs for these sizes."""
+    return int(load_library().gdn_attention_bwd_workspace_size(N, Tq, Tk, HQ, HK, D))
+
+
+def gdn_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                      cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
+                      causal: bool = True, scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                      dev_status: Optional[torch.Tensor] = None):
+    """Gradients of gdn_attention_fwd: do, o bf16 [Tq, HQ, D] and lse fp32 [Tq, HQ] as it returned them, the rest as it
+    took them.  Returns (dq, dk, dv), bf16 and dense."""
+    return (stack._c or stack._load()).attention_bwd(do, q, k, v, o, lse, cu_seqlens, cu_seqlens_k, 1 if causal else 0,
+                                                     -1.0 if scale is None else scale, workspace, dev_status)
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, cu_seqlens_k, causal, scale):
+        o, lse = gdn_attention_fwd(q, k, v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, causal=causal, scale=scale)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
+        ctx.args = (causal, scale)
+        return o
+
+    @staticmethod
+    @once_differentiable  # the gradient kernels have no gradient of their own: a second derivative is an error
+    def backward(ctx, do):
+        q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
+        causal, scale = ctx.args
+        dq, dk, dv = gdn_attention_bwd(do.to(torch.bfloat16).contiguous(), q, k, v, o, lse, cu_seqlens=cu, cu_seqlens_k=cu_k,
+                                       causal=causal, scale=scale)
+        return dq, dk, dv, None, None, None, None
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+              cu_seqlens_k: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None) -> torch.Tensor:
+    """Differentiable (once) gdn_attention_fwd; returns o.  The forward keeps q, k, v, o and lse for the gradient."""
+    return _Attention.apply(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale)

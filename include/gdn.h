@@ -661,6 +661,64 @@ int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, co
                       int page_size, int max_q_len, int max_seq_len, float scale, uint16_t *o, float *lse,
                       void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A training step's attention.
+ */
+
+/*
+ * gdn_attention_fwd -- softmax attention of packed sequences.  Sequence n has the
+ * rows [cu_seqlens[n], cu_seqlens[n + 1]) of q and the keys [cu_seqlens_k[n],
+ * cu_seqlens_k[n + 1]) of k and v; row i of m sees the keys 0 .. L - m + i of its L
+ * with causal != 0 (the last row sees all of them), else every key.
+ *     o = softmax(scale q k^T) v,  lse = log sum exp(scale q k^T)
+ * A row that sees nothing has o = 0 and lse = -inf.  Two calls with the same
+ * arguments agree bit for bit.  The softmax weights enter the second product in
+ * bf16 (2^-8 of each at most), sums and maxima are fp32.
+ *   q             : bf16 [Tq, HQ, D], k, v: bf16 [Tk, HK, D]; ldq, ldk, ldv
+ *                   elements between tokens, heads dense; query head h reads kv
+ *                   head h / (HQ / HK)
+ *   cu_seqlens    : int32 [N + 1] device offsets (0, non-decreasing, at most Tq),
+ *                   or NULL: one sequence of all rows and keys (N = 1)
+ *   cu_seqlens_k  : the same of the keys (at most Tk), or NULL: those of the rows
+ *                   (then Tk = Tq)
+ *   causal        : 0 or 1
+ *   scale         : <= 0 or NaN selects 1/sqrt(D)
+ *   o             : bf16 [Tq, HQ, D];  lse: fp32 [Tq, HQ]
+ * Rows behind the last sequence see nothing.  Offsets that break the rules set
+ * GDN_DEV_BAD_CU_SEQLENS and the sequence is skipped (its rows are not written).
+ * What other sequences hold, NaN and infinities among it, does not reach a
+ * sequence; one of its own keys or values that is not finite may reach all of its
+ * rows.  D 64 or 128 (else GDN_EUNSUPPORTED, as for N or HQ > 65535); HQ % HK
+ * == 0; q, k, v and o must start on a 16-byte boundary and strides be multiples
+ * of 8 (else GDN_EINVAL).  Tq = 0 is a no-op.  One launch.
+ */
+int gdn_attention_fwd(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                      const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int N, int Tq, int Tk, int HQ, int HK, int D,
+                      int causal, float scale, uint16_t *o, float *lse, int32_t *dev_status, void *stream);
+
+/* gdn_attention_bwd_workspace_size -- bytes of device workspace gdn_attention_bwd needs. */
+size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, int D);
+
+/*
+ * gdn_attention_bwd -- gradients of gdn_attention_fwd.  The probabilities are formed
+ * again from lse: P = exp(scale q k^T - lse); with delta = sum_d dout o,
+ *     dv = P^T dout,  dS = P (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q
+ * summed over a group's query heads for dk and dv.
+ *   dout, o       : bf16 [Tq, HQ, D], lse: fp32 [Tq, HQ]: the gradient of o, and
+ *                   what the forward returned
+ *   dq            : bf16 [Tq, HQ, D];  dk, dv: bf16 [Tk, HK, D], dense
+ *   workspace     : gdn_attention_bwd_workspace_size() bytes, 16-byte aligned
+ * Everything else as in gdn_attention_fwd; rows and keys behind the last sequence
+ * have zero gradients.  P and dS enter the products in bf16, sums are fp32 and have a
+ * fixed order: two calls agree bit for bit.  dout, o, dq, dk, dv must start on a
+ * 16-byte boundary; GDN_EWORKSPACE for a small workspace.  Three launches, four
+ * where few keys are cut between more blocks.
+ */
+int gdn_attention_bwd(const uint16_t *dout, const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
+                      int64_t ldv, const uint16_t *o, const float *lse, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                      int N, int Tq, int Tk, int HQ, int HK, int D, int causal, float scale, uint16_t *dq, uint16_t *dk,
+                      uint16_t *dv, void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
