@@ -32,7 +32,8 @@ __all__ = ["gdn_gating", "gdn_chunk_fwd", "gdn_recurrent_decode", "chunk_fwd_wor
            "testing_force_wait_expiry", "DEV_NO_PAGE", "DEV_BAD_SEQ_LEN",
            "gdn_norm_gate", "gdn_norm_gate_bwd", "norm_gate", "gdn_rope", "rotary_embedding", "rope_frequencies",
            "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention", "kv8_attention_workspace_size",
-           "gdn_attention_fwd", "gdn_attention_bwd", "attention", "attention_bwd_workspace_size"]
+           "gdn_attention_fwd", "gdn_attention_bwd", "attention", "attention_bwd_workspace_size",
+           "gdn_act8_save", "gdn_act8_load", "linear8", "gdn_norm_gate_save8", "gdn_norm_gate_bwd8"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libgdn.so")
@@ -53,7 +54,8 @@ EXPORTED_SYMBOLS = ("gdn_status_string", "gdn_version", "gdn_gating", "gdn_chunk
                     "gdn_causal_conv1d_update_spec",
                     "gdn_norm_gate", "gdn_norm_gate_bwd_workspace_size", "gdn_norm_gate_bwd", "gdn_rope",
                     "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention_workspace_size", "gdn_kv8_attention",
-                    "gdn_attention_fwd", "gdn_attention_bwd_workspace_size", "gdn_attention_bwd")
+                    "gdn_attention_fwd", "gdn_attention_bwd_workspace_size", "gdn_attention_bwd",
+                    "gdn_act8_save", "gdn_act8_load", "gdn_norm_gate_save8", "gdn_norm_gate_bwd8")
 
 #: Size of the fixed scratch buffer behind gdn_chunk_fwd_noalloc (bytes).
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -139,6 +141,14 @@ def load_library():
         lib.gdn_kv8_attention_workspace_size.restype = SZ
         lib.gdn_kv8_attention.argtypes = [P, I64, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P, P]
         lib.gdn_kv8_attention.restype = I
+        lib.gdn_act8_save.argtypes = [P, I64, I, I64, I64, P, P, P]
+        lib.gdn_act8_save.restype = I
+        lib.gdn_act8_load.argtypes = [P, P, I64, I, P, P]
+        lib.gdn_act8_load.restype = I
+        lib.gdn_norm_gate_save8.argtypes = [P, P, P, P, F, F, I, I64, I, I64, I64, P, P, P, P, P, P, P]
+        lib.gdn_norm_gate_save8.restype = I
+        lib.gdn_norm_gate_bwd8.argtypes = [P, P, P, P, P, P, P, F, F, I, I64, I, P, P, P, P, P, SZ, P]
+        lib.gdn_norm_gate_bwd8.restype = I
         lib.gdn_attention_fwd.argtypes = [P, I64, P, I64, P, I64, P, P, I, I, I, I, I, I, I, F, P, P, P, P]
         lib.gdn_attention_fwd.restype = I
         lib.gdn_attention_bwd_workspace_size.argtypes = [I, I, I, I, I, I]
@@ -717,6 +727,7 @@ def chunk_gated_delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
 
 
 # Norms, rotary positions and the paged 8-bit cache (after the helpers above, which they use).
-from .stack import (gdn_kv8_append, gdn_kv8_attention, gdn_norm_gate, gdn_norm_gate_bwd, gdn_paged_plan,  # noqa: E402
-                    gdn_rope, kv8_attention_workspace_size, norm_gate, rope_frequencies, rotary_embedding)
-from .train import attention, attention_bwd_workspace_size, gdn_attention_bwd, gdn_attention_fwd  # noqa: E402
+from .stack import (gdn_kv8_append, gdn_kv8_attention, gdn_norm_gate, gdn_norm_gate_bwd, gdn_norm_gate_bwd8,  # noqa: E402
+                    gdn_norm_gate_save8, gdn_paged_plan, gdn_rope, kv8_attention_workspace_size, norm_gate, rope_frequencies, rotary_embedding)
+from .train import (attention, attention_bwd_workspace_size, gdn_act8_load, gdn_act8_save, gdn_attention_bwd,  # noqa: E402
+                    gdn_attention_fwd, linear8)

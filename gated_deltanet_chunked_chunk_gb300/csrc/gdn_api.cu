@@ -394,6 +394,56 @@ int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, co
   return cuda_status(gdn_host::launch_kv8_attn(a, static_cast<cudaStream_t>(stream)));
 }
 
+int gdn_act8_save(const uint16_t *x, int64_t rows, int D, int64_t x_rows, int64_t x_stride, uint8_t *codes, float *scale,
+                  void *stream) {
+  if (rows < 0 || D <= 0 || x_rows < 0) return GDN_EINVAL;
+  if (rows == 0) return GDN_OK;
+  if (!x || !codes || !scale) return GDN_EINVAL;
+  return cuda_status(gdn_host::launch_act8_save(x, rows, D, x_rows, x_rows ? x_stride : 0, codes, scale, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_act8_load(const uint8_t *codes, const float *scale, int64_t rows, int D, uint16_t *y, void *stream) {
+  if (rows < 0 || D <= 0) return GDN_EINVAL;
+  if (rows == 0) return GDN_OK;
+  if (!codes || !scale || !y) return GDN_EINVAL;
+  return cuda_status(gdn_host::launch_act8_load(codes, scale, rows, D, y, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_norm_gate_save8(const uint16_t *x, const uint16_t *residual, const uint16_t *z, const float *weight, float res_scale,
+                        float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride, uint16_t *y,
+                        uint16_t *h, uint8_t *h_codes, float *h_scale, uint8_t *z_codes, float *z_scale, void *stream) {
+  if (rows < 0 || D <= 0 || activation < 0 || activation > 2 || !(eps >= 0.f)) return GDN_EINVAL;
+  if (!gdn_host::norm8_takes(D)) return GDN_EUNSUPPORTED;
+  if (rows == 0) return GDN_OK;
+  if ((activation != 0) != (z != nullptr) || (residual != nullptr) != (h != nullptr)) return GDN_EINVAL;
+  if ((activation != 0) != (z_codes != nullptr) || (activation != 0) != (z_scale != nullptr)) return GDN_EINVAL;
+  if (!x || !weight || !y || !h_codes || !h_scale || (z && z_rows < 0)) return GDN_EINVAL;
+  if (z_rows == 0) z_stride = 0;
+  if (z_stride % 8 || !aligned16({x, residual, z, y, h, h_codes, z_codes})) return GDN_EINVAL;
+  return cuda_status(gdn_host::launch_norm8_fwd(x, residual, z, weight, res_scale, eps, activation, rows, D, z_rows, z_stride, y, h,
+                                                h_codes, h_scale, z_codes, z_scale, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_norm_gate_bwd8(const uint16_t *dy, const uint8_t *h_codes, const float *h_scale, const uint8_t *z_codes,
+                       const float *z_scale, const uint16_t *dh, const float *weight, float res_scale, float eps,
+                       int activation, int64_t rows, int D, uint16_t *dx, uint16_t *dresidual, uint16_t *dz, float *dweight,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+  if (rows < 0 || D <= 0 || activation < 0 || activation > 2 || !(eps >= 0.f)) return GDN_EINVAL;
+  if (!gdn_host::norm8_takes(D)) return GDN_EUNSUPPORTED;
+  if (!dweight) return GDN_EINVAL;
+  if (rows > 0) {  // the pointers of empty tensors are null
+    const bool gate = activation != 0;
+    if (gate != (z_codes != nullptr) || gate != (z_scale != nullptr) || gate != (dz != nullptr)) return GDN_EINVAL;
+    if ((dh != nullptr) != (dresidual != nullptr) || !dy || !h_codes || !h_scale || !weight || !dx) return GDN_EINVAL;
+    if (!aligned16({dy, h_codes, z_codes, dh, dx, dresidual, dz})) return GDN_EINVAL;
+  }
+  const size_t need = gdn_host::norm_bwd_workspace_bytes(rows, D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_EWORKSPACE;
+  if (!aligned16({workspace})) return GDN_EINVAL;
+  return cuda_status(gdn_host::launch_norm8_bwd(dy, h_codes, h_scale, z_codes, z_scale, dh, weight, res_scale, eps, activation, rows,
+                                                D, dx, dresidual, dz, dweight, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 // Checks that both directions of training attention share.
 static int attention_args(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
                           const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int N, int Tq, int Tk, int HQ, int HK, int D,

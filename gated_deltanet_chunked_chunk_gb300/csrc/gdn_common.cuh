@@ -261,6 +261,18 @@ struct Kv8AttnArgs {
 };
 size_t kv8_attn_workspace_bytes(int N, int T, int G, int D, int max_q);
 cudaError_t launch_kv8_attn(const Kv8AttnArgs &a, cudaStream_t s);
+// The norm with 8-bit codes of h and z (gdn_norm8.cu), scales [rows][ceil(D / 128)], and
+// activations as such codes (gdn_act8.cu).
+bool norm8_takes(int D);
+cudaError_t launch_norm8_fwd(const uint16_t *x, const uint16_t *res, const uint16_t *z, const float *w, float res_scale,
+                             float eps, int act, int64_t rows, int D, int64_t z_group, int64_t z_stride, uint16_t *y,
+                             uint16_t *h, uint8_t *h8, float *hs, uint8_t *z8, float *zs, cudaStream_t s);
+cudaError_t launch_norm8_bwd(const uint16_t *dy, const uint8_t *h8, const float *hs, const uint8_t *z8, const float *zs,
+                             const uint16_t *dh, const float *w, float res_scale, float eps, int act, int64_t rows, int D,
+                             uint16_t *dx, uint16_t *dres, uint16_t *dz, float *dw, void *ws, cudaStream_t s);
+cudaError_t launch_act8_save(const uint16_t *x, int64_t rows, int D, int64_t x_group, int64_t x_stride, uint8_t *codes,
+                             float *scale, cudaStream_t s);
+cudaError_t launch_act8_load(const uint8_t *codes, const float *scale, int64_t rows, int D, uint16_t *y, cudaStream_t s);
 // Attention of packed sequences for training (gdn_attn_fwd.cu, gdn_attn_bwd.cu).
 struct TrainAttnArgs {
   const uint16_t *q, *k, *v;

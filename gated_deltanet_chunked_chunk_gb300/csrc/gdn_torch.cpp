@@ -17,6 +17,7 @@
 
 #include <cstdio>
 #include <string>
+#include <vector>
 
 #include "../../include/gdn.h"
 
@@ -184,12 +185,10 @@ struct Gate {
   int act;
   int64_t rows, stride;  // 0: dense
 };
-Gate gate_of(const Tensor &z, const Tensor &x, int act, const char *fn) {
-  if (!z.defined()) return {0, 0, 0};
-  if (act == 0) value_error(std::string(fn) + ": a gate z needs an activation");
-  kind(z, "z", at::kBFloat16, x.device());
-  if (z.sizes() != x.sizes()) value_error(std::string(fn) + ": z must have the shape of x, " + shape_text(x));
-  if (z.is_contiguous()) return {act, 0, 0};
+// Where the rows of a tensor lie: dense, or [.., heads, D] / [.., D] with one longer
+// stride between its tokens.
+Gate rows_of(const Tensor &z, const char *name, const char *fn) {
+  if (z.is_contiguous()) return {0, 0, 0};
   // From the last dimension on: those that lie densely make a group (the heads of a
   // token), those before them one walk from group to group.
   int64_t i = z.dim() - 1, dense = 1, rows = 1;
@@ -204,8 +203,16 @@ Gate gate_of(const Tensor &z, const Tensor &x, int act, const char *fn) {
     even = even && (z.size(i) == 1 || z.stride(i) == next);
     next *= z.size(i);
   }
-  if (!even) value_error(std::string(fn) + ": z must be dense, or [.., heads, D] / [.., D] with one longer stride between its tokens");
-  return {act, rows, stride};
+  if (!even) value_error(std::string(fn) + ": " + name + " must be dense, or [.., heads, D] / [.., D] with one longer stride between its tokens");
+  return {0, rows, stride};
+}
+Gate gate_of(const Tensor &z, const Tensor &x, int act, const char *fn) {
+  if (!z.defined()) return {0, 0, 0};
+  if (act == 0) value_error(std::string(fn) + ": a gate z needs an activation");
+  kind(z, "z", at::kBFloat16, x.device());
+  if (z.sizes() != x.sizes()) value_error(std::string(fn) + ": z must have the shape of x, " + shape_text(x));
+  const Gate g = rows_of(z, "z", fn);
+  return {act, g.rows, g.stride};
 }
 void like(const Tensor &t, const char *name, const Tensor &x, const char *fn) {
   need(t, name, at::kBFloat16, x.device(), -1);
@@ -417,6 +424,116 @@ PyObject *kv8_attention(Args &a) {
   return wrap(o);
 }
 
+// ---------------------------------------------------- activations in 8 bits
+std::vector<int64_t> scales_of(const Tensor &x) {
+  std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+  shape.back() = (shape.back() + 127) / 128;
+  return shape;
+}
+void coded(const Tensor &codes, const Tensor &scale, const char *name, const char *scale_name, const at::Device &dev, const char *fn) {
+  need(codes, name, at::kFloat8_e4m3fn, dev, -1);
+  need(scale, scale_name, at::kFloat, dev, -1);
+  if (codes.dim() < 1 || codes.size(-1) < 1) value_error(std::string(fn) + ": " + name + " must be [.., D], got " + shape_text(codes));
+  const std::vector<int64_t> want = scales_of(codes);
+  if (scale.sizes() != at::IntArrayRef(want)) value_error(std::string(fn) + ": " + scale_name + " must be [.., ceil(D / 128)]");
+}
+int64_t rows_in(const Tensor &x) {  // of the last dimension's size
+  int64_t n = 1;
+  for (int64_t i = 0; i + 1 < x.dim(); ++i) n *= x.size(i);
+  return n;
+}
+
+PyObject *act8_save(Args &a) {
+  const char *fn = "gdn_act8_save";
+  const Tensor &x = a.tensor("x");
+  Tensor codes = a.maybe("codes"), scale = a.maybe("scale");
+  const auto device = on_gpu(x, "x");
+  const at::Device dev = x.device();
+  kind(x, "x", at::kBFloat16, dev);
+  if (x.dim() < 1 || x.size(-1) < 1) value_error(std::string(fn) + ": x must be [.., D], got " + shape_text(x));
+  const Gate g = rows_of(x, "x", fn);
+  if (!codes.defined()) codes = empty(x.sizes(), at::kFloat8_e4m3fn, dev);
+  else if (codes.sizes() != x.sizes()) value_error(std::string(fn) + ": codes must have the shape " + shape_text(x));
+  if (!scale.defined()) scale = empty(scales_of(x), at::kFloat, dev);
+  coded(codes, scale, "codes", "scale", dev, fn);
+  done(fn, gdn_act8_save(bf(x), rows_in(x), fits32(x.size(-1), "D"), g.rows, g.stride, ptr<uint8_t>(codes), ptr<float>(scale),
+                         stream_of(dev)));
+  const Tensor out[2] = {codes, scale};
+  return tuple_of(out);
+}
+
+PyObject *act8_load(Args &a) {
+  const char *fn = "gdn_act8_load";
+  const Tensor &codes = a.tensor("codes"), &scale = a.tensor("scale");
+  Tensor y = a.maybe("out");
+  const auto device = on_gpu(codes, "codes");
+  const at::Device dev = codes.device();
+  coded(codes, scale, "codes", "scale", dev, fn);
+  if (y.defined()) like(y, "out", codes, fn);
+  else y = empty(codes.sizes(), at::kBFloat16, dev);
+  done(fn, gdn_act8_load(ptr<const uint8_t>(codes), ptr<const float>(scale), rows_in(codes), fits32(codes.size(-1), "D"), bf_out(y),
+                         stream_of(dev)));
+  return wrap(y);
+}
+
+PyObject *norm_gate_save8(Args &a) {
+  const char *fn = "gdn_norm_gate_save8";
+  const Tensor &x = a.tensor("x"), &w = a.tensor("weight"), &res = a.maybe("residual"), &z = a.maybe("z");
+  const int act = a.int32("activation");
+  const float eps = a.real("eps"), rs = a.real("res_scale");
+  const auto device = on_gpu(x, "x");
+  const at::Device dev = x.device();
+  need(x, "x", at::kBFloat16, dev, -1);
+  const int D = width_of(x, w, fn);
+  const Gate g = gate_of(z, x, act, fn);
+  if (res.defined()) like(res, "residual", x, fn);
+  const std::vector<int64_t> groups = scales_of(x);
+  const Tensor y = empty(x.sizes(), at::kBFloat16, dev), h = res.defined() ? empty(x.sizes(), at::kBFloat16, dev) : Tensor();
+  const Tensor h8 = empty(x.sizes(), at::kFloat8_e4m3fn, dev), hs = empty(groups, at::kFloat, dev);
+  const Tensor z8 = g.act ? empty(x.sizes(), at::kFloat8_e4m3fn, dev) : Tensor(), zs = g.act ? empty(groups, at::kFloat, dev) : Tensor();
+  done(fn, gdn_norm_gate_save8(bf(x), bf(res), g.act ? bf(z) : nullptr, ptr<const float>(w), rs, eps, g.act, x.numel() / D, D, g.rows,
+                               g.stride, bf_out(y), bf_out(h), ptr<uint8_t>(h8), ptr<float>(hs), ptr<uint8_t>(z8), ptr<float>(zs),
+                               stream_of(dev)));
+  const Tensor out[6] = {y, h, h8, hs, z8, zs};
+  return tuple_of(out);
+}
+
+PyObject *norm_gate_bwd8(Args &a) {
+  const char *fn = "gdn_norm_gate_bwd8";
+  const Tensor &dy = a.tensor("dy"), &h8 = a.tensor("h_codes"), &hs = a.tensor("h_scale"), &w = a.tensor("weight");
+  const Tensor &z8 = a.maybe("z_codes"), &zs = a.maybe("z_scale"), &dh = a.maybe("dh");
+  const int act = a.int32("activation");
+  const float eps = a.real("eps"), rs = a.real("res_scale");
+  Tensor ws = a.maybe("workspace");
+  const auto device = on_gpu(dy, "dy");
+  const at::Device dev = dy.device();
+  need(dy, "dy", at::kBFloat16, dev, -1);
+  const int D = width_of(dy, w, fn);
+  auto coded_like = [&](const Tensor &codes, const Tensor &scale, const char *name, const char *scale_name) {
+    coded(codes, scale, name, scale_name, dev, fn);
+    if (codes.sizes() != dy.sizes()) value_error(std::string(fn) + ": " + name + " must have the shape " + shape_text(dy));
+  };
+  coded_like(h8, hs, "h_codes", "h_scale");
+  if (z8.defined() != zs.defined()) value_error(std::string(fn) + ": z_codes and z_scale belong together");
+  if (z8.defined()) {
+    if (act == 0) value_error(std::string(fn) + ": a gate z needs an activation");
+    coded_like(z8, zs, "z_codes", "z_scale");
+  }
+  if (dh.defined()) like(dh, "dh", dy, fn);
+  const int used = z8.defined() ? act : 0;
+  const Tensor dx = empty(dy.sizes(), at::kBFloat16, dev), dw = empty(w.sizes(), at::kFloat, dev);
+  const Tensor dres = dh.defined() ? empty(dy.sizes(), at::kBFloat16, dev) : Tensor();
+  const Tensor dz = used ? empty(dy.sizes(), at::kBFloat16, dev) : Tensor();
+  const int64_t rows = dy.numel() / D;
+  if (ws.defined()) need(ws, "workspace", at::kByte, dev, 1);
+  else ws = empty({(int64_t)gdn_norm_gate_bwd_workspace_size(rows, D)}, at::kByte, dev);
+  done(fn, gdn_norm_gate_bwd8(bf(dy), ptr<const uint8_t>(h8), ptr<const float>(hs), ptr<const uint8_t>(z8), ptr<const float>(zs), bf(dh),
+                              ptr<const float>(w), rs, eps, used, rows, D, bf_out(dx), bf_out(dres), bf_out(dz), ptr<float>(dw),
+                              ptr<void>(ws), (size_t)ws.numel(), stream_of(dev)));
+  const Tensor out[4] = {dx, dres, dz, dw};
+  return tuple_of(out);
+}
+
 // ---------------------------------------------------- training attention
 struct Attn {
   int64_t ldq, ldk, ldv;
@@ -514,6 +631,7 @@ PyObject *set_errors(Args &a) {  // the exceptions that this module raises besid
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(norm_gate),  ENTRY(norm_gate_bwd), ENTRY(rope),      ENTRY(paged_plan),
                            ENTRY(kv8_append), ENTRY(kv8_attention), ENTRY(attention_fwd), ENTRY(attention_bwd),
+                           ENTRY(act8_save),  ENTRY(act8_load),  ENTRY(norm_gate_save8), ENTRY(norm_gate_bwd8),
                            ENTRY(set_errors), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_gdn_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

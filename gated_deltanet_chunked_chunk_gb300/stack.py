@@ -18,7 +18,8 @@ from torch.autograd.function import once_differentiable
 
 from . import GDNError, lib_path, load_library
 
-__all__ = ["gdn_norm_gate", "gdn_norm_gate_bwd", "norm_gate", "gdn_rope", "rotary_embedding", "rope_frequencies",
+__all__ = ["gdn_norm_gate", "gdn_norm_gate_bwd", "norm_gate", "gdn_norm_gate_save8", "gdn_norm_gate_bwd8", "gdn_rope",
+           "rotary_embedding", "rope_frequencies",
            "gdn_paged_plan", "gdn_kv8_append", "gdn_kv8_attention", "kv8_attention_workspace_size", "KV8_PAGE_SIZES",
            "KV8_EXP_MIN"]
 
@@ -105,9 +106,48 @@ class _NormGate(torch.autograd.Function):
         return dx, dw, dres, dz, None, None, None
 
 
-def norm_gate(x, weight, residual=None, z=None, activation="silu", eps: float = 1e-6, res_scale: float = 1.0):
-    """Differentiable (once) gdn_norm_gate: returns (y, h), h None without a residual; gradients for x, weight, residual, z."""
-    out = _NormGate.apply(x, weight, residual, z, activation, eps, res_scale)
+def gdn_norm_gate_save8(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                        z: Optional[torch.Tensor] = None, activation="silu", eps: float = 1e-6, res_scale: float = 1.0):
+    """gdn_norm_gate that also writes 8-bit codes of what its backward needs (``gdn_act8_save``): returns (y, h, h_codes,
+    h_scale, z_codes, z_scale), the last two None without a gate.  D a multiple of 8, at most 16384."""
+    return (_c or _load()).norm_gate_save8(x, weight, residual, z, _act_of(activation, "gdn_norm_gate_save8"), eps, res_scale)
+
+
+def gdn_norm_gate_bwd8(dy: torch.Tensor, h_codes: torch.Tensor, h_scale: torch.Tensor, weight: torch.Tensor,
+                       z_codes: Optional[torch.Tensor] = None, z_scale: Optional[torch.Tensor] = None,
+                       dh: Optional[torch.Tensor] = None, activation="silu", eps: float = 1e-6, res_scale: float = 1.0,
+                       workspace: Optional[torch.Tensor] = None):
+    """gdn_norm_gate_bwd at the values that the codes of gdn_norm_gate_save8 stand for; the same results, (dx, dresidual,
+    dz, dweight)."""
+    return (_c or _load()).norm_gate_bwd8(dy, h_codes, h_scale, weight, z_codes, z_scale, dh,
+                                          _act_of(activation, "gdn_norm_gate_bwd8"), eps, res_scale, workspace)
+
+
+class _NormGate8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, z, activation, eps, res_scale):
+        y, h, *codes = gdn_norm_gate_save8(x, weight, residual=residual, z=z, activation=activation, eps=eps, res_scale=res_scale)
+        ctx.save_for_backward(weight, *codes)
+        ctx.args = (activation, eps, 1.0 if residual is None else res_scale, residual is not None)
+        return y if h is None else (y, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        weight, h8, hs, z8, zs = ctx.saved_tensors
+        activation, eps, res_scale, has_res = ctx.args
+        dy = dy.to(torch.bfloat16).contiguous()
+        if has_res:
+            dh = torch.zeros_like(dy) if dh is None else dh.to(torch.bfloat16).contiguous()
+        dx, dres, dz, dw = gdn_norm_gate_bwd8(dy, h8, hs, weight, z_codes=z8, z_scale=zs, dh=dh if has_res else None,
+                                              activation=activation, eps=eps, res_scale=res_scale)
+        return dx, dw, dres, dz, None, None, None
+
+
+def norm_gate(x, weight, residual=None, z=None, activation="silu", eps: float = 1e-6, res_scale: float = 1.0, save8: bool = False):
+    """Differentiable (once) gdn_norm_gate: returns (y, h), h None without a residual; gradients for x, weight, residual, z.
+    With ``save8`` the forward keeps 8-bit codes of h and z for the gradient instead of the tensors themselves."""
+    out = (_NormGate8 if save8 else _NormGate).apply(x, weight, residual, z, activation, eps, res_scale)
     return out if isinstance(out, tuple) else (out, None)
 
 

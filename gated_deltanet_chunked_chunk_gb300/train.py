@@ -1,6 +1,6 @@
-"""A training step's attention: the forward over packed sequences, and its gradients.  Same manner as ``stack.py``: the
-compiled module ``_gdn_torch`` checks the tensors, allocates outputs and passes raw pointers and the current stream to
-libgdn (``include/gdn.h``)."""
+"""A training step: attention of packed sequences with its gradients, and activations kept in 8 bits.  Same manner as
+``stack.py``: the compiled module ``_gdn_torch`` checks the tensors, allocates outputs and passes raw pointers and the
+current stream to libgdn (``include/gdn.h``)."""
 from __future__ import annotations
 
 from typing import Optional, Tuple
@@ -10,7 +10,48 @@ from torch.autograd.function import once_differentiable
 
 from . import load_library, stack
 
-__all__ = ["gdn_attention_fwd", "gdn_attention_bwd", "attention", "attention_bwd_workspace_size"]
+__all__ = ["gdn_attention_fwd", "gdn_attention_bwd", "attention", "attention_bwd_workspace_size", "gdn_act8_save",
+           "gdn_act8_load", "linear8", "ACT8_GROUP"]
+
+#: Elements of a row that share a scale.
+ACT8_GROUP = 128
+
+
+# ----------------------------------------------------- activations in 8 bits
+def gdn_act8_save(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """8-bit codes of x bf16 [..., D] (dense, or with a longer stride between its tokens): (codes float8_e4m3fn [..., D],
+    scale fp32 [..., ceil(D / 128)]), one power of two for each 128 elements of a row.  See include/gdn.h."""
+    return (stack._c or stack._load()).act8_save(x, codes, scale)
+
+
+def gdn_act8_load(codes: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that codes and scales stand for, bf16 [..., D]."""
+    return (stack._c or stack._load()).act8_load(codes, scale, out)
+
+
+class _Linear8(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight):
+        ctx.save_for_backward(weight, *(gdn_act8_save(x) if ctx.needs_input_grad[1] else ()))
+        return x @ weight.T
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        weight, *kept = ctx.saved_tensors
+        dx = dy @ weight if ctx.needs_input_grad[0] else None
+        dw = dy.flatten(0, -2).T @ gdn_act8_load(*kept).flatten(0, -2) if kept else None
+        return dx, dw
+
+
+def linear8(x: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
+    """x @ weight.T (x bf16 [..., in], weight bf16 [out, in]), differentiable once, that keeps x in 8 bits for the weight's
+    gradient."""
+    return _Linear8.apply(x, weight)
+
+
+# -------------------------------------------------------------- attention
 
 
 def gdn_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,

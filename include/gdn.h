@@ -662,8 +662,56 @@ int gdn_kv8_attention(const uint16_t *q, int64_t ldq, const uint8_t *k_cache, co
                       void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /* ------------------------------------------------------------------------
- * A training step's attention.
+ * A training step: activations kept in 8 bits, and attention.
  */
+
+/*
+ * Activations as 8-bit codes: codes e4m3 [rows, D], scale fp32 [rows, ceil(D / 128)],
+ * value = code * scale of its group of 128 consecutive elements of the row (the last
+ * group of a row may be shorter).
+ *
+ * gdn_act8_save -- for each group
+ *     scale = 2^e, e the least exponent >= -60 with every finite |x| <= 448 2^e
+ *     codes = x 2^-e rounded to e4m3 (to nearest, ties to even); what is not finite
+ *             becomes NaN
+ *   x : bf16, row r at (r / x_rows) x_stride + (r % x_rows) D elements: a dense [rows,
+ *       D] with x_rows = 0, or a slice of a wider tensor ([tokens, x_rows heads, D] with
+ *       x_stride elements between tokens)
+ * Any D >= 1; rows of D % 8 == 0 on 16-byte boundaries (x_stride % 8 == 0, codes on 8)
+ * move in 16-byte accesses, others element by element.  rows = 0 is a no-op.  One launch.
+ */
+int gdn_act8_save(const uint16_t *x, int64_t rows, int D, int64_t x_rows, int64_t x_stride, uint8_t *codes, float *scale,
+                  void *stream);
+
+/*
+ * gdn_act8_load -- the values back: y bf16 [rows, D] = code * scale (any finite scale),
+ * exact for the scales that gdn_act8_save writes but for values below bf16's range.
+ * One launch.
+ */
+int gdn_act8_load(const uint8_t *codes, const float *scale, int64_t rows, int D, uint16_t *y, void *stream);
+
+/*
+ * gdn_norm_gate_save8 -- gdn_norm_gate that also writes the codes of what its backward
+ * needs, as gdn_act8_save would: h_codes, h_scale of what was normed (the stream as it
+ * is stored to h; x without a residual), z_codes, z_scale of the gate (NULL without one).
+ * y and h are those of gdn_norm_gate.  Codes are dense.  D % 8 == 0, at most 16384 (else
+ * GDN_EUNSUPPORTED); x, residual, z, y, h and the codes must start on a 16-byte boundary
+ * and z_stride be a multiple of 8 (else GDN_EINVAL).  One launch.
+ */
+int gdn_norm_gate_save8(const uint16_t *x, const uint16_t *residual, const uint16_t *z, const float *weight, float res_scale,
+                        float eps, int activation, int64_t rows, int D, int64_t z_rows, int64_t z_stride, uint16_t *y,
+                        uint16_t *h, uint8_t *h_codes, float *h_scale, uint8_t *z_codes, float *z_scale, void *stream);
+
+/*
+ * gdn_norm_gate_bwd8 -- gdn_norm_gate_bwd with h and z given as codes and scales: the
+ * gradients at the values that these stand for.  Everything else, the workspace's size
+ * and the fixed order of sums among it, as there; D and boundaries as in
+ * gdn_norm_gate_save8 (dy, dh and the gradients among them).
+ */
+int gdn_norm_gate_bwd8(const uint16_t *dy, const uint8_t *h_codes, const float *h_scale, const uint8_t *z_codes,
+                       const float *z_scale, const uint16_t *dh, const float *weight, float res_scale, float eps,
+                       int activation, int64_t rows, int D, uint16_t *dx, uint16_t *dresidual, uint16_t *dz, float *dweight,
+                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * gdn_attention_fwd -- softmax attention of packed sequences.  Sequence n has the

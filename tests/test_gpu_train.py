@@ -8,9 +8,11 @@ hardware's exponential; delta and dP likewise.  2^-15 (1 + M) of the terms' magn
 takes o in bf16, as the forward gave it: delta is off by 2^-8 sum |do o|, which is a term like the rounded ones."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
+import stack_util as S
 import train_util as U
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +105,128 @@ def test_forward(case, causal):
 @pytest.mark.parametrize("case", range(len(SIZES)))
 def test_gradients(case, causal):
     _run(*SIZES[case], causal, 100 + case)
+
+
+# ----------------------------------------------------- activations in 8 bits
+# Codes, scales and their values are exact: they are compared for equality.
+
+def _codes(x):
+    """Values of the codes, and scales, of a float64 array [rows, D] by the definition."""
+    rows, D = x.shape
+    codes, scale = np.zeros_like(x), np.zeros((rows, -(-D // 128)))
+    for r in range(rows):
+        for g in range(scale.shape[1]):
+            part = x[r, 128 * g:128 * g + 128]
+            fin = np.abs(part[np.isfinite(part)])
+            e = S.least_exponent(float(fin.max()) if fin.size else 0.0)
+            scale[r, g] = 2.0 ** e
+            codes[r, 128 * g:128 * g + 128] = np.where(np.isfinite(part), S.to_e4m3(np.where(np.isfinite(part), part, 0) * 2.0 ** -e), np.nan)
+    return codes, scale
+
+
+def _same(got, ref):
+    np.testing.assert_array_equal(S.f64(got).reshape(ref.shape), ref)
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (3, 7), (5, 64), (7, 96), (33, 128), (4, 3, 136), (2, 5, 1000), (3, 4096), (9, 130), (1000, 8),
+                                   (2, 257), (70, 1, 256)])
+def test_act8(shape):
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(sum(shape))
+    x = (torch.randn(shape, generator=g) * torch.exp(2 * torch.randn(shape[:-1] + (1,), generator=g))).to(BF)
+    codes, scale = gdn.gdn_act8_save(x.cuda())
+    ref, rs = _codes(S.f64(x).reshape(-1, shape[-1]))
+    assert codes.shape == x.shape and scale.shape == x.shape[:-1] + (-(-shape[-1] // 128),)
+    _same(codes, ref)
+    _same(scale, rs)
+    y = gdn.gdn_act8_load(codes, scale)
+    _same(y, ref * np.repeat(rs, 128, 1)[:, :shape[-1]])
+    # from a slice of a wider tensor, and into buffers of the caller's
+    wide = torch.full(shape[:-1] + (shape[-1] + 24,), math.nan, dtype=BF)
+    wide[..., 8:8 + shape[-1]] = x
+    part = wide.cuda()[..., 8:8 + shape[-1]]
+    if len(shape) == 2:
+        c2, s2 = torch.empty_like(codes), torch.empty_like(scale)
+        assert gdn.gdn_act8_save(part, codes=c2, scale=s2)[0] is not None
+        assert torch.equal(c2.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(s2, scale)
+
+
+def test_act8_of_heads_within_a_token_and_of_odd_addresses():
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(5)
+    w = torch.randn(37, 4 * 96 + 16, generator=g).to(BF).cuda()
+    x = w[:, 16:].unflatten(1, (4, 96))
+    codes, scale = gdn.gdn_act8_save(x)
+    ref, rs = _codes(S.f64(x).reshape(-1, 96))
+    _same(codes, ref)
+    _same(scale, rs)
+    odd = torch.empty(x.numel() + 1, dtype=BF, device="cuda")[1:].view(37, 4, 96)  # 2-byte aligned
+    odd.copy_(x)
+    c2, s2 = gdn.gdn_act8_save(odd)
+    assert torch.equal(c2.view(torch.uint8), codes.view(torch.uint8)) and torch.equal(s2, scale)
+    c3 = torch.empty(codes.numel() + 1, dtype=torch.uint8, device="cuda")[1:].view(codes.shape)
+    c3.copy_(codes.view(torch.uint8))
+    assert torch.equal(gdn.gdn_act8_load(c3.view(torch.float8_e4m3fn), scale, out=torch.empty_like(odd)), gdn.gdn_act8_load(codes, scale))
+
+
+@pytest.mark.parametrize("D", [128, 100, 8])
+def test_act8_of_extremes(D):
+    gdn = _gdn()
+    x = torch.zeros(9, D)
+    x[1, 0], x[1, 1] = math.inf, 1.0
+    x[2, 3], x[2, 4] = -math.inf, math.nan
+    x[3] = math.nan
+    x[4, 0], x[4, 5] = 3.3895313892515355e38, -1.0  # the largest bf16
+    x[5, 0], x[5, 1] = 1e-38, 9.2e-41               # below what the smallest scale holds
+    x[6, 0], x[6, 1] = 448.0, 449.0
+    x[7, 0] = -448.0
+    x[8] = torch.linspace(-1.0, 1.0, D)
+    x = x.to(BF)
+    codes, scale = gdn.gdn_act8_save(x.cuda())
+    ref, rs = _codes(S.f64(x))
+    _same(codes, ref)
+    _same(scale, rs)
+    _same(gdn.gdn_act8_load(codes, scale), S.f64(torch.from_numpy(ref * rs).to(BF)))
+
+
+NORM_SHAPES = [(1, 128), (257, 2, 128), (33, 4, 64), (5, 3, 96), (130, 256), (9, 512), (5, 1000), (7, 1024), (5, 2048), (3, 4096), (3, 8192),
+               (2, 16384), (1000, 8)]
+
+
+@pytest.mark.parametrize("shape", NORM_SHAPES)
+@pytest.mark.parametrize("kind,res", [(None, False), ("silu", True), ("sigmoid", False), (None, True)])
+def test_norm_gate_with_codes(shape, kind, res):
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(sum(shape))
+    x = (2 * torch.randn(shape, generator=g)).to(BF)
+    w = 1 + 0.1 * torch.randn(shape[-1], generator=g)
+    z = torch.randn(shape, generator=g).to(BF) if kind else None
+    r = torch.randn(shape, generator=g).to(BF) if res else None
+    dy, dh = torch.randn(shape, generator=g).to(BF), torch.randn(shape, generator=g).to(BF) if res else None
+    c = lambda t: None if t is None else t.cuda()  # noqa: E731
+    args = dict(activation=kind, res_scale=0.5 if res else 1.0)
+    y, h, h8, hs, z8, zs = gdn.gdn_norm_gate_save8(c(x), c(w), residual=c(r), z=c(z), **args)
+    ry, rh = S.norm_fwd(S.f64(x), S.f64(w), S.f64(r), S.f64(z), kind, res_scale=args["res_scale"])
+    _near(y, torch.from_numpy(ry), 2.0 ** -8 * torch.from_numpy(np.abs(ry)) + 1e-37, "y")
+    if res:
+        _near(h, torch.from_numpy(rh), torch.from_numpy(2.0 ** -8 * np.abs(rh) + 2.0 ** -18 * np.abs(rh).max()), "h")
+    assert (h is None) == (not res) and (z8 is None) == (zs is None) == (kind is None)
+    for t, codes, scale in ((x if h is None else h, h8, hs), (z, z8, zs)):
+        if t is not None:
+            want = gdn.gdn_act8_save(t.cuda())
+            assert torch.equal(codes.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(scale, want[1])
+    dx, dres, dz, dw = gdn.gdn_norm_gate_bwd8(c(dy), h8, hs, c(w), z_codes=z8, z_scale=zs, dh=c(dh), **args)
+    h64 = S.f64(gdn.gdn_act8_load(h8, hs))  # exact: an e4m3 number and a power of two
+    z64 = None if z is None else S.f64(gdn.gdn_act8_load(z8, zs))
+    rx, rr, rz, rw = S.norm_bwd(S.f64(dy), h64, S.f64(w), z64, S.f64(dh), kind, res_scale=args["res_scale"])
+    rstd = 1 / np.sqrt((h64 ** 2).mean(-1, keepdims=True) + 1e-6)
+    terms = rstd * np.abs(S.f64(dy)).max(-1, keepdims=True) * 4 + (2.0 if res else 0.0)
+    n = h64 * rstd
+    for got, ref, mag in ((dx, rx, terms), (dres, rr, terms), (dz, rz, np.abs(S.f64(dy) * n))):
+        if got is not None:
+            _near(got, torch.from_numpy(ref), torch.from_numpy(2.0 ** -8 * np.abs(ref) + 2.0 ** -18 * mag + 1e-37), "gradient")
+    assert (dres is None) == (not res) and (dz is None) == (kind is None)
+    mags = np.abs(S.f64(dy) * n * (1.0 if kind is None else S.act(z64, kind)[0])).reshape(-1, shape[-1]).sum(0)
+    assert (np.abs(S.f64(dw) - rw) <= 2.0 ** -19 * mags + 1e-30).all()
+    again = gdn.gdn_norm_gate_bwd8(c(dy), h8, hs, c(w), z_codes=z8, z_scale=zs, dh=c(dh), **args)
+    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dres, dz, dw)) if a is not None)
