@@ -39,12 +39,26 @@ using namespace gdnat;
 
 constexpr int kThreads = 384;  // warps 0-7 P and dS, 8 copies, 9 products, 10 clears rows past the end
 
+constexpr int kBlocks = 152;  // SMs
+constexpr int kItems = 4;  // items between the warp that finds them and the others
+
 struct BwdArgs : Args {
   float *stats;  // [HQ][q slots][2][kTile]: -lse log2 e, delta
   float *part;   // [piece][k slots][HK][2][kTile][D]: sums of dK and dV
+  int *cut;      // steps that a piece of a walk has at least
   int64_t q_slots, k_slots;
-  int pieces;
+  int pieces;  // most pieces of a walk
 };
+
+// The row tiles that see some key of the tile from key k0 on: [t0, t0 + nt).
+__device__ __forceinline__ void seen_by(const Args &a, int rows, int keys, int k0, int &t0, int &nt) {
+  const int tn = tiles_in(rows, kTile);
+  t0 = min(tn, a.causal ? max(0, k0 - (keys - rows)) / kTile : 0);
+  nt = tn - t0;
+}
+__device__ __forceinline__ int pieces_for(const BwdArgs &a, int64_t steps, int cut) {
+  return (int)max((int64_t)1, min((int64_t)a.pieces, (steps + cut - 1) / cut));
+}
 
 // ------------------------------------------------------------ of each row
 template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs a) {
@@ -52,7 +66,26 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
   const int64_t slot = blockIdx.x / a.HQ;
   const int head = blockIdx.x % a.HQ, l = threadIdx.x % L;
   grid_wait();
-  if (blockIdx.x == 0) check_offsets(a);
+  if (blockIdx.x == 0) {
+    check_offsets(a);
+    // The walks of dK, dV have some steps in all (here by a sum over their tiles, to a tile
+    // for the diagonal): a piece has a quarter of a block's share at least, and 16.
+    __shared__ unsigned long long total;
+    if (threadIdx.x == 0) total = 0;
+    __syncthreads();
+    unsigned long long mine = 0;
+    for (int n = threadIdx.x; n < a.N; n += blockDim.x) {
+      Run rows, keys;
+      if (!run_of(rows_of(a), n, rows) || !run_of(keys_of(a), n, keys)) continue;
+      const int64_t tn = tiles_in(rows.count, kTile), kn = tiles_in(keys.count, kTile);
+      // under the mask, tiles from `free` on lose one row tile each, two, ..
+      const int64_t free = max(0, keys.count - rows.count) / kTile, cut = a.causal ? max((int64_t)0, kn - free) : 0;
+      mine += max((int64_t)1, tn * kn - cut * (cut - 1) / 2);
+    }
+    atomicAdd(&total, mine);
+    __syncthreads();
+    if (threadIdx.x == 0) *a.cut = (int)min((unsigned long long)INT_MAX, max(16ull, total * a.HQ / (4 * kBlocks)));
+  }
   Tile t;
   if (!tile_of(a, slot, kTile, false, t)) return;
   float *out = a.stats + ((int64_t)head * a.q_slots + slot) * 2 * kTile;
@@ -82,24 +115,24 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
 }
 
 // ----------------------------------------------------------------- dK, dV
+// An item, 32-bit words in shared memory: first row of q, rows of the sequence, the place of
+// its first row tile; first key, keys; the item's first key, keys - rows; the first row tile
+// that sees them, how many there are; the piece's first step and its steps (step s is head
+// s / nt of the group, row tile t0 + s % nt); kv head; where the sums go (-1: they are whole),
+// whether it is an item (0: there are no more).
+enum KvWord { K_Q = 0, K_ROWS = 4, K_QSLOT = 8, K_K = 12, K_KEYS = 16, K_K0 = 20, K_PAST = 24, K_T0 = 28, K_NT = 32, K_S0 = 36, K_STEPS = 40,
+              K_HK = 44, K_PART = 48, K_ON = 52, K_BYTES = 64 };
 template <int D> struct KvLay {
   static constexpr int TB = tile_bytes<D>();
   static constexpr int NQ = 3, NO = 2, NT = 2;  // stages of Q, dO, the rows' numbers
   static constexpr int OFF_K = 0, OFF_V = TB, OFF_Q = 2 * TB, OFF_O = OFF_Q + NQ * TB;
   static constexpr int OFF_T = OFF_O + NO * TB;
-  static constexpr int OFF_BAR = OFF_T + NT * 2 * kTile * 4;
-  static constexpr int BARS = 2 * (NQ + NO + NT) + 9;
+  static constexpr int OFF_WORK = OFF_T + NT * 2 * kTile * 4;
+  static constexpr int OFF_BAR = OFF_WORK + kItems * K_BYTES;
+  static constexpr int BARS = 2 * (NQ + NO + NT + kItems) + 11;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
-  static constexpr int BYTES = OFF_MISC + 80;
+  static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 227 * 1024, "one block an SM");
-};
-struct KvWork {
-  int q_first, rows, k_first, keys;  // the sequence's
-  int k0, past;                      // the block's first key; keys - rows
-  int t0, nt;                        // first row tile that sees them, row tiles from there on
-  int s0, steps;                     // the piece's steps: step s is head s / nt of the group, row tile t0 + s % nt
-  int q_slot;                        // slot of the sequence's first row tile
-  int on;
 };
 
 template <int D>
@@ -110,277 +143,349 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t slot = blockIdx.x / (a.HK * a.pieces);
-  const int hk = blockIdx.x / a.pieces % a.HK, piece = blockIdx.x % a.pieces;
   grid_wait();
-  volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_MISC);
+  const uint32_t failed = sb + Ly::OFF_MISC;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
-  volatile KvWork *work = reinterpret_cast<volatile KvWork *>(smem + Ly::OFF_MISC + 16);
-  static_assert(sizeof(KvWork) <= 64, "room for it");
   const uint32_t bar = sb + Ly::OFF_BAR;
   auto QF = [&](int i) { return bar + 8 * i; };
   auto QE = [&](int i) { return bar + 8 * (Ly::NQ + i); };
-  auto OF = [&](int i) { return bar + 8 * (2 * Ly::NQ + i); };
-  auto OE = [&](int i) { return bar + 8 * (2 * Ly::NQ + Ly::NO + i); };
-  auto TF = [&](int i) { return bar + 8 * (2 * Ly::NQ + 2 * Ly::NO + i); };
-  auto TE = [&](int i) { return bar + 8 * (2 * Ly::NQ + 2 * Ly::NO + Ly::NT + i); };
-  const uint32_t bx = bar + 16 * (Ly::NQ + Ly::NO + Ly::NT);
-  const uint32_t KF = bx, SF = bx + 8, DF = bx + 16, PF = bx + 24, GF = bx + 32;  // K and V, S, dP, P, dS are there
-  const uint32_t DONE = bx + 40, VR = bx + 48, VZ = bx + 56, DR = bx + 64;
-  if (warp == 0) {
-    Tile t;
-    const bool on = tile_of(a, slot, kTile, true, t);
-    if (lane == 0) {
-      work->on = on;
-      if (on) {
-        const int past = t.keys.count - t.rows.count, tn = (t.rows.count + kTile - 1) / kTile;
-        const int t0 = min(tn, a.causal ? max(0, t.row0 - past) / kTile : 0);
-        const int64_t all = (int64_t)a.G * (tn - t0);
-        work->q_first = t.rows.first;
-        work->rows = t.rows.count;
-        work->k_first = t.keys.first;
-        work->keys = t.keys.count;
-        work->q_slot = t.rows.first / kTile + t.n;
-        work->k0 = t.row0;
-        work->past = past;
-        work->t0 = t0;
-        work->nt = tn - t0;
-        work->s0 = (int)(all * piece / a.pieces);
-        work->steps = (int)(all * (piece + 1) / a.pieces) - work->s0;
-      }
-      for (int i = 0; i < Ly::NQ; ++i) { mbar_init(QF(i), 1); mbar_init(QE(i), 1); }
-      for (int i = 0; i < Ly::NO; ++i) { mbar_init(OF(i), 1); mbar_init(OE(i), 1); }
-      for (int i = 0; i < Ly::NT; ++i) { mbar_init(TF(i), 1); mbar_init(TE(i), 8); }
-      mbar_init(KF, 1);
-      mbar_init(SF, 1);
-      mbar_init(DF, 1);
-      mbar_init(PF, 8);
-      mbar_init(GF, 8);
-      mbar_init(DONE, 1);
-      mbar_init(VR, 1);
-      mbar_init(VZ, 1);
-      mbar_init(DR, 1);
-      mbar_fence_init();
-      *failed = 0;
-    }
+  const uint32_t bo = bar + 16 * Ly::NQ, bt = bo + 16 * Ly::NO, bw = bt + 16 * Ly::NT, bx = bw + 16 * kItems;
+  auto OF = [&](int i) { return bo + 8 * i; };
+  auto OE = [&](int i) { return bo + 8 * (Ly::NO + i); };
+  auto TF = [&](int i) { return bt + 8 * i; };
+  auto TE = [&](int i) { return bt + 8 * (Ly::NT + i); };
+  auto WF = [&](int i) { return bw + 8 * i; };  // an item is there, all have read it
+  auto WE = [&](int i) { return bw + 8 * (kItems + i); };
+  const uint32_t KF = bx, KE = bx + 8, SF = bx + 16, DF = bx + 24, PF = bx + 32, GF = bx + 40;  // K and V are there, done with; S, dP, P, dS are there
+  const uint32_t DONE = bx + 48, AE = bx + 56, VR = bx + 64, VZ = bx + 72;  // dK and dV are whole, are read; a tile to clear is there, is clean
+  const uint32_t DR = bx + 80;
+  if (tid == 0) {
+    for (int i = 0; i < Ly::NQ; ++i) { mbar_init(QF(i), 1); mbar_init(QE(i), 1); }
+    for (int i = 0; i < Ly::NO; ++i) { mbar_init(OF(i), 1); mbar_init(OE(i), 1); }
+    for (int i = 0; i < Ly::NT; ++i) { mbar_init(TF(i), 1); mbar_init(TE(i), 8); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(WF(i), 1); mbar_init(WE(i), 11); }
+    for (uint32_t b : {KF, KE, SF, DF, DONE, VR, VZ, DR}) mbar_init(b, 1);
+    for (uint32_t b : {PF, GF, AE}) mbar_init(b, 8);
+    mbar_fence_init();
+    sts_i(failed, 0);
   }
-  __syncthreads();
-  if (!work->on) return;
   if (warp == 9) tmem_alloc(sb + Ly::OFF_MISC + 8, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int steps = work->steps, s0 = work->s0, nt = work->nt, t0 = work->t0, rows = work->rows;
-  const int wg = warp >> 2, r = tid & 127;
-  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-  const uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D;  // columns of S^T, dP^T, dV, dK
+  const int wg = warp >> 2;
+  constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D;  // columns of S^T, dP^T, dV, dK
+  auto item = [&](int it, uint32_t &w) {
+    w = sb + Ly::OFF_WORK + it % kItems * K_BYTES;
+    return wait_bar(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
+  };
+  auto item_read = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(WE(it % kItems));
+  };
 
   if (wg < 2) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 3 x 168 = 2 x 208 + 88
     // -------------------------------------------------------------- P and dS
-    const int half = wg * 64, k0 = work->k0, past = work->past;
+    const int half = wg * 64, r = tid & 127;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    if (lane == 0) mbar_arrive(AE);  // there are no sums yet
     bool ok = true;
     if (a.force_expiry && !mbar_wait_bounded(DR, 0, gdnc::kTestWaitLimit)) {
-      *failed = 1;
+      sts_i(failed, 1);
       set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
       ok = false;
     }
-    int t = nt > 0 ? s0 % nt : 0;
-    for (int i = 0; i < steps; ++i) {
-      const uint32_t numbers = sb + Ly::OFF_T + (i % Ly::NT) * (2 * kTile * 4) + half * 4;
-      const int q0 = (t0 + t) * kTile + half;  // first of this thread's rows
-      t = t + 1 == nt ? 0 : t + 1;
-      const bool masked = a.causal && q0 + past < k0 + kTile - 1;
-      const int from = k0 + r - past - q0;  // its first column that sees key r
-      if (ok) ok = wait_bar(TF(i % Ly::NT), (i / Ly::NT) & 1, failed, a.dev_status) && wait_bar(SF, i & 1, failed, a.dev_status);
+    uint32_t n = 0, whole = 0;  // steps, items with some
+    for (int it = 0;; ++it) {
+      uint32_t work;
+      ok = ok && item(it, work);
+      if (!__all_sync(0xffffffffu, ok) || !lds_i(work + K_ON)) break;
+      const int steps = lds_i(work + K_STEPS), k0 = lds_i(work + K_K0), past = lds_i(work + K_PAST), t0 = lds_i(work + K_T0), nt = lds_i(work + K_NT);
+      const int key = k0 + r, hk = lds_i(work + K_HK), part_at = lds_i(work + K_PART);
+      const bool on = key < lds_i(work + K_KEYS);
+      const int64_t at = ((int64_t)(lds_i(work + K_K) + key) * a.HK + hk) * D + wg * (D / 2);
+      int t = steps > 0 ? lds_i(work + K_S0) % nt : 0;
+      item_read(it);
+      for (int i = 0; i < steps; ++i, ++n) {
+        const uint32_t numbers = sb + Ly::OFF_T + (n % Ly::NT) * (2 * kTile * 4) + half * 4;
+        const int q0 = (t0 + t) * kTile + half;  // first of this thread's rows
+        t = t + 1 == nt ? 0 : t + 1;
+        const bool masked = a.causal && q0 + past < k0 + kTile - 1;
+        const int from = key - past - q0;  // its first column that sees the key
+        ok = wait_bar(TF(n % Ly::NT), (n / Ly::NT) & 1, failed, a.dev_status) && wait_bar(SF, n & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        uint32_t p[64], b[64];
+        load64(lanes + kS + half, p);
+        wait64(p);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 m = gdnkv::lds_f4(numbers + c * 4);
+          const float2 x = fma2v(pair(p, c / 2), a.scale_log2e, make_float2(m.x, m.y)), y = fma2v(pair(p, c / 2 + 1), a.scale_log2e, make_float2(m.z, m.w));
+          p[c] = __float_as_uint(ex2f(x.x));
+          p[c + 1] = __float_as_uint(ex2f(x.y));
+          p[c + 2] = __float_as_uint(ex2f(y.x));
+          p[c + 3] = __float_as_uint(ex2f(y.y));
+        }
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c < from) p[c] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) b[c] = pack_bf16(__uint_as_float(p[2 * c]), __uint_as_float(p[2 * c + 1]));
+        tmem_st32(lanes + kS + half, b);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(PF);
+        ok = wait_bar(DF, n & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        load64(lanes + kP + half, b);
+        wait64(b);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 m = gdnkv::lds_f4(numbers + kTile * 4 + c * 4);
+          const float2 x = mul2(pair(p, c / 2), gdnkv::add2(pair(b, c / 2), make_float2(-m.x, -m.y)));
+          const float2 y = mul2(pair(p, c / 2 + 1), gdnkv::add2(pair(b, c / 2 + 1), make_float2(-m.z, -m.w)));
+          // a weight of 0 has no gradient, whatever a masked row's dP is
+          p[c / 2] = masked ? pack_bf16(c < from ? 0.f : x.x, c + 1 < from ? 0.f : x.y) : pack_bf16(x.x, x.y);
+          p[c / 2 + 1] = masked ? pack_bf16(c + 2 < from ? 0.f : y.x, c + 3 < from ? 0.f : y.y) : pack_bf16(y.x, y.y);
+        }
+        tmem_st32(lanes + kP + half, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(GF);
+          mbar_arrive(TE(n % Ly::NT));
+        }
+      }
+      // ------------------------------------------------------------- output
+      if (ok && steps > 0) ok = wait_bar(DONE, whole++ & 1, failed, a.dev_status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      uint32_t p[64], b[64];
-      load64(tmem + lanes + kS + half, p);
-      wait64(p);
-#pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 n = gdnkv::lds_f4(numbers + c * 4);
-        float2 x = fma2v(pair(p, c / 2), a.scale_log2e, make_float2(n.x, n.y)), y = fma2v(pair(p, c / 2 + 1), a.scale_log2e, make_float2(n.z, n.w));
-        p[c] = __float_as_uint(ex2f(x.x));
-        p[c + 1] = __float_as_uint(ex2f(x.y));
-        p[c + 2] = __float_as_uint(ex2f(y.x));
-        p[c + 3] = __float_as_uint(ex2f(y.y));
-      }
-      if (masked) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c < from) p[c] = 0;
-      }
-#pragma unroll
-      for (int c = 0; c < 32; ++c) b[c] = pack_bf16(__uint_as_float(p[2 * c]), __uint_as_float(p[2 * c + 1]));
-      tmem_st32(tmem + lanes + kS + half, b);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(PF);
-      ok = wait_bar(DF, i & 1, failed, a.dev_status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      load64(tmem + lanes + kP + half, b);
-      wait64(b);
-#pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 n = gdnkv::lds_f4(numbers + kTile * 4 + c * 4);
-        const float2 x = mul2(pair(p, c / 2), gdnkv::add2(pair(b, c / 2), make_float2(-n.x, -n.y)));
-        const float2 y = mul2(pair(p, c / 2 + 1), gdnkv::add2(pair(b, c / 2 + 1), make_float2(-n.z, -n.w)));
-        // a weight of 0 has no gradient, whatever a masked row's dP is
-        p[c / 2] = masked ? pack_bf16(c < from ? 0.f : x.x, c + 1 < from ? 0.f : x.y) : pack_bf16(x.x, x.y);
-        p[c / 2 + 1] = masked ? pack_bf16(c + 2 < from ? 0.f : y.x, c + 3 < from ? 0.f : y.y) : pack_bf16(y.x, y.y);
-      }
-      tmem_st32(tmem + lanes + kP + half, p);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(GF);
-        mbar_arrive(TE(i % Ly::NT));
-      }
-    }
-    if (ok && !*failed && steps > 0) wait_bar(DONE, 0, failed, a.dev_status);
-  } else {
-    const int tail = rows % kTile, last = nt - 1;  // rows of a last row tile that is not full
-    if (warp == 8) {
-      // ----------------------------------------------------------- producer
-      if (steps > 0 && elect_one()) {
-        mbar_arrive_expect_tx(KF, 2 * Ly::TB);
-        load_tile<D>(sb + Ly::OFF_K, &mk, KF, hk, work->k_first + work->k0);
-        load_tile<D>(sb + Ly::OFF_V, &mv, KF, hk, work->k_first + work->k0);
-        int g = s0 / nt, t = s0 % nt, q_in = 0, o_in = 0, t_in = 0;  // and what has been asked for
-        for (int i = 0; i < steps; ++i) {
-          const int head = hk * a.G + g, row = work->q_first + (t0 + t) * kTile;
-          const int iq = i % Ly::NQ, io = i % Ly::NO, it = i % Ly::NT;
-          if (i >= Ly::NQ && !wait_bar(QE(iq), (i / Ly::NQ - 1) & 1, failed, a.dev_status)) break;
-          mbar_arrive_expect_tx(QF(iq), Ly::TB);
-          load_tile<D>(sb + Ly::OFF_Q + iq * Ly::TB, &mq, QF(iq), head, row);
-          q_in = i + 1;
-          if (i >= Ly::NT && !wait_bar(TE(it), (i / Ly::NT - 1) & 1, failed, a.dev_status)) break;
-          mbar_arrive_expect_tx(TF(it), 2 * kTile * 4);
-          bulk_load(sb + Ly::OFF_T + it * (2 * kTile * 4), a.stats + ((int64_t)head * a.q_slots + work->q_slot + t0 + t) * 2 * kTile,
-                    2 * kTile * 4, TF(it));
-          t_in = i + 1;
-          if (i >= Ly::NO && !wait_bar(OE(io), (i / Ly::NO - 1) & 1, failed, a.dev_status)) break;
-          mbar_arrive_expect_tx(OF(io), Ly::TB);
-          load_tile<D>(sb + Ly::OFF_O + io * Ly::TB, &mo, OF(io), head, row);
-          o_in = i + 1;
-          if (++t == nt) {
-            t = 0;
-            ++g;
+      float *part = a.part + ((int64_t)part_at * 2 * kTile + r) * D + wg * (D / 2);
+#pragma unroll 1
+      for (int i = 0; i < D; i += 32) {  // dK, then dV: half a row each
+        const bool second = i >= D / 2;
+        const int c = second ? i - D / 2 : i;
+        uint32_t o[32];
+        if (steps > 0) {
+          tmem_ld32_issue(lanes + (second ? kV : kK) + wg * (D / 2) + c, o);
+          tmem_ld_wait(o);
+          if (i + 32 == D) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(AE);
           }
         }
-        if (*failed) {  // copies in flight
-          bool ok = mbar_wait_bounded(KF, 0, gdnc::kWaitLimit);
-          for (int i = 0; i < Ly::NQ && i < q_in; ++i) ok &= mbar_wait_bounded(QF(i), ((q_in - 1 - i) / Ly::NQ) & 1, gdnc::kWaitLimit);
-          for (int i = 0; i < Ly::NT && i < t_in; ++i) ok &= mbar_wait_bounded(TF(i), ((t_in - 1 - i) / Ly::NT) & 1, gdnc::kWaitLimit);
-          for (int i = 0; i < Ly::NO && i < o_in; ++i) ok &= mbar_wait_bounded(OF(i), ((o_in - 1 - i) / Ly::NO) & 1, gdnc::kWaitLimit);
-          if (!ok) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
+        const float f = second ? 1.f : a.scale;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = steps > 0 ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
+        if (on && part_at < 0) {
+          uint16_t *dst = (second ? a.dv : a.dk) + at + c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4 *>(dst + e) = make_uint4(
+                pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+        } else if (on) {
+          float *dst = part + (second ? kTile * D : 0) + c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4 *>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-    } else if (warp == 10) {
-      // Rows past the sequence in its last row tile: their P and dS are 0, but 0 times
-      // what stands there need not be.
-      if (tail != 0) {
-        int turn = 0;
-        for (int i = 0; i < steps; ++i) {
-          if ((s0 + i) % nt != last) continue;
-          bool there = true;  // (no limit of its own: the products' warp gets there, or gives up and says so)
-          while (there && !mbar_try_wait(VR, turn & 1)) there = !*failed;
-          if (!__all_sync(0xffffffffu, there)) break;
-          ++turn;
-          zero_rows<D>(sb + Ly::OFF_Q + i % Ly::NQ * Ly::TB, tail);
-          zero_rows<D>(sb + Ly::OFF_O + i % Ly::NO * Ly::TB, tail);
-          if (lane == 0) mbar_arrive(VZ);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      // ------------------------------------------------------------- copies
+      if (elect_one()) {
+        uint32_t q_in = 0, o_in = 0, t_in = 0, kv_in = 0;  // what has been asked for
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+          uint32_t work;
+          if (!item(it, work) || !lds_i(work + K_ON)) break;
+          const int steps = lds_i(work + K_STEPS), nt = lds_i(work + K_NT), t0 = lds_i(work + K_T0), s0 = lds_i(work + K_S0), hk = lds_i(work + K_HK);
+          const int key = lds_i(work + K_K) + lds_i(work + K_K0), first = lds_i(work + K_Q), q_slot = lds_i(work + K_QSLOT);
+          mbar_arrive(WE(it % kItems));
+          if (steps == 0) continue;
+          if (kv_in > 0) ok = wait_bar(KE, (kv_in - 1) & 1, failed, a.dev_status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(KF, 2 * Ly::TB);
+          load_tile<D>(sb + Ly::OFF_K, &mk, KF, hk, key);
+          load_tile<D>(sb + Ly::OFF_V, &mv, KF, hk, key);
+          ++kv_in;
+          int head = hk * a.G + s0 / nt, t = s0 % nt;
+          for (int i = 0; i < steps; ++i) {
+            const int row = first + (t0 + t) * kTile;
+            const uint32_t iq = q_in % Ly::NQ, io = o_in % Ly::NO, is = t_in % Ly::NT;
+            if (q_in >= Ly::NQ) ok = wait_bar(QE(iq), (q_in / Ly::NQ - 1) & 1, failed, a.dev_status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(QF(iq), Ly::TB);
+            load_tile<D>(sb + Ly::OFF_Q + iq * Ly::TB, &mq, QF(iq), head, row);
+            ++q_in;
+            if (t_in >= Ly::NT) ok = wait_bar(TE(is), (t_in / Ly::NT - 1) & 1, failed, a.dev_status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(TF(is), 2 * kTile * 4);
+            bulk_load(sb + Ly::OFF_T + is * (2 * kTile * 4), a.stats + ((int64_t)head * a.q_slots + q_slot + t0 + t) * 2 * kTile, 2 * kTile * 4,
+                      TF(is));
+            ++t_in;
+            if (o_in >= Ly::NO) ok = wait_bar(OE(io), (o_in / Ly::NO - 1) & 1, failed, a.dev_status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(OF(io), Ly::TB);
+            load_tile<D>(sb + Ly::OFF_O + io * Ly::TB, &mo, OF(io), head, row);
+            ++o_in;
+            if (++t == nt) {
+              t = 0;
+              ++head;
+            }
+          }
+        }
+        if (lds_i(failed)) {  // copies in flight
+          ok = kv_in == 0 || mbar_wait_bounded(KF, (kv_in - 1) & 1, gdnc::kWaitLimit);
+          for (uint32_t i = 0; i < Ly::NQ && i < q_in; ++i) ok &= mbar_wait_bounded(QF(i), ((q_in - 1 - i) / Ly::NQ) & 1, gdnc::kWaitLimit);
+          for (uint32_t i = 0; i < Ly::NT && i < t_in; ++i) ok &= mbar_wait_bounded(TF(i), ((t_in - 1 - i) / Ly::NT) & 1, gdnc::kWaitLimit);
+          for (uint32_t i = 0; i < Ly::NO && i < o_in; ++i) ok &= mbar_wait_bounded(OF(i), ((o_in - 1 - i) / Ly::NO) & 1, gdnc::kWaitLimit);
+          if (!ok) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
         }
       }
     } else if (warp == 9) {
       // ----------------------------------------------------------- products
-      if (steps > 0 && elect_one()) {
-        int turn = 0;
-        auto q_tile = [&](int i) { return sb + Ly::OFF_Q + i % Ly::NQ * Ly::TB; };
-        auto o_tile = [&](int i) { return sb + Ly::OFF_O + i % Ly::NO * Ly::TB; };
-        auto logits = [&](int i) {
-          if (!wait_bar(QF(i % Ly::NQ), (i / Ly::NQ) & 1, failed, a.dev_status)) return false;
-          if (tail != 0 && (s0 + i) % nt == last) {
-            if (!wait_bar(OF(i % Ly::NO), (i / Ly::NO) & 1, failed, a.dev_status)) return false;
-            mbar_arrive(VR);
-            if (!wait_bar(VZ, turn++ & 1, failed, a.dev_status)) return false;
+      if (elect_one()) {
+        uint32_t n = 0, cleared = 0, items = 0;  // steps, tiles cleared, items with steps
+        for (int it = 0;; ++it) {
+          uint32_t work;
+          if (!item(it, work) || !lds_i(work + K_ON)) break;
+          const int steps = lds_i(work + K_STEPS), nt = lds_i(work + K_NT), tail = lds_i(work + K_ROWS) % kTile;
+          int t = steps > 0 ? lds_i(work + K_S0) % nt : 0;
+          mbar_arrive(WE(it % kItems));
+          if (steps == 0) continue;
+          auto wait = [&](uint32_t b, uint32_t phase) { return wait_bar(b, phase & 1, failed, a.dev_status); };
+          auto q_tile = [&](uint32_t m) { return sb + Ly::OFF_Q + m % Ly::NQ * Ly::TB; };
+          auto o_tile = [&](uint32_t m) { return sb + Ly::OFF_O + m % Ly::NO * Ly::TB; };
+          auto logits = [&](uint32_t m) {
+            if (!wait(QF(m % Ly::NQ), m / Ly::NQ)) return false;
+            if (tail != 0 && t + 1 == nt) {
+              if (!wait(OF(m % Ly::NO), m / Ly::NO)) return false;
+              mbar_arrive(VR);
+              if (!wait(VZ, cleared++)) return false;
+            }
+            t = t + 1 == nt ? 0 : t + 1;
+            tc_fence_after();
+            mma_rows<D>(tmem + kS, sb + Ly::OFF_K, q_tile(m));
+            umma_commit(SF);
+            return true;
+          };
+          auto slopes = [&](uint32_t m, bool last) {
+            if (!wait(OF(m % Ly::NO), m / Ly::NO)) return false;
+            tc_fence_after();
+            mma_rows<D>(tmem + kP, sb + Ly::OFF_V, o_tile(m));
+            umma_commit(DF);
+            if (last) umma_commit(KE);  // the last use of K and V
+            return true;
+          };
+          bool ok = wait(KF, items) && logits(n) && slopes(n, steps == 1);
+          for (int i = 0; ok && i < steps; ++i, ++n) {
+            const bool more = i + 1 < steps;
+            ok = wait(PF, n) && (i > 0 || wait(AE, items));
+            if (!ok) break;
+            tc_fence_after();
+            mma_cols<D>(tmem + kV, tmem + kS, o_tile(n), i > 0);
+            umma_commit(OE(n % Ly::NO));
+            if (more) ok = logits(n + 1);
+            ok = ok && wait(GF, n);
+            if (!ok) break;
+            tc_fence_after();
+            mma_cols<D>(tmem + kK, tmem + kP, q_tile(n), i > 0);
+            umma_commit(QE(n % Ly::NQ));
+            if (more) ok = slopes(n + 1, i + 2 == steps);
+            else umma_commit(DONE);
           }
-          tc_fence_after();
-          mma_rows<D>(tmem + kS, sb + Ly::OFF_K, q_tile(i));
-          umma_commit(SF);
-          return true;
-        };
-        auto slopes = [&](int i) {
-          if (!wait_bar(OF(i % Ly::NO), (i / Ly::NO) & 1, failed, a.dev_status)) return false;
-          tc_fence_after();
-          mma_rows<D>(tmem + kP, sb + Ly::OFF_V, o_tile(i));
-          umma_commit(DF);
-          return true;
-        };
-        bool ok = wait_bar(KF, 0, failed, a.dev_status) && logits(0) && slopes(0);
-        for (int i = 0; ok && i < steps; ++i) {
-          ok = wait_bar(PF, i & 1, failed, a.dev_status);
           if (!ok) break;
-          tc_fence_after();
-          mma_cols<D>(tmem + kV, tmem + kS, o_tile(i), i > 0);
-          umma_commit(OE(i % Ly::NO));
-          if (i + 1 < steps) ok = logits(i + 1);
-          ok = ok && wait_bar(GF, i & 1, failed, a.dev_status);
-          if (!ok) break;
-          tc_fence_after();
-          mma_cols<D>(tmem + kK, tmem + kP, q_tile(i), i > 0);
-          umma_commit(QE(i % Ly::NQ));
-          if (i + 1 < steps) ok = slopes(i + 1);
-          else umma_commit(DONE);
+          ++items;
         }
-        if (!ok) {  // let the products in flight finish before the block leaves
+        if (lds_i(failed)) {  // let the products in flight finish before the block leaves
           umma_commit(DR);
           if (!mbar_wait_bounded(DR, 0, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
         }
       }
-    }
-    __syncwarp();
-  }
-  __syncthreads();
-  if (wg < 2 && !*failed) {
-    // ---------------------------------------------------------------- output
-    tc_fence_after();
-    const int key = work->k0 + r;
-    const bool on = key < work->keys, whole = a.pieces == 1;
-    const int64_t at = ((int64_t)(work->k_first + key) * a.HK + hk) * D + wg * (D / 2);
-    const int64_t part = (((piece * a.k_slots + slot) * a.HK + hk) * 2 * kTile + r) * D + wg * (D / 2);
-#pragma unroll 1
-    for (int i = 0; i < D; i += 32) {  // dK, then dV: half a row each
-      const bool second = i >= D / 2;
-      const int c = second ? i - D / 2 : i;
-      uint32_t o[32];
-      if (steps > 0) {
-        tmem_ld32_issue(tmem + lanes + (second ? kV : kK) + wg * (D / 2) + c, o);
-        tmem_ld_wait(o);
+    } else if (warp == 10) {
+      // Rows past the sequence in its last row tile: their P and dS are 0, but 0 times what
+      // stands there need not be.
+      uint32_t n = 0, turn = 0;
+      bool there = true;
+      for (int it = 0; there; ++it) {
+        uint32_t work;
+        if (!__all_sync(0xffffffffu, item(it, work)) || !lds_i(work + K_ON)) break;
+        const int steps = lds_i(work + K_STEPS), nt = lds_i(work + K_NT), s0 = lds_i(work + K_S0), tail = lds_i(work + K_ROWS) % kTile;
+        item_read(it);
+        for (int i = 0; tail != 0 && i < steps; ++i) {
+          if ((s0 + i) % nt != nt - 1) continue;
+          // (no limit of its own: the products' warp gets there, or gives up and says so)
+          while (there && !mbar_try_wait(VR, turn & 1)) there = !lds_i(failed);
+          there = __all_sync(0xffffffffu, there);
+          if (!there) break;
+          ++turn;
+          zero_rows<D>(sb + Ly::OFF_Q + (n + i) % Ly::NQ * Ly::TB, tail);
+          zero_rows<D>(sb + Ly::OFF_O + (n + i) % Ly::NO * Ly::TB, tail);
+          if (lane == 0) mbar_arrive(VZ);
+        }
+        n += steps;
       }
-      const float f = second ? 1.f : a.scale;
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = steps > 0 ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
-      if (on && whole) {
-        uint16_t *dst = (second ? a.dv : a.dk) + at + c;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4 *>(dst + e) =
-              make_uint4(pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                         pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-      } else if (on) {
-        float *dst = a.part + part + (second ? kTile * D : 0) + c;
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4 *>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    } else {
+      // -------------------------------------------------------------- items
+      Walk walk;
+      walk_begin(a, walk, kTile, true, a.HK * a.pieces);
+      const int cut = *a.cut;
+      int it = 0;
+      for (int64_t k = 0;; ++k) {
+        Found f;
+        const bool on = walk_to(a, walk, kTile, true, true, turn_item(k), f);
+        int t0 = 0, nt = 0, pieces = 1, piece = 0;
+        int64_t all = 0;
+        if (on) {
+          seen_by(a, f.rows.count, f.keys.count, f.tile * kTile, t0, nt);
+          all = (int64_t)a.G * nt;
+          pieces = pieces_for(a, all, cut);
+          piece = f.in % a.pieces;
+          if (piece >= pieces) continue;
+        }
+        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
+        if (lane == 0) {
+          const uint32_t work = sb + Ly::OFF_WORK + it % kItems * K_BYTES;
+          sts_i(work + K_ON, on);
+          if (on) {
+            const int s0 = (int)(all * piece / pieces), hk = f.in / a.pieces;
+            const int64_t slot = f.keys.first / kTile + f.n + f.tile;
+            sts_i(work + K_Q, f.rows.first);
+            sts_i(work + K_ROWS, f.rows.count);
+            sts_i(work + K_QSLOT, f.rows.first / kTile + f.n);
+            sts_i(work + K_K, f.keys.first);
+            sts_i(work + K_KEYS, f.keys.count);
+            sts_i(work + K_K0, f.tile * kTile);
+            sts_i(work + K_PAST, f.keys.count - f.rows.count);
+            sts_i(work + K_T0, t0);
+            sts_i(work + K_NT, nt);
+            sts_i(work + K_S0, s0);
+            sts_i(work + K_STEPS, (int)(all * (piece + 1) / pieces) - s0);
+            sts_i(work + K_HK, hk);
+            sts_i(work + K_PART, pieces == 1 ? -1 : (int)((piece * a.k_slots + slot) * a.HK + hk));
+          }
+          mbar_arrive(WF(it % kItems));
+        }
+        __syncwarp();
+        if (!on) break;
+        ++it;
       }
     }
-    tc_fence_before();
   }
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
@@ -392,12 +497,16 @@ template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const B
   grid_wait();
   Tile t;
   if (!tile_of(a, slot, kTile, true, t)) return;
+  int t0, nt;
+  seen_by(a, t.rows.count, t.keys.count, t.row0, t0, nt);
+  const int pieces = pieces_for(a, (int64_t)a.G * nt, *a.cut);
+  if (pieces == 1) return;
   const int rows = min(kTile, t.keys.count - t.row0);
   for (int i = threadIdx.x; i < 2 * rows * (D / 8); i += 256) {
     const bool second = i >= rows * (D / 8);
     const int e = second ? i - rows * (D / 8) : i, r = e / (D / 8), c = e % (D / 8) * 8;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int p = 0; p < a.pieces; ++p) {
+    for (int p = 0; p < pieces; ++p) {
       const float4 *src =
           reinterpret_cast<const float4 *>(a.part + ((((p * a.k_slots + slot) * a.HK + hk) * 2 + (second ? 1 : 0)) * kTile + r) * D + c);
       const float4 u = __ldcs(src), v = __ldcs(src + 1);
@@ -410,22 +519,38 @@ template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const B
 }
 
 // --------------------------------------------------------------------- dQ
+// An item, 32-bit words in shared memory: first row of q of the sequence, the item's first
+// row in it, its rows; first key, keys, keys - rows; key tiles; the head; the place of the
+// rows' numbers; whether it is one (0: there are no more).
+enum QWord { Q_Q = 0, Q_ROW0 = 4, Q_COUNT = 8, Q_K = 12, Q_KEYS = 16, Q_PAST = 20, Q_TILES = 24, Q_HEAD = 28, Q_SLOT = 32, Q_ON = 36, Q_BYTES = 48 };
 template <int D> struct QLay {
   static constexpr int TB = tile_bytes<D>();
   static constexpr int NK = 3, NV = 2;
   static constexpr int OFF_Q = 0, OFF_O = TB, OFF_K = 2 * TB, OFF_V = OFF_K + NK * TB;
-  static constexpr int OFF_BAR = OFF_V + NV * TB;
-  static constexpr int BARS = 2 * (NK + NV) + 10;
+  static constexpr int OFF_WORK = OFF_V + NV * TB;
+  static constexpr int OFF_BAR = OFF_WORK + kItems * Q_BYTES;
+  static constexpr int BARS = 2 * (NK + NV + kItems) + 12;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
-  static constexpr int BYTES = OFF_MISC + 64;
+  static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 227 * 1024, "one block an SM");
 };
-struct QWork {
-  int q_first, row0, count;  // first row of the sequence, the block's first one in it, its rows
-  int k_first, keys, past;
-  int tiles;
-  int on;
-};
+// Half a row (D / 2 bf16) of a tile in shared memory to tensor memory.
+template <int D> __device__ __forceinline__ void row_to_tmem(uint32_t taddr, uint32_t tile, int r, int half) {
+#pragma unroll
+  for (int i = 0; i < D / 16; i += 2) {
+    const int c = half * (D / 16) + i;  // 16-byte chunks of the row
+    const uint4 x = gdnkv::lds128(tile + (c / 8) * kTile * 128 + sw128(r, c % 8)), y = gdnkv::lds128(tile + (c / 8) * kTile * 128 + sw128(r, c % 8 + 1));
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    gdnkv::tmem_st8(taddr + c * 4, w);
+  }
+}
+// D[128 x 128] = A B^T: A 128 x D bf16 in tensor memory, B 128 rows of D in shared memory.
+template <int D> __device__ __forceinline__ void mma_rows_ta(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = umma_idesc_bf16(128, 128);
+  const uint64_t db = umma_desc_sw128(b);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) umma_f16_ta(d, a + k * 8, db + (k / 4) * (kTile * 128 / 16) + (k % 4) * 2, id, k > 0);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -435,229 +560,319 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the last rows, which see most keys, first
-  const int64_t slot = a.q_slots - 1 - blockIdx.x / a.HQ;
-  const int head = blockIdx.x % a.HQ;
   grid_wait();
-  volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_MISC);
+  const uint32_t failed = sb + Ly::OFF_MISC;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
-  volatile QWork *work = reinterpret_cast<volatile QWork *>(smem + Ly::OFF_MISC + 16);
-  static_assert(sizeof(QWork) <= 48, "room for it");
   const uint32_t bar = sb + Ly::OFF_BAR;
   auto KF = [&](int i) { return bar + 8 * i; };
   auto KE = [&](int i) { return bar + 8 * (Ly::NK + i); };
-  auto VF = [&](int i) { return bar + 8 * (2 * Ly::NK + i); };
-  auto VE = [&](int i) { return bar + 8 * (2 * Ly::NK + Ly::NV + i); };
-  const uint32_t bx = bar + 16 * (Ly::NK + Ly::NV);
-  auto SF = [&](int i) { return bx + 8 * i; };
-  const uint32_t QF = bx + 16, DF = bx + 24, PR = bx + 32, GF = bx + 40;  // Q and dO, dP are there; dP is read; dS is there
-  const uint32_t DONE = bx + 48, VR = bx + 56, VZ = bx + 64, DR = bx + 72;
-  if (warp == 0) {
-    Tile t;
-    const bool on = tile_of(a, slot, kTile, false, t);
-    if (lane == 0) {
-      work->on = on;
-      if (on) {
-        const int past = t.keys.count - t.rows.count, count = min(kTile, t.rows.count - t.row0);
-        const int seen = a.causal ? min(t.keys.count, past + t.row0 + count) : t.keys.count;
-        work->q_first = t.rows.first;
-        work->row0 = t.row0;
-        work->count = count;
-        work->k_first = t.keys.first;
-        work->keys = t.keys.count;
-        work->past = past;
-        work->tiles = (max(0, seen) + kTile - 1) / kTile;
-      }
-      for (int i = 0; i < Ly::NK; ++i) { mbar_init(KF(i), 1); mbar_init(KE(i), 1); }
-      for (int i = 0; i < Ly::NV; ++i) { mbar_init(VF(i), 1); mbar_init(VE(i), 1); }
-      for (int i = 0; i < 2; ++i) mbar_init(SF(i), 1);
-      mbar_init(QF, 1);
-      mbar_init(DF, 1);
-      mbar_init(PR, 8);
-      mbar_init(GF, 8);
-      mbar_init(DONE, 1);
-      mbar_init(VR, 1);
-      mbar_init(VZ, 1);
-      mbar_init(DR, 1);
-      mbar_fence_init();
-      *failed = 0;
-    }
+  const uint32_t bv = bar + 16 * Ly::NK, bw = bv + 16 * Ly::NV, bx = bw + 16 * kItems;
+  auto VF = [&](int i) { return bv + 8 * i; };
+  auto VE = [&](int i) { return bv + 8 * (Ly::NV + i); };
+  auto WF = [&](int i) { return bw + 8 * i; };  // an item is there, all have read it
+  auto WE = [&](int i) { return bw + 8 * (kItems + i); };
+  const uint32_t QF = bx, QE = bx + 8, QT = bx + 16;                            // Q and dO are in shared memory, are read, are in tensor memory
+  const uint32_t SF = bx + 24, SE = bx + 32, DF = bx + 40, GF = bx + 48;        // S is there, is read; dP, dS are there
+  const uint32_t DONE = bx + 56, AE = bx + 64, VR = bx + 72, VZ = bx + 80;      // dQ is whole, is read; the last keys are there, are clean
+  const uint32_t DR = bx + 88;
+  if (tid == 0) {
+    for (int i = 0; i < Ly::NK; ++i) { mbar_init(KF(i), 1); mbar_init(KE(i), 1); }
+    for (int i = 0; i < Ly::NV; ++i) { mbar_init(VF(i), 1); mbar_init(VE(i), 1); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(WF(i), 1); mbar_init(WE(i), 11); }
+    for (uint32_t b : {QF, SF, DF, DONE, VR, VZ, DR}) mbar_init(b, 1);
+    for (uint32_t b : {QE, QT, SE, GF, AE}) mbar_init(b, 8);
+    mbar_fence_init();
+    sts_i(failed, 0);
   }
-  __syncthreads();
-  if (!work->on) return;
   if (warp == 9) tmem_alloc(sb + Ly::OFF_MISC + 8, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int tiles = work->tiles, keys = work->keys;
-  const int wg = warp >> 2, r = tid & 127;
-  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-  const uint32_t kP = 256, kQ = 384;  // columns of dP, dQ; S at 0 and 128
+  const int wg = warp >> 2;
+  constexpr uint32_t kS = 0, kP = 128, kA = 256, kQ = 384, kO = 448;  // columns of S, dP, dQ, Q, dO
+  auto item = [&](int it, uint32_t &w) {
+    w = sb + Ly::OFF_WORK + it % kItems * Q_BYTES;
+    return wait_bar(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
+  };
+  auto item_read = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(WE(it % kItems));
+  };
 
   if (wg < 2) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");  // 3 x 168 = 2 x 208 + 88
     // -------------------------------------------------------------------- dS
-    const int half = wg * 64, past = work->past, row0 = work->row0;
-    const int low = a.causal ? past + row0 : keys - 1;
-    const int limit = a.causal ? min(low + r, keys - 1) : low;
-    const float *stats = a.stats + ((int64_t)head * a.q_slots + slot) * 2 * kTile;
-    const float n_lse = stats[r], n_delta = -stats[kTile + r];
+    const int half = wg * 64, r = tid & 127;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+    if (lane == 0) mbar_arrive(AE);  // there is no dQ yet
     bool ok = true;
     if (a.force_expiry && !mbar_wait_bounded(DR, 0, gdnc::kTestWaitLimit)) {
-      *failed = 1;
+      sts_i(failed, 1);
       set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
       ok = false;
     }
-    for (int j = 0; j < tiles; ++j) {
-      const uint32_t S = tmem + lanes + (j & 1) * 128 + half;
-      if (ok) ok = wait_bar(SF(j & 1), (j >> 1) & 1, failed, a.dev_status) && wait_bar(DF, j & 1, failed, a.dev_status);
+    uint32_t n = 0, with = 0, whole = 0;  // key tiles, items with some, of which dQ is out
+    int64_t out = -1;                     // where the item before has its row; -1: it has none
+    bool before = false, sums = false;    // there was an item before, with key tiles
+    for (int it = 0;; ++it) {
+      uint32_t work;
+      ok = ok && item(it, work);
       if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      uint32_t s[64], b[64];
-      load64(S, s);
-      load64(tmem + lanes + kP + half, b);
-      wait64(s);
-      gdnkv::tie32(b);
-      gdnkv::tie32(b + 32);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(PR);
-      const int k0 = j * kTile + half;
-      const bool masked = k0 + 63 > low || k0 + 63 >= keys;
+      const bool on = lds_i(work + Q_ON);
+      int tiles = 0, low = 0, limit = 0;
+      int64_t at = -1;
+      float n_lse = 0.f, n_delta = 0.f;
+      if (on) {
+        const int past = lds_i(work + Q_PAST), row0 = lds_i(work + Q_ROW0), keys = lds_i(work + Q_KEYS), head = lds_i(work + Q_HEAD);
+        tiles = lds_i(work + Q_TILES);
+        low = a.causal ? min(past + row0, keys - 1) : keys - 1;  // what the first row sees last
+        limit = a.causal ? min(low + r, keys - 1) : low;
+        if (r < lds_i(work + Q_COUNT)) at = ((int64_t)(lds_i(work + Q_Q) + row0 + r) * a.HQ + head) * D + wg * (D / 2);
+        const float *stats = a.stats + ((int64_t)head * a.q_slots + lds_i(work + Q_SLOT)) * 2 * kTile;
+        n_lse = stats[r];
+        n_delta = -stats[kTile + r];
+        item_read(it);
+        if (tiles > 0) {
+          // Q and dO go to tensor memory, from where the products take them without a
+          // reading of shared memory: the products of the item before that read them are done
+          ok = wait_bar(QF, with & 1, failed, a.dev_status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          row_to_tmem<D>(lanes + kQ, sb + Ly::OFF_Q, r, wg);
+          row_to_tmem<D>(lanes + kO, sb + Ly::OFF_O, r, wg);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(QE);
+            mbar_arrive(QT);
+          }
+          ++with;
+        }
+      }
+      if (before) {
+        // ----------------------------------------------------------- output
+        if (sums) ok = wait_bar(DONE, whole++ & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < D / 2; i += 32) {
+          uint32_t o[32];
+          if (sums) {
+            tmem_ld32_issue(lanes + kA + wg * (D / 2) + i, o);
+            tmem_ld_wait(o);
+            if (i + 32 == D / 2) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(AE);
+            }
+          }
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float2 x = gdnkv::fma2(pair(s, c), a.scale_log2e, n_lse), d = gdnkv::add2(pair(b, c), make_float2(n_delta, n_delta));
-        const float2 g = mul2(make_float2(ex2f(x.x), ex2f(x.y)), d);
-        s[c] = masked ? pack_bf16(k0 + 2 * c > limit ? 0.f : g.x, k0 + 2 * c + 1 > limit ? 0.f : g.y) : pack_bf16(g.x, g.y);
+          for (int e = 0; e < 32; ++e) o[e] = sums ? __float_as_uint(__uint_as_float(o[e]) * a.scale) : 0u;
+          if (out >= 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4 *>(a.dq + out + i + e) = make_uint4(
+                  pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                  pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+          }
+        }
       }
-      tmem_st32(S, s);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(GF);
+      if (!on) break;
+      before = true;
+      sums = tiles > 0;
+      out = at;
+      for (int j = 0; j < tiles; ++j, ++n) {
+        ok = wait_bar(SF, n & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        uint32_t p[64], b[64];
+        load64(lanes + kS + half, p);
+        wait64(p);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(SE);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 x = gdnkv::fma2(pair(p, c), a.scale_log2e, n_lse);
+          p[2 * c] = __float_as_uint(ex2f(x.x));
+          p[2 * c + 1] = __float_as_uint(ex2f(x.y));
+        }
+        ok = wait_bar(DF, n & 1, failed, a.dev_status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        load64(lanes + kP + half, b);
+        wait64(b);
+        const int k0 = j * kTile + half;
+        const bool masked = k0 + 63 > low;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 g = mul2(pair(p, c), gdnkv::add2(pair(b, c), make_float2(n_delta, n_delta)));
+          // what is masked has no gradient, whatever its S and dP are
+          b[c] = masked ? pack_bf16(k0 + 2 * c > limit ? 0.f : g.x, k0 + 2 * c + 1 > limit ? 0.f : g.y) : pack_bf16(g.x, g.y);
+        }
+        tmem_st32(lanes + kP + half, b);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(GF);
+      }
     }
-    if (ok && !*failed && tiles > 0) wait_bar(DONE, 0, failed, a.dev_status);
   } else {
-    const int tail = keys % kTile;  // keys of a last tile that is not full
-    const bool clear = tail != 0 && tiles * kTile > keys;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      // ----------------------------------------------------------- producer
-      if (tiles > 0 && elect_one()) {
-        const int row = work->q_first + work->row0, key = work->k_first, hk = head / a.G;
-        mbar_arrive_expect_tx(QF, 2 * Ly::TB);
-        load_tile<D>(sb + Ly::OFF_Q, &mq, QF, head, row);
-        load_tile<D>(sb + Ly::OFF_O, &mo, QF, head, row);
-        int k_in = 0, v_in = 0;
-        for (int j = 0; j < tiles; ++j) {
-          const int ik = j % Ly::NK, iv = j % Ly::NV;
-          if (j >= Ly::NK && !wait_bar(KE(ik), (j / Ly::NK - 1) & 1, failed, a.dev_status)) break;
-          mbar_arrive_expect_tx(KF(ik), Ly::TB);
-          load_tile<D>(sb + Ly::OFF_K + ik * Ly::TB, &mk, KF(ik), hk, key + j * kTile);
-          k_in = j + 1;
-          if (j >= Ly::NV && !wait_bar(VE(iv), (j / Ly::NV - 1) & 1, failed, a.dev_status)) break;
-          mbar_arrive_expect_tx(VF(iv), Ly::TB);
-          load_tile<D>(sb + Ly::OFF_V + iv * Ly::TB, &mv, VF(iv), hk, key + j * kTile);
-          v_in = j + 1;
+      // ------------------------------------------------------------- copies
+      if (elect_one()) {
+        uint32_t k_in = 0, v_in = 0, q_in = 0;  // what has been asked for
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+          uint32_t work;
+          if (!item(it, work) || !lds_i(work + Q_ON)) break;
+          const int tiles = lds_i(work + Q_TILES), row = lds_i(work + Q_Q) + lds_i(work + Q_ROW0), key = lds_i(work + Q_K), head = lds_i(work + Q_HEAD);
+          mbar_arrive(WE(it % kItems));
+          if (tiles == 0) continue;
+          if (q_in > 0) ok = wait_bar(QE, (q_in - 1) & 1, failed, a.dev_status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(QF, 2 * Ly::TB);
+          load_tile<D>(sb + Ly::OFF_Q, &mq, QF, head, row);
+          load_tile<D>(sb + Ly::OFF_O, &mo, QF, head, row);
+          ++q_in;
+          for (int j = 0; j < tiles; ++j) {
+            const uint32_t ik = k_in % Ly::NK, iv = v_in % Ly::NV;
+            if (k_in >= Ly::NK) ok = wait_bar(KE(ik), (k_in / Ly::NK - 1) & 1, failed, a.dev_status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(KF(ik), Ly::TB);
+            load_tile<D>(sb + Ly::OFF_K + ik * Ly::TB, &mk, KF(ik), head / a.G, key + j * kTile);
+            ++k_in;
+            if (v_in >= Ly::NV) ok = wait_bar(VE(iv), (v_in / Ly::NV - 1) & 1, failed, a.dev_status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(VF(iv), Ly::TB);
+            load_tile<D>(sb + Ly::OFF_V + iv * Ly::TB, &mv, VF(iv), head / a.G, key + j * kTile);
+            ++v_in;
+          }
         }
-        if (*failed) {  // copies in flight
-          bool ok = mbar_wait_bounded(QF, 0, gdnc::kWaitLimit);
-          for (int i = 0; i < Ly::NK && i < k_in; ++i) ok &= mbar_wait_bounded(KF(i), ((k_in - 1 - i) / Ly::NK) & 1, gdnc::kWaitLimit);
-          for (int i = 0; i < Ly::NV && i < v_in; ++i) ok &= mbar_wait_bounded(VF(i), ((v_in - 1 - i) / Ly::NV) & 1, gdnc::kWaitLimit);
+        if (lds_i(failed)) {  // copies in flight
+          ok = q_in == 0 || mbar_wait_bounded(QF, (q_in - 1) & 1, gdnc::kWaitLimit);
+          for (uint32_t i = 0; i < Ly::NK && i < k_in; ++i) ok &= mbar_wait_bounded(KF(i), ((k_in - 1 - i) / Ly::NK) & 1, gdnc::kWaitLimit);
+          for (uint32_t i = 0; i < Ly::NV && i < v_in; ++i) ok &= mbar_wait_bounded(VF(i), ((v_in - 1 - i) / Ly::NV) & 1, gdnc::kWaitLimit);
           if (!ok) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
-        }
-      }
-    } else if (warp == 10) {
-      // dS is 0 past the sequence's keys, but 0 times what stands there need not be
-      if (clear) {
-        bool there = true;  // (no limit of its own: the products' warp gets there, or gives up and says so)
-        while (there && !mbar_try_wait(VR, 0)) there = !*failed;
-        if (__all_sync(0xffffffffu, there)) {
-          zero_rows<D>(sb + Ly::OFF_K + (tiles - 1) % Ly::NK * Ly::TB, tail);
-          if (lane == 0) mbar_arrive(VZ);
         }
       }
     } else if (warp == 9) {
       // ----------------------------------------------------------- products
-      if (tiles > 0 && elect_one()) {
-        auto k_tile = [&](int j) { return sb + Ly::OFF_K + j % Ly::NK * Ly::TB; };
-        auto logits = [&](int j) {
-          if (!wait_bar(KF(j % Ly::NK), (j / Ly::NK) & 1, failed, a.dev_status)) return false;
-          if (clear && j == tiles - 1) {
-            mbar_arrive(VR);
-            if (!wait_bar(VZ, 0, failed, a.dev_status)) return false;
+      if (elect_one()) {
+        uint32_t n = 0, cleared = 0, items = 0;  // key tiles, last ones cleared, items with some
+        for (int it = 0;; ++it) {
+          uint32_t work;
+          if (!item(it, work) || !lds_i(work + Q_ON)) break;
+          const int tiles = lds_i(work + Q_TILES);
+          const bool clear = tiles * kTile > lds_i(work + Q_KEYS);
+          mbar_arrive(WE(it % kItems));
+          if (tiles == 0) continue;
+          auto wait = [&](uint32_t b, uint32_t phase) { return wait_bar(b, phase & 1, failed, a.dev_status); };
+          auto k_tile = [&](uint32_t m) { return sb + Ly::OFF_K + m % Ly::NK * Ly::TB; };
+          auto logits = [&](uint32_t m, bool last) {
+            if (!wait(KF(m % Ly::NK), m / Ly::NK)) return false;
+            if (clear && last) {
+              mbar_arrive(VR);
+              if (!wait(VZ, cleared++)) return false;
+            }
+            tc_fence_after();
+            mma_rows_ta<D>(tmem + kS, tmem + kQ, k_tile(m));
+            umma_commit(SF);
+            return true;
+          };
+          auto slopes = [&](uint32_t m) {
+            if (!wait(VF(m % Ly::NV), m / Ly::NV)) return false;
+            tc_fence_after();
+            mma_rows_ta<D>(tmem + kP, tmem + kO, sb + Ly::OFF_V + m % Ly::NV * Ly::TB);
+            umma_commit(DF);
+            umma_commit(VE(m % Ly::NV));
+            return true;
+          };
+          bool ok = wait(QT, items) && logits(n, tiles == 1) && slopes(n);
+          if (ok && tiles > 1) ok = wait(SE, n) && logits(n + 1, tiles == 2);
+          for (int j = 0; ok && j < tiles; ++j, ++n) {
+            ok = wait(GF, n) && (j > 0 || wait(AE, items));
+            if (!ok) break;
+            tc_fence_after();
+            mma_cols<D>(tmem + kA, tmem + kP, k_tile(n), j > 0);
+            umma_commit(KE(n % Ly::NK));
+            if (j + 1 < tiles) ok = slopes(n + 1);
+            else umma_commit(DONE);
+            if (ok && j + 2 < tiles) ok = wait(SE, n + 1) && logits(n + 2, j + 3 == tiles);
           }
-          tc_fence_after();
-          mma_rows<D>(tmem + (j & 1) * 128, sb + Ly::OFF_Q, k_tile(j));
-          umma_commit(SF(j & 1));
-          return true;
-        };
-        auto slopes = [&](int j) {
-          if (!wait_bar(VF(j % Ly::NV), (j / Ly::NV) & 1, failed, a.dev_status)) return false;
-          tc_fence_after();
-          mma_rows<D>(tmem + kP, sb + Ly::OFF_O, sb + Ly::OFF_V + j % Ly::NV * Ly::TB);
-          umma_commit(DF);
-          umma_commit(VE(j % Ly::NV));
-          return true;
-        };
-        bool ok = wait_bar(QF, 0, failed, a.dev_status) && logits(0) && slopes(0);
-        if (ok && tiles > 1) ok = logits(1);
-        for (int j = 0; ok && j < tiles; ++j) {
-          if (j + 1 < tiles) ok = wait_bar(PR, j & 1, failed, a.dev_status) && slopes(j + 1);
-          ok = ok && wait_bar(GF, j & 1, failed, a.dev_status);
           if (!ok) break;
-          tc_fence_after();
-          mma_cols<D>(tmem + kQ, tmem + (j & 1) * 128, k_tile(j), j > 0);
-          umma_commit(KE(j % Ly::NK));
-          if (j + 2 < tiles) ok = logits(j + 2);
-          if (j + 1 == tiles) umma_commit(DONE);
+          ++items;
         }
-        if (!ok) {  // let the products in flight finish before the block leaves
+        if (lds_i(failed)) {  // let the products in flight finish before the block leaves
           umma_commit(DR);
           if (!mbar_wait_bounded(DR, 0, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
         }
       }
-    }
-    __syncwarp();
-  }
-  __syncthreads();
-  if (wg < 2 && !*failed) {
-    // ---------------------------------------------------------------- output
-    tc_fence_after();
-    const bool on = r < work->count;
-    uint16_t *dst = a.dq + ((int64_t)(work->q_first + work->row0 + r) * a.HQ + head) * D + wg * (D / 2);
-#pragma unroll 1
-    for (int i = 0; i < D / 2; i += 32) {
-      uint32_t o[32];
-      if (tiles > 0) {
-        tmem_ld32_issue(tmem + lanes + kQ + wg * (D / 2) + i, o);
-        tmem_ld_wait(o);
+    } else if (warp == 10) {
+      // dS is 0 past the sequence's keys, but 0 times what stands there need not be.
+      uint32_t n = 0, turn = 0;
+      for (int it = 0;; ++it) {
+        uint32_t work;
+        if (!__all_sync(0xffffffffu, item(it, work)) || !lds_i(work + Q_ON)) break;
+        const int tiles = lds_i(work + Q_TILES), keys = lds_i(work + Q_KEYS);
+        item_read(it);
+        n += tiles;
+        if (tiles * kTile <= keys) continue;
+        bool there = true;  // (no limit of its own: the products' warp gets there, or gives up and says so)
+        while (there && !mbar_try_wait(VR, turn & 1)) there = !lds_i(failed);
+        if (!__all_sync(0xffffffffu, there)) break;
+        ++turn;
+        zero_rows<D>(sb + Ly::OFF_K + (n - 1) % Ly::NK * Ly::TB, keys % kTile);
+        if (lane == 0) mbar_arrive(VZ);
       }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = tiles > 0 ? __float_as_uint(__uint_as_float(o[e]) * a.scale) : 0u;
-      if (on) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4 *>(dst + i + e) =
-              make_uint4(pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                         pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+    } else {
+      // -------------------------------------------------------------- items
+      Walk walk;
+      walk_begin(a, walk, kTile, false, a.HQ);
+      for (int it = 0;; ++it) {
+        Found f;
+        const bool on = walk_to(a, walk, kTile, false, false, turn_item(it), f);
+        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
+        if (lane == 0) {
+          const uint32_t work = sb + Ly::OFF_WORK + it % kItems * Q_BYTES;
+          sts_i(work + Q_ON, on);
+          if (on) {
+            const int row0 = f.tile * kTile, past = f.keys.count - f.rows.count, count = min(kTile, f.rows.count - row0);
+            sts_i(work + Q_Q, f.rows.first);
+            sts_i(work + Q_ROW0, row0);
+            sts_i(work + Q_COUNT, count);
+            sts_i(work + Q_K, f.keys.first);
+            sts_i(work + Q_KEYS, f.keys.count);
+            sts_i(work + Q_PAST, past);
+            sts_i(work + Q_TILES, tiles_in(max(0, a.causal ? min(f.keys.count, past + row0 + count) : f.keys.count), kTile));
+            sts_i(work + Q_HEAD, f.in);
+            sts_i(work + Q_SLOT, f.rows.first / kTile + f.n + f.tile);
+          }
+          mbar_arrive(WF(it % kItems));
+        }
+        __syncwarp();
+        if (!on) break;
       }
     }
-    tc_fence_before();
   }
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Pieces that the walk of a (key tile, kv head) is cut into: where there are fewer than
-// four for each SM, up to one for each head of the group, 8 at most.
-int pieces_of(int64_t k_slots, int HQ, int HK) {
-  const int64_t items = k_slots * HK, want = (4 * 152 + items - 1) / items;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 8), HQ / HK));
+// Most pieces of a (key tile, kv head)'s walk: enough for eight items an SM.
+int pieces_of(int64_t k_tiles, int HK) {
+  const int64_t items = std::max<int64_t>(1, k_tiles * HK), want = (8 * kBlocks + items - 1) / items;
+  return (int)std::min<int64_t>(want, 8);
 }
 
 template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   const int64_t q_blocks = a.q_slots * a.HQ, k_blocks = a.k_slots * a.HK;
-  if (q_blocks > INT_MAX || k_blocks * a.pieces > INT_MAX) return cudaErrorInvalidConfiguration;
+  if (q_blocks > INT_MAX || k_blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  const int64_t sms = gdn_host::sm_count();
   CUtensorMap mq, mk, mv, mo;
   // a side without rows is never loaded
   const bool rows = a.Tq > 0, keys = a.Tk > 0;
@@ -670,10 +885,17 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   cudaError_t e = gdn_host::allow_smem(attn_dkdv_kernel<D>, KvLay<D>::BYTES, done_kv);
   if (e == cudaSuccess) e = gdn_host::allow_smem(attn_dq_kernel<D>, QLay<D>::BYTES, done_q);
   if (e != cudaSuccess) return e;
+  // the warps' shares of the registers are those of a launch with 168 a thread
+  static const bool shares = [] {
+    cudaFuncAttributes f, g;
+    return cudaFuncGetAttributes(&f, attn_dkdv_kernel<D>) == cudaSuccess && f.numRegs == 168 &&
+           cudaFuncGetAttributes(&g, attn_dq_kernel<D>) == cudaSuccess && g.numRegs == 168;
+  }();
+  if (!shares) return cudaErrorInvalidConfiguration;
   e = gdn_host::launch_dependent(attn_stats_kernel<D>, dim3((unsigned)q_blocks), 256, 0, s, a);
   if (e == cudaSuccess && keys)
-    e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)(k_blocks * a.pieces)), kThreads, KvLay<D>::BYTES, s, a, mq, mk, mv, mo);
-  if (e == cudaSuccess && rows) e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)q_blocks), kThreads, QLay<D>::BYTES, s, a, mq, mk, mv, mo);
+    e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tk, a.N, kTile) * a.HK * a.pieces, sms)), kThreads, KvLay<D>::BYTES, s, a, mq, mk, mv, mo);
+  if (e == cudaSuccess && rows) e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tq, a.N, kTile) * a.HQ, sms)), kThreads, QLay<D>::BYTES, s, a, mq, mk, mv, mo);
   if (e == cudaSuccess && keys && a.pieces > 1) e = gdn_host::launch_dependent(attn_join_kernel<D>, dim3((unsigned)k_blocks), 256, 0, s, a);
   return e;
 }
@@ -684,8 +906,8 @@ namespace gdn_host {
 static size_t stats_bytes(int N, int Tq, int HQ) { return (size_t)HQ * gdnat::slots_of(Tq, N, gdnat::kTile) * 2 * gdnat::kTile * sizeof(float); }
 size_t attn_bwd_workspace_bytes(int N, int Tq, int Tk, int HQ, int HK, int D) {
   const int64_t k_slots = gdnat::slots_of(Tk, N, gdnat::kTile);
-  const int pieces = pieces_of(k_slots, HQ, HK);
-  return stats_bytes(N, Tq, HQ) + (pieces > 1 ? (size_t)pieces * k_slots * HK * 2 * gdnat::kTile * D * sizeof(float) : 0);
+  const int pieces = pieces_of(gdnat::most_tiles(Tk, N, gdnat::kTile), HK);
+  return 16 + stats_bytes(N, Tq, HQ) + (pieces > 1 ? (size_t)pieces * k_slots * HK * 2 * gdnat::kTile * D * sizeof(float) : 0);
 }
 cudaError_t launch_attn_bwd(const TrainAttnArgs &c, cudaStream_t s) {
   BwdArgs a{};
@@ -694,8 +916,9 @@ cudaError_t launch_attn_bwd(const TrainAttnArgs &c, cudaStream_t s) {
   a.scale_log2e = c.scale * gdnc::kLog2e;
   a.q_slots = gdnat::slots_of(c.Tq, c.N, gdnat::kTile);
   a.k_slots = gdnat::slots_of(c.Tk, c.N, gdnat::kTile);
-  a.pieces = pieces_of(a.k_slots, c.HQ, c.HK);
-  a.stats = static_cast<float *>(c.ws);
+  a.pieces = pieces_of(gdnat::most_tiles(c.Tk, c.N, gdnat::kTile), c.HK);
+  a.cut = static_cast<int *>(c.ws);
+  a.stats = reinterpret_cast<float *>(static_cast<char *>(c.ws) + 16);
   a.part = a.stats + stats_bytes(c.N, c.Tq, c.HQ) / sizeof(float);
   return c.D == 128 ? launch<128>(a, s) : launch<64>(a, s);
 }

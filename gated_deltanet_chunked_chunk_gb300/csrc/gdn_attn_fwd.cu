@@ -6,11 +6,12 @@
 // with m the running maximum of c S.  Bound: the tensor cores, 4 D operations a (row,
 // key, head).
 //
-// A block works on two tiles of 128 rows of one head, which share the keys and values
+// An item is two tiles of 128 rows of one head, which share the keys and values
 // that TMA brings, and whose softmaxes take turns on the tensor cores (one tile, where
-// fewer blocks than SMs would come out).  Warps 0-7 and 8-15 are the softmax of the two
+// fewer items than SMs would come out).  Warps 0-7 and 8-15 are the softmax of the two
 // tiles: a thread holds half a row, 64 logits; 16 brings the tiles, 17 issues the
-// products, 18 clears what the last tile of values holds past the sequence.
+// products, 18 clears what a last tile of values holds past the sequence, 19 finds the
+// items.
 //
 // Tensor memory (512 columns): S of both tiles, P in bf16 over its S (each half over
 // the half that its threads read), O of both tiles.  Products of one thread execute in
@@ -22,7 +23,8 @@
 // P has 8 significant bits (bf16 keeps fp32's range, so any m near the maximum is as
 // good), l is the sum before that rounding, whose errors (2^-8 of a weight at most, either
 // way) mostly cancel in o.
-#include <limits.h>
+#include <algorithm>
+#include <type_traits>
 
 #include "gdn_attn.cuh"
 
@@ -32,6 +34,14 @@ using namespace gdnat;
 
 constexpr int kThreads = 640;
 constexpr float kMost = 8.f;
+constexpr int kItems = 4;  // items between the warp that finds them and the others
+
+// An item, 32-bit words in shared memory: first row of q and of k of the sequence, its
+// keys; the item's first row in the sequence; keys - rows; rows and key tiles of both row
+// tiles; the head; whether it is one (0: there are no more); what the first row of both row
+// tiles sees last.  (What the softmax's loop rarely needs it reads there: the logits take
+// the registers.)
+enum Word { W_Q = 0, W_K = 4, W_KEYS = 8, W_ROW0 = 12, W_PAST = 16, W_COUNT = 20, W_TILES = 28, W_HEAD = 36, W_ON = 40, W_LOW = 44, W_BYTES = 64 };
 
 template <int D> struct Lay {
   static constexpr int TB = tile_bytes<D>();
@@ -39,18 +49,11 @@ template <int D> struct Lay {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * TB;
   static constexpr int OFF_X = OFF_KV + NS * TB;  // float [tile][half][row]: what a row's threads tell each other
-  static constexpr int OFF_BAR = OFF_X + 2 * 2 * 128 * 4;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 10) * 8;
-  static constexpr int BYTES = OFF_MISC + 64;
-  static_assert(BYTES <= 227 * 1024, "one block an SM");
-};
-
-// What the block works on, in shared memory.
-struct Work {
-  int q_first, k_first, keys;  // first row of q and of k of the sequence, its keys
-  int row0, past;              // the block's first row in the sequence; keys - rows
-  int count[2], tiles[2];      // rows and key tiles of both row tiles
-  int on;
+  static constexpr int OFF_WORK = OFF_X + 2 * 2 * 128 * 4;
+  static constexpr int OFF_BAR = OFF_WORK + kItems * W_BYTES;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 2 * kItems + 13) * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static_assert(OFF_X % 1024 == 0 && BYTES <= 227 * 1024, "one block an SM");
 };
 
 __device__ __forceinline__ bool vote_any(int id, bool mine) {
@@ -64,267 +67,338 @@ __device__ __forceinline__ bool vote_any(int id, bool mine) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_fwd_kernel(const Args a, int tiles_a_block, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+    attn_fwd_kernel(const Args a, int tiles_an_item, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv) {
   using Ly = Lay<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // a head's blocks from the last rows on: those that see most keys come first
-  const int head = blockIdx.x % a.HQ;
   grid_wait();
-  volatile Work *work = reinterpret_cast<volatile Work *>(smem + Ly::OFF_MISC + 16);
-  volatile int *failed = reinterpret_cast<volatile int *>(smem + Ly::OFF_MISC);
+  const uint32_t failed = sb + Ly::OFF_MISC;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
-  static_assert(sizeof(Work) <= 48, "room for it");
   const uint32_t bar = sb + Ly::OFF_BAR;
   auto FULL = [&](int i) { return bar + 8 * i; };
   auto EMPTY = [&](int i) { return bar + 8 * (Ly::NS + i); };
-  const uint32_t bx = bar + 16 * Ly::NS;
+  const uint32_t bw = bar + 16 * Ly::NS, bx = bw + 16 * kItems;
+  auto WF = [&](int i) { return bw + 8 * i; };  // an item is there, all have read it
+  auto WE = [&](int i) { return bw + 8 * (kItems + i); };
   auto SF = [&](int w) { return bx + 8 * w; };       // S is there
   auto PF = [&](int w) { return bx + 16 + 8 * w; };  // P is there
   auto OD = [&](int w) { return bx + 32 + 8 * w; };  // O is whole
-  const uint32_t QF = bx + 48, VR = bx + 56, VZ = bx + 64;  // VR: the last values are there, VZ: and clean behind the keys
-  const uint32_t DR = bx + 72;                              // also what the test's wait finds never done
-  if (warp == 0) {
-    const int R = tiles_a_block * kTile;
-    const int64_t slot = slots_of(a.Tq, a.N, R) - 1 - blockIdx.x / a.HQ;
-    Tile t;
-    const bool on = tile_of(a, slot, R, false, t);
-    if (lane == 0) {
-      work->on = on;
-      if (on) {
-        work->q_first = t.rows.first;
-        work->k_first = t.keys.first;
-        work->keys = t.keys.count;
-        work->row0 = t.row0;
-        work->past = t.keys.count - t.rows.count;
-        for (int w = 0; w < 2; ++w) {
-          const int left = t.rows.count - t.row0 - w * kTile, count = w < tiles_a_block ? max(0, min(kTile, left)) : 0;
-          const int seen = a.causal ? min(t.keys.count, t.keys.count - t.rows.count + t.row0 + w * kTile + count) : t.keys.count;
-          work->count[w] = count;
-          work->tiles[w] = count > 0 ? (max(0, seen) + kTile - 1) / kTile : 0;
-        }
-      }
-      for (int i = 0; i < Ly::NS; ++i) { mbar_init(FULL(i), 1); mbar_init(EMPTY(i), 1); }
-      for (int w = 0; w < 2; ++w) { mbar_init(SF(w), 1); mbar_init(PF(w), 8); mbar_init(OD(w), 1); }
-      mbar_init(QF, 1);
-      mbar_init(VR, 1);
-      mbar_init(VZ, 1);
-      mbar_init(DR, 1);
-      mbar_fence_init();
-      *failed = 0;
-    }
+  auto OE = [&](int w) { return bx + 48 + 8 * w; };  // O is read
+  const uint32_t QF = bx + 64, QE = bx + 72;         // Q is there, is done with
+  const uint32_t VR = bx + 80, VZ = bx + 88;         // the last values are there, and clean behind the keys
+  const uint32_t DR = bx + 96;                       // also what the test's wait finds never done
+  if (tid == 0) {
+    for (int i = 0; i < Ly::NS; ++i) { mbar_init(FULL(i), 1); mbar_init(EMPTY(i), 1); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(WF(i), 1); mbar_init(WE(i), 19); }
+    for (int w = 0; w < 2; ++w) { mbar_init(SF(w), 1); mbar_init(PF(w), 8); mbar_init(OD(w), 1); mbar_init(OE(w), 8); }
+    mbar_init(QF, 1);
+    mbar_init(QE, 1);
+    mbar_init(VR, 1);
+    mbar_init(VZ, 1);
+    mbar_init(DR, 1);
+    mbar_fence_init();
+    sts_i(failed, 0);
   }
   if (blockIdx.x == 0) check_offsets(a);
-  __syncthreads();
-  if (!work->on) return;
   if (warp == 17) tmem_alloc(sb + Ly::OFF_MISC + 8, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int wg = warp >> 2, w = wg >> 1, half = wg & 1, r = tid & 127;
-  const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-  const uint32_t S_col = tmem + lanes + w * 128 + half * 64, O_col = tmem + lanes + 256 + w * D + half * (D / 2);
-  float m_ref = -INFINITY, l_sum = 0.f;
-  int issued = 0;  // stages that the producer has filled
-  bool q_issued = false;
+  const int wg = warp >> 2;
+  // Waits for the it-th item; its place is given back, after its last use, by item_read.
+  auto item = [&](int it, uint32_t &w) {
+    w = sb + Ly::OFF_WORK + it % kItems * W_BYTES;
+    return wait_bar(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
+  };
+  auto item_read = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(WE(it % kItems));
+  };
 
   // 640 threads x 96 registers at the start: 512 x 104 + 128 x 64
   if (wg < 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // -------------------------------------------------------------- softmax
-    const int tiles = work->tiles[w], keys = work->keys, row0 = work->row0 + w * kTile;
-    const int low = a.causal ? work->past + row0 : keys - 1;  // what the tile's first row sees last
-    const int limit = a.causal ? min(low + r, keys - 1) : low;
-    volatile float *told = reinterpret_cast<volatile float *>(smem + Ly::OFF_X) + w * 256 + r;
+    const int w = wg >> 1, half = wg & 1, r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t S_col = tmem + lanes + w * 128 + half * 64, O_col = S_col + 256 - half * (64 - D / 2);
+    const uint32_t told = sb + Ly::OFF_X + tid * 4;  // the row's other thread's is told ^ 512
     bool ok = true;
     if (a.force_expiry && !mbar_wait_bounded(DR, 0, gdnc::kTestWaitLimit)) {
-      *failed = 1;
+      sts_i(failed, 1);
       set_status(a.dev_status, GDN_DEV_WAIT_TIMEOUT);
       ok = false;
     }
-    for (int j = 0; j < tiles; ++j) {
-      if (ok) ok = wait_bar(SF(w), j & 1, failed, a.dev_status);
-      tc_fence_after();
-      uint32_t s[64];
-      load64(S_col, s);
-      wait64(s);
-      const int k0 = j * kTile + half * 64;
-      if (k0 + 63 > low || k0 + 63 >= keys) {
+    uint32_t phases = 0;  // bit 0: of the tile's next S, bit 1: of its next O
+    if (lane == 0) mbar_arrive(OE(w));  // there is no O yet
+    for (int it = 0;; ++it) {
+      uint32_t work;
+      if (ok) ok = item(it, work);
+      if (vote_any(1 + w, !ok)) break;  // all 256 threads of a tile leave together, or none
+      if (!lds_i(work + W_ON)) break;
+      float m_ref = -INFINITY, l_sum = 0.f;
+      for (int j = 0; j < lds_i(work + W_TILES + 4 * w); ++j) {
+        if (ok) ok = wait_bar(SF(w), phases & 1, failed, a.dev_status);
+        phases ^= 1;
+        tc_fence_after();
+        uint32_t s[64];
+        load64(S_col, s);
+        wait64(s);
+        const int k0 = j * kTile + half * 64;
+        const int low = lds_i(work + W_LOW + 4 * w);
+        if (k0 + 63 > low) {
+          const int limit = a.causal ? min(low + r, lds_i(work + W_KEYS) - 1) : low;  // what this row sees last
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (k0 + i > limit) s[i] = __float_as_uint(-INFINITY);
-      }
-      float x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = __uint_as_float(s[16 * i]);
-#pragma unroll
-        for (int e = 1; e < 15; e += 2) x[i] = gdnkv::max3(x[i], __uint_as_float(s[16 * i + e]), __uint_as_float(s[16 * i + e + 1]));
-        x[i] = fmaxf(x[i], __uint_as_float(s[16 * i + 15]));
-      }
-      float top = fmaxf(gdnkv::max3(x[0], x[1], x[2]), x[3]) * a.scale_log2e;
-      // (of -inf both, NaN: no.  A wait that gave up votes too, so that all leave together.)
-      if (vote_any(1 + w, top - m_ref > kMost || !ok)) {
-        told[half * 128] = top;
-        if (vote_any(1 + w, !ok)) break;
-        top = fmaxf(top, told[(half ^ 1) * 128]);
-        float grow = 1.f;
-        if (top - m_ref > kMost) {
-          grow = ex2f(m_ref - top);
-          m_ref = top;
-          l_sum *= grow;
+          for (int i = 0; i < 64; ++i)
+            if (k0 + i > limit) s[i] = __float_as_uint(-INFINITY);
         }
-        if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {
-#pragma unroll 1
-          for (int i = 0; i < D / 2; i += 8) {  // few at a time: the logits hold 64 registers
-            uint32_t o[8];
-            gdnkv::tmem_ld8(O_col + i, o);
+        float top = __uint_as_float(s[0]), next = __uint_as_float(s[1]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * grow);
-            gdnkv::tmem_st8(O_col + i, o);
+        for (int i = 2; i < 62; i += 4) {
+          top = gdnkv::max3(top, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          next = gdnkv::max3(next, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+        }
+        top = gdnkv::max3(top, __uint_as_float(s[62]), __uint_as_float(s[63]));
+        top = fmaxf(top, next) * a.scale_log2e;
+        // (of -inf both, NaN: no.  A wait that gave up votes too.)
+        if (vote_any(1 + w, top - m_ref > kMost || !ok)) {
+          sts_f(told, top);
+          if (vote_any(1 + w, !ok)) goto leave;
+          top = fmaxf(top, lds_f(told ^ 512));
+          float grow = 1.f;
+          if (top - m_ref > kMost) {
+            grow = ex2f(m_ref - top);
+            m_ref = top;
+            l_sum *= grow;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {
+#pragma unroll 1
+            for (int i = 0; i < D / 2; i += 8) {  // few at a time: the logits hold 64 registers
+              uint32_t o[8];
+              gdnkv::tmem_ld8(O_col + i, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * grow);
+              gdnkv::tmem_st8(O_col + i, o);
+            }
           }
         }
-      }
-      const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-      float2 sum = make_float2(0.f, 0.f);
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float2 t = gdnkv::fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), a.scale_log2e, -ref);
-        t.x = ex2f(t.x);
-        t.y = ex2f(t.y);
-        sum = gdnkv::add2(sum, t);
-        s[i] = pack_bf16(t.x, t.y);
+        for (int i = 0; i < 32; ++i) {
+          float2 t = gdnkv::fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), a.scale_log2e, -ref);
+          t.x = ex2f(t.x);
+          t.y = ex2f(t.y);
+          sum = gdnkv::add2(sum, t);
+          s[i] = pack_bf16(t.x, t.y);
+        }
+        l_sum += sum.x + sum.y;
+        tmem_st32(S_col, s);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(PF(w));
       }
-      l_sum += sum.x + sum.y;
-      tmem_st32(S_col, s);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(PF(w));
+      // ------------------------------------------------------------- output
+      const int count = lds_i(work + W_COUNT + 4 * w);
+      const bool tiles = lds_i(work + W_TILES + 4 * w) > 0;
+      const int64_t at = (int64_t)(lds_i(work + W_Q) + lds_i(work + W_ROW0) + w * kTile + r) * a.HQ + lds_i(work + W_HEAD);
+      item_read(it);
+      if (count == 0) continue;
+      sts_f(told, l_sum);
+      if (tiles) {
+        ok = wait_bar(OD(w), phases >> 1 & 1, failed, a.dev_status);
+        phases ^= 2;
+      }
+      if (vote_any(1 + w, !ok)) break;
+      tc_fence_after();
+      const float l = l_sum + lds_f(told ^ 512), inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t *dst = a.o + at * D + half * (D / 2);
+#pragma unroll 1
+      for (int i = 0; i < D / 2; i += 8) {  // few at a time, as above
+        uint32_t o[8];
+        if (tiles) gdnkv::tmem_ld8(O_col + i, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = tiles && l != 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+        if (r < count)
+          *reinterpret_cast<uint4 *>(dst + i) = make_uint4(
+              pack_bf16(__uint_as_float(o[0]), __uint_as_float(o[1])), pack_bf16(__uint_as_float(o[2]), __uint_as_float(o[3])),
+              pack_bf16(__uint_as_float(o[4]), __uint_as_float(o[5])), pack_bf16(__uint_as_float(o[6]), __uint_as_float(o[7])));
+      }
+      if (tiles) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(OE(w));
+      }
+      if (r < count && half == 0) a.lse[at] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
     }
-    if (ok && !*failed && tiles > 0) wait_bar(OD(w), 0, failed, a.dev_status);
+  leave:;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    const int tiles0 = work->tiles[0], tiles1 = work->tiles[1], tiles = max(tiles0, tiles1), keys = work->keys;
-    const int tail = keys % kTile;  // keys of a last tile that is not full
-    const bool clear = tail != 0 && tiles * kTile > keys;
     if (warp == 16) {
-      // ----------------------------------------------------------- producer
-      if (tiles > 0 && elect_one()) {
-        const int row = work->q_first + work->row0, key = work->k_first, hk = head / a.G;
-        q_issued = true;
-        mbar_arrive_expect_tx(QF, (tiles0 > 0 && tiles1 > 0 ? 2 : 1) * Ly::TB);
-        if (tiles0 > 0) load_tile<D>(sb + Ly::OFF_Q, &mq, QF, head, row);
-        if (tiles1 > 0) load_tile<D>(sb + Ly::OFF_Q + Ly::TB, &mq, QF, head, row + kTile);
-        for (int i = 0; i < 2 * tiles; ++i) {
-          const int st = i % Ly::NS;
-          if (i >= Ly::NS && !wait_bar(EMPTY(st), (i / Ly::NS - 1) & 1, failed, a.dev_status)) break;
-          mbar_arrive_expect_tx(FULL(st), Ly::TB);
-          load_tile<D>(sb + Ly::OFF_KV + st * Ly::TB, (i & 1) ? &mv : &mk, FULL(st), hk, key + (i >> 1) * kTile);
-          issued = i + 1;
+      // ------------------------------------------------------------- copies
+      if (elect_one()) {
+        int issued = 0, asked = 0;  // stages filled, Q
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+          uint32_t work;
+          if (!item(it, work) || !lds_i(work + W_ON)) break;
+          const int tiles0 = lds_i(work + W_TILES), tiles1 = lds_i(work + W_TILES + 4), tiles = max(tiles0, tiles1);
+          const int row = lds_i(work + W_Q) + lds_i(work + W_ROW0), key = lds_i(work + W_K), head = lds_i(work + W_HEAD);
+          mbar_arrive(WE(it % kItems));
+          if (tiles == 0) continue;
+          ok = asked == 0 || wait_bar(QE, (asked - 1) & 1, failed, a.dev_status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(QF, (tiles0 > 0 && tiles1 > 0 ? 2 : 1) * Ly::TB);
+          if (tiles0 > 0) load_tile<D>(sb + Ly::OFF_Q, &mq, QF, head, row);
+          if (tiles1 > 0) load_tile<D>(sb + Ly::OFF_Q + Ly::TB, &mq, QF, head, row + kTile);
+          ++asked;
+          for (int i = 0; i < 2 * tiles; ++i, ++issued) {
+            const int st = issued % Ly::NS;
+            if (issued >= Ly::NS) ok = wait_bar(EMPTY(st), (issued / Ly::NS - 1) & 1, failed, a.dev_status);
+            if (!ok) break;
+            mbar_arrive_expect_tx(FULL(st), Ly::TB);
+            load_tile<D>(sb + Ly::OFF_KV + st * Ly::TB, (i & 1) ? &mv : &mk, FULL(st), head / a.G, key + (i >> 1) * kTile);
+          }
         }
-        if (*failed) {  // copies in flight
-          bool ok = mbar_wait_bounded(QF, 0, gdnc::kWaitLimit);
+        if (lds_i(failed)) {  // copies in flight
+          ok = asked == 0 || mbar_wait_bounded(QF, (asked - 1) & 1, gdnc::kWaitLimit);
           for (int i = 0; i < Ly::NS && i < issued; ++i)
             ok &= mbar_wait_bounded(FULL(i), ((issued - 1 - i) / Ly::NS) & 1, gdnc::kWaitLimit);
           if (!ok) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
         }
       }
-    } else if (warp == 18) {
-      // P is 0 past the sequence's keys, but 0 times what stands there need not be
-      if (clear) {
-        // (no limit of its own: the products' warp gets there, or gives up and says so)
-        bool there = true;
-        while (there && !mbar_try_wait(VR, 0)) there = !*failed;
-        if (__all_sync(0xffffffffu, there)) {
-          zero_rows<D>(sb + Ly::OFF_KV + (2 * tiles - 1) % Ly::NS * Ly::TB, tail);
-          if (lane == 0) mbar_arrive(VZ);
+    } else if (warp == 19) {
+      // -------------------------------------------------------------- items
+      const int R = tiles_an_item * kTile;
+      Walk walk;
+      walk_begin(a, walk, R, false, a.HQ);
+      for (int it = 0;; ++it) {
+        Found f;
+        const bool on = walk_to(a, walk, R, false, false, turn_item(it), f);
+        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
+        if (lane == 0) {
+          const uint32_t work = sb + Ly::OFF_WORK + it % kItems * W_BYTES;
+          sts_i(work + W_ON, on);
+          if (on) {
+            const int row0 = f.tile * R, past = f.keys.count - f.rows.count;
+            sts_i(work + W_Q, f.rows.first);
+            sts_i(work + W_K, f.keys.first);
+            sts_i(work + W_KEYS, f.keys.count);
+            sts_i(work + W_ROW0, row0);
+            sts_i(work + W_PAST, past);
+            sts_i(work + W_HEAD, f.in);
+            for (int w = 0; w < 2; ++w) {
+              const int count = w < tiles_an_item ? max(0, min(kTile, f.rows.count - row0 - w * kTile)) : 0;
+              const int seen = a.causal ? min(f.keys.count, past + row0 + w * kTile + count) : f.keys.count;
+              sts_i(work + W_LOW + 4 * w, a.causal ? min(f.keys.count - 1, past + row0 + w * kTile) : f.keys.count - 1);
+              sts_i(work + W_COUNT + 4 * w, count);
+              sts_i(work + W_TILES + 4 * w, count > 0 ? tiles_in(max(0, seen), kTile) : 0);
+            }
+          }
+          mbar_arrive(WF(it % kItems));
         }
+        __syncwarp();
+        if (!on) break;
       }
     } else if (warp == 17) {
       // ----------------------------------------------------------- products
-      if (tiles > 0 && elect_one()) {
-        auto stage = [&](int i) { return sb + Ly::OFF_KV + (i % Ly::NS) * Ly::TB; };
-        auto here = [&](int i) { return wait_bar(FULL(i % Ly::NS), (i / Ly::NS) & 1, failed, a.dev_status); };
-        // the row tiles that take part in key tile j: the first, the last
-        auto first = [&](int j) { return j < tiles0 ? 0 : 1; };
-        auto last = [&](int j) { return j < tiles1 ? 1 : 0; };
-        auto logits = [&](int x, int j) {
-          if (x == first(j)) {
-            if (!here(2 * j)) return false;
-            tc_fence_after();
-          }
-          mma_rows<D>(tmem + x * 128, sb + Ly::OFF_Q + x * Ly::TB, stage(2 * j));
-          umma_commit(SF(x));
-          if (x == last(j)) umma_commit(EMPTY(2 * j % Ly::NS));
-          return true;
+      // (by one thread throughout, and one that elect.sync names: a warp that waits together
+      // and elects one for each product took 1582 us for 16384 tokens, lane 0 by comparison
+      // 1866)
+      if (elect_one()) {
+        uint32_t pair = 0, phases = 0;  // (K, V) pairs of stages before; a bit for each barrier's next phase
+        auto wait = [&](uint32_t b, uint32_t phase) { return wait_bar(b, phase & 1, failed, a.dev_status); };
+        auto in_turn = [&](uint32_t b, int bit) {  // the next phase of a barrier that is waited for in each turn
+          const bool there = wait(b, phases >> bit);
+          phases ^= 1u << bit;
+          return there;
         };
-        bool ok = wait_bar(QF, 0, failed, a.dev_status);
-        for (int x = 0; x < 2; ++x)
-          if (ok && work->tiles[x] > 0) ok = logits(x, 0);
-        for (int j = 0; ok && j < tiles; ++j) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int mine = x ? tiles1 : tiles0;
-            if (!ok || j >= mine) continue;
-            ok = wait_bar(PF(x), j & 1, failed, a.dev_status);
-            if (ok && x == first(j)) {
-              ok = here(2 * j + 1);
-              if (ok && clear && j == tiles - 1) {
+        constexpr int NP = Ly::NS / 2;
+        for (int it = 0;; ++it) {
+          uint32_t work;
+          if (!item(it, work) || !lds_i(work + W_ON)) break;
+          const int tiles0 = lds_i(work + W_TILES), tiles1 = lds_i(work + W_TILES + 4), tiles = max(tiles0, tiles1);
+          const bool clear = tiles * kTile > lds_i(work + W_KEYS);
+          mbar_arrive(WE(it % kItems));
+          if (tiles == 0) continue;
+          // S of row tile x with key tile j; `alone`: the only row tile that j is for, or the last one
+          auto logits = [&](auto x, int j, bool first, bool last) {
+            const uint32_t st = 2 * ((pair + j) % NP);
+            if (first && !wait(FULL(st), (pair + j) / NP)) return false;
+            tc_fence_after();
+            mma_rows<D>(tmem + x * 128, sb + Ly::OFF_Q + x * Ly::TB, sb + Ly::OFF_KV + st * Ly::TB);
+            umma_commit(SF(x));
+            if (last) {
+              umma_commit(EMPTY(st));
+              if (j == tiles - 1) umma_commit(QE);
+            }
+            return true;
+          };
+          // P V of row tile x with key tile j, and the S that may follow it
+          auto values = [&](auto x, int j, int mine, int other) {
+            const bool first = x == 0 || j >= other, last = x == 1 || j >= other;
+            const uint32_t st = 2 * ((pair + j) % NP) + 1;
+            if (first) {
+              if (!wait(FULL(st), (pair + j) / NP)) return false;
+              if (clear && j == tiles - 1) {
                 mbar_arrive(VR);
-                ok = wait_bar(VZ, 0, failed, a.dev_status);
+                if (!in_turn(VZ, 0)) return false;
               }
             }
-            if (!ok) break;
+            if (!in_turn(PF(x), 1 + x)) return false;
+            if (j == 0 && !in_turn(OE(x), 3 + x)) return false;
             tc_fence_after();
-            mma_cols<D>(tmem + 256 + x * D, tmem + x * 128, stage(2 * j + 1), j > 0);
-            if (x == last(j)) umma_commit(EMPTY((2 * j + 1) % Ly::NS));
-            if (j + 1 < mine) ok = logits(x, j + 1);
-            else umma_commit(OD(x));
+            mma_cols<D>(tmem + 256 + x * 128, tmem + x * 128, sb + Ly::OFF_KV + st * Ly::TB, j > 0);
+            if (last) umma_commit(EMPTY(st));
+            if (j + 1 == mine) {
+              umma_commit(OD(x));
+              return true;
+            }
+            return logits(x, j + 1, x == 0 || j + 1 >= other, x == 1 || j + 1 >= other);
+          };
+          constexpr std::integral_constant<int, 0> X0{};
+          constexpr std::integral_constant<int, 1> X1{};
+          bool ok = in_turn(QF, 5);
+          if (tiles0 > 0) ok = ok && logits(X0, 0, true, tiles1 == 0);
+          if (tiles1 > 0) ok = ok && logits(X1, 0, tiles0 == 0, true);
+          for (int j = 0; ok && j < tiles; ++j) {
+            if (j < tiles0) ok = values(X0, j, tiles0, tiles1);
+            if (ok && j < tiles1) ok = values(X1, j, tiles1, tiles0);
           }
+          if (!ok) break;
+          pair += tiles;
         }
-        if (!ok) {  // let the products in flight finish before the block leaves
+        if (lds_i(failed)) {  // let the products in flight finish before the block leaves
           umma_commit(DR);
           if (!mbar_wait_bounded(DR, 0, gdnc::kWaitLimit)) set_status(a.dev_status, GDN_DEV_DRAIN_TIMEOUT);
         }
       }
+    } else if (warp == 18) {
+      // ------------------------------------- values past the sequence's keys
+      // P is 0 there, but 0 times what stands there need not be
+      int stages = 0, turn = 0;
+      for (int it = 0;; ++it) {
+        uint32_t work;
+        if (!__all_sync(0xffffffffu, item(it, work)) || !lds_i(work + W_ON)) break;
+        const int tiles = max(lds_i(work + W_TILES), lds_i(work + W_TILES + 4)), keys = lds_i(work + W_KEYS);
+        item_read(it);
+        stages += 2 * tiles;
+        if (tiles * kTile <= keys) continue;
+        bool there = true;  // (no limit of its own: the products' warp gets there, or gives up and says so)
+        while (there && !mbar_try_wait(VR, turn & 1)) there = !lds_i(failed);
+        if (!__all_sync(0xffffffffu, there)) break;
+        ++turn;
+        zero_rows<D>(sb + Ly::OFF_KV + (stages - 1) % Ly::NS * Ly::TB, keys % kTile);
+        if (lane == 0) mbar_arrive(VZ);
+      }
     }
     __syncwarp();
   }
-  __syncthreads();
-  if (wg < 4 && !*failed) {
-    // ---------------------------------------------------------------- output
-    tc_fence_after();
-    const int count = work->count[w], tiles = work->tiles[w];
-    volatile float *told = reinterpret_cast<volatile float *>(smem + Ly::OFF_X) + w * 256 + r;
-    told[half * 128] = l_sum;
-    named_bar_sync(1 + w, 256);
-    const float l = told[0] + told[128], inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = (int64_t)(work->q_first + work->row0 + w * kTile + r) * a.HQ + head;
-#pragma unroll 1
-    for (int i = 0; i < D / 2; i += 32) {
-      uint32_t o[32];
-      if (tiles > 0) {
-        tmem_ld32_issue(O_col + i, o);
-        tmem_ld_wait(o);
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = tiles > 0 && l != 0.f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-      if (r < count) {
-        uint16_t *dst = a.o + at * D + half * (D / 2) + i;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4 *>(dst + e) =
-              make_uint4(pack_bf16(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), pack_bf16(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                         pack_bf16(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])), pack_bf16(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-      }
-    }
-    if (r < count && half == 0) a.lse[at] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
-    tc_fence_before();
-  }
+  tc_fence_before();
   __syncthreads();
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
@@ -344,9 +418,9 @@ template <int D> cudaError_t launch(const Args &a, cudaStream_t s) {
     return cudaFuncGetAttributes(&f, attn_fwd_kernel<D>) == cudaSuccess && f.numRegs == 96;
   }();
   if (!shares) return cudaErrorInvalidConfiguration;
-  const int each = slots_of(a.Tq, a.N, 2 * kTile) * a.HQ >= gdn_host::sm_count() ? 2 : 1;
-  const int64_t blocks = slots_of(a.Tq, a.N, each * kTile) * a.HQ;
-  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+  const int sms = gdn_host::sm_count();
+  const int each = most_tiles(a.Tq, a.N, 2 * kTile) * a.HQ >= sms ? 2 : 1;
+  const int64_t blocks = std::min<int64_t>(most_tiles(a.Tq, a.N, each * kTile) * a.HQ, sms);
   return gdn_host::launch_dependent(attn_fwd_kernel<D>, dim3((unsigned)blocks), kThreads, Lay<D>::BYTES, s, a, each, mq, mk, mv);
 }
 

@@ -10,13 +10,13 @@ from __future__ import annotations
 import argparse
 import dataclasses
 import math
-from typing import List
+from typing import List, Optional
 
 import torch
 
-from . import (chunk_gated_delta_rule, gdn_causal_conv1d_fwd, gdn_chunk_fwd_gated, gdn_conv_decode_pack, gdn_kv8_append,
-               gdn_kv8_attention, gdn_norm_gate, gdn_paged_plan, gdn_recurrent_decode, gdn_rope, norm_gate,
-               rope_frequencies, rotary_embedding)
+from . import (attention, chunk_gated_delta_rule, gdn_causal_conv1d_fwd, gdn_chunk_fwd_gated, gdn_conv_decode_pack, gdn_kv8_append,
+               gdn_kv8_attention, gdn_norm_gate, gdn_paged_plan, gdn_recurrent_decode, gdn_rope, linear8,
+               norm_gate, rope_frequencies, rotary_embedding)
 
 BF = torch.bfloat16
 
@@ -138,38 +138,40 @@ class HybridStack:
             out += [layer.norm, layer.w_in, layer.w_out] + ([layer.out_norm] if layer.kind == "g" else [])
         return out
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
-        """Differentiable, for one sequence x bf16 [T, hidden] from its beginning (no convolution; attention in plain
-        torch operations, as the cache's attention is for serving)."""
+    def forward(self, x: torch.Tensor, lens: Optional[List[int]] = None, save8: bool = False) -> torch.Tensor:
+        """Differentiable, for packed sequences x bf16 [T, hidden] of these lengths (None: one) from their beginnings (no
+        convolution).  With ``save8`` the norms and projections keep their inputs for the gradient in 8 bits."""
         cfg, T = self.cfg, x.shape[0]
-        positions = torch.arange(T, dtype=torch.int32, device=x.device)
+        lens = [T] if lens is None else lens
+        cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(x.device)
+        positions = torch.cat([torch.arange(m, dtype=torch.int32) for m in lens]).to(x.device)
+        linear = linear8 if save8 else lambda x, w: x @ w.T
         h, y = x, None
         for layer in self.layers:
             if y is None:
-                n, _ = norm_gate(h, layer.norm)
+                n, _ = norm_gate(h, layer.norm, save8=save8)
             else:
-                n, h = norm_gate(y, layer.norm, residual=h)
-            u = n @ layer.w_in.T
+                n, h = norm_gate(y, layer.norm, residual=h, save8=save8)
+            u = linear(n, layer.w_in)
             if layer.kind == "a":
                 q, k, v = u.view(T, -1, cfg.D).split([cfg.HQ, cfg.HK, cfg.HK], dim=1)
                 q, k = rotary_embedding(q, k, positions, self.inv_freq, attention_factor=self.rope_factor)
-                k, v = (t.repeat_interleave(cfg.HQ // cfg.HK, dim=1).transpose(0, 1).float() for t in (k, v))
-                s = q.transpose(0, 1).float() @ k.transpose(1, 2) / math.sqrt(cfg.D)
-                s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device=x.device).triu(1), -math.inf)
-                o = (s.softmax(-1) @ v).transpose(0, 1).to(BF)
+                o = attention(q, k, v, cu_seqlens=cu)
             else:
                 q, k, v, z, a, b = u.split([cfg.H * cfg.K, cfg.H * cfg.K, cfg.HV * cfg.K, cfg.HV * cfg.K, cfg.HV, cfg.HV], dim=1)
                 q, k, v = (t.contiguous().view(1, T, -1, cfg.K) for t in (q, k, v))
                 g = -layer.A_log.exp() * torch.nn.functional.softplus(a.float() + layer.dt_bias)
-                o, _ = chunk_gated_delta_rule(q, k, v, g.view(1, T, -1), b.float().sigmoid().view(1, T, -1), output_final_state=False)
-                o, _ = norm_gate(o.view(T, cfg.HV, cfg.K), layer.out_norm, z=z.unflatten(1, (cfg.HV, cfg.K)))
-            y = o.reshape(T, -1) @ layer.w_out.T
-        return norm_gate(y, self.norm, residual=h)[0]
+                o, _ = chunk_gated_delta_rule(q, k, v, g.view(1, T, -1), b.float().sigmoid().view(1, T, -1), output_final_state=False,
+                                              cu_seqlens=cu, num_seqs=len(lens))
+                o, _ = norm_gate(o.view(T, cfg.HV, cfg.K), layer.out_norm, z=z.unflatten(1, (cfg.HV, cfg.K)), save8=save8)
+            y = linear(o.reshape(T, -1), layer.w_out)
+        return norm_gate(y, self.norm, residual=h, save8=save8)[0]
 
-    def train_step(self, x: torch.Tensor, target: torch.Tensor, rate: float = 1e-2) -> float:
+    def train_step(self, x: torch.Tensor, target: torch.Tensor, rate: float = 1e-2, lens: Optional[List[int]] = None,
+                   save8: bool = False) -> float:
         """One step of gradient descent on the mean square difference from target; returns the loss before it."""
         params = [p.requires_grad_(True) for p in self.parameters()]
-        loss = (self.forward(x).float() - target.float()).square().mean()
+        loss = (self.forward(x, lens, save8).float() - target.float()).square().mean()
         grads = torch.autograd.grad(loss, params)
         with torch.no_grad():
             for p, g in zip(params, grads):
@@ -197,6 +199,8 @@ def main(argv=None) -> None:
     train = HybridStack(seed=2, requests=1)
     x, t = (torch.randn(256, train.cfg.hidden, generator=gen).to(train.device, BF) for _ in range(2))
     print("training, mean square difference:", " ".join(f"{train.train_step(x, t, 0.5):.4f}" for _ in range(5)))
+    lens = [100, 1, 155]
+    print("packed sequences, inputs kept in 8 bits:", " ".join(f"{train.train_step(x, t, 0.5, lens, True):.4f}" for _ in range(5)))
 
 
 if __name__ == "__main__":
