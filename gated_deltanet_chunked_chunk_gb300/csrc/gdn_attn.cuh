@@ -237,7 +237,23 @@ template <int D> __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a
   for (int k = 0; k < 8; ++k) umma_f16_ta(d, a + (k / 4) * 64 + (k % 4) * 8, db + k * 128, id, add || k > 0);
 }
 
-// a b + c, a b and a - b of two numbers each.
+// Half of mma_cols: the columns 0-31 and 64-95 of A (part 0), or the others, added.
+template <int D> __device__ __forceinline__ void mma_cols_half(uint32_t d, uint32_t a, uint32_t b, int part, bool add) {
+  constexpr uint32_t id = umma_idesc_bf16(128, D, 0, 1);
+  const uint64_t db = umma_desc_sw128_mn(b, kTile * 128);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = (i >> 1) * 4 + part * 2 + (i & 1);
+    umma_f16_ta(d, a + (k / 4) * 64 + (k % 4) * 8, db + k * 128, id, add || part > 0 || i > 0);
+  }
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+               "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+               : "memory");
+}
+// a b + c and a b of two numbers each.
 __device__ __forceinline__ float2 fma2v(float2 a, float b, float2 c) {
   float2 r;
   asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %4}; mov.b64 z, {%5, %6}; fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x; }"
