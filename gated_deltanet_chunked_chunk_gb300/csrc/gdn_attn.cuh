@@ -123,67 +123,88 @@ __device__ __forceinline__ bool tile_of(const Args &a, int64_t slot, int R, bool
   t.row0 = (int)row0;
   return true;
 }
-// The items of a call in the order in which blocks take them: chunks of 32 sequences, in
-// each those of most work first (of all its sequences the u-th tiles from the cheap end,
-// u from the largest down), `inner` items a tile.  All lanes of the walking warp are
-// in step; lane l holds sequence chunk + l.
+// The items of a call in the order in which blocks take them: chunks of up to 32 sequences,
+// in each those of most work first (of all its sequences the u-th tiles from the cheap end,
+// u from the largest down).  What a tile walks along (the keys, or the rows of all heads of
+// a group) is walked by every other tile of its sequence, so a chunk has no more of it than
+// stays in L2: `most` tokens.  All lanes of the walking warp are in step; lane l holds
+// sequence chunk + l.
 struct Walk {
-  int chunk, level, inner;
-  int64_t base;  // index of the level's first item
+  int chunk, count, level;  // first sequence, sequences; tiles from the cheap end
+  int64_t base;             // index of the level's first item
   Run rows, keys;
-  int tiles;     // this lane's sequence's
+  int tiles;                // this lane's sequence's
 };
 struct Found {
   int n;           // sequence
   Run rows, keys;  // its rows and keys
-  int tile, in;    // tile of R, which of the inner ones
+  int tile, in;    // tile of R, which of the tile's items
+  int of;          // items of the tile
 };
+constexpr int64_t kStays = 64 << 20;  // bytes: half of L2
 __device__ __forceinline__ int tiles_in(int count, int R) { return (count + R - 1) / R; }
-__device__ __forceinline__ void walk_chunk(const Args &a, Walk &w, int R, bool by_keys) {
-  const int n = w.chunk + (threadIdx.x & 31);
+__device__ __forceinline__ int64_t most_tokens(int heads, int D) { return kStays / ((int64_t)heads * D * 4); }  // of two bf16 tensors
+__device__ __forceinline__ void walk_chunk(const Args &a, Walk &w, int R, bool by_keys, int64_t most) {
+  const int lane = threadIdx.x & 31, n = w.chunk + lane;
   w.rows = Run{0, 0};
   w.keys = Run{0, 0};
   w.tiles = 0;
-  if (n <= a.N && run_of(rows_of(a), n, w.rows) && run_of(keys_of(a), n, w.keys)) {
-    if (n == a.N) (by_keys ? w.rows : w.keys).count = 0;
-    w.tiles = tiles_in((by_keys ? w.keys : w.rows).count, R);
+  const bool ok = n <= a.N && run_of(rows_of(a), n, w.rows) && run_of(keys_of(a), n, w.keys);
+  if (ok && n == a.N) (by_keys ? w.rows : w.keys).count = 0;
+  int64_t upto = ok ? (by_keys ? w.rows : w.keys).count : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
   }
+  w.count = max(1, __popc(__ballot_sync(0xffffffffu, upto <= most)));
+  if (ok && lane < w.count) w.tiles = tiles_in((by_keys ? w.keys : w.rows).count, R);
   w.level = (int)__reduce_max_sync(0xffffffffu, (unsigned)w.tiles) - 1;
 }
-__device__ __forceinline__ void walk_begin(const Args &a, Walk &w, int R, bool by_keys, int inner) {
+__device__ __forceinline__ void walk_begin(const Args &a, Walk &w, int R, bool by_keys, int64_t most) {
   w.chunk = 0;
-  w.inner = inner;
   w.base = 0;
-  walk_chunk(a, w, R, by_keys);
+  walk_chunk(a, w, R, by_keys, most);
 }
 // Item `index` (not below the one before); false: there are no more.  `first_most`: the
-// first tiles of a sequence have most work, else the last ones.
-__device__ __forceinline__ bool walk_to(const Args &a, Walk &w, int R, bool by_keys, bool first_most, int64_t index, Found &f) {
+// first tiles of a sequence have most work, else the last ones.  items(tile): how many
+// items the tile of this lane's sequence is.
+template <class F>
+__device__ __forceinline__ bool walk_to(const Args &a, Walk &w, int R, bool by_keys, bool first_most, int64_t most, int64_t index, Found &f,
+                                        F items) {
+  const int lane = threadIdx.x & 31;
   for (;;) {
     if (w.level >= 0) {
-      const uint32_t m = __ballot_sync(0xffffffffu, w.tiles > w.level);
-      const int64_t items = (int64_t)__popc(m) * w.inner;
-      if (index < w.base + items) {
-        const int64_t at = index - w.base;
-        const int l = __fns(m, 0, (int)(at / w.inner) + 1);
+      const int tile = first_most ? w.tiles - 1 - w.level : w.level, mine = w.tiles > w.level ? items(tile) : 0;
+      int upto = mine;  // (below 2^31: 32 sequences)
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const int all = __shfl_sync(0xffffffffu, upto, 31);
+      if (index < w.base + all) {
+        const int at = (int)(index - w.base), l = __ffs((int)__ballot_sync(0xffffffffu, at < upto)) - 1;
         f.n = w.chunk + l;
-        f.in = (int)(at % w.inner);
+        f.of = __shfl_sync(0xffffffffu, mine, l);
+        f.in = at - (__shfl_sync(0xffffffffu, upto, l) - f.of);
         f.rows.first = __shfl_sync(0xffffffffu, w.rows.first, l);
         f.rows.count = __shfl_sync(0xffffffffu, w.rows.count, l);
         f.keys.first = __shfl_sync(0xffffffffu, w.keys.first, l);
         f.keys.count = __shfl_sync(0xffffffffu, w.keys.count, l);
-        f.tile = first_most ? __shfl_sync(0xffffffffu, w.tiles, l) - 1 - w.level : w.level;
+        f.tile = __shfl_sync(0xffffffffu, tile, l);
         return true;
       }
-      w.base += items;
+      w.base += all;
       --w.level;
     } else {
-      w.chunk += 32;
+      w.chunk += w.count;
       if (w.chunk > a.N) return false;
-      walk_chunk(a, w, R, by_keys);
+      walk_chunk(a, w, R, by_keys, most);
     }
   }
 }
+
 // The item that a block takes in its k-th turn: every other turn the other way round, so
 // that no block has the larger one of every turn.
 __device__ __forceinline__ int64_t turn_item(int64_t k) {

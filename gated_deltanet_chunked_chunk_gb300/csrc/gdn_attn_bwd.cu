@@ -44,24 +44,31 @@ using namespace gdnat;
 constexpr int kThreads = 384;  // warps 0-7 P and dS, 8 copies, 9 products, 10 clears rows past the end
 
 constexpr int kBlocks = 152;  // SMs
-constexpr int kItems = 4;  // items between the warp that finds them and the others
+constexpr int kNear = 4;      // steps before its end from which a walk is about to end
+constexpr int kItems = 1;  // items between the warp that finds them and the others: it takes the next when all have one
 
 struct BwdArgs : Args {
   float *stats;  // [HQ][q slots][2][kTile]: -lse log2 e, delta
   float *part;   // [piece][k slots][HK][2][kTile][D]: sums of dK and dV
-  int *cut;      // steps that a piece of a walk has at least
+  struct Shared {
+    int cut;               // steps that a piece of a walk has at least
+    int next_kv, next_q;   // items that the blocks of the two kernels have taken
+  } *shared;
   int64_t q_slots, k_slots;
   int pieces;  // most pieces of a walk
 };
 
-// The row tiles that see some key of the tile from key k0 on: [t0, t0 + nt).
-__device__ __forceinline__ void seen_by(const Args &a, int rows, int keys, int k0, int &t0, int &nt) {
-  const int tn = tiles_in(rows, kTile);
-  t0 = min(tn, a.causal ? max(0, k0 - (keys - rows)) / kTile : 0);
-  nt = tn - t0;
+// The row tiles that see some key of the tile from key k0 on are [t0, tn).
+__device__ __forceinline__ int first_seen_by(const Args &a, int tn, int rows, int keys, int k0) {
+  return min(tn, a.causal ? max(0, k0 - (keys - rows)) / kTile : 0);
 }
-__device__ __forceinline__ int pieces_for(const BwdArgs &a, int64_t steps, int cut) {
-  return (int)max((int64_t)1, min((int64_t)a.pieces, (steps + cut - 1) / cut));
+__device__ __forceinline__ int pieces_for(const BwdArgs &a, int steps, int cut) { return max(1, min(a.pieces, (steps + cut - 1) / cut)); }
+// The next item that no block has taken, for a warp: blocks take them as they come free, as
+// walks have from one to many thousand steps.  (Which block has an item changes no result.)
+__device__ __forceinline__ int64_t take_item(int *next) {
+  int i = 0;
+  if ((threadIdx.x & 31) == 0) i = atomicAdd(next, 1);
+  return __shfl_sync(0xffffffffu, i, 0);
 }
 
 // ------------------------------------------------------------ of each row
@@ -74,6 +81,8 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
     check_offsets(a);
     // The walks of dK, dV have some steps in all (here by a sum over their tiles, to a tile
     // for the diagonal): a piece has a quarter of a block's share at least, and 16.
+    // The walks of dK, dV have some steps in all (to a tile for the diagonal): a piece has a
+    // quarter of a block's share at least, and 4.
     __shared__ unsigned long long total;
     if (threadIdx.x == 0) total = 0;
     __syncthreads();
@@ -83,12 +92,16 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
       if (!run_of(rows_of(a), n, rows) || !run_of(keys_of(a), n, keys)) continue;
       const int64_t tn = tiles_in(rows.count, kTile), kn = tiles_in(keys.count, kTile);
       // under the mask, tiles from `free` on lose one row tile each, two, ..
-      const int64_t free = max(0, keys.count - rows.count) / kTile, cut = a.causal ? max((int64_t)0, kn - free) : 0;
-      mine += max((int64_t)1, tn * kn - cut * (cut - 1) / 2);
+      const int64_t free = max(0, keys.count - rows.count) / kTile, lost = a.causal ? max((int64_t)0, kn - free) : 0;
+      mine += max((int64_t)1, tn * kn - lost * (lost - 1) / 2);
     }
     atomicAdd(&total, mine);
     __syncthreads();
-    if (threadIdx.x == 0) *a.cut = (int)min((unsigned long long)INT_MAX, max(16ull, total * a.HQ / (4 * kBlocks)));
+    if (threadIdx.x == 0) {
+      a.shared->cut = (int)min((unsigned long long)INT_MAX, max(4ull, total * a.HQ / (4 * kBlocks)));
+      a.shared->next_kv = 0;
+      a.shared->next_q = 0;
+    }
   }
   Tile t;
   if (!tile_of(a, slot, kTile, false, t)) return;
@@ -133,7 +146,7 @@ template <int D> struct KvLay {
   static constexpr int OFF_T = OFF_O + NO * TB;
   static constexpr int OFF_WORK = OFF_T + NT * 2 * kTile * 4;
   static constexpr int OFF_BAR = OFF_WORK + kItems * K_BYTES;
-  static constexpr int BARS = 2 * (NQ + NO + NT + kItems) + 12;
+  static constexpr int BARS = 2 * (NQ + NO + NT + kItems) + 13;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static_assert(BYTES <= 227 * 1024, "one block an SM");
@@ -162,13 +175,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto WE = [&](int i) { return bw + 8 * (kItems + i); };
   const uint32_t KF = bx, KE = bx + 8, SF = bx + 16, DF = bx + 24, PF = bx + 32, GF = bx + 40;  // K and V are there, done with; S, dP, P, dS are there
   const uint32_t DONE = bx + 48, AE = bx + 56, VR = bx + 64, VZ = bx + 72;  // dK and dV are whole, are read; a tile to clear is there, is clean
-  const uint32_t DR = bx + 80, PH = bx + 88;  // PH: half of P
+  const uint32_t DR = bx + 80, PH = bx + 88, NEAR = bx + 96;  // PH: half of P; NEAR: the item is about to end
   if (tid == 0) {
     for (int i = 0; i < Ly::NQ; ++i) { mbar_init(QF(i), 1); mbar_init(QE(i), 1); }
     for (int i = 0; i < Ly::NO; ++i) { mbar_init(OF(i), 1); mbar_init(OE(i), 1); }
     for (int i = 0; i < Ly::NT; ++i) { mbar_init(TF(i), 1); mbar_init(TE(i), 8); }
     for (int i = 0; i < kItems; ++i) { mbar_init(WF(i), 1); mbar_init(WE(i), 11); }
-    for (uint32_t b : {KF, KE, SF, DF, DONE, VR, VZ, DR}) mbar_init(b, 1);
+    for (uint32_t b : {KF, KE, SF, DF, DONE, VR, VZ, DR, NEAR}) mbar_init(b, 1);
     for (uint32_t b : {PF, PH, GF, AE}) mbar_init(b, 8);
     mbar_fence_init();
     sts_i(failed, 0);
@@ -385,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int steps = lds_i(work + K_STEPS), nt = lds_i(work + K_NT), tail = lds_i(work + K_ROWS) % kTile;
           int t = steps > 0 ? lds_i(work + K_S0) % nt : 0;
           mbar_arrive(WE(it % kItems));
+          if (steps <= kNear) mbar_arrive(NEAR);
           if (steps == 0) continue;
           auto wait = [&](uint32_t b, uint32_t phase) { return wait_bar(b, phase & 1, failed, a.dev_status); };
           auto q_tile = [&](uint32_t m) { return sb + Ly::OFF_Q + m % Ly::NQ * Ly::TB; };
@@ -413,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool ok = wait(KF, items) && logits(n) && slopes(n, steps == 1);
           for (int i = 0; ok && i < steps; ++i, ++n) {
             const bool more = i + 1 < steps;
+            if (i > 0 && i == steps - kNear) mbar_arrive(NEAR);
             ok = wait(PH, n) && (i > 0 || wait(AE, items));
             if (!ok) break;
             tc_fence_after();
@@ -464,28 +479,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // -------------------------------------------------------------- items
-      Walk walk;
-      walk_begin(a, walk, kTile, true, a.HK * a.pieces);
-      const int cut = *a.cut;
-      int it = 0;
-      for (int64_t k = 0;; ++k) {
+      const int cut = a.shared->cut;
+      const int64_t most = most_tokens(a.HQ, D);
+      Walk w;
+      walk_begin(a, w, kTile, true, most);
+      for (int it = 0;; ++it) {
         Found f;
-        const bool on = walk_to(a, walk, kTile, true, true, turn_item(k), f);
-        int t0 = 0, nt = 0, pieces = 1, piece = 0;
-        int64_t all = 0;
+        // taken when the one before is about to end, which leaves time for its copies
+        if (it > 0 && !__all_sync(0xffffffffu, wait_bar(NEAR, (it - 1) & 1, failed, a.dev_status))) break;
+        const bool on = walk_to(a, w, kTile, true, true, most, take_item(&a.shared->next_kv), f, [&](int tile) {
+          const int tn = tiles_in(w.rows.count, kTile);
+          return a.HK * pieces_for(a, a.G * (tn - first_seen_by(a, tn, w.rows.count, w.keys.count, tile * kTile)), cut);
+        });
+        int t0 = 0, nt = 0, pieces = 1;
         if (on) {
-          seen_by(a, f.rows.count, f.keys.count, f.tile * kTile, t0, nt);
-          all = (int64_t)a.G * nt;
-          pieces = pieces_for(a, all, cut);
-          piece = f.in % a.pieces;
-          if (piece >= pieces) continue;
+          const int tn = tiles_in(f.rows.count, kTile);
+          t0 = first_seen_by(a, tn, f.rows.count, f.keys.count, f.tile * kTile);
+          nt = tn - t0;
+          pieces = f.of / a.HK;
         }
+        const int64_t all = (int64_t)a.G * nt;
+        const int piece = f.in % pieces;
         if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
         if (lane == 0) {
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * K_BYTES;
           sts_i(work + K_ON, on);
           if (on) {
-            const int s0 = (int)(all * piece / pieces), hk = f.in / a.pieces;
+            const int s0 = (int)(all * piece / pieces), hk = f.in / pieces;
             const int64_t slot = f.keys.first / kTile + f.n + f.tile;
             sts_i(work + K_Q, f.rows.first);
             sts_i(work + K_ROWS, f.rows.count);
@@ -505,7 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!on) break;
-        ++it;
       }
     }
   }
@@ -522,15 +541,15 @@ template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const B
   grid_wait();
   Tile t;
   if (!tile_of(a, slot, kTile, true, t)) return;
-  int t0, nt;
-  seen_by(a, t.rows.count, t.keys.count, t.row0, t0, nt);
-  const int pieces = pieces_for(a, (int64_t)a.G * nt, *a.cut);
+  const int tn = tiles_in(t.rows.count, kTile);
+  const int pieces = pieces_for(a, a.G * (tn - first_seen_by(a, tn, t.rows.count, t.keys.count, t.row0)), a.shared->cut);
   if (pieces == 1) return;
   const int rows = min(kTile, t.keys.count - t.row0);
-  for (int i = threadIdx.x; i < 2 * rows * (D / 8); i += 256) {
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < 2 * rows * (D / 8); i += gridDim.y * 256) {
     const bool second = i >= rows * (D / 8);
     const int e = second ? i - rows * (D / 8) : i, r = e / (D / 8), c = e % (D / 8) * 8;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+#pragma unroll 4
     for (int p = 0; p < pieces; ++p) {
       const float4 *src =
           reinterpret_cast<const float4 *>(a.part + ((((p * a.k_slots + slot) * a.HK + hk) * 2 + (second ? 1 : 0)) * kTile + r) * D + c);
@@ -873,11 +892,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // -------------------------------------------------------------- items
-      Walk walk;
-      walk_begin(a, walk, kTile, false, a.HQ);
+      const int64_t most = most_tokens(a.HK, D);
+      Walk w;
+      walk_begin(a, w, kTile, false, most);
       for (int it = 0;; ++it) {
         Found f;
-        const bool on = walk_to(a, walk, kTile, false, false, turn_item(it), f);
+        const bool on = walk_to(a, w, kTile, false, false, most, take_item(&a.shared->next_q), f, [&](int) { return a.HQ; });
         if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
         if (lane == 0) {
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * Q_BYTES;
@@ -907,9 +927,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-// Most pieces of a (key tile, kv head)'s walk: enough for eight items an SM.
+// Most pieces of a (key tile, kv head)'s walk: enough for two items an SM.
 int pieces_of(int64_t k_tiles, int HK) {
-  const int64_t items = std::max<int64_t>(1, k_tiles * HK), want = (8 * kBlocks + items - 1) / items;
+  const int64_t items = std::max<int64_t>(1, k_tiles * HK), want = (2 * kBlocks + items - 1) / items;
   return (int)std::min<int64_t>(want, 8);
 }
 
@@ -940,7 +960,7 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   if (e == cudaSuccess && keys)
     e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tk, a.N, kTile) * a.HK * a.pieces, sms)), kThreads, KvLay<D>::BYTES, s, a, mq, mk, mv, mo);
   if (e == cudaSuccess && rows) e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tq, a.N, kTile) * a.HQ, sms)), kThreads, QLay<D>::BYTES, s, a, mq, mk, mv, mo);
-  if (e == cudaSuccess && keys && a.pieces > 1) e = gdn_host::launch_dependent(attn_join_kernel<D>, dim3((unsigned)k_blocks), 256, 0, s, a);
+  if (e == cudaSuccess && keys && a.pieces > 1) e = gdn_host::launch_dependent(attn_join_kernel<D>, dim3((unsigned)k_blocks, 8), 256, 0, s, a);
   return e;
 }
 
@@ -961,7 +981,7 @@ cudaError_t launch_attn_bwd(const TrainAttnArgs &c, cudaStream_t s) {
   a.q_slots = gdnat::slots_of(c.Tq, c.N, gdnat::kTile);
   a.k_slots = gdnat::slots_of(c.Tk, c.N, gdnat::kTile);
   a.pieces = pieces_of(gdnat::most_tiles(c.Tk, c.N, gdnat::kTile), c.HK);
-  a.cut = static_cast<int *>(c.ws);
+  a.shared = static_cast<BwdArgs::Shared *>(c.ws);
   a.stats = reinterpret_cast<float *>(static_cast<char *>(c.ws) + 16);
   a.part = a.stats + stats_bytes(c.N, c.Tq, c.HQ) / sizeof(float);
   return c.D == 128 ? launch<128>(a, s) : launch<64>(a, s);

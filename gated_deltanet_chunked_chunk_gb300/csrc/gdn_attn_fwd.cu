@@ -275,10 +275,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -------------------------------------------------------------- items
       const int R = tiles_an_item * kTile;
       Walk walk;
-      walk_begin(a, walk, R, false, a.HQ);
+      const int64_t most = most_tokens(a.HK, D);
+      walk_begin(a, walk, R, false, most);
       for (int it = 0;; ++it) {
         Found f;
-        const bool on = walk_to(a, walk, R, false, false, turn_item(it), f);
+        const bool on = walk_to(a, walk, R, false, false, most, turn_item(it), f, [&](int) { return a.HQ; });
         if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
         if (lane == 0) {
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * W_BYTES;
