@@ -11,12 +11,8 @@ namespace gdn8 {
 
 constexpr int kGroup = 128;
 
-struct Codes {
-  uint2 bits;
-  float scale;
-};
-// Largest finite magnitude of 8 bf16 (of bf16 without their signs, the order is that of
-// the bits), and whether all are finite.
+// Largest finite magnitude of 8 bf16, as their bits (without signs the order is theirs),
+// and whether all are finite.
 __device__ __forceinline__ uint32_t largest(const uint4 &v, bool &finite) {
   const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
   uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
@@ -31,14 +27,10 @@ __device__ __forceinline__ uint32_t largest(const uint4 &v, bool &finite) {
   }
   return m;
 }
-// Codes of a lane's 8 bf16; GL lanes (a power of two, the whole warp in step) hold a group.
-template <int GL> __device__ __forceinline__ Codes encode(const uint4 &v) {
-  bool finite;
-  uint32_t m = largest(v, finite);
-#pragma unroll
-  for (int o = GL / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const int e = gdnkv::scale_exponent(__uint_as_float(m << 16));
-  const float f = gdnkv::pow2(-e);
+// The exponent of a group whose largest magnitude has these bits.
+__device__ __forceinline__ int exponent_of(uint32_t m) { return gdnkv::scale_exponent(__uint_as_float(m << 16)); }
+// Codes of 8 bf16 times f = 2^-e.
+__device__ __forceinline__ uint2 codes8(const uint4 &v, float f, bool finite) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
@@ -49,10 +41,7 @@ template <int GL> __device__ __forceinline__ Codes encode(const uint4 &v) {
       if ((w[i] & 0x7f800000u) == 0x7f800000u) c[i] |= 0x7f00u;
     }
   }
-  Codes r;
-  r.bits = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-  r.scale = gdnkv::pow2(e);
-  return r;
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 }  // namespace gdn8

@@ -121,19 +121,30 @@ __device__ __forceinline__ float f2_sum(f2 a) {
   return x.x + x.y;
 }
 
-// The codes of a lane's 8 bf16 (`on`: it has some), whose group's other elements are with
-// the GL lanes around it, and the group's scale.
-template <int GL>
-__device__ __forceinline__ void encode8(const uint4 &v, bool on, uint8_t *codes, float *scale, bool first) {
-  const gdn8::Codes c = gdn8::encode<GL>(v);
+// The codes of a lane's 8 bf16 of h and (GATE) of z, whose groups' other elements are with
+// the GL lanes around it, and the groups' scales; `on`: it has some.
+template <int GL, bool GATE>
+__device__ __forceinline__ void encode_row(const uint4 &h, const uint4 &z, bool on, bool first, uint8_t *h8, float *hs, uint8_t *z8, float *zs) {
+  bool h_finite, z_finite = true;
+  uint32_t m = gdn8::largest(h, h_finite);
+  if (GATE) m |= gdn8::largest(z, z_finite) << 16;  // both maxima in one word
+#pragma unroll
+  for (int o = GL / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!on) return;
-  __stcs(reinterpret_cast<uint2 *>(codes), c.bits);
-  if (first) __stcs(scale, c.scale);
+  const int eh = gdn8::exponent_of(m & 0xffffu);
+  __stcs(reinterpret_cast<uint2 *>(h8), gdn8::codes8(h, gdnkv::pow2(-eh), h_finite));
+  if (first) __stcs(hs, gdnkv::pow2(eh));
+  if (GATE) {
+    const int ez = gdn8::exponent_of(m >> 16);
+    __stcs(reinterpret_cast<uint2 *>(z8), gdn8::codes8(z, gdnkv::pow2(-ez), z_finite));
+    if (first) __stcs(zs, gdnkv::pow2(ez));
+  }
 }
 
-// C8: codes of h and of z are written as well.
+// C8: codes of h and of z are written as well.  (262144 rows of 128 with a SiLU gate: 53 us,
+// 5.0 TB/s, at four blocks an SM; 63 at three, 56 at five, whose registers are too few.)
 template <int L, int NV, int THREADS, int ACT, bool RES, bool C8>
-__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(THREADS, C8 && NV == 1 ? 1024 / THREADS : 1) norm_fwd_kernel(const NormArgs a) {
   using S = Shape<L, NV, THREADS>;
   __shared__ float sh[2][32];
   grid_release();
@@ -199,8 +210,8 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
         const bool on = in && v < nvec;
         const int64_t s = row * a.groups + v / 16;
         // the stream as it is stored
-        encode8<GL>(RES ? pack8(h[i]) : xv[i], on, a.h8 + at + v * 8, a.hs + s, v % 16 == 0);
-        if (ACT != ACT_NONE) encode8<GL>(zv[i], on, a.z8 + at + v * 8, a.zs + s, v % 16 == 0);
+        encode_row<GL, ACT != ACT_NONE>(RES ? pack8(h[i]) : xv[i], zv[i], on, v % 16 == 0, a.h8 + at + v * 8, a.hs + s, a.z8 + at + v * 8,
+                                        a.zs + s);
       }
     }
   }
@@ -210,7 +221,6 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
 // kAhead rows ahead; a thread copies and reads places of its own only, so no
 // barrier is needed.  262144 rows of 128 with a SiLU gate: 56.4 us for both
 // kernels (5.95 TB/s), three rows ahead 57.6; loads to registers took 10 us more.
-template <int NV> struct Ahead { static constexpr int kRows = NV <= 2 ? 2 : 1; };
 __device__ __forceinline__ void copy16(void *dst, const uint16_t *src, bool on) {
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -220,20 +230,26 @@ template <int BYTES> __device__ __forceinline__ void copy_small(void *dst, const
   const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0) : "memory");
 }
-// 16-byte places of a thread in a stage of the ring.
-template <int ACT, bool RES, bool C8> struct Places {
-  static constexpr bool kGate = ACT != ACT_NONE;
-  static constexpr int kTensors = C8 ? 2 + (RES ? 1 : 0) + (kGate ? 1 : 0) : 2 + (kGate ? 1 : 0) + (RES ? 1 : 0);
+// A stage of the ring: kTensors 16-byte places of each vector of each thread and, with codes,
+// kCoded 8-byte ones, behind which the groups' scales stand (one for each 8 lanes at most).
+template <int NV, int THREADS, int ACT, bool RES, bool C8> struct Stage {
+  static constexpr int kGate = ACT != ACT_NONE ? 1 : 0;
+  static constexpr int kTensors = C8 ? 1 + (RES ? 1 : 0) : 2 + kGate + (RES ? 1 : 0);
+  static constexpr int kCoded = C8 ? 1 + kGate : 0;
+  static constexpr int kCodes = kTensors * NV * THREADS * 16, kScales = kCodes + kCoded * NV * THREADS * 8;
+  static constexpr int kBytes = kScales + kCoded * NV * (THREADS / 8) * 4;
+  static constexpr int kAhead = NV <= 2 ? 2 : 1;
 };
 
-// C8: h and z come as codes.  A thread's 16-byte places are then those of the codes of h
-// (8 bytes) and its scale, dy, the codes of z and its scale, dh.
+// C8: h and z come as codes, a group's scale by the copy of its first lane.  (262144 rows of
+// 128 with a SiLU gate: 60 us, 4.5 TB/s, 70 % of the issue slots; 81 with loads to registers a
+// row ahead, 60 with three or four rows ahead.)
 template <int L, int NV, int THREADS, int ACT, bool RES, bool C8>
 __global__ void __launch_bounds__(THREADS, (NV == 1 && L <= 32) ? 4 : 1) norm_bwd_kernel(const NormArgs a) {
   using S = Shape<L, NV, THREADS>;
-  constexpr int kAhead = Ahead<NV>::kRows;
-  constexpr int kTensors = Places<ACT, RES, C8>::kTensors;
-  extern __shared__ uint4 ring[];  // [kAhead][kTensors][NV][THREADS], then the blocks' sums
+  using R = Stage<NV, THREADS, ACT, RES, C8>;
+  constexpr int kAhead = R::kAhead, kTensors = R::kTensors;
+  extern __shared__ uint4 ring[];  // [kAhead] stages, then the blocks' sums
   __shared__ float sh[2][32];
   grid_wait();
   int turn = 0;
@@ -248,7 +264,14 @@ __global__ void __launch_bounds__(THREADS, (NV == 1 && L <= 32) ? 4 : 1) norm_bw
   keep_weights<S::kKept>(a.w, l, L, nvec, w);
   const int64_t step = (int64_t)gridDim.x * S::kRows;
   const int rg = S::kBlock ? 0 : (int)threadIdx.x / L;
-  auto place = [&](int stage, int tensor, int i) { return ring + ((stage * kTensors + tensor) * NV + i) * THREADS + threadIdx.x; };
+  auto place = [&](int stage, int tensor, int i) { return ring + stage * (R::kBytes / 16) + (tensor * NV + i) * THREADS + threadIdx.x; };
+  auto code = [&](int stage, int which, int i) {
+    return reinterpret_cast<uint2 *>(reinterpret_cast<char *>(ring) + stage * R::kBytes + R::kCodes) + (which * NV + i) * THREADS + threadIdx.x;
+  };
+  auto scale = [&](int stage, int which, int i) {  // the group's: of 16 lanes, or of the 8 of a short row
+    return reinterpret_cast<float *>(reinterpret_cast<char *>(ring) + stage * R::kBytes + R::kScales) + (which * NV + i) * (THREADS / 8) +
+           threadIdx.x / (L < 16 ? 8 : 16);
+  };
   auto call = [&](int64_t row, int stage) {
     const bool in = row < a.rows;
     const int64_t at = in ? row * a.D : 0, zat = (ACT != ACT_NONE && !C8 && in) ? z_offset(a, row) : 0;
@@ -259,17 +282,18 @@ __global__ void __launch_bounds__(THREADS, (NV == 1 && L <= 32) ? 4 : 1) norm_bw
       const int e = on ? v * 8 : 0;
       const int64_t g = C8 && on ? row * a.groups + v / 16 : 0;
       if (C8) {
-        copy_small<8>(place(stage, 0, i), a.h8 + at + e, on);
-        copy_small<4>(reinterpret_cast<uint32_t *>(place(stage, 0, i)) + 2, a.hs + g, on);
+        copy_small<8>(code(stage, 0, i), a.h8 + at + e, on);
+        if (l % (L < 16 ? 8 : 16) == 0) copy_small<4>(scale(stage, 0, i), a.hs + g, on);
         if (ACT != ACT_NONE) {
-          copy_small<8>(place(stage, 2, i), a.z8 + at + e, on);
-          copy_small<4>(reinterpret_cast<uint32_t *>(place(stage, 2, i)) + 2, a.zs + g, on);
+          copy_small<8>(code(stage, 1, i), a.z8 + at + e, on);
+          if (l % (L < 16 ? 8 : 16) == 0) copy_small<4>(scale(stage, 1, i), a.zs + g, on);
         }
+        copy16(place(stage, 0, i), a.dy + at + e, on);
       } else {
         copy16(place(stage, 0, i), a.x + at + e, on);
+        copy16(place(stage, 1, i), a.dy + at + e, on);
+        if (ACT != ACT_NONE) copy16(place(stage, 2, i), a.z + zat + e, on);
       }
-      copy16(place(stage, 1, i), a.dy + at + e, on);
-      if (ACT != ACT_NONE && !C8) copy16(place(stage, 2, i), a.z + zat + e, on);
       if (RES) copy16(place(stage, kTensors - 1, i), a.dh + at + e, on);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -284,14 +308,26 @@ __global__ void __launch_bounds__(THREADS, (NV == 1 && L <= 32) ? 4 : 1) norm_bw
     const bool in = row < a.rows;
     const int64_t at = row * a.D;
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    if (C8) __syncwarp();  // a group's scale is its first lane's copy
     uint4 xc[NV], yc[NV], zc[NV], gc[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      xc[i] = *place(stage, 0, i);
-      yc[i] = *place(stage, 1, i);
-      if (ACT != ACT_NONE) zc[i] = *place(stage, 2, i);
+      if (C8) {
+        auto coded = [&](int which) {
+          const uint2 c = *code(stage, which, i);
+          return make_uint4(c.x, c.y, __float_as_uint(*scale(stage, which, i)), 0);
+        };
+        xc[i] = coded(0);
+        if (ACT != ACT_NONE) zc[i] = coded(1);
+        yc[i] = *place(stage, 0, i);
+      } else {
+        xc[i] = *place(stage, 0, i);
+        yc[i] = *place(stage, 1, i);
+        if (ACT != ACT_NONE) zc[i] = *place(stage, 2, i);
+      }
       if (RES) gc[i] = *place(stage, kTensors - 1, i);
     }
+    if (C8) __syncwarp();  // all have read it before the next one comes
     call(row + kAhead * step, stage);
     stage = stage + 1 == kAhead ? 0 : stage + 1;
     // First pass: the sums of h^2 and of p h, p = dy w act(z).  The sigmoid stays
@@ -424,8 +460,8 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *__restrict__
 template <int L, int NV, int THREADS, int ACT, bool RES, bool C8>
 cudaError_t launch_bwd(const NormArgs &a, int blocks, cudaStream_t s) {
   using S = Shape<L, NV, THREADS>;
-  constexpr int kTensors = Places<ACT, RES, C8>::kTensors;
-  constexpr int ring = Ahead<NV>::kRows * kTensors * NV * THREADS * 16, sums = S::kBlock ? 0 : S::kRows * L * NV * 32;
+  using R = Stage<NV, THREADS, ACT, RES, C8>;
+  constexpr int ring = R::kAhead * R::kBytes, sums = S::kBlock ? 0 : S::kRows * L * NV * 32;
   constexpr int bytes = ring > sums ? ring : sums;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = gdn_host::allow_smem(norm_bwd_kernel<L, NV, THREADS, ACT, RES, C8>, bytes, done);
