@@ -79,8 +79,6 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
   grid_wait();
   if (blockIdx.x == 0) {
     check_offsets(a);
-    // The walks of dK, dV have some steps in all (here by a sum over their tiles, to a tile
-    // for the diagonal): a piece has a quarter of a block's share at least, and 16.
     // The walks of dK, dV have some steps in all (to a tile for the diagonal): a piece has a
     // quarter of a block's share at least, and 4.
     __shared__ unsigned long long total;
@@ -161,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_wait();
+  grid_release();  // the kernel of dQ, which needs nothing of this one, takes the SMs that come free
   const uint32_t failed = sb + Ly::OFF_MISC;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
   const uint32_t bar = sb + Ly::OFF_BAR;
@@ -606,13 +605,15 @@ template <int D> __device__ __forceinline__ void mma_packed(uint32_t d, uint32_t
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_dq_kernel(const BwdArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+    attn_dq_kernel(const BwdArgs a, int waits, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
   using Ly = QLay<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  grid_wait();
+  // What the kernel of dK, dV has waited for is done when this one comes in; its end is waited
+  // for at this one's, for the kernel after both.
+  if (waits) grid_wait();
   const uint32_t failed = sb + Ly::OFF_MISC;
   volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + Ly::OFF_MISC + 8);
   const uint32_t bar = sb + Ly::OFF_BAR;
@@ -683,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         limit = a.causal ? min(low + r, keys - 1) : low;
         if (r < lds_i(work + Q_COUNT)) at = ((int64_t)(lds_i(work + Q_Q) + row0 + r) * a.HQ + head) * D + wg * (D / 2);
         const float *stats = a.stats + ((int64_t)head * a.q_slots + lds_i(work + Q_SLOT)) * 2 * kTile;
-        n_lse = stats[r];
-        n_delta = -stats[kTile + r];
+        n_lse = __ldcg(stats + r);
+        n_delta = -__ldcg(stats + kTile + r);
         item_read(it);
         if (tiles > 0) {
           // dO goes to tensor memory, from where the products take it without a reading of
@@ -925,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 9) tmem_dealloc(tmem, 512);
+  if (!waits) grid_wait();
 }
 
 // Most pieces of a (key tile, kv head)'s walk: enough for two items an SM.
@@ -958,8 +960,11 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   if (!shares) return cudaErrorInvalidConfiguration;
   e = gdn_host::launch_dependent(attn_stats_kernel<D>, dim3((unsigned)q_blocks), 256, 0, s, a);
   if (e == cudaSuccess && keys)
-    e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tk, a.N, kTile) * a.HK * a.pieces, sms)), kThreads, KvLay<D>::BYTES, s, a, mq, mk, mv, mo);
-  if (e == cudaSuccess && rows) e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tq, a.N, kTile) * a.HQ, sms)), kThreads, QLay<D>::BYTES, s, a, mq, mk, mv, mo);
+    e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tk, a.N, kTile) * a.HK * a.pieces, sms)), kThreads,
+                                   KvLay<D>::BYTES, s, a, mq, mk, mv, mo);
+  if (e == cudaSuccess && rows)
+    e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tq, a.N, kTile) * a.HQ, sms)), kThreads, QLay<D>::BYTES,
+                                   s, a, keys ? 0 : 1, mq, mk, mv, mo);
   if (e == cudaSuccess && keys && a.pieces > 1) e = gdn_host::launch_dependent(attn_join_kernel<D>, dim3((unsigned)k_blocks, 8), 256, 0, s, a);
   return e;
 }
