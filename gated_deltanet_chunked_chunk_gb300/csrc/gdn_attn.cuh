@@ -304,6 +304,17 @@ __device__ __forceinline__ void wait64(uint32_t *r) {
 }
 
 // ---------------------------------------------------------------- host side
+// Whether a kernel has the registers a thread that its warps' shares add up to: with fewer
+// a warp would wait for ever for its own.  `known`: a static of the caller.
+template <class F> cudaError_t check_registers(F *kernel, int registers, std::atomic<bool> &known) {
+  if (known.load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaFuncAttributes f;
+  const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+  if (e != cudaSuccess) return e;
+  if (f.numRegs != registers) return cudaErrorInvalidConfiguration;
+  known.store(true, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 // Map over [T][heads][D] bf16 with ld elements between tokens, box of 128 rows of 64
 // elements of one head.
 inline bool rows_map(CUtensorMap *m, const void *ptr, int D, int heads, int64_t T, int64_t ld) {

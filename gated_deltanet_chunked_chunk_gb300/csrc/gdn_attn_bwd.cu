@@ -950,14 +950,10 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   static std::atomic<uint64_t> done_kv{0}, done_q{0};
   cudaError_t e = gdn_host::allow_smem(attn_dkdv_kernel<D>, KvLay<D>::BYTES, done_kv);
   if (e == cudaSuccess) e = gdn_host::allow_smem(attn_dq_kernel<D>, QLay<D>::BYTES, done_q);
+  static std::atomic<bool> known_kv{false}, known_q{false};
+  if (e == cudaSuccess) e = check_registers(attn_dkdv_kernel<D>, 168, known_kv);
+  if (e == cudaSuccess) e = check_registers(attn_dq_kernel<D>, 168, known_q);
   if (e != cudaSuccess) return e;
-  // the warps' shares of the registers are those of a launch with 168 a thread
-  static const bool shares = [] {
-    cudaFuncAttributes f, g;
-    return cudaFuncGetAttributes(&f, attn_dkdv_kernel<D>) == cudaSuccess && f.numRegs == 168 &&
-           cudaFuncGetAttributes(&g, attn_dq_kernel<D>) == cudaSuccess && g.numRegs == 168;
-  }();
-  if (!shares) return cudaErrorInvalidConfiguration;
   e = gdn_host::launch_dependent(attn_stats_kernel<D>, dim3((unsigned)q_blocks), 256, 0, s, a);
   if (e == cudaSuccess && keys)
     e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tk, a.N, kTile) * a.HK * a.pieces, sms)), kThreads,

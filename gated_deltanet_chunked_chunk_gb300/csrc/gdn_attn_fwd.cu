@@ -411,14 +411,10 @@ template <int D> cudaError_t launch(const Args &a, cudaStream_t s) {
       !rows_map(&mv, keys ? a.v : a.q, D, keys ? a.HK : a.HQ, keys ? a.Tk : a.Tq, keys ? a.ldv : a.ldq))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = gdn_host::allow_smem(attn_fwd_kernel<D>, Lay<D>::BYTES, done);
+  static std::atomic<bool> known{false};
+  cudaError_t e = gdn_host::allow_smem(attn_fwd_kernel<D>, Lay<D>::BYTES, done);
+  if (e == cudaSuccess) e = check_registers(attn_fwd_kernel<D>, 96, known);
   if (e != cudaSuccess) return e;
-  // the warps' shares of the registers are those of a launch with 96 a thread
-  static const bool shares = [] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, attn_fwd_kernel<D>) == cudaSuccess && f.numRegs == 96;
-  }();
-  if (!shares) return cudaErrorInvalidConfiguration;
   const int sms = gdn_host::sm_count();
   const int each = most_tiles(a.Tq, a.N, 2 * kTile) * a.HQ >= sms ? 2 : 1;
   const int64_t blocks = std::min<int64_t>(most_tiles(a.Tq, a.N, each * kTile) * a.HQ, sms);

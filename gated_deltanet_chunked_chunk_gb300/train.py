@@ -41,7 +41,7 @@ class _Linear8(torch.autograd.Function):
     def backward(ctx, dy):
         weight, *kept = ctx.saved_tensors
         dx = dy @ weight if ctx.needs_input_grad[0] else None
-        dw = dy.flatten(0, -2).T @ gdn_act8_load(*kept).flatten(0, -2) if kept else None
+        dw = dy.reshape(-1, dy.shape[-1]).T @ gdn_act8_load(*kept).view(-1, weight.shape[1]) if kept else None
         return dx, dw
 
 
