@@ -758,7 +758,8 @@ size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, i
  *   workspace     : gdn_attention_bwd_workspace_size() bytes, 16-byte aligned
  * Everything else as in gdn_attention_fwd; rows and keys behind the last sequence
  * have zero gradients.  P and dS enter the products in bf16, sums are fp32 and have a
- * fixed order: two calls agree bit for bit.  dout, o, dq, dk, dv must start on a
+ * fixed order: two calls agree bit for bit (where the sums of dk and dv are cut depends
+ * on the lengths of the whole batch, so in another batch their last bits can differ).  dout, o, dq, dk, dv must start on a
  * 16-byte boundary; GDN_EWORKSPACE for a small workspace.  Three launches, four
  * where few keys are cut between more blocks.
  */

@@ -1,0 +1,107 @@
+"""The hybrid stack's training path on packed sequences: outputs and gradients against the same stack in plain 64-bit torch
+operations.
+
+Bounds, as the length of the difference over the length of the value.  A rounding to bf16 is off by 2^-8 at most and about
+2^-9.5 as a root mean square; some twenty follow one another on the way through three layers and back, and they add as
+squares: 20^(1/2) 2^-9.5 = 0.6 %, the norms' and gates' slopes some more: 4 %.  An 8-bit code is off by 2^-4 at most, 2.6 %
+as a root mean square; a weight's gradient takes one such input, a stream's those of the norms after it, seven in all:
+12 %."""
+import math
+
+import pytest
+import torch
+import torch.nn.functional as nn
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_deltanet_chunked_chunk_gb300 import build
+    build.build()
+
+
+def _rms(x, w):
+    return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6) * w
+
+
+def _rope(x, inv_freq):
+    rot = 2 * inv_freq.numel()
+    t = torch.arange(x.shape[0], device=x.device, dtype=x.dtype)[:, None, None] * inv_freq
+    a, b = x[..., :rot // 2], x[..., rot // 2:rot]
+    return torch.cat((a * t.cos() - b * t.sin(), a * t.sin() + b * t.cos(), x[..., rot:]), -1)
+
+
+def _plain(stack, params, x, lens):
+    cfg, it = stack.cfg, iter(params)
+    last = next(it)
+    h, y = x, None
+    for layer in stack.layers:
+        norm, w_in, w_out = next(it), next(it), next(it)
+        h = h if y is None else h + y
+        u = _rms(h, norm) @ w_in.T
+        outs = []
+        if layer.kind == "a":
+            for part in u.split(lens):
+                m = part.shape[0]
+                q, k, v = part.view(m, -1, cfg.D).split([cfg.HQ, cfg.HK, cfg.HK], dim=1)
+                q, k = (_rope(t, stack.inv_freq.double()) for t in (q, k))
+                k, v = (t.repeat_interleave(cfg.HQ // cfg.HK, dim=1) for t in (k, v))
+                s = torch.einsum("ihd,jhd->hij", q, k) / math.sqrt(cfg.D)
+                s = s.masked_fill(torch.ones(m, m, dtype=torch.bool, device=x.device).triu(1), -math.inf)
+                outs.append(torch.einsum("hij,jhd->ihd", s.softmax(-1), v).reshape(m, -1))
+        else:
+            out_norm = next(it)
+            for part in u.split(lens):
+                q, k, v, z, a, b = part.split([cfg.H * cfg.K, cfg.H * cfg.K, cfg.HV * cfg.K, cfg.HV * cfg.K, cfg.HV, cfg.HV], dim=1)
+                q, k, v, z = (t.unflatten(1, (-1, cfg.K)) for t in (q, k, v, z))
+                q, k = (t * torch.rsqrt(t.square().sum(-1, keepdim=True) + 1e-6) for t in (q, k))
+                q, k = (t.repeat_interleave(cfg.HV // cfg.H, dim=1) for t in (q, k))
+                decay = torch.exp(-layer.A_log.double().exp() * nn.softplus(a + layer.dt_bias.double()))
+                beta, state, rows = b.sigmoid(), x.new_zeros(cfg.HV, cfg.K, cfg.K), []
+                for t in range(part.shape[0]):
+                    state = state * decay[t, :, None, None]
+                    change = beta[t, :, None] * (v[t] - torch.einsum("hkv,hk->hv", state, k[t]))
+                    state = state + k[t, :, :, None] * change[:, None]
+                    rows.append(torch.einsum("hkv,hk->hv", state, q[t]) / math.sqrt(cfg.K))
+                outs.append((_rms(torch.stack(rows), out_norm) * z * z.sigmoid()).reshape(part.shape[0], -1))
+        y = torch.cat(outs) @ w_out.T
+    return _rms(h + y, last)
+
+
+@pytest.mark.parametrize("save8,bound", [(False, 0.04), (True, 0.12)])
+def test_gradients_of_packed_sequences(save8, bound):
+    from gated_deltanet_chunked_chunk_gb300.hybrid import HybridStack
+    lens = [40, 1, 23]
+    gen = torch.Generator().manual_seed(11)
+    x, up = (torch.randn(sum(lens), 512, generator=gen).to("cuda", BF) for _ in range(2))
+    stack = HybridStack(requests=1, seed=4)
+    params = [p.requires_grad_(True) for p in stack.parameters()]
+    out = stack.forward(x, lens, save8)
+    grads = torch.autograd.grad(out, params, up)
+    exact = [p.detach().double().requires_grad_(True) for p in params]
+    want = _plain(stack, exact, x.double(), lens)
+    ref = torch.autograd.grad(want, exact, up.double())
+
+    def off(a, b):
+        return float((a.double() - b).norm() / b.norm())
+
+    assert off(out.detach(), want.detach()) < 0.04  # the forward is the same either way
+    for i, (g, r) in enumerate(zip(grads, ref)):
+        assert g.shape == r.shape and off(g, r) < bound, (i, tuple(g.shape), off(g, r))
+
+
+def test_packed_sequences_are_those_alone():
+    """A sequence's outputs do not depend on what it is packed with, but for the last bits of sums whose order the batch's
+    shape sets (a matrix product's): 1 %."""
+    from gated_deltanet_chunked_chunk_gb300.hybrid import HybridStack
+    lens = [70, 130, 1]
+    gen = torch.Generator().manual_seed(12)
+    x = torch.randn(sum(lens), 512, generator=gen).to("cuda", BF)
+    stack = HybridStack(requests=1, seed=5)
+    with torch.no_grad():
+        packed = stack.forward(x, lens).split(lens)
+        for a, b in zip(packed, x.split(lens)):
+            alone = stack.forward(b)
+            assert float((a.float() - alone.float()).norm() / alone.float().norm()) < 0.01

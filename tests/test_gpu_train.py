@@ -230,3 +230,344 @@ def test_norm_gate_with_codes(shape, kind, res):
     assert (np.abs(S.f64(dw) - rw) <= 2.0 ** -19 * mags + 1e-30).all()
     again = gdn.gdn_norm_gate_bwd8(c(dy), h8, hs, c(w), z_codes=z8, z_scale=zs, dh=c(dh), **args)
     assert all(torch.equal(a, b) for a, b in zip(again, (dx, dres, dz, dw)) if a is not None)
+
+
+# ------------------------------------------------- attention, where it can go wrong
+def _same_bits(a, b):
+    return all(torch.equal(x.view(torch.int16) if x.dtype == BF else x.view(torch.int32), y.view(torch.int16) if y.dtype == BF else y.view(torch.int32))
+               for x, y in zip(a, b))
+
+
+def _all(q, k, v, do, **args):
+    gdn = _gdn()
+    o, lse = gdn.gdn_attention_fwd(q, k, v, **args)
+    return (o, lse) + tuple(gdn.gdn_attention_bwd(do, q, k, v, o, lse, **args))
+
+
+@pytest.mark.parametrize("D,HQ,HK", [(128, 4, 2), (64, 3, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_sequences(D, HQ, HK, causal):
+    """More sequences than a warp has lanes, empty ones among them, and keys of other lengths."""
+    g = torch.Generator().manual_seed(D + HQ)
+    lens = torch.randint(0, 160, (75,), generator=g).tolist()
+    lens[10] = lens[70] = 0
+    _run(lens, None, HQ, HK, D, causal, 7)
+    lens_k = [max(0, m + d) for m, d in zip(lens, torch.randint(-40, 90, (75,), generator=g).tolist())]
+    _run(lens, lens_k, HQ, HK, D, causal, 8)
+
+
+@pytest.mark.parametrize("kind", ["grow", "fall", "equal", "large", "tiny"])
+def test_running_maximum(kind):
+    """Logits that grow along the keys by more than the reference may lag, fall, are all equal, large, or tiny."""
+    T, D = 700, 128
+    g = torch.Generator().manual_seed(3)
+    q, k, v, do = (torch.randn(T, 1, D, generator=g) for _ in range(4))
+    u = torch.nn.functional.normalize(torch.randn(D, generator=g), dim=0)
+    if kind in ("grow", "fall"):
+        at = torch.arange(T)[:, None, None] / T * (60.0 if kind == "grow" else -60.0)
+        q, k = q * 0.2 + u * D ** 0.5, k * 0.2 + at * u
+    elif kind == "equal":
+        k = k[:1].expand(T, 1, D).contiguous()
+    else:
+        q, k = (t * (30.0 if kind == "large" else 1e-3) for t in (q, k))
+    q, k, v, do = (t.to(BF) for t in (q, k, v, do))
+    r = U.attention(q, k, v, [(0, T, 0, T)], True, D ** -0.5, do)
+    o, lse, *grads = _all(*(t.cuda() for t in (q, k, v, do)))
+    _check_fwd(o, lse, r)
+    _check_bwd(grads, r)
+
+
+@pytest.mark.parametrize("scale", [0.5, 1e-4, 3.0])
+def test_scale(scale):
+    _run([130, 77], None, 2, 1, 64, True, 21, scale=scale)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_other_sequences_do_not_reach_one(causal):
+    """NaN and infinities in the sequences before and after, whose rows share tiles with it, and in what stands between
+    the heads' tokens: the same bits as without."""
+    lens = [37, 201, 90]
+    q, k, v, do = _inputs(lens, None, 4, 2, 128, 5)
+    a, b = 37, 238
+    clean = _all(*(t[a:b].contiguous().cuda() for t in (q, k, v, do)), causal=causal)
+    for t in (q, k, v, do):
+        t[:a:2], t[1:a:2], t[b:] = math.nan, math.inf, -math.inf
+        t[b + 1::3] = math.nan
+    cq, ck, cv = _gpu(q, k, v, True)
+    dirty = _all(cq, ck, cv, do.cuda(), cu_seqlens=U.offsets(lens).cuda(), causal=causal)
+    assert _same_bits([t[a:b] for t in dirty], clean)
+
+
+def test_rows_behind_the_last_sequence_are_zero():
+    lens, pad = [150, 20], 300
+    q, k, v, do = _inputs(lens + [pad], None, 4, 2, 64, 6)
+    for t in (q, k, v, do):
+        t[170:] = math.nan
+    cu = U.offsets(lens).cuda()
+    got = _all(*(t.cuda() for t in (q, k, v, do)), cu_seqlens=cu)
+    want = _all(*(t[:170].contiguous().cuda() for t in (q, k, v, do)), cu_seqlens=cu)
+    assert _same_bits([t[:170] for t in got], want)
+    assert (got[0][170:] == 0).all() and (got[1][170:] == -math.inf).all() and all((t[170:] == 0).all() for t in got[2:])
+
+
+def test_no_rows_no_keys_no_sequences():
+    gdn = _gdn()
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    new = lambda t, h: torch.randn(t, h, 64, device="cuda").to(BF)  # noqa: E731
+    q, k, v = new(5, 2), new(7, 1), new(7, 1)
+    # rows without keys
+    o, lse, dq, dk, dv = _all(q, k[:0], v[:0], torch.ones_like(q), cu_seqlens=ints(0, 5), cu_seqlens_k=ints(0, 0))
+    assert (o == 0).all() and (lse == -math.inf).all() and (dq == 0).all() and dk.shape == (0, 1, 64)
+    # keys without rows
+    o, lse, dq, dk, dv = _all(q[:0], k, v, q[:0], cu_seqlens=ints(0, 0), cu_seqlens_k=ints(0, 7))
+    assert o.shape == (0, 2, 64) and dq.shape == (0, 2, 64) and (dk == 0).all() and (dv == 0).all()
+    # no sequences at all
+    o, lse, dq, dk, dv = _all(q, new(5, 1), new(5, 1), torch.ones_like(q), cu_seqlens=ints(0))
+    assert (o == 0).all() and (lse == -math.inf).all() and all((t == 0).all() for t in (dq, dk, dv))
+    # nothing
+    assert gdn.gdn_attention_fwd(q[:0], k[:0], v[:0])[0].shape == (0, 2, 64)
+
+
+def test_bad_offsets_are_reported():
+    gdn = _gdn()
+    q, k, v, do = (t.cuda() for t in _inputs([300], None, 2, 1, 64, 9))
+    good = _all(q[:100], k[:100], v[:100], do[:100])
+    for cu in ([0, 100, 90, 300], [0, 100, 400], [-1, 100, 300], [5, 100, 300], [0, 100, -7]):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        o, lse = gdn.gdn_attention_fwd(q, k, v, cu_seqlens=c, dev_status=st)
+        assert int(st) == gdn.DEV_BAD_CU_SEQLENS
+        st.zero_()
+        grads = gdn.gdn_attention_bwd(do, q, k, v, o, lse, cu_seqlens=c, dev_status=st)
+        assert int(st) == gdn.DEV_BAD_CU_SEQLENS
+        if cu == [0, 100, 400]:  # the good sequence gets its results
+            assert _same_bits([o[:100], lse[:100]] + [t[:100] for t in grads], good)
+
+
+def test_runs_agree_bit_for_bit():
+    lens = [513, 260, 1000]
+    q, k, v, do = (t.cuda() for t in _inputs(lens, None, 8, 2, 128, 11))
+    cu = U.offsets(lens).cuda()
+    a = _all(q, k, v, do, cu_seqlens=cu)
+    for _ in range(3):
+        assert _same_bits(a, _all(q, k, v, do, cu_seqlens=cu))
+
+
+def test_two_streams_at_once():
+    """Two calls at once on two streams, each with its own outputs and workspace."""
+    gdn = _gdn()
+    sets = [tuple(t.cuda() for t in _inputs([900, 300], None, 8, 2, 128, s)) for s in (1, 2)]
+    cu = U.offsets([900, 300]).cuda()
+    want = [_all(*s, cu_seqlens=cu) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for (q, k, v, do), st in zip(sets, streams):
+        with torch.cuda.stream(st):
+            o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+            ws = torch.empty(gdn.attention_bwd_workspace_size(2, 1200, 1200, 8, 2, 128), dtype=torch.uint8, device="cuda")
+            for _ in range(4):
+                gdn.gdn_attention_fwd(q, k, v, cu_seqlens=cu, o=o, lse=lse)
+                grads = gdn.gdn_attention_bwd(do, q, k, v, o, lse, cu_seqlens=cu, workspace=ws)
+            got.append((o, lse) + tuple(grads))
+    torch.cuda.synchronize()
+    assert all(_same_bits(a, b) for a, b in zip(want, got))
+
+
+def test_captured_and_replayed_with_other_inputs():
+    gdn = _gdn()
+    a, b = (tuple(t.cuda() for t in _inputs([300, 45], None, 4, 1, 128, s)) for s in (1, 2))
+    cu, cu_b = U.offsets([300, 45]).cuda(), U.offsets([20, 325]).cuda()
+    want_a, want_b = _all(*a, cu_seqlens=cu), _all(*b, cu_seqlens=cu_b)
+    held, held_cu = [t.clone() for t in a], cu.clone()
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        _all(*held, cu_seqlens=held_cu)
+    torch.cuda.current_stream().wait_stream(s)
+    with torch.cuda.graph(graph):
+        out = _all(*held, cu_seqlens=held_cu)
+        codes = gdn.gdn_act8_save(held[0])
+        back = gdn.gdn_act8_load(*codes)
+    graph.replay()
+    assert _same_bits(out, want_a)
+    for t, x in zip(held, b):
+        t.copy_(x)
+    held_cu.copy_(cu_b)
+    graph.replay()
+    assert _same_bits(out, want_b)
+    assert torch.equal(back, gdn.gdn_act8_load(*gdn.gdn_act8_save(b[0])))
+
+
+def test_offsets_past_32_bits():
+    """Token strides and outputs whose offsets need more than 32 bits."""
+    gdn = _gdn()
+    T, D, ld = 700, 64, 4 << 20  # 2.9e9 elements from end to end
+    base = torch.empty(T * ld, dtype=BF, device="cuda")
+    q0, k0, v0, do = _inputs([T], None, 2, 1, D, 4)
+    views = []
+    for at, x in ((0, q0), (1024, k0), (2048, v0)):
+        t = base.as_strided((T, x.shape[1], D), (ld, D, 1), at)
+        t.copy_(x)
+        views.append(t)
+    got = _all(*views, do.cuda())
+    assert _same_bits(got, _all(*(t.cuda() for t in (q0, k0, v0, do))))
+    del base, views
+    # many short sequences of many heads: 2.4e9 elements of q, o and their gradients
+    lens, HQ = [37] * 640, 800
+    T = sum(lens)
+    q = torch.zeros(T, HQ, 128, dtype=BF, device="cuda")
+    k, v = (torch.zeros(T, 2, 128, dtype=BF, device="cuda") for _ in range(2))
+    do = torch.zeros_like(q)
+    q1, k1, v1, do1 = _inputs([74], None, HQ, 2, 128, 14)
+    for t, x in ((q, q1), (k, k1), (v, v1), (do, do1)):
+        t[-74:].copy_(x)
+    o, lse, dq, dk, dv = _all(q, k, v, do, cu_seqlens=U.offsets(lens).cuda())
+    want = _all(*(t.cuda() for t in (q1, k1, v1, do1)), cu_seqlens=U.offsets([37, 37]).cuda())
+    assert _same_bits([t[-74:] for t in (o, lse, dq)], want[:3])
+    # (dk and dv are sums of parts, cut by the work of the whole batch: the same to rounding)
+    r = U.attention(q1, k1, v1, U.spans([37, 37]), True, 128 ** -0.5, do1)
+    _check_bwd([t[-74:] for t in (dq, dk, dv)], r)
+
+
+def test_act8_past_32_bits():
+    gdn = _gdn()
+    x = torch.zeros(270000, 8192, dtype=BF, device="cuda")
+    tail = torch.randn(3, 8192, generator=torch.Generator().manual_seed(1)).to(BF)
+    x[-3:].copy_(tail)
+    codes, scale = gdn.gdn_act8_save(x)
+    want = gdn.gdn_act8_save(tail.cuda())
+    assert torch.equal(codes[-3:].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(scale[-3:], want[1])
+    del x
+    assert torch.equal(gdn.gdn_act8_load(codes, scale)[-3:], gdn.gdn_act8_load(*want))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_against_64_bits_on_many_tiles(causal):
+    """Longer sequences, more items than SMs, walks cut into pieces: against 64 bits on the GPU, one head at a time."""
+    gdn = _gdn()
+    lens, HQ, HK, D = [1900, 333], 8, 2, 128
+    q, k, v, do = _inputs(lens, None, HQ, HK, D, 31)
+    c = tuple(t.cuda() for t in (q, k, v, do))
+    o, lse, dq, dk, dv = _all(*c, cu_seqlens=U.offsets(lens).cuda(), causal=causal)
+    r = {}
+    for hk in range(HK):
+        part = U.attention(c[0][:, 4 * hk:4 * hk + 4], c[1][:, hk:hk + 1], c[2][:, hk:hk + 1], U.spans(lens), causal, D ** -0.5,
+                           c[3][:, 4 * hk:4 * hk + 4])
+        for n, t in part.items():
+            r.setdefault(n, []).append(t.cpu())
+    r = {n: torch.cat(t, 1) for n, t in r.items()}
+    _check_fwd(o, lse, r)
+    _check_bwd((dq, dk, dv), r)
+
+
+def test_gradients_against_differences():
+    """The gradient along a direction against central differences of a loss, both in 64 bits on the kernels' values: the
+    loss is linear in o, whose roundings (2^-8 of each element, independent) bound the difference's error."""
+    gdn = _gdn()
+    q, k, v, w = _inputs([160], None, 2, 1, 64, 41, q_size=1.0)
+    cq, ck, cv, cw = (t.cuda() for t in (q, k, v, w))
+    o, lse = gdn.gdn_attention_fwd(cq, ck, cv)
+    grads = gdn.gdn_attention_bwd(cw, cq, ck, cv, o, lse)
+    g = torch.Generator().manual_seed(5)
+    for which, base in enumerate((q, k, v)):
+        step = (0.5 * torch.randn(base.shape, generator=g)).to(BF)
+        ends = []
+        for sign in (1, -1):
+            moved = [t.double() for t in (q, k, v)]
+            moved[which] = moved[which] + sign * step.double() * 2.0 ** -6
+            rows = [(0, 160, 0, 160)]
+            ends.append((U.attention(*moved, rows, True, 64 ** -0.5)["o"] * w.double()).sum())
+        slope = (ends[0] - ends[1]) / 2.0 ** -5
+        got = (grads[which].double().cpu() * step.double()).sum()
+        # each gradient element is off by 2^-8 of itself and of its terms at most; along a random direction these add as
+        # a root of squares; 4 of them
+        r = U.attention(q, k, v, [(0, 160, 0, 160)], True, 64 ** -0.5, w)
+        n = ("dq", "dk", "dv")[which]
+        err = 2.0 ** -8 * (r[n].abs() + r[n + "_round"] + r[n + "_delta"]) * step.double().abs()
+        assert (got - slope).abs() <= 4 * err.square().sum().sqrt() + 1e-3 * slope.abs(), (n, float(got), float(slope))
+
+
+def test_autograd_entries():
+    gdn = _gdn()
+    q, k, v, do = (t.cuda() for t in _inputs([90, 41], None, 4, 2, 64, 51))
+    cu = U.offsets([90, 41]).cuda()
+    leaves = [t.clone().requires_grad_(True) for t in (q, k, v)]
+    o = gdn.attention(*leaves, cu_seqlens=cu)
+    grads = torch.autograd.grad(o, leaves, do)
+    want = _all(q, k, v, do, cu_seqlens=cu)
+    assert _same_bits([o] + list(grads), [want[0]] + list(want[2:]))
+    with pytest.raises(RuntimeError):  # no second derivative
+        first = torch.autograd.grad(gdn.attention(*leaves, cu_seqlens=cu).float().sum(), leaves, create_graph=True)
+        torch.autograd.grad(sum(t.float().sum() for t in first), leaves)
+    # a projection that keeps its input in 8 bits: the input's gradient is that of a plain one, the weight's that of the
+    # input's codes
+    x = torch.randn(70, 256, device="cuda").to(BF).requires_grad_(True)
+    w = torch.randn(96, 256, device="cuda").to(BF).requires_grad_(True)
+    dy = torch.randn(70, 96, device="cuda").to(BF)
+    y = gdn.linear8(x, w)
+    assert torch.equal(y, x @ w.T)
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    assert torch.equal(dx, dy @ w) and torch.equal(dw, dy.T @ gdn.gdn_act8_load(*gdn.gdn_act8_save(x.detach())))
+    (dx,) = torch.autograd.grad(gdn.linear8(x, w.detach()), x, dy)
+    assert torch.equal(dx, dy @ w)
+    # the norm with codes
+    x = torch.randn(40, 4, 128, device="cuda").to(BF).requires_grad_(True)
+    z, res = (torch.randn(40, 4, 128, device="cuda").to(BF).requires_grad_(True) for _ in range(2))
+    w = (1 + 0.1 * torch.randn(128, device="cuda")).requires_grad_(True)
+    y, h = gdn.norm_gate(x, w, residual=res, z=z, res_scale=0.5, save8=True)
+    dy, dh = torch.randn_like(y), torch.randn_like(h)
+    got = torch.autograd.grad((y, h), (x, w, res, z), (dy, dh))
+    _, _, h8, hs, z8, zs = gdn.gdn_norm_gate_save8(x.detach(), w.detach(), residual=res.detach(), z=z.detach(), res_scale=0.5)
+    dx, dres, dz, dw = gdn.gdn_norm_gate_bwd8(dy, h8, hs, w.detach(), z_codes=z8, z_scale=zs, dh=dh, res_scale=0.5)
+    assert all(torch.equal(a, b) for a, b in zip(got, (dx, dw, dres, dz)))
+    y, h = gdn.norm_gate(x, w, save8=True)
+    assert h is None and torch.autograd.grad(y.float().sum(), x)[0].shape == x.shape
+
+
+def test_refused_types_and_layouts():
+    gdn = _gdn()
+    q, k, v, do = (t.cuda() for t in _inputs([32], None, 4, 2, 64, 61))
+    lse = torch.zeros(32, 4, device="cuda")
+    for bad in (lambda: gdn.gdn_attention_fwd(q.half(), k, v), lambda: gdn.gdn_attention_fwd(q, k.float(), v),
+                lambda: gdn.gdn_attention_fwd(q, k, v, cu_seqlens=torch.tensor([0, 32], device="cuda")),
+                lambda: gdn.gdn_attention_bwd(do, q, k, v, q, lse.double())):
+        with pytest.raises(TypeError):
+            bad()
+    cu = U.offsets([32]).cuda()
+    for bad in (lambda: gdn.gdn_attention_fwd(q[0], k, v), lambda: gdn.gdn_attention_fwd(q, k[:, :, :32], v),
+                lambda: gdn.gdn_attention_fwd(q.transpose(0, 1), k, v), lambda: gdn.gdn_attention_fwd(q, k, v[:-1]),
+                lambda: gdn.gdn_attention_fwd(q, k, v.cpu()), lambda: gdn.gdn_attention_fwd(q, k[:16], v[:16], cu_seqlens=cu),
+                lambda: gdn.gdn_attention_fwd(q, k, v, cu_seqlens_k=cu), lambda: gdn.gdn_attention_fwd(q, k, v, lse=lse[:, :2].contiguous()),
+                lambda: gdn.gdn_attention_bwd(do[:, :2], q, k, v, q, lse), lambda: gdn.gdn_act8_load(torch.zeros(3, 256, device="cuda").to(torch.float8_e4m3fn), torch.ones(3, 1, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: gdn.gdn_attention_fwd(q[:, :3], k, v),  # 3 heads over 2
+                lambda: gdn.gdn_attention_fwd(*(torch.zeros(8, 2, 96, device="cuda", dtype=BF),) * 3),
+                lambda: gdn.gdn_attention_fwd(torch.zeros(32 * 260 + 8, device="cuda", dtype=BF).as_strided((32, 4, 64), (260, 64, 1)), k, v),
+                lambda: gdn.gdn_norm_gate_save8(torch.zeros(3, 130, device="cuda", dtype=BF), torch.ones(130, device="cuda"))):
+        with pytest.raises(gdn.GDNError):
+            bad()
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_a_wait_that_runs_out(D):
+    """The testing switch makes a bounded wait of every block run out: the call reports it and ends, and the next one is
+    right."""
+    gdn = _gdn()
+    q, k, v, do = (t.cuda() for t in _inputs([700, 133], None, 4, 2, D, 71))
+    cu = U.offsets([700, 133]).cuda()
+    want = _all(q, k, v, do, cu_seqlens=cu)
+    for call in (lambda st: gdn.gdn_attention_fwd(q, k, v, cu_seqlens=cu, dev_status=st),
+                 lambda st: gdn.gdn_attention_bwd(do, q, k, v, *want[:2], cu_seqlens=cu, dev_status=st)):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        prev = gdn.testing_force_wait_expiry(True)
+        try:
+            call(st)
+            torch.cuda.synchronize()
+        finally:
+            gdn.testing_force_wait_expiry(prev)
+        assert int(st) & gdn.DEV_WAIT_TIMEOUT and not int(st) & gdn.DEV_DRAIN_TIMEOUT
+        st.zero_()
+        assert _same_bits(_all(q, k, v, do, cu_seqlens=cu, dev_status=st), want) and int(st) == 0

@@ -21,7 +21,7 @@ def offsets(lens):
 
 
 def attention(q, k, v, spans, causal, scale, do=None):
-    """Values and, with do, gradients; beside each result what bounds its roundings.  CPU tensors of any type.
+    """Values and, with do, gradients; beside each result what bounds its roundings.  Tensors of any type, on one device.
 
     Returns a dict: o, o_mag = sum p |v|, lse, lse_mag = 1 + the largest scale sum |q| |k| that is seen;
     dq, dk, dv and for each of them *_round = the sum of the magnitudes of the terms that are rounded to bf16 on their
@@ -30,9 +30,8 @@ def attention(q, k, v, spans, causal, scale, do=None):
     Tq, HQ, D = q.shape
     Tk, HK, _ = k.shape
     G = HQ // HK
-    z = torch.zeros
-    r = dict(o=z(Tq, HQ, D, dtype=F), o_mag=z(Tq, HQ, D, dtype=F), lse=torch.full((Tq, HQ), -math.inf, dtype=F),
-             lse_mag=torch.ones(Tq, HQ, dtype=F))
+    f = dict(dtype=F, device=q.device)
+    r = dict(o=torch.zeros_like(q), o_mag=torch.zeros_like(q), lse=torch.full((Tq, HQ), -math.inf, **f), lse_mag=torch.ones(Tq, HQ, **f))
     if do is not None:
         do = do.to(F)
         for n, t in (("dq", q), ("dk", k), ("dv", v)):
@@ -42,9 +41,9 @@ def attention(q, k, v, spans, causal, scale, do=None):
         if m == 0 or n == 0:
             continue
         rows, keys = slice(a, a + m), slice(b, b + n)
-        seen = torch.ones(m, n, dtype=torch.bool)
+        seen = torch.ones(m, n, dtype=torch.bool, device=q.device)
         if causal:
-            seen = torch.arange(n)[None, :] <= torch.arange(m)[:, None] + (n - m)
+            seen = seen.tril(n - m)
         for h in range(HQ):
             K, V, Q = k[keys, h // G], v[keys, h // G], q[rows, h]
             s = (Q @ K.T * scale).masked_fill(~seen, -math.inf)
