@@ -1,8 +1,9 @@
 // gdn_act8.cu -- activations to 8-bit codes and back (gdn_act8.cuh).
 //
 // Two bytes in and one out an element, or the other way, and a few operations: HBM.  A
-// lane has 8 elements (16 bytes) of a row, the lanes of a group find its largest magnitude
-// by shuffles, and kAhead of a lane's loads are in flight together.  Rows whose width,
+// lane has 16 elements of a row (8, where a row is no multiple of 16), the lanes of a group
+// find its largest magnitude by shuffles, and kAhead 16-byte loads of a lane are in flight
+// together.  Rows whose width,
 // stride or address do not allow 16-byte accesses take a warp a group, element by element.
 #include <algorithm>
 
@@ -30,8 +31,8 @@ __device__ __forceinline__ int64_t row_start(const SaveArgs &a, int64_t row) {
 }
 
 // V vectors of 8 elements a lane, 16 / V lanes a group; FLAT: the rows are whole groups one
-// after another.  (8192 rows of 4096, a slice of wider ones: 19.7 us, 5.2 TB/s; 27.6 with one vector a lane,
-// whose arithmetic took 69 % of the issue slots.)
+// after another.  (8192 rows of 4096, a slice of wider ones: 19.7 us, 5.2 TB/s; 27.6 with
+// one vector a lane, whose arithmetic took 69 % of the issue slots.)
 template <int V, bool FLAT> __global__ void __launch_bounds__(kThreads) act8_save_kernel(const SaveArgs a) {
   constexpr int GL = 16 / V, AHEAD = kAhead / V;
   grid_wait();

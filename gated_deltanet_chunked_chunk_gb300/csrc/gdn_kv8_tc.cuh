@@ -1,5 +1,6 @@
-// gdn_kv8_tc.cuh -- what the two tcgen05 kernels over the paged 8-bit cache share:
-// descriptors, products, tensor memory, bounded waits.
+// gdn_kv8_tc.cuh -- what the tcgen05 kernels of attention share, those over the paged
+// 8-bit cache and those of packed sequences: descriptors, products, tensor memory, bounded
+// waits.
 #pragma once
 
 #include "gdn_kv8_attn.cuh"

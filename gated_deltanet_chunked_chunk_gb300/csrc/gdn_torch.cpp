@@ -1,6 +1,6 @@
 // gdn_torch.cpp -- the Python binding of the operators around the recurrence
-// (norms, rotary positions, the paged 8-bit cache): argument checks, output
-// allocation and the call of the C ABI, for PyTorch tensors.
+// (norms, rotary positions, the paged 8-bit cache, attention of packed sequences,
+// activations in 8 bits): argument checks, output allocation and the call of the C ABI, for PyTorch tensors.
 //
 // These operators take 1 to 4 us on the GPU for a decode step, and a binding in
 // Python took 9 to 23 us of the host a call (checks of up to nine tensors, the
