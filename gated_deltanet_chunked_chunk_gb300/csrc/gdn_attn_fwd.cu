@@ -226,11 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = (int64_t)(lds_i(work + W_Q) + lds_i(work + W_ROW0) + w * kTile + r) * a.HQ + lds_i(work + W_HEAD);
       item_read(it);
       if (count == 0) continue;
-      sts_f(told, l_sum);
       if (tiles) {
         ok = wait_bar(OD(w), phases >> 1 & 1, failed, a.dev_status);
         phases ^= 2;
       }
+      sts_f(told, l_sum);  // (after O is whole: the row's other thread has read the maximum here before its P)
       if (vote_any(1 + w, !ok)) break;
       tc_fence_after();
       const float l = l_sum + lds_f(told ^ 512), inv = l == 0.f ? 0.f : 1.f / l;
