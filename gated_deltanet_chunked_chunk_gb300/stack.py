@@ -123,6 +123,12 @@ def gdn_norm_gate_bwd8(dy: torch.Tensor, h_codes: torch.Tensor, h_scale: torch.T
                                           _act_of(activation, "gdn_norm_gate_bwd8"), eps, res_scale, workspace)
 
 
+def _gradient(t):
+    """An arriving gradient as the kernels take it: bf16, dense, on a 16-byte boundary (a piece of a wider one may start anywhere)."""
+    t = t.to(torch.bfloat16).contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _NormGate8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, z, activation, eps, res_scale):
@@ -136,9 +142,9 @@ class _NormGate8(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         weight, h8, hs, z8, zs = ctx.saved_tensors
         activation, eps, res_scale, has_res = ctx.args
-        dy = dy.to(torch.bfloat16).contiguous()
+        dy = _gradient(dy)
         if has_res:
-            dh = torch.zeros_like(dy) if dh is None else dh.to(torch.bfloat16).contiguous()
+            dh = torch.zeros_like(dy) if dh is None else _gradient(dh)
         dx, dres, dz, dw = gdn_norm_gate_bwd8(dy, h8, hs, weight, z_codes=z8, z_scale=zs, dh=dh if has_res else None,
                                               activation=activation, eps=eps, res_scale=res_scale)
         return dx, dw, dres, dz, None, None, None

@@ -95,8 +95,8 @@ class _Attention(torch.autograd.Function):
     def backward(ctx, do):
         q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
         causal, scale = ctx.args
-        dq, dk, dv = gdn_attention_bwd(do.to(torch.bfloat16).contiguous(), q, k, v, o, lse, cu_seqlens=cu, cu_seqlens_k=cu_k,
-                                       causal=causal, scale=scale)
+        dq, dk, dv = gdn_attention_bwd(stack._gradient(do), q, k, v, o, lse, cu_seqlens=cu, cu_seqlens_k=cu_k, causal=causal,
+                                       scale=scale)
         return dq, dk, dv, None, None, None, None
 
 

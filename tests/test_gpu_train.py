@@ -571,3 +571,26 @@ def test_a_wait_that_runs_out(D):
         assert int(st) & gdn.DEV_WAIT_TIMEOUT and not int(st) & gdn.DEV_DRAIN_TIMEOUT
         st.zero_()
         assert _same_bits(_all(q, k, v, do, cu_seqlens=cu, dev_status=st), want) and int(st) == 0
+
+
+def test_gradients_that_arrive_at_an_odd_address():
+    """The gradient of a piece of a concatenation is a view that starts where the piece does."""
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(5)
+    T, H, D = 37, 2, 64
+
+    def leaf(*shape):
+        return torch.randn(*shape, generator=g).to(BF).cuda().requires_grad_()
+
+    q, k, v, x, r, z = (leaf(T, H, D) for _ in range(6))
+    w = (1.0 + 0.1 * torch.randn(D, generator=g)).cuda().requires_grad_()
+    up = torch.randn(3 * T * H * D + 3, generator=g).to(BF).cuda()
+    leaves = (q, k, v, x, r, z, w)
+    out = [gdn.attention(q, k, v), *gdn.norm_gate(x, w, residual=r, z=z, save8=True)]
+    n = out[0].numel()
+    one = torch.zeros(1, dtype=BF, device="cuda")
+    odd = torch.cat([t for o in out for t in (one, o.flatten())])
+    got = torch.autograd.grad(odd, leaves, up, retain_graph=True)
+    want = torch.autograd.grad(out, leaves, [up[i * (n + 1) + 1:(i + 1) * (n + 1)].clone().view(T, H, D) for i in range(3)])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
