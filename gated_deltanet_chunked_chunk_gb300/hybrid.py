@@ -4,7 +4,8 @@ turn, each behind a norm with a residual, random weights.
     python -m gated_deltanet_chunked_chunk_gb300.hybrid
 
 serves a few ragged prompts (prefill, then single tokens) with a state pool for the recurrence and a paged 8-bit cache
-for the attention, and runs one training step.  Projections are plain matrix products."""
+for the attention, and runs training steps on packed sequences, with the inputs that the gradients need kept in bf16 and
+in 8 bits.  Projections are plain matrix products."""
 from __future__ import annotations
 
 import argparse
