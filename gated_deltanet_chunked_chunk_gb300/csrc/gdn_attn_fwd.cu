@@ -1,9 +1,9 @@
 // gdn_attn_fwd.cu -- attention of packed sequences, forward, on tcgen05.
 //
-//   S = q K^T,  p_j = 2^(c S_j - m),  l = sum p_j,  o = sum p_j v_j / l,
-//   lse = (m + log2 l) ln 2,  c = scale log2 e
+//   S = q K^T,  p_j = 2^(c S_j - c m),  l = sum p_j,  o = sum p_j v_j / l,
+//   lse = (c m + log2 l) ln 2,  c = scale log2 e
 //
-// with m the running maximum of c S.  Bound: the tensor cores, 4 D operations a (row,
+// with m the running maximum of S.  Bound: the tensor cores, 4 D operations a (row,
 // key, head).  16384 rows of one sequence, 32 heads, D = 128: 1370 us, 1.61 PFLOP/s, 83 %
 // of a large library matrix product's rate.  24 sequences of 200 to 2000 rows: 324
 // us.  A pair of tiles takes some 3000 cycles for 128 keys, of which the products alone
@@ -21,11 +21,17 @@
 // order, so an S of the next keys, issued after the P V that reads the same columns, is
 // safe, and "S is there" also says that O may be touched.
 //
-// m grows only where an exponent is more than kMost above it: both threads of a row
+// m grows only where an exponent is more than kMost above c m: both threads of a row
 // agree on that in one barrier that also joins their votes, and O is then rescaled.
 // P has 8 significant bits (bf16 keeps fp32's range, so any m near the maximum is as
 // good), l is the sum before that rounding, whose errors (2^-8 of a weight at most, either
 // way) mostly cancel in o.
+//
+// c m is rounded, the same for all weights of a row, which cancels in o and is in lse.  Past
+// |c m| = kFar the rounding could reach 2^6 and, twice as far, overflow the weights: there a
+// power of two between c / 4 and c / 2 takes the place of c, whose products are exact.  Numbers
+// S of that size that differ at all do so by 2^6 / c or more, so the largest has all the weight,
+// but 2^-16, either way.
 #include <algorithm>
 #include <type_traits>
 
@@ -37,6 +43,7 @@ using namespace gdnat;
 
 constexpr int kThreads = 640;
 constexpr float kMost = 8.f;
+constexpr float kFar = 1073741824.f;  // 2^30
 constexpr int kItems = 4;  // items between the warp that finds them and the others
 
 // An item, 32-bit words in shared memory: first row of q and of k of the sequence, its
@@ -66,6 +73,11 @@ __device__ __forceinline__ bool vote_any(int id, bool mine) {
                : "r"(id), "r"((uint32_t)mine)
                : "memory");
   return r != 0;
+}
+
+// The factor of S in the exponents of a row whose reference is m.
+__device__ __forceinline__ float factor(float c, float m) {
+  return fabsf(__fmul_rn(m, c)) > kFar ? __uint_as_float((__float_as_uint(c) & 0x7f800000u) - 0x00800000u) : c;
 }
 
 // Half a row of O, times inv, to dst; flags: 1: it is a row of the sequence, 2: it saw a
@@ -180,15 +192,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           next = gdnkv::max3(next, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
         }
         top = gdnkv::max3(top, __uint_as_float(s[62]), __uint_as_float(s[63]));
-        top = fmaxf(top, next) * a.scale_log2e;
+        top = fmaxf(top, next);
         // (of -inf both, NaN: no.  A wait that gave up votes too.)
-        if (vote_any(1 + w, top - m_ref > kMost || !ok)) {
+        if (vote_any(1 + w, (top - m_ref) * a.scale_log2e > kMost || !ok)) {
           sts_f(told, top);
           if (vote_any(1 + w, !ok)) goto leave;
           top = fmaxf(top, lds_f(told ^ 512));
           float grow = 1.f;
-          if (top - m_ref > kMost) {
-            grow = ex2f(m_ref - top);
+          if ((top - m_ref) * a.scale_log2e > kMost) {
+            const float was = __fmul_rn(m_ref, a.scale_log2e), now = __fmul_rn(top, a.scale_log2e);
+            grow = ex2f(fmaxf(fabsf(was), fabsf(now)) > kFar ? (m_ref - top) * a.scale_log2e : was - now);
             m_ref = top;
             l_sum *= grow;
           }
@@ -203,11 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        const float c = factor(a.scale_log2e, m_ref), ref = m_ref == -INFINITY ? 0.f : __fmul_rn(m_ref, c);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float2 t = gdnkv::fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), a.scale_log2e, -ref);
+          float2 t = gdnkv::fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c, -ref);
           t.x = ex2f(t.x);
           t.y = ex2f(t.y);
           sum = gdnkv::add2(sum, t);
@@ -241,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(OE(w));
       }
-      if (r < count && half == 0) a.lse[at] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+      if (r < count && half == 0) {
+        const float ref = __fmul_rn(m_ref, a.scale_log2e), more = log2f(l);
+        a.lse[at] = l == 0.f ? -INFINITY : fabsf(ref) > kFar ? fmaf(m_ref, a.scale, more * kLn2) : (ref + more) * kLn2;
+      }
     }
   leave:;
   } else {

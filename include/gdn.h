@@ -721,7 +721,8 @@ int gdn_norm_gate_bwd8(const uint16_t *dy, const uint8_t *h_codes, const float *
  *     o = softmax(scale q k^T) v,  lse = log sum exp(scale q k^T)
  * A row that sees nothing has o = 0 and lse = -inf.  Two calls with the same
  * arguments agree bit for bit.  The softmax weights enter the second product in
- * bf16 (2^-8 of each at most), sums and maxima are fp32.
+ * bf16 (2^-8 of each at most), sums and maxima are fp32.  Logits may have any size
+ * as long as scale q k stays within fp32.
  *   q             : bf16 [Tq, HQ, D], k, v: bf16 [Tk, HK, D]; ldq, ldk, ldv
  *                   elements between tokens, heads dense; query head h reads kv
  *                   head h / (HQ / HK)
@@ -757,7 +758,9 @@ size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, i
  *   dq            : bf16 [Tq, HQ, D];  dk, dv: bf16 [Tk, HK, D], dense
  *   workspace     : gdn_attention_bwd_workspace_size() bytes, 16-byte aligned
  * Everything else as in gdn_attention_fwd; rows and keys behind the last sequence
- * have zero gradients.  P and dS enter the products in bf16, sums are fp32 and have a
+ * have zero gradients.  P is off by some 2^-23 |lse| of itself, as lse is one fp32
+ * number: 2^-8, as by its rounding to bf16, at |lse| = 2^15, a factor of e
+ * at 2^23, and from 2^30 on it may be infinite.  P and dS enter the products in bf16, sums are fp32 and have a
  * fixed order: two calls agree bit for bit (where the sums of dk and dv are cut depends
  * on the lengths of the whole batch, so in another batch their last bits can differ).  dout, o, dq, dk, dv must start on a
  * 16-byte boundary; GDN_EWORKSPACE for a small workspace.  Three launches, four

@@ -594,3 +594,33 @@ def test_gradients_that_arrive_at_an_odd_address():
     want = torch.autograd.grad(out, leaves, [up[i * (n + 1) + 1:(i + 1) * (n + 1)].clone().view(T, H, D) for i in range(3)])
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("order", ["random", "grow", "fall"])
+@pytest.mark.parametrize("D,causal", [(128, True), (64, True), (64, False)])
+@pytest.mark.parametrize("power,scale", [(8, 1.0), (17, 1.0), (23, 1.0), (24, 1.0), (25, 3.0), (31, 1.0), (60, 0.5), (100, 1.0), (119, 3.0)])
+def test_logits_of_any_size(power, scale, D, causal, order):
+    """Logits of 2^power times whole numbers, exact in bf16 and in the products, up to where scale q k itself passes fp32:
+    the largest of a row take all the weight.  o is a mean of some values.  Its weights are 2^(c S - c m) with c m rounded,
+    the same number near 1 for all of them, which enters the product in bf16, off by 2^-8 of itself, and the sum l before
+    that rounding: 2^-8 of the mean's terms, and 2^-8 of the mean for the output's rounding.  The factors of lse are off
+    by 2^-24 each, four of them."""
+    gdn = _gdn()
+    T = 300
+    g = torch.Generator().manual_seed(power)
+    n = torch.randint(-120, 121, (T,), generator=g).double()
+    n = n if order == "random" else n.sort(descending=order == "fall")[0]
+    q, k = torch.zeros(T, 1, D), torch.zeros(T, 1, D)
+    q[:, 0, 3], k[:, 0, 3] = 2.0 ** power, n.float()
+    v = torch.randn(T, 1, D, generator=g).to(BF)
+    o, lse = gdn.gdn_attention_fwd(q.to(BF).cuda(), k.to(BF).cuda(), v.cuda(), causal=causal, scale=scale)
+    s = (n * 2.0 ** power * scale).expand(T, T)
+    if causal:
+        s = s.masked_fill(torch.ones(T, T, dtype=torch.bool).triu(1), -math.inf)
+    p = (s == s.amax(-1, keepdim=True)).double()
+    p /= p.sum(-1, keepdim=True)
+    want, mag = p @ v[:, 0].double(), p @ v[:, 0].double().abs()
+    _near(o[:, 0], want, 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -20) * mag, "o")
+    ref = torch.logsumexp(s, -1)
+    ref = torch.where(ref.abs() > torch.finfo(torch.float32).max, ref.sign() * math.inf, ref)
+    _near(lse[:, 0], ref, 2.0 ** -22 * ref.abs() + 2.0 ** -20, "lse")
