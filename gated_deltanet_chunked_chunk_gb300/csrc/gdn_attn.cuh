@@ -57,22 +57,23 @@ struct Args : gdn_host::TrainAttnArgs {
   float scale_log2e;
 };
 
-// A sequence's tiles have places in the workspace without a search: sequence n's are from
-// floor(cu[n] / R) + n on.  With a = R A + r and b = R B + s, ceil((b - a) / R) <= B - A + 1,
+// A sequence's tiles have places in the workspace without a search.  Sequence n's are from
+// floor(cu[n] / R) + n on: with a = R A + r and b = R B + s, ceil((b - a) / R) <= B - A + 1,
 // so no two sequences share a place, and with the rows behind the last one there are at
-// most this many, which the host knows.
-__host__ __device__ __forceinline__ int64_t slots_of(int64_t T, int N, int R) { return T / R + N + 1; }
-// Tiles of R rows that T rows of N sequences have at most.
-__host__ __device__ __forceinline__ int64_t most_tiles(int64_t T, int N, int R) {
-  const int64_t most = slots_of(T, N, R);
-  return most < T ? most : T;
-}
+// most T / R + N + 1.  Where there are fewer rows than that (most sequences are empty or
+// short) a tile's place is its first row, of which there are T.
+__host__ __device__ __forceinline__ bool by_row(int64_t T, int N, int R) { return T < T / R + N + 1; }
+// Places, and tiles that T rows of N sequences have at most.
+__host__ __device__ __forceinline__ int64_t most_tiles(int64_t T, int N, int R) { return by_row(T, N, R) ? T : T / R + N + 1; }
 
 // One side's sequences: offsets, or one sequence of all rows (cu NULL).
 struct Side {
   const int32_t *cu;
   int N, T;
   __device__ __forceinline__ int at(int n) const { return cu ? cu[n] : (n == 0 ? 0 : T); }
+  // The place of tile 0 of sequence n, whose first row this is, and from a tile's to the next one's.
+  __device__ __forceinline__ int64_t place(int n, int first, int R) const { return by_row(T, N, R) ? first : (int64_t)(first / R) + n; }
+  __device__ __forceinline__ int apart(int R) const { return by_row(T, N, R) ? R : 1; }
 };
 __device__ __forceinline__ Side rows_of(const Args &a) { return Side{a.cu, a.N, a.Tq}; }
 // Keys: their own offsets, else the rows'.
@@ -90,14 +91,14 @@ __device__ __forceinline__ bool run_of(const Side &s, int n, Run &r) {
   r.count = c1 - c0;
   return true;
 }
-// The sequence that owns a slot, found by a warp (every lane gets it): 32 places are
+// The sequence that owns a place, found by a warp (every lane gets it): 32 sequences are
 // looked at in each turn.  Offsets that are not sorted give some sequence.
-__device__ __forceinline__ int owner_of(const Side &s, int64_t slot, int R) {
+__device__ __forceinline__ int owner_of(const Side &s, int64_t place, int R) {
   const int lane = threadIdx.x & 31;
   int lo = 0, span = s.N + 1;
   while (span > 1) {
     const int step = (span + 31) / 32, n = lo + lane * step;
-    const bool there = lane * step < span && (int64_t)(s.at(n) / R) + n <= slot;
+    const bool there = lane * step < span && s.place(n, s.at(n), R) <= place;
     const uint32_t m = __ballot_sync(0xffffffffu, there || lane == 0);
     const int top = 31 - __clz((int)m);
     lo += top * step;
@@ -106,20 +107,21 @@ __device__ __forceinline__ int owner_of(const Side &s, int64_t slot, int R) {
   return lo;
 }
 
-// What the tile of a slot works on.
+// What the tile of a place works on.
 struct Tile {
   int n;           // its sequence
   Run rows, keys;  // the sequence's
-  int row0;        // its first row in the sequence (of the slot's side)
+  int row0;        // its first row in the sequence (of the place's side)
 };
-// `by_keys`: slots of the keys' side.  False: nothing to do.
-__device__ __forceinline__ bool tile_of(const Args &a, int64_t slot, int R, bool by_keys, Tile &t) {
+// `by_keys`: places of the keys' side.  False: nothing to do.
+__device__ __forceinline__ bool tile_of(const Args &a, int64_t place, int R, bool by_keys, Tile &t) {
   const Side rows = rows_of(a), keys = keys_of(a), mine = by_keys ? keys : rows;
-  t.n = owner_of(mine, slot, R);
+  t.n = owner_of(mine, place, R);
   if (!run_of(rows, t.n, t.rows) || !run_of(keys, t.n, t.keys)) return false;
   if (t.n == a.N) (by_keys ? t.rows : t.keys).count = 0;
-  const int64_t row0 = (slot - ((int64_t)(mine.at(t.n) / R) + t.n)) * R;
-  if (row0 < 0 || row0 >= (by_keys ? t.keys : t.rows).count) return false;
+  const bool rowwise = by_row(mine.T, mine.N, R);
+  const int64_t past = place - mine.place(t.n, mine.at(t.n), R), row0 = rowwise ? past : past * R;
+  if (past < 0 || (rowwise && past % R) || row0 >= (by_keys ? t.keys : t.rows).count) return false;
   t.row0 = (int)row0;
   return true;
 }

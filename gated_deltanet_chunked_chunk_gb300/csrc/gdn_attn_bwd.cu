@@ -51,13 +51,13 @@ constexpr int kNear = 4;      // steps before its end from which a walk is about
 constexpr int kItems = 1;  // items between the warp that finds them and the others: it takes the next when all have one
 
 struct BwdArgs : Args {
-  float *stats;  // [HQ][q slots][2][kTile]: -lse log2 e, delta
-  float *part;   // [piece][k slots][HK][2][kTile][D]: sums of dK and dV
+  float *stats;  // [HQ][q places][2][kTile]: -lse log2 e, delta
+  float *part;   // [piece][k places][HK][2][kTile][D]: sums of dK and dV
   struct Shared {
     int cut;               // steps that a piece of a walk has at least
     int next_kv, next_q;   // items that the blocks of the two kernels have taken
   } *shared;
-  int64_t q_slots, k_slots;
+  int64_t q_places, k_places;
   int pieces;  // most pieces of a walk
 };
 
@@ -77,7 +77,7 @@ __device__ __forceinline__ int64_t take_item(int *next) {
 // ------------------------------------------------------------ of each row
 template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs a) {
   constexpr int L = D / 8, PER = 256 / L;  // lanes a row, rows at once
-  const int64_t slot = blockIdx.x / a.HQ;
+  const int64_t place = blockIdx.x / a.HQ;
   const int head = blockIdx.x % a.HQ, l = threadIdx.x % L;
   grid_wait();
   if (blockIdx.x == 0) {
@@ -105,8 +105,8 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
     }
   }
   Tile t;
-  if (!tile_of(a, slot, kTile, false, t)) return;
-  float *out = a.stats + ((int64_t)head * a.q_slots + slot) * 2 * kTile;
+  if (!tile_of(a, place, kTile, false, t)) return;
+  float *out = a.stats + ((int64_t)head * a.q_places + place) * 2 * kTile;
 #pragma unroll 4
   for (int r = threadIdx.x / L; r < kTile; r += PER) {
     const bool on = t.row0 + r < t.rows.count;
@@ -138,7 +138,7 @@ template <int D> __global__ void __launch_bounds__(256) attn_stats_kernel(const 
 // that sees them, how many there are; the piece's first step and its steps (step s is head
 // s / nt of the group, row tile t0 + s % nt); kv head; where the sums go (-1: they are whole),
 // whether it is an item (0: there are no more).
-enum KvWord { K_Q = 0, K_ROWS = 4, K_QSLOT = 8, K_K = 12, K_KEYS = 16, K_K0 = 20, K_PAST = 24, K_T0 = 28, K_NT = 32, K_S0 = 36, K_STEPS = 40,
+enum KvWord { K_Q = 0, K_ROWS = 4, K_QPLACE = 8, K_K = 12, K_KEYS = 16, K_K0 = 20, K_PAST = 24, K_T0 = 28, K_NT = 32, K_S0 = 36, K_STEPS = 40,
               K_HK = 44, K_PART = 48, K_ON = 52, K_BYTES = 64 };
 template <int D> struct KvLay {
   static constexpr int TB = tile_bytes<D>();
@@ -342,12 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------- copies
       if (elect_one()) {
         uint32_t q_in = 0, o_in = 0, t_in = 0, kv_in = 0;  // what has been asked for
+        const int apart = rows_of(a).apart(kTile);
         bool ok = true;
         for (int it = 0; ok; ++it) {
           uint32_t work;
           if (!item(it, work) || !lds_i(work + K_ON)) break;
           const int steps = lds_i(work + K_STEPS), nt = lds_i(work + K_NT), t0 = lds_i(work + K_T0), s0 = lds_i(work + K_S0), hk = lds_i(work + K_HK);
-          const int key = lds_i(work + K_K) + lds_i(work + K_K0), first = lds_i(work + K_Q), q_slot = lds_i(work + K_QSLOT);
+          const int key = lds_i(work + K_K) + lds_i(work + K_K0), first = lds_i(work + K_Q), q_place = lds_i(work + K_QPLACE);
           mbar_arrive(WE(it % kItems));
           if (steps == 0) continue;
           if (kv_in > 0) ok = wait_bar(KE, (kv_in - 1) & 1, failed, a.dev_status);
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t_in >= Ly::NT) ok = wait_bar(TE(is), (t_in / Ly::NT - 1) & 1, failed, a.dev_status);
             if (!ok) break;
             mbar_arrive_expect_tx(TF(is), 2 * kTile * 4);
-            bulk_load(sb + Ly::OFF_T + is * (2 * kTile * 4), a.stats + ((int64_t)head * a.q_slots + q_slot + t0 + t) * 2 * kTile, 2 * kTile * 4,
+            bulk_load(sb + Ly::OFF_T + is * (2 * kTile * 4), a.stats + ((int64_t)head * a.q_places + q_place + (t0 + t) * apart) * 2 * kTile, 2 * kTile * 4,
                       TF(is));
             ++t_in;
             if (o_in >= Ly::NO) ok = wait_bar(OE(io), (o_in / Ly::NO - 1) & 1, failed, a.dev_status);
@@ -508,10 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           sts_i(work + K_ON, on);
           if (on) {
             const int s0 = (int)(all * piece / pieces), hk = f.in / pieces;
-            const int64_t slot = f.keys.first / kTile + f.n + f.tile;
+            const Side rows = rows_of(a), keys = keys_of(a);
+            const int64_t place = keys.place(f.n, f.keys.first, kTile) + f.tile * keys.apart(kTile);
             sts_i(work + K_Q, f.rows.first);
             sts_i(work + K_ROWS, f.rows.count);
-            sts_i(work + K_QSLOT, f.rows.first / kTile + f.n);
+            sts_i(work + K_QPLACE, (int)rows.place(f.n, f.rows.first, kTile));
             sts_i(work + K_K, f.keys.first);
             sts_i(work + K_KEYS, f.keys.count);
             sts_i(work + K_K0, f.tile * kTile);
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts_i(work + K_S0, s0);
             sts_i(work + K_STEPS, (int)(all * (piece + 1) / pieces) - s0);
             sts_i(work + K_HK, hk);
-            sts_i(work + K_PART, pieces == 1 ? -1 : (int)((piece * a.k_slots + slot) * a.HK + hk));
+            sts_i(work + K_PART, pieces == 1 ? -1 : (int)((piece * a.k_places + place) * a.HK + hk));
           }
           mbar_arrive(WF(it % kItems));
         }
@@ -538,11 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Adds the pieces' sums of a (key tile, kv head) in order.
 template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const BwdArgs a) {
-  const int64_t slot = blockIdx.x / a.HK;
+  const int64_t place = blockIdx.x / a.HK;
   const int hk = blockIdx.x % a.HK;
   grid_wait();
   Tile t;
-  if (!tile_of(a, slot, kTile, true, t)) return;
+  if (!tile_of(a, place, kTile, true, t)) return;
   const int tn = tiles_in(t.rows.count, kTile);
   const int pieces = pieces_for(a, a.G * (tn - first_seen_by(a, tn, t.rows.count, t.keys.count, t.row0)), a.shared->cut);
   if (pieces == 1) return;
@@ -554,7 +556,7 @@ template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const B
 #pragma unroll 4
     for (int p = 0; p < pieces; ++p) {
       const float4 *src =
-          reinterpret_cast<const float4 *>(a.part + ((((p * a.k_slots + slot) * a.HK + hk) * 2 + (second ? 1 : 0)) * kTile + r) * D + c);
+          reinterpret_cast<const float4 *>(a.part + ((((p * a.k_places + place) * a.HK + hk) * 2 + (second ? 1 : 0)) * kTile + r) * D + c);
       const float4 u = __ldcs(src), v = __ldcs(src + 1);
       x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
       y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
@@ -568,7 +570,7 @@ template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const B
 // An item, 32-bit words in shared memory: first row of q of the sequence, the item's first
 // row in it, its rows; first key, keys, keys - rows; key tiles; the head; the place of the
 // rows' numbers; whether it is one (0: there are no more).
-enum QWord { Q_Q = 0, Q_ROW0 = 4, Q_COUNT = 8, Q_K = 12, Q_KEYS = 16, Q_PAST = 20, Q_TILES = 24, Q_HEAD = 28, Q_SLOT = 32, Q_ON = 36, Q_BYTES = 48 };
+enum QWord { Q_Q = 0, Q_ROW0 = 4, Q_COUNT = 8, Q_K = 12, Q_KEYS = 16, Q_PAST = 20, Q_TILES = 24, Q_HEAD = 28, Q_PLACE = 32, Q_ON = 36, Q_BYTES = 48 };
 template <int D> struct QLay {
   static constexpr int TB = tile_bytes<D>();
   static constexpr int NK = 3, NV = 2;
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         low = a.causal ? min(past + row0, keys - 1) : keys - 1;  // what the first row sees last
         limit = a.causal ? min(low + r, keys - 1) : low;
         if (r < lds_i(work + Q_COUNT)) at = ((int64_t)(lds_i(work + Q_Q) + row0 + r) * a.HQ + head) * D + wg * (D / 2);
-        const float *stats = a.stats + ((int64_t)head * a.q_slots + lds_i(work + Q_SLOT)) * 2 * kTile;
+        const float *stats = a.stats + ((int64_t)head * a.q_places + lds_i(work + Q_PLACE)) * 2 * kTile;
         n_lse = __ldcg(stats + r);
         n_delta = -__ldcg(stats + kTile + r);
         item_read(it);
@@ -907,6 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * Q_BYTES;
           sts_i(work + Q_ON, on);
           if (on) {
+            const Side rows = rows_of(a);
             const int row0 = f.tile * kTile, past = f.keys.count - f.rows.count, count = min(kTile, f.rows.count - row0);
             sts_i(work + Q_Q, f.rows.first);
             sts_i(work + Q_ROW0, row0);
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts_i(work + Q_PAST, past);
             sts_i(work + Q_TILES, tiles_in(max(0, a.causal ? min(f.keys.count, past + row0 + count) : f.keys.count), kTile));
             sts_i(work + Q_HEAD, f.in);
-            sts_i(work + Q_SLOT, f.rows.first / kTile + f.n + f.tile);
+            sts_i(work + Q_PLACE, (int)rows.place(f.n, f.rows.first, kTile) + f.tile * rows.apart(kTile));
           }
           mbar_arrive(WF(it % kItems));
         }
@@ -939,7 +942,7 @@ int pieces_of(int64_t k_tiles, int HK) {
 }
 
 template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
-  const int64_t q_blocks = a.q_slots * a.HQ, k_blocks = a.k_slots * a.HK;
+  const int64_t q_blocks = std::max<int64_t>(1, a.q_places) * a.HQ, k_blocks = a.k_places * a.HK;  // (block 0 does more than its rows)
   if (q_blocks > INT_MAX || k_blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const int64_t sms = gdn_host::sm_count();
   CUtensorMap mq, mk, mv, mo;
@@ -959,10 +962,10 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = gdn_host::launch_dependent(attn_stats_kernel<D>, dim3((unsigned)q_blocks), 256, 0, s, a);
   if (e == cudaSuccess && keys)
-    e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tk, a.N, kTile) * a.HK * a.pieces, sms)), kThreads,
+    e = gdn_host::launch_dependent(attn_dkdv_kernel<D>, dim3((unsigned)std::min(a.k_places * a.HK * a.pieces, sms)), kThreads,
                                    KvLay<D>::BYTES, s, a, mq, mk, mv, mo);
   if (e == cudaSuccess && rows)
-    e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)std::min(most_tiles(a.Tq, a.N, kTile) * a.HQ, sms)), kThreads, QLay<D>::BYTES,
+    e = gdn_host::launch_dependent(attn_dq_kernel<D>, dim3((unsigned)std::min(a.q_places * a.HQ, sms)), kThreads, QLay<D>::BYTES,
                                    s, a, keys ? 0 : 1, mq, mk, mv, mo);
   if (e == cudaSuccess && keys && a.pieces > 1) e = gdn_host::launch_dependent(attn_join_kernel<D>, dim3((unsigned)k_blocks, 8), 256, 0, s, a);
   return e;
@@ -971,20 +974,20 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
 }  // namespace
 
 namespace gdn_host {
-static size_t stats_bytes(int N, int Tq, int HQ) { return (size_t)HQ * gdnat::slots_of(Tq, N, gdnat::kTile) * 2 * gdnat::kTile * sizeof(float); }
+static size_t stats_bytes(int N, int Tq, int HQ) { return (size_t)HQ * gdnat::most_tiles(Tq, N, gdnat::kTile) * 2 * gdnat::kTile * sizeof(float); }
 size_t attn_bwd_workspace_bytes(int N, int Tq, int Tk, int HQ, int HK, int D) {
-  const int64_t k_slots = gdnat::slots_of(Tk, N, gdnat::kTile);
-  const int pieces = pieces_of(gdnat::most_tiles(Tk, N, gdnat::kTile), HK);
-  return 16 + stats_bytes(N, Tq, HQ) + (pieces > 1 ? (size_t)pieces * k_slots * HK * 2 * gdnat::kTile * D * sizeof(float) : 0);
+  const int64_t k_places = gdnat::most_tiles(Tk, N, gdnat::kTile);
+  const int pieces = pieces_of(k_places, HK);
+  return 16 + stats_bytes(N, Tq, HQ) + (pieces > 1 ? (size_t)pieces * k_places * HK * 2 * gdnat::kTile * D * sizeof(float) : 0);
 }
 cudaError_t launch_attn_bwd(const TrainAttnArgs &c, cudaStream_t s) {
   BwdArgs a{};
   static_cast<TrainAttnArgs &>(a) = c;
   a.G = c.HQ / c.HK;
   a.scale_log2e = c.scale * gdnc::kLog2e;
-  a.q_slots = gdnat::slots_of(c.Tq, c.N, gdnat::kTile);
-  a.k_slots = gdnat::slots_of(c.Tk, c.N, gdnat::kTile);
-  a.pieces = pieces_of(gdnat::most_tiles(c.Tk, c.N, gdnat::kTile), c.HK);
+  a.q_places = gdnat::most_tiles(c.Tq, c.N, gdnat::kTile);
+  a.k_places = gdnat::most_tiles(c.Tk, c.N, gdnat::kTile);
+  a.pieces = pieces_of(a.k_places, c.HK);
   a.shared = static_cast<BwdArgs::Shared *>(c.ws);
   a.stats = reinterpret_cast<float *>(static_cast<char *>(c.ws) + 16);
   a.part = a.stats + stats_bytes(c.N, c.Tq, c.HQ) / sizeof(float);

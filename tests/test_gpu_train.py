@@ -624,3 +624,36 @@ def test_logits_of_any_size(power, scale, D, causal, order):
     ref = torch.logsumexp(s, -1)
     ref = torch.where(ref.abs() > torch.finfo(torch.float32).max, ref.sign() * math.inf, ref)
     _near(lse[:, 0], ref, 2.0 ** -22 * ref.abs() + 2.0 ** -20, "lse")
+
+
+def _few(N, at):
+    lens = [0] * N
+    for n, m in at.items():
+        lens[n] = m
+    return lens
+
+
+@pytest.mark.parametrize("lens,lens_k,HQ,HK,D", [
+    (_few(600, {3: 200, 4: 7, 300: 60, 599: 23}), None, 4, 1, 128),       # walks that are cut, places by rows
+    (_few(1024, {0: 37}), None, 2, 2, 64),
+    (_few(300, {5: 400, 200: 130}), _few(300, {5: 100, 200: 150}), 2, 1, 128),  # rows and keys find theirs in different ways
+    (_few(300, {5: 30, 200: 13}), _few(300, {5: 500, 200: 150, 250: 9}), 2, 1, 64),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_mostly_empty_sequences(lens, lens_k, HQ, HK, D, causal):
+    """Offsets of many empty sequences, as a padded batch has them: a workspace as large as it has to be, nothing behind it
+    written."""
+    gdn = _gdn()
+    q, k, v, do = _inputs(lens, lens_k, HQ, HK, D, 3)
+    cu, cu_k = U.offsets(lens).cuda(), None if lens_k is None else U.offsets(lens_k).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dict(cu_seqlens=cu, cu_seqlens_k=cu_k, causal=causal, dev_status=status)
+    c = [t.cuda() for t in (q, k, v)]
+    o, lse = gdn.gdn_attention_fwd(*c, **args)
+    need = gdn.attention_bwd_workspace_size(len(lens), sum(lens), len(k), HQ, HK, D)
+    buffer = torch.full((need + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    grads = gdn.gdn_attention_bwd(do.cuda(), *c, o, lse, workspace=buffer[:need], **args)
+    assert int(status) == 0 and bool((buffer[need:] == 0x5a).all())
+    r = U.attention(q, k, v, U.spans(lens, lens_k), causal, D ** -0.5, do)
+    _check_fwd(o, lse, r)
+    _check_bwd(grads, r)

@@ -160,3 +160,13 @@ def test_python_entries_refuse_the_cpu(lib):
         gdn.gdn_attention_fwd(None, q, q)
     with pytest.raises(ValueError, match="activation"):
         gdn.gdn_norm_gate_save8(x, torch.ones(128), z=x, activation="tanh")
+
+
+@pytest.mark.parametrize("N", [1, 7, 100, 1024, 4096, 65535])
+@pytest.mark.parametrize("T,Tk", [(10, 10), (37, 37), (300, 64), (64, 300), (4096, 1), (1, 9000)])
+def test_attention_workspace_of_few_tokens(lib, N, T, Tk):
+    """What empty sequences add is nothing: a row has 1024 bytes a head at most, and the walks of all keys' tiles (a tile
+    has a key at least) are cut into 8 pieces each at most, and into twice the 152 SMs and one for each tile in all."""
+    for HQ, HK, D in ((8, 2, 128), (1, 1, 64), (32, 32, 128)):
+        pieces = min(8 * Tk * HK, 2 * 152 + min(Tk * HK, 2 * 152))
+        assert 0 < gdn.attention_bwd_workspace_size(N, T, Tk, HQ, HK, D) <= 16 + 1024 * HQ * T + pieces * 2 * 128 * D * 4
