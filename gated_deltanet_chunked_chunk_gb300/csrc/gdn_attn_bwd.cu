@@ -940,6 +940,13 @@ int pieces_of(int64_t k_tiles, int HK) {
   const int64_t items = std::max<int64_t>(1, k_tiles * HK), want = (2 * kBlocks + items - 1) / items;
   return (int)std::min<int64_t>(want, 8);
 }
+// Pieces that this many (key tile, kv head)s, or fewer, have in all at most, so that the
+// workspace of a call is large enough for every smaller one: x of them have 8 x or, as
+// pieces_of rounds up, less than 2 kBlocks + x, and those from 2 kBlocks on are not cut.
+int64_t most_pieces(int64_t k_tiles, int HK) {
+  const int64_t items = k_tiles * HK, cut = std::min<int64_t>(items, 2 * kBlocks - 1);
+  return std::min(8 * items, 2 * kBlocks - 1 + cut);
+}
 
 template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   const int64_t q_blocks = std::max<int64_t>(1, a.q_places) * a.HQ, k_blocks = a.k_places * a.HK;  // (block 0 does more than its rows)
@@ -976,9 +983,8 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
 namespace gdn_host {
 static size_t stats_bytes(int N, int Tq, int HQ) { return (size_t)HQ * gdnat::most_tiles(Tq, N, gdnat::kTile) * 2 * gdnat::kTile * sizeof(float); }
 size_t attn_bwd_workspace_bytes(int N, int Tq, int Tk, int HQ, int HK, int D) {
-  const int64_t k_places = gdnat::most_tiles(Tk, N, gdnat::kTile);
-  const int pieces = pieces_of(k_places, HK);
-  return 16 + stats_bytes(N, Tq, HQ) + (pieces > 1 ? (size_t)pieces * k_places * HK * 2 * gdnat::kTile * D * sizeof(float) : 0);
+  return 16 + stats_bytes(N, Tq, HQ) +
+         (size_t)most_pieces(gdnat::most_tiles(Tk, N, gdnat::kTile), HK) * 2 * gdnat::kTile * D * sizeof(float);
 }
 cudaError_t launch_attn_bwd(const TrainAttnArgs &c, cudaStream_t s) {
   BwdArgs a{};

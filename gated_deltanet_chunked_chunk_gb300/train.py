@@ -68,7 +68,7 @@ def gdn_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
 
 
 def attention_bwd_workspace_size(N, Tq, Tk, HQ, HK, D) -> int:
-    """Bytes of workspace that gdn_attention_bwd needs for these sizes."""
+    """Bytes of workspace that gdn_attention_bwd needs for these sizes, enough for all smaller ones too."""
     return int(load_library().gdn_attention_bwd_workspace_size(N, Tq, Tk, HQ, HK, D))
 
 

@@ -745,7 +745,11 @@ int gdn_attention_fwd(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t
                       const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int N, int Tq, int Tk, int HQ, int HK, int D,
                       int causal, float scale, uint16_t *o, float *lse, int32_t *dev_status, void *stream);
 
-/* gdn_attention_bwd_workspace_size -- bytes of device workspace gdn_attention_bwd needs. */
+/*
+ * gdn_attention_bwd_workspace_size -- bytes of device workspace gdn_attention_bwd needs;
+ * as much or more than with any of the sizes smaller, so one workspace serves all
+ * smaller calls too.
+ */
 size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, int D);
 
 /*

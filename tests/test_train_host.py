@@ -170,3 +170,19 @@ def test_attention_workspace_of_few_tokens(lib, N, T, Tk):
     for HQ, HK, D in ((8, 2, 128), (1, 1, 64), (32, 32, 128)):
         pieces = min(8 * Tk * HK, 2 * 152 + min(Tk * HK, 2 * 152))
         assert 0 < gdn.attention_bwd_workspace_size(N, T, Tk, HQ, HK, D) <= 16 + 1024 * HQ * T + pieces * 2 * 128 * D * 4
+
+
+@pytest.mark.parametrize("which", ["N", "Tq", "Tk", "HQ", "HK", "D"])
+def test_attention_workspace_serves_smaller_calls(lib, which):
+    """The workspace of one call is enough for every call of smaller sizes."""
+    order = ("N", "Tq", "Tk", "HQ", "HK", "D")
+    lengths = sorted({m for x in range(17) for m in (2 ** x - 1, 2 ** x, 2 ** x + 1, 5 << x)})
+    ranges = dict(N=[n for n in lengths if 0 < n < 65536], Tq=lengths, Tk=lengths, HQ=range(8, 264, 8), HK=[1, 2, 4, 8], D=[64, 128])
+    bases = [(1, 8192, 8192, 32, 4, 128), (24, 27160, 27160, 32, 4, 128), (1, 256, 256, 8, 2, 64), (300, 1000, 64, 8, 8, 128),
+             (4096, 50, 16384, 64, 1, 64), (1, 1, 40000, 8, 1, 128)]
+    for base in bases:
+        sizes = dict(zip(order, base))
+        got = [gdn.attention_bwd_workspace_size(*(x if n == which else sizes[n] for n in order)) for x in ranges[which]
+               if which != "HK" or sizes["HQ"] % x == 0]
+        assert all(a <= b for a, b in zip(got, got[1:])), (base, got)
+        assert got[0] > 0
