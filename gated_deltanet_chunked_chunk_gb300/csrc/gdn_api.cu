@@ -480,6 +480,7 @@ int gdn_attention_fwd(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t
 
 size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, int D) {
   if (N < 0 || N > 65535 || Tq < 0 || Tk < 0 || HK <= 0 || HQ <= 0 || HQ > 65535 || HQ % HK || !head_dim_ok(D)) return 0;
+  if (!gdn_host::attn_bwd_takes(N, Tq, Tk, HQ, HK)) return 0;
   return gdn_host::attn_bwd_workspace_bytes(N, Tq, Tk, HQ, HK, D);
 }
 
@@ -490,6 +491,7 @@ int gdn_attention_bwd(const uint16_t *dout, const uint16_t *q, int64_t ldq, cons
   gdn_host::TrainAttnArgs a{};
   const int rc = attention_args(q, ldq, k, ldk, v, ldv, cu_seqlens, cu_seqlens_k, N, Tq, Tk, HQ, HK, D, causal, scale, dev_status, a);
   if (rc != GDN_OK) return rc;
+  if (!gdn_host::attn_bwd_takes(N, Tq, Tk, HQ, HK)) return GDN_EUNSUPPORTED;
   if (Tq == 0 && Tk == 0) return GDN_OK;
   if (Tq > 0 && (!dout || !o || !lse || !dq)) return GDN_EINVAL;
   if (Tk > 0 && (!dk || !dv)) return GDN_EINVAL;

@@ -950,7 +950,6 @@ int64_t most_pieces(int64_t k_tiles, int HK) {
 
 template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
   const int64_t q_blocks = std::max<int64_t>(1, a.q_places) * a.HQ, k_blocks = a.k_places * a.HK;  // (block 0 does more than its rows)
-  if (q_blocks > INT_MAX || k_blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const int64_t sms = gdn_host::sm_count();
   CUtensorMap mq, mk, mv, mo;
   // a side without rows is never loaded
@@ -982,6 +981,9 @@ template <int D> cudaError_t launch(const BwdArgs &a, cudaStream_t s) {
 
 namespace gdn_host {
 static size_t stats_bytes(int N, int Tq, int HQ) { return (size_t)HQ * gdnat::most_tiles(Tq, N, gdnat::kTile) * 2 * gdnat::kTile * sizeof(float); }
+bool attn_bwd_takes(int N, int Tq, int Tk, int HQ, int HK) {
+  return gdnat::most_tiles(Tq, N, gdnat::kTile) * HQ <= INT_MAX && gdnat::most_tiles(Tk, N, gdnat::kTile) * HK <= INT_MAX;
+}
 size_t attn_bwd_workspace_bytes(int N, int Tq, int Tk, int HQ, int HK, int D) {
   return 16 + stats_bytes(N, Tq, HQ) +
          (size_t)most_pieces(gdnat::most_tiles(Tk, N, gdnat::kTile), HK) * 2 * gdnat::kTile * D * sizeof(float);

@@ -290,6 +290,7 @@ struct TrainAttnArgs {
   int force_expiry;  // testing hook: the first bounded wait of every block runs out
 };
 cudaError_t launch_attn_fwd(const TrainAttnArgs &a, cudaStream_t s);
+bool attn_bwd_takes(int N, int Tq, int Tk, int HQ, int HK);  // fewer tiles than 2^31
 size_t attn_bwd_workspace_bytes(int N, int Tq, int Tk, int HQ, int HK, int D);
 cudaError_t launch_attn_bwd(const TrainAttnArgs &a, cudaStream_t s);
 }  // namespace gdn_host

@@ -767,7 +767,9 @@ size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, i
  * at 2^23, and from 2^30 on it may be infinite.  P and dS enter the products in bf16, sums are fp32 and have a
  * fixed order: two calls agree bit for bit (where the sums of dk and dv are cut depends
  * on the lengths of the whole batch, so in another batch their last bits can differ).  dout, o, dq, dk, dv must start on a
- * 16-byte boundary; GDN_EWORKSPACE for a small workspace.  Three launches, four
+ * 16-byte boundary; GDN_EWORKSPACE for a small workspace, GDN_EUNSUPPORTED (and a
+ * workspace size of 0) where min(T, T / 128 + N + 1) heads, of the rows or of the
+ * keys, pass 2^31 - 1.  Three launches, four
  * where few keys are cut between more blocks.
  */
 int gdn_attention_bwd(const uint16_t *dout, const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,

@@ -186,3 +186,12 @@ def test_attention_workspace_serves_smaller_calls(lib, which):
                if which != "HK" or sizes["HQ"] % x == 0]
         assert all(a <= b for a, b in zip(got, got[1:])), (base, got)
         assert got[0] > 0
+
+
+def test_attention_gradients_of_too_many_tiles(lib):
+    """Tiles of all heads past 2^31: refused as not supported, with no size of a workspace, rather than by the launch."""
+    big = dict(N=65535, cu=F, Tq=100000, Tk=100000, HQ=65535, HK=1, D=64, ldq=65535 * 64)
+    assert gdn.attention_bwd_workspace_size(65535, 100000, 100000, 65535, 1, 64) == 0
+    assert _bwd(lib, **big) == gdn.GDN_EUNSUPPORTED
+    assert _bwd(lib, **dict(big, HK=65535, ldk=65535 * 64, ldv=65535 * 64)) == gdn.GDN_EUNSUPPORTED
+    assert gdn.attention_bwd_workspace_size(65535, 32000, 32000, 65535, 1, 64) > 0
