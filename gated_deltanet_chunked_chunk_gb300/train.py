@@ -84,23 +84,27 @@ def gdn_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, cu_seqlens, cu_seqlens_k, causal, scale):
-        o, lse = gdn_attention_fwd(q, k, v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, causal=causal, scale=scale)
+    def forward(ctx, q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, dev_status):
+        o, lse = gdn_attention_fwd(q, k, v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, causal=causal, scale=scale,
+                                   dev_status=dev_status)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
-        ctx.args = (causal, scale)
+        ctx.args = (causal, scale, dev_status)  # (the status is the caller's to clear meanwhile)
         return o
 
     @staticmethod
     @once_differentiable  # the gradient kernels have no gradient of their own: a second derivative is an error
     def backward(ctx, do):
         q, k, v, o, lse, cu, cu_k = ctx.saved_tensors
-        causal, scale = ctx.args
+        causal, scale, status = ctx.args
         dq, dk, dv = gdn_attention_bwd(stack._gradient(do), q, k, v, o, lse, cu_seqlens=cu, cu_seqlens_k=cu_k, causal=causal,
-                                       scale=scale)
-        return dq, dk, dv, None, None, None, None
+                                       scale=scale, dev_status=status)
+        return dq, dk, dv, None, None, None, None, None
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
-              cu_seqlens_k: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None) -> torch.Tensor:
-    """Differentiable (once) gdn_attention_fwd; returns o.  The forward keeps q, k, v, o and lse for the gradient."""
-    return _Attention.apply(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale)
+              cu_seqlens_k: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
+              dev_status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable (once) gdn_attention_fwd; returns o.  The forward keeps q, k, v, o and lse for the gradient.  Both
+    directions report to ``dev_status`` what they could not do (offsets that break the rules: rows of that sequence are not
+    written, in the gradients neither)."""
+    return _Attention.apply(q, k, v, cu_seqlens, cu_seqlens_k, causal, scale, dev_status)

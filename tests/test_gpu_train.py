@@ -657,3 +657,18 @@ def test_mostly_empty_sequences(lens, lens_k, HQ, HK, D, causal):
     r = U.attention(q, k, v, U.spans(lens, lens_k), causal, D ** -0.5, do)
     _check_fwd(o, lse, r)
     _check_bwd(grads, r)
+
+
+def test_autograd_reports_bad_offsets():
+    gdn = _gdn()
+    q, k, v, do = (t.cuda() for t in _inputs([300], None, 2, 1, 64, 9))
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = gdn.attention(*leaves, cu_seqlens=torch.tensor([0, 100, 400], dtype=torch.int32, device="cuda"), dev_status=st)
+    assert int(st) == gdn.DEV_BAD_CU_SEQLENS
+    st.zero_()  # between the directions: the caller's to do
+    torch.autograd.grad(o, leaves, do)
+    assert int(st) == gdn.DEV_BAD_CU_SEQLENS
+    st.zero_()
+    torch.autograd.grad(gdn.attention(*leaves, cu_seqlens=U.offsets([100, 200]).cuda(), dev_status=st), leaves, do)
+    assert int(st) == 0
