@@ -4,8 +4,8 @@ turn, each behind a norm with a residual, random weights.
     python -m gated_deltanet_chunked_chunk_gb300.hybrid
 
 serves a few ragged prompts (prefill, then single tokens) with a state pool for the recurrence and a paged 8-bit cache
-for the attention, and runs training steps on packed sequences, with the inputs that the gradients need kept in bf16 and
-in 8 bits.  Projections are plain matrix products."""
+for the attention, and runs training steps: on one sequence, and on packed ones with the inputs that the gradients need
+kept in bf16 and in 8 bits.  Projections are plain matrix products."""
 from __future__ import annotations
 
 import argparse
@@ -139,13 +139,26 @@ class HybridStack:
             out += [layer.norm, layer.w_in, layer.w_out] + ([layer.out_norm] if layer.kind == "g" else [])
         return out
 
+    def _plain_attention(self, q, k, v):
+        """Causal attention of one sequence in fp32, from elementary operations."""
+        cfg, T = self.cfg, q.shape[0]
+        k, v = (t.repeat_interleave(cfg.HQ // cfg.HK, dim=1).transpose(0, 1).float() for t in (k, v))
+        s = q.transpose(0, 1).float() @ k.transpose(1, 2) / math.sqrt(cfg.D)
+        s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device=q.device).triu(1), -math.inf)
+        return (s.softmax(-1) @ v).transpose(0, 1).to(BF)
+
     def forward(self, x: torch.Tensor, lens: Optional[List[int]] = None, save8: bool = False) -> torch.Tensor:
-        """Differentiable, for packed sequences x bf16 [T, hidden] of these lengths (None: one) from their beginnings (no
-        convolution).  With ``save8`` the norms and projections keep their inputs for the gradient in 8 bits."""
+        """Differentiable, for x bf16 [T, hidden] from its beginning (no convolution): one sequence, whose attention has fp32
+        logits and weights ([heads, T, T] of them in memory), or packed sequences of the lengths ``lens`` ([T] for one), whose
+        attention is ``attention``, with its weights in bf16 (heads of other sizes than 64 and 128: as without lens).  With
+        ``save8``, which takes ``attention`` too, the norms and projections keep their inputs for the gradient in 8 bits."""
         cfg, T = self.cfg, x.shape[0]
-        lens = [T] if lens is None else lens
-        cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(x.device)
-        positions = torch.cat([torch.arange(m, dtype=torch.int32) for m in lens]).to(x.device)
+        kernels = (lens is not None or save8) and cfg.D in (64, 128)
+        if lens is None:
+            cu, num_seqs, positions = None, None, torch.arange(T, dtype=torch.int32, device=x.device)
+        else:
+            cu, num_seqs = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(x.device), len(lens)
+            positions = torch.cat([torch.arange(m, dtype=torch.int32) for m in lens]).to(x.device)
         linear = linear8 if save8 else lambda x, w: x @ w.T
         h, y = x, None
         for layer in self.layers:
@@ -157,13 +170,18 @@ class HybridStack:
             if layer.kind == "a":
                 q, k, v = u.view(T, -1, cfg.D).split([cfg.HQ, cfg.HK, cfg.HK], dim=1)
                 q, k = rotary_embedding(q, k, positions, self.inv_freq, attention_factor=self.rope_factor)
-                o = attention(q, k, v, cu_seqlens=cu)
+                if kernels:
+                    o = attention(q, k, v, cu_seqlens=cu, dev_status=self.status)
+                elif lens is None:
+                    o = self._plain_attention(q, k, v)
+                else:
+                    o = torch.cat([self._plain_attention(*part) for part in zip(*(t.split(lens) for t in (q, k, v)))])
             else:
                 q, k, v, z, a, b = u.split([cfg.H * cfg.K, cfg.H * cfg.K, cfg.HV * cfg.K, cfg.HV * cfg.K, cfg.HV, cfg.HV], dim=1)
                 q, k, v = (t.contiguous().view(1, T, -1, cfg.K) for t in (q, k, v))
                 g = -layer.A_log.exp() * torch.nn.functional.softplus(a.float() + layer.dt_bias)
                 o, _ = chunk_gated_delta_rule(q, k, v, g.view(1, T, -1), b.float().sigmoid().view(1, T, -1), output_final_state=False,
-                                              cu_seqlens=cu, num_seqs=len(lens))
+                                              cu_seqlens=cu, num_seqs=num_seqs)
                 o, _ = norm_gate(o.view(T, cfg.HV, cfg.K), layer.out_norm, z=z.unflatten(1, (cfg.HV, cfg.K)), save8=save8)
             y = linear(o.reshape(T, -1), layer.w_out)
         return norm_gate(y, self.norm, residual=h, save8=save8)[0]
@@ -201,7 +219,9 @@ def main(argv=None) -> None:
     x, t = (torch.randn(256, train.cfg.hidden, generator=gen).to(train.device, BF) for _ in range(2))
     print("training, mean square difference:", " ".join(f"{train.train_step(x, t, 0.5):.4f}" for _ in range(5)))
     lens = [100, 1, 155]
-    print("packed sequences, inputs kept in 8 bits:", " ".join(f"{train.train_step(x, t, 0.5, lens, True):.4f}" for _ in range(5)))
+    print("packed sequences:", " ".join(f"{train.train_step(x, t, 0.5, lens):.4f}" for _ in range(5)))
+    print("inputs kept in 8 bits:", " ".join(f"{train.train_step(x, t, 0.5, lens, True):.4f}" for _ in range(5)))
+    print("status", int(train.status))
 
 
 if __name__ == "__main__":

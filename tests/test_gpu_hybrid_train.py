@@ -105,3 +105,68 @@ def test_packed_sequences_are_those_alone():
         for a, b in zip(packed, x.split(lens)):
             alone = stack.forward(b)
             assert float((a.float() - alone.float()).norm() / alone.float().norm()) < 0.01
+
+
+def _one_sequence(stack, x):
+    """The stack on one sequence with fp32 attention from elementary operations, as it is without lengths."""
+    from gated_deltanet_chunked_chunk_gb300 import norm_gate, rotary_embedding
+    cfg, T = stack.cfg, x.shape[0]
+    positions = torch.arange(T, dtype=torch.int32, device=x.device)
+    h, y = x, None
+    for layer in stack.layers:
+        n, h = (norm_gate(h, layer.norm)[0], h) if y is None else norm_gate(y, layer.norm, residual=h)
+        q, k, v = (n @ layer.w_in.T).view(T, -1, cfg.D).split([cfg.HQ, cfg.HK, cfg.HK], dim=1)
+        q, k = rotary_embedding(q, k, positions, stack.inv_freq, attention_factor=stack.rope_factor)
+        k, v = (t.repeat_interleave(cfg.HQ // cfg.HK, dim=1).transpose(0, 1).float() for t in (k, v))
+        s = q.transpose(0, 1).float() @ k.transpose(1, 2) / math.sqrt(cfg.D)
+        s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device=x.device).triu(1), -math.inf)
+        y = (s.softmax(-1) @ v).transpose(0, 1).to(BF).reshape(T, -1) @ layer.w_out.T
+    return norm_gate(y, stack.norm, residual=h)[0]
+
+
+@pytest.mark.parametrize("D,rotary", [(128, 64), (64, 64), (32, 32), (96, 64), (256, 64)])
+def test_one_sequence_has_fp32_attention(D, rotary):
+    """Without lengths the attention's logits, weights and their gradients stay in fp32, for heads of any size: the very
+    results of the elementary operations."""
+    from gated_deltanet_chunked_chunk_gb300.hybrid import Config, HybridStack
+    gen = torch.Generator().manual_seed(13)
+    x, up = (torch.randn(150, 512, generator=gen).to("cuda", BF) for _ in range(2))
+    stack = HybridStack(Config(layers="aa", D=D, rotary=rotary), requests=1, seed=6)
+    params = [p.requires_grad_(True) for p in stack.parameters()]
+    got, want = (f(x) for f in (stack.forward, lambda t: _one_sequence(stack, t)))
+    assert torch.equal(got, want)
+    for a, b in zip(torch.autograd.grad(got, params, up), torch.autograd.grad(want, params, up)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("save8", [False, True])
+def test_packed_sequences_with_other_heads(save8):
+    """Heads that the kernels do not take: each sequence as it is alone, but for the batch's shape in matrix products (1 %)."""
+    from gated_deltanet_chunked_chunk_gb300.hybrid import Config, HybridStack
+    lens = [70, 1, 79]
+    gen = torch.Generator().manual_seed(14)
+    x = torch.randn(sum(lens), 512, generator=gen).to("cuda", BF)
+    stack = HybridStack(Config(layers="ga", D=32, rotary=32), requests=1, seed=6)
+    with torch.no_grad():
+        for a, b in zip(stack.forward(x, lens, save8).split(lens), x.split(lens)):
+            alone = stack.forward(b)
+            assert float((a.float() - alone.float()).norm() / alone.float().norm()) < 0.01
+
+
+def test_forward_of_one_sequence_is_captured():
+    """Nothing of it comes from the host."""
+    from gated_deltanet_chunked_chunk_gb300.hybrid import HybridStack
+    gen = torch.Generator().manual_seed(15)
+    x = torch.randn(130, 512, generator=gen).to("cuda", BF)
+    stack = HybridStack(requests=1, seed=7)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.no_grad():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            want = stack.forward(x)
+        torch.cuda.current_stream().wait_stream(side)
+        with torch.cuda.graph(graph):
+            out = stack.forward(x)
+        out.zero_()
+        graph.replay()
+    assert torch.equal(out, want)
