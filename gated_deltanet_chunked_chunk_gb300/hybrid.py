@@ -157,6 +157,9 @@ class HybridStack:
         if lens is None:
             cu, num_seqs, positions = None, None, torch.arange(T, dtype=torch.int32, device=x.device)
         else:
+            lens = [int(m) for m in lens]
+            if not lens or min(lens) < 0 or sum(lens) != T:
+                raise ValueError(f"HybridStack: lens must be lengths that add up to x's {T} tokens, got {lens}")
             cu, num_seqs = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(x.device), len(lens)
             positions = torch.cat([torch.arange(m, dtype=torch.int32) for m in lens]).to(x.device)
         linear = linear8 if save8 else lambda x, w: x @ w.T

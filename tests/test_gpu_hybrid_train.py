@@ -170,3 +170,14 @@ def test_forward_of_one_sequence_is_captured():
         out.zero_()
         graph.replay()
     assert torch.equal(out, want)
+
+
+def test_lengths_that_are_not_those_of_the_tokens():
+    from gated_deltanet_chunked_chunk_gb300.hybrid import Config, HybridStack
+    stack = HybridStack(Config(layers="g"), requests=1, seed=8)
+    x = torch.zeros(10, 512, dtype=BF, device="cuda")
+    for lens in ([], [4], [4, 7], [12, -2], [11, 0]):
+        with pytest.raises(ValueError, match="lens"):
+            stack.forward(x, lens)
+    with torch.no_grad():
+        assert torch.equal(stack.forward(x, (4, 0, 6)), stack.forward(x, [4, 0, 6]))
