@@ -129,10 +129,24 @@ def _gradient(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _on_boundary(t, strides=False):
+    """An input as the kernels with codes take it: from a 16-byte boundary on and, with ``strides``, in steps of 8 elements."""
+    if not torch.is_tensor(t) or (t.data_ptr() % 16 == 0 and not (strides and any(s % 8 for s in t.stride()[:-1]))):
+        return t
+    return t.clone(memory_format=torch.contiguous_format) if t.is_contiguous() else t.contiguous() if strides else t
+
+
 class _NormGate8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, z, activation, eps, res_scale):
-        y, h, *codes = gdn_norm_gate_save8(x, weight, residual=residual, z=z, activation=activation, eps=eps, res_scale=res_scale)
+        args = dict(activation=activation, eps=eps, res_scale=res_scale)
+        ctx.fused = not torch.is_tensor(x) or (x.dim() > 0 and x.shape[-1] % 8 == 0 and x.shape[-1] <= 16384)
+        if ctx.fused:
+            y, h, *codes = gdn_norm_gate_save8(_on_boundary(x), weight, residual=_on_boundary(residual), z=_on_boundary(z, True), **args)
+        else:  # a width that only gdn_norm_gate takes
+            y, h = gdn_norm_gate(x, weight, residual=residual, z=z, **args)
+            save = (_c or _load()).act8_save
+            codes = save(x if h is None else h, None, None) + ((None, None) if z is None else save(z, None, None))
         ctx.save_for_backward(weight, *codes)
         ctx.args = (activation, eps, 1.0 if residual is None else res_scale, residual is not None)
         return y if h is None else (y, h)
@@ -145,14 +159,20 @@ class _NormGate8(torch.autograd.Function):
         dy = _gradient(dy)
         if has_res:
             dh = torch.zeros_like(dy) if dh is None else _gradient(dh)
-        dx, dres, dz, dw = gdn_norm_gate_bwd8(dy, h8, hs, weight, z_codes=z8, z_scale=zs, dh=dh if has_res else None,
-                                              activation=activation, eps=eps, res_scale=res_scale)
+        args = dict(dh=dh if has_res else None, activation=activation, eps=eps, res_scale=res_scale)
+        if ctx.fused:
+            dx, dres, dz, dw = gdn_norm_gate_bwd8(dy, h8, hs, weight, z_codes=z8, z_scale=zs, **args)
+        else:
+            load = (_c or _load()).act8_load
+            dx, dres, dz, dw = gdn_norm_gate_bwd(dy, load(h8, hs, None), weight, z=None if z8 is None else load(z8, zs, None), **args)
         return dx, dw, dres, dz, None, None, None
 
 
 def norm_gate(x, weight, residual=None, z=None, activation="silu", eps: float = 1e-6, res_scale: float = 1.0, save8: bool = False):
     """Differentiable (once) gdn_norm_gate: returns (y, h), h None without a residual; gradients for x, weight, residual, z.
-    With ``save8`` the forward keeps 8-bit codes of h and z for the gradient instead of the tensors themselves."""
+    With ``save8`` the forward keeps 8-bit codes of h and z for the gradient instead of the tensors themselves: in the same pass
+    for widths that are a multiple of 8 and at most 16384 (inputs that do not lie as gdn_norm_gate_save8 wants are copied), in
+    passes of their own for others."""
     out = (_NormGate8 if save8 else _NormGate).apply(x, weight, residual, z, activation, eps, res_scale)
     return out if isinstance(out, tuple) else (out, None)
 

@@ -672,3 +672,56 @@ def test_autograd_reports_bad_offsets():
     st.zero_()
     torch.autograd.grad(gdn.attention(*leaves, cu_seqlens=U.offsets([100, 200]).cuda(), dev_status=st), leaves, do)
     assert int(st) == 0
+
+
+def _odd(t):
+    """The same values two bytes past a boundary."""
+    o = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view(t.shape)
+    return o.copy_(t)
+
+
+@pytest.mark.parametrize("kind,res", [("silu", True), (None, False), ("sigmoid", False)])
+@pytest.mark.parametrize("layout", ["odd", "stride", "both"])
+def test_norm_with_codes_of_inputs_that_lie_anywhere(kind, res, layout):
+    """What norm_gate takes without codes it takes with them: the same results as of aligned copies."""
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(8)
+    x, r, z, dy, dh = (torch.randn(37, 4, 96, generator=g).to(BF).cuda() for _ in range(5))
+    w = (1 + 0.1 * torch.randn(96, generator=g)).cuda()
+    args = dict(activation=kind or "silu", res_scale=0.5 if res else 1.0)
+
+    def run(x, r, z, save8=True):
+        leaves = [x.detach().requires_grad_(), w.detach().requires_grad_()] + [t.detach().requires_grad_() for t, on in ((r, res), (z, kind)) if on]
+        y, h = gdn.norm_gate(leaves[0], leaves[1], residual=leaves[2] if res else None, z=leaves[-1] if kind else None, save8=save8, **args)
+        grads = torch.autograd.grad((y, h) if res else y, leaves, (dy, dh) if res else dy)
+        return [y.detach(), *grads] + ([h.detach()] if res else [])
+
+    want = run(x, r, z)
+    if layout != "stride":
+        x, r = _odd(x), _odd(r)
+    if layout != "odd":  # rows of 4 x 96 + 4
+        wide = torch.zeros(37, 4 * 96 + 4, dtype=BF, device="cuda")
+        z = wide[:, 4 if layout == "both" else 0:][:, :4 * 96].unflatten(1, (4, 96)).copy_(z)
+    else:
+        z = _odd(z)
+    assert all(torch.equal(a, b) for a, b in zip(run(x, r, z), want))
+    assert torch.equal(run(x, r, z, False)[0], want[0])
+
+
+@pytest.mark.parametrize("D", [1, 100, 130, 16392])
+@pytest.mark.parametrize("kind,res", [("silu", True), (None, False)])
+def test_norm_with_codes_of_any_width(D, kind, res):
+    """Widths that only the norm without codes takes: its results, and its gradients at the values of the codes."""
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(D)
+    x, r, z, dy, dh = (torch.randn(5, 2, D, generator=g).to(BF).cuda() for _ in range(5))
+    w = (1 + 0.1 * torch.randn(D, generator=g)).cuda()
+    leaves = [t.requires_grad_() for t in (x, w, *([r] if res else []), *([z] if kind else []))]
+    args = dict(residual=r if res else None, z=z if kind else None)
+    y, h = gdn.norm_gate(x, w, save8=True, **args)
+    want, stream = gdn.gdn_norm_gate(x.detach(), w.detach(), **{n: None if t is None else t.detach() for n, t in args.items()})
+    assert torch.equal(y, want) and (h is None if not res else torch.equal(h, stream))
+    values = lambda t: gdn.gdn_act8_load(*gdn.gdn_act8_save(t.detach()))  # noqa: E731
+    dx, dres, dz, dw = gdn.gdn_norm_gate_bwd(dy, values(h if res else x), w.detach(), z=values(z) if kind else None, dh=dh if res else None)
+    got = torch.autograd.grad((y, h) if res else y, leaves, (dy, dh) if res else dy)
+    assert all(torch.equal(a, b) for a, b in zip(got, [dx, dw] + ([dres] if res else []) + ([dz] if kind else [])))
