@@ -33,8 +33,12 @@ def gdn_act8_load(codes: torch.Tensor, scale: torch.Tensor, out: Optional[torch.
 class _Linear8(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight):
-        ctx.save_for_backward(weight, *(gdn_act8_save(x) if ctx.needs_input_grad[1] else ()))
-        return x @ weight.T
+        y, kept = x @ weight.T, ()
+        if ctx.needs_input_grad[1]:
+            rows = x.reshape(-1, x.shape[-1])  # (a copy where they have no single stride)
+            kept = gdn_act8_save(rows if rows.stride(1) == 1 else rows.contiguous())
+        ctx.save_for_backward(weight, *kept)
+        return y
 
     @staticmethod
     @once_differentiable
@@ -46,8 +50,8 @@ class _Linear8(torch.autograd.Function):
 
 
 def linear8(x: torch.Tensor, weight: torch.Tensor) -> torch.Tensor:
-    """x @ weight.T (x bf16 [..., in], weight bf16 [out, in]), differentiable once, that keeps x in 8 bits for the weight's
-    gradient."""
+    """x @ weight.T (x bf16 [..., in] of any strides, weight bf16 [out, in]), differentiable once, that keeps x in 8 bits for
+    the weight's gradient."""
     return _Linear8.apply(x, weight)
 
 

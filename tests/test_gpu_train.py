@@ -725,3 +725,19 @@ def test_norm_with_codes_of_any_width(D, kind, res):
     dx, dres, dz, dw = gdn.gdn_norm_gate_bwd(dy, values(h if res else x), w.detach(), z=values(z) if kind else None, dh=dh if res else None)
     got = torch.autograd.grad((y, h) if res else y, leaves, (dy, dh) if res else dy)
     assert all(torch.equal(a, b) for a, b in zip(got, [dx, dw] + ([dres] if res else []) + ([dz] if kind else [])))
+
+
+def test_linear8_of_any_strides():
+    gdn = _gdn()
+    g = torch.Generator().manual_seed(9)
+    w = torch.randn(40, 96, generator=g).to(BF).cuda().requires_grad_()
+    base = torch.randn(6, 7, 96, generator=g).to(BF).cuda()
+    for x in (base.transpose(0, 1), base.transpose(1, 2).contiguous().transpose(1, 2), _odd(base), base[0].T.contiguous().T, base[0, 0],
+              base[:, :1].expand(6, 7, 96), base[:0]):
+        x = x.detach().requires_grad_()
+        y = gdn.linear8(x, w)
+        dy = torch.randn(y.shape, generator=g).to(BF).cuda()
+        dx, dw = torch.autograd.grad(y, (x, w), dy)
+        rows, d = x.detach().reshape(-1, 96).contiguous(), dy.reshape(-1, 40)
+        assert torch.equal(y, x @ w.T) and dx.shape == x.shape and torch.equal(dx, dy @ w.detach())
+        assert torch.equal(dw, d.T @ gdn.gdn_act8_load(*gdn.gdn_act8_save(rows)))
