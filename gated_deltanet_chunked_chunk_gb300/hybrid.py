@@ -162,7 +162,8 @@ class HybridStack:
                 raise ValueError(f"HybridStack: lens must be lengths that add up to x's {T} tokens, got {lens}")
             cu, num_seqs = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0, dtype=torch.int32).to(x.device), len(lens)
             positions = torch.cat([torch.arange(m, dtype=torch.int32) for m in lens]).to(x.device)
-        linear = linear8 if save8 else lambda x, w: x @ w.T
+        plain = lambda x, w: x @ w.T  # noqa: E731
+        linear = linear8 if save8 else plain
         h, y = x, None
         for layer in self.layers:
             if y is None:
@@ -174,6 +175,8 @@ class HybridStack:
                 q, k, v = u.view(T, -1, cfg.D).split([cfg.HQ, cfg.HK, cfg.HK], dim=1)
                 q, k = rotary_embedding(q, k, positions, self.inv_freq, attention_factor=self.rope_factor)
                 if kernels:
+                    if save8:  # it keeps v, and with a view of the projection all of that
+                        v = v.contiguous()
                     o = attention(q, k, v, cu_seqlens=cu, dev_status=self.status)
                 elif lens is None:
                     o = self._plain_attention(q, k, v)
@@ -186,7 +189,8 @@ class HybridStack:
                 o, _ = chunk_gated_delta_rule(q, k, v, g.view(1, T, -1), b.float().sigmoid().view(1, T, -1), output_final_state=False,
                                               cu_seqlens=cu, num_seqs=num_seqs)
                 o, _ = norm_gate(o.view(T, cfg.HV, cfg.K), layer.out_norm, z=z.unflatten(1, (cfg.HV, cfg.K)), save8=save8)
-            y = linear(o.reshape(T, -1), layer.w_out)
+            # (the attention keeps o itself, which a plain product shares)
+            y = (plain if layer.kind == "a" and kernels else linear)(o.reshape(T, -1), layer.w_out)
         return norm_gate(y, self.norm, residual=h, save8=save8)[0]
 
     def train_step(self, x: torch.Tensor, target: torch.Tensor, rate: float = 1e-2, lens: Optional[List[int]] = None,

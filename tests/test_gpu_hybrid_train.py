@@ -181,3 +181,40 @@ def test_lengths_that_are_not_those_of_the_tokens():
             stack.forward(x, lens)
     with torch.no_grad():
         assert torch.equal(stack.forward(x, (4, 0, 6)), stack.forward(x, [4, 0, 6]))
+
+
+def _kept(stack, T, save8):
+    """Bytes of all storages that the graph of a forward keeps."""
+    held = {}
+
+    def pack(t):
+        held[t.untyped_storage().data_ptr()] = t.untyped_storage().nbytes()
+        return t
+
+    for p in stack.parameters():
+        p.requires_grad_(True)
+    x = torch.randn(T, 512, generator=torch.Generator().manual_seed(16)).to("cuda", BF)
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        out = stack.forward(x, [T], save8)
+    total = sum(held.values())
+    del out
+    return total
+
+
+@pytest.mark.parametrize("layers,bf16,save8", [
+    # bf16: the stream twice, the input, the projection, rotated q and k, o and lse; save8: three codes, q, k, v, o and lse
+    ("a", 2 * 1024 + 1024 + 3072 + 2560 + 2048 + 32, 3 * 528 + 3072 + 2048 + 32),
+    # bf16: the stream twice, the input, the projection (for z), q, k, v, the recurrence's output, the normed one; save8:
+    # three codes of the stream and the input, q, k, v, three codes of 8 heads of 128 (o, z and the projection's input);
+    # both: gates in fp32
+    ("g", 2 * 1024 + 1024 + 6176 + 4096 + 2048 + 2048, 3 * 528 + 4096 + 3 * 1056),
+])
+def test_bytes_that_a_step_keeps(layers, bf16, save8):
+    """What save8 is for: bytes a token that the forward keeps for the gradients (positions, and the few numbers of the
+    gates' formulas, 8 of 4 bytes each a head, come on top)."""
+    from gated_deltanet_chunked_chunk_gb300.hybrid import Config, HybridStack
+    stack = HybridStack(Config(layers=layers), requests=1, seed=9)
+    few = 8 + (0 if layers == "a" else 8 * 4 * 8)
+    for on, want in ((False, bf16), (True, save8)):
+        got = (_kept(stack, 768, on) - _kept(stack, 256, on)) / 512
+        assert want <= got <= want + few, (on, got, want)
