@@ -35,15 +35,20 @@ __device__ __forceinline__ int lds_i(uint32_t at) {
 __device__ __forceinline__ float lds_f(uint32_t at) { return __int_as_float(lds_i(at)); }
 __device__ __forceinline__ void sts_i(uint32_t at, int x) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(x) : "memory"); }
 __device__ __forceinline__ void sts_f(uint32_t at, float x) { sts_i(at, __float_as_int(x)); }
+// What a wait may take that lasts as long as an item: its walk is the rows of a group's heads
+// or the keys of one, of which 280 GB hold 10^9 at most (D = 64), 8 million tiles at some 1800
+// cycles: 1.5e10.
+constexpr long long kItemLimit = 16 * gdnc::kWaitLimit;
 // Waits for a barrier's phase; gives up after the limit or once another warp has, which
 // the word at `failed` in shared memory says.  (Shared memory by 32-bit addresses: the
 // loops need the registers.)
+template <long long LIMIT = gdnc::kWaitLimit>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t failed, int32_t *status) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long from = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (lds_i(failed)) return false;
-    if (clock64() - from > gdnc::kWaitLimit) {
+    if (clock64() - from > LIMIT) {
       sts_i(failed, 1);
       set_status(status, GDN_DEV_WAIT_TIMEOUT);
       return false;

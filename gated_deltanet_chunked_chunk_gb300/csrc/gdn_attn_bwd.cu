@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kS = 0, kP = 128, kV = 256, kK = 256 + D;  // columns of S^T, dP^T, dV, dK
   auto item = [&](int it, uint32_t &w) {
     w = sb + Ly::OFF_WORK + it % kItems * K_BYTES;
-    return wait_bar(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
+    return wait_bar<kItemLimit>(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
   };
   auto item_read = [&](int it) {
     __syncwarp();
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0;; ++it) {
         Found f;
         // taken when the one before is about to end, which leaves time for its copies
-        if (it > 0 && !__all_sync(0xffffffffu, wait_bar(NEAR, (it - 1) & 1, failed, a.dev_status))) break;
+        if (it > 0 && !__all_sync(0xffffffffu, wait_bar<kItemLimit>(NEAR, (it - 1) & 1, failed, a.dev_status))) break;
         const bool on = walk_to(a, w, kTile, true, true, most, take_item(&a.shared->next_kv), f, [&](int tile) {
           const int tn = tiles_in(w.rows.count, kTile);
           return a.HK * pieces_for(a, a.G * (tn - first_seen_by(a, tn, w.rows.count, w.keys.count, tile * kTile)), cut);
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int64_t all = (int64_t)a.G * nt;
         const int piece = f.in % pieces;
-        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
+        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar<kItemLimit>(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
         if (lane == 0) {
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * K_BYTES;
           sts_i(work + K_ON, on);
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kS = 0, kP = 128, kA = 256, kO = 384, kG = 448;  // columns of S, dP, dQ, dO, dS
   auto item = [&](int it, uint32_t &w) {
     w = sb + Ly::OFF_WORK + it % kItems * Q_BYTES;
-    return wait_bar(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
+    return wait_bar<kItemLimit>(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
   };
   auto item_read = [&](int it) {
     __syncwarp();
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0;; ++it) {
         Found f;
         const bool on = walk_to(a, w, kTile, false, false, most, take_item(&a.shared->next_q), f, [&](int) { return a.HQ; });
-        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
+        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar<kItemLimit>(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
         if (lane == 0) {
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * Q_BYTES;
           sts_i(work + Q_ON, on);

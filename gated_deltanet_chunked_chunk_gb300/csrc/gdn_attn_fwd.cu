@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Waits for the it-th item; its place is given back, after its last use, by item_read.
   auto item = [&](int it, uint32_t &w) {
     w = sb + Ly::OFF_WORK + it % kItems * W_BYTES;
-    return wait_bar(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
+    return wait_bar<kItemLimit>(WF(it % kItems), (it / kItems) & 1, failed, a.dev_status);
   };
   auto item_read = [&](int it) {
     __syncwarp();
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!lds_i(work + W_ON)) break;
       float m_ref = -INFINITY, l_sum = 0.f;
       for (int j = 0; j < lds_i(work + W_TILES + 4 * w); ++j) {
-        if (ok) ok = wait_bar(SF(w), phases & 1, failed, a.dev_status);
+        // (an item before, which this tile has no rows of, may be under way)
+        if (ok) ok = wait_bar<kItemLimit>(SF(w), phases & 1, failed, a.dev_status);
         phases ^= 1;
         tc_fence_after();
         uint32_t s[64];
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0;; ++it) {
         Found f;
         const bool on = walk_to(a, walk, R, false, false, most, turn_item(it), f, [&](int) { return a.HQ; });
-        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
+        if (it >= kItems && !__all_sync(0xffffffffu, wait_bar<kItemLimit>(WE(it % kItems), (it / kItems - 1) & 1, failed, a.dev_status))) break;
         if (lane == 0) {
           const uint32_t work = sb + Ly::OFF_WORK + it % kItems * W_BYTES;
           sts_i(work + W_ON, on);

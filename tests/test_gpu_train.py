@@ -741,3 +741,18 @@ def test_linear8_of_any_strides():
         rows, d = x.detach().reshape(-1, 96).contiguous(), dy.reshape(-1, 40)
         assert torch.equal(y, x @ w.T) and dx.shape == x.shape and torch.equal(dx, dy @ w.detach())
         assert torch.equal(dw, d.T @ gdn.gdn_act8_load(*gdn.gdn_act8_save(rows)))
+
+
+def test_walks_of_more_than_a_second():
+    """304 key tiles, one kv head, 1024 query heads: a walk has 2 million steps of 128 rows, whose 128 x 128 exponentials
+    take 1024 cycles a step at least (16 a cycle), so 2.1e9 cycles: no wait takes that for a partner that is gone."""
+    gdn = _gdn()
+    T, HQ, keys, D = 1984 * 128, 1024, 304 * 128, 64
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = torch.zeros(T, HQ, D, dtype=BF, device="cuda")  # o and its gradient too
+    k, v = (torch.ones(keys, 1, D, dtype=BF, device="cuda") for _ in range(2))
+    status = ints(0)
+    dq, dk, dv = gdn.gdn_attention_bwd(q, q, k, v, q, torch.zeros(T, HQ, device="cuda"), cu_seqlens=ints(0, T),
+                                       cu_seqlens_k=ints(0, keys), causal=False, dev_status=status)
+    assert int(status) == 0
+    assert not dk.any() and not dv.any() and all(not t.any() for t in dq.split(4096))
