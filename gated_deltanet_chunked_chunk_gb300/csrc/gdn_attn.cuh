@@ -141,6 +141,7 @@ struct Walk {
   int64_t base;             // index of the level's first item
   Run rows, keys;
   int tiles;                // this lane's sequence's
+  int rows_end, keys_end;   // of all sequences before the chunk
 };
 struct Found {
   int n;           // sequence
@@ -156,7 +157,26 @@ __device__ __forceinline__ void walk_chunk(const Args &a, Walk &w, int R, bool b
   w.rows = Run{0, 0};
   w.keys = Run{0, 0};
   w.tiles = 0;
-  const bool ok = n <= a.N && run_of(rows_of(a), n, w.rows) && run_of(keys_of(a), n, w.keys);
+  bool ok = n <= a.N && run_of(rows_of(a), n, w.rows) && run_of(keys_of(a), n, w.keys);
+  // One that begins before the end of an earlier one (offsets that decrease somewhere) is left
+  // out: no row comes twice, however bad the offsets are.
+  int rows_end = ok ? w.rows.first + w.rows.count : 0, keys_end = ok ? w.keys.first + w.keys.count : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, rows_end, o), y = __shfl_up_sync(0xffffffffu, keys_end, o);
+    if (lane >= o) {
+      rows_end = max(rows_end, x);
+      keys_end = max(keys_end, y);
+    }
+  }
+  rows_end = max(rows_end, w.rows_end);
+  keys_end = max(keys_end, w.keys_end);
+  int rows_from = __shfl_up_sync(0xffffffffu, rows_end, 1), keys_from = __shfl_up_sync(0xffffffffu, keys_end, 1);
+  if (lane == 0) {
+    rows_from = w.rows_end;
+    keys_from = w.keys_end;
+  }
+  ok = ok && w.rows.first >= rows_from && w.keys.first >= keys_from;
   if (ok && n == a.N) (by_keys ? w.rows : w.keys).count = 0;
   int64_t upto = ok ? (by_keys ? w.rows : w.keys).count : 0;
 #pragma unroll
@@ -166,11 +186,15 @@ __device__ __forceinline__ void walk_chunk(const Args &a, Walk &w, int R, bool b
   }
   w.count = max(1, __popc(__ballot_sync(0xffffffffu, upto <= most)));
   if (ok && lane < w.count) w.tiles = tiles_in((by_keys ? w.keys : w.rows).count, R);
+  w.rows_end = __shfl_sync(0xffffffffu, rows_end, w.count - 1);
+  w.keys_end = __shfl_sync(0xffffffffu, keys_end, w.count - 1);
   w.level = (int)__reduce_max_sync(0xffffffffu, (unsigned)w.tiles) - 1;
 }
 __device__ __forceinline__ void walk_begin(const Args &a, Walk &w, int R, bool by_keys, int64_t most) {
   w.chunk = 0;
   w.base = 0;
+  w.rows_end = 0;
+  w.keys_end = 0;
   walk_chunk(a, w, R, by_keys, most);
 }
 // Item `index` (not below the one before); false: there are no more.  `first_most`: the

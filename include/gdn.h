@@ -734,7 +734,8 @@ int gdn_norm_gate_bwd8(const uint16_t *dy, const uint8_t *h_codes, const float *
  *   scale         : <= 0 or NaN selects 1/sqrt(D)
  *   o             : bf16 [Tq, HQ, D];  lse: fp32 [Tq, HQ]
  * Rows behind the last sequence see nothing.  Offsets that break the rules set
- * GDN_DEV_BAD_CU_SEQLENS and the sequence is skipped (its rows are not written).
+ * GDN_DEV_BAD_CU_SEQLENS and the sequence is skipped (its rows are not written), as
+ * is one that begins before the end of an earlier one.
  * What other sequences hold, NaN and infinities among it, does not reach a
  * sequence; one of its own keys or values that is not finite may reach all of its
  * rows.  D 64 or 128 (else GDN_EUNSUPPORTED, as for N or HQ > 65535); HQ % HK
@@ -761,7 +762,8 @@ size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, i
  *                   what the forward returned
  *   dq            : bf16 [Tq, HQ, D];  dk, dv: bf16 [Tk, HK, D], dense
  *   workspace     : gdn_attention_bwd_workspace_size() bytes, 16-byte aligned
- * Everything else as in gdn_attention_fwd; rows and keys behind the last sequence
+ * Everything else as in gdn_attention_fwd (where offsets decrease somewhere, the
+ * gradients of the whole call are unspecified); rows and keys behind the last sequence
  * have zero gradients.  P is off by some 2^-23 |lse| of itself, as lse is one fp32
  * number: 2^-8, as by its rounding to bf16, at |lse| = 2^15, a factor of e
  * at 2^23, and from 2^30 on it may be infinite.  P and dS enter the products in bf16, sums are fp32 and have a

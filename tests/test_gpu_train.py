@@ -756,3 +756,21 @@ def test_walks_of_more_than_a_second():
                                        cu_seqlens_k=ints(0, keys), causal=False, dev_status=status)
     assert int(status) == 0
     assert not dk.any() and not dv.any() and all(not t.any() for t in dq.split(4096))
+
+
+def test_sequences_that_overlap_are_left_out():
+    """Offsets that go back and forth: of the sequences that name the same rows the first has them, and the call does no
+    more work than the rows are, in every chunk of 32 sequences."""
+    gdn = _gdn()
+    T = 300
+    q, k, v, do = (t.cuda() for t in _inputs([T], [2 * T], 2, 1, 64, 10))
+    for N in (3, 501):
+        cu = torch.tensor([0, T] * (N // 2 + 1), dtype=torch.int32, device="cuda")
+        cu_k = torch.tensor([0, T] + [T, 2 * T] * (N // 2), dtype=torch.int32, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o, lse = gdn.gdn_attention_fwd(q, k, v, cu_seqlens=cu, cu_seqlens_k=cu_k, causal=False, dev_status=st)
+        assert int(st) == gdn.DEV_BAD_CU_SEQLENS
+        assert _same_bits((o, lse), gdn.gdn_attention_fwd(q, k[:T], v[:T], causal=False))
+        st.zero_()
+        gdn.gdn_attention_bwd(do, q, k, v, o, lse, cu_seqlens=cu, cu_seqlens_k=cu_k, causal=False, dev_status=st)
+        assert int(st) == gdn.DEV_BAD_CU_SEQLENS
