@@ -774,3 +774,52 @@ def test_sequences_that_overlap_are_left_out():
         st.zero_()
         gdn.gdn_attention_bwd(do, q, k, v, o, lse, cu_seqlens=cu, cu_seqlens_k=cu_k, causal=False, dev_status=st)
         assert int(st) == gdn.DEV_BAD_CU_SEQLENS
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_as_many_sequences_as_there_may_be(causal):
+    g = torch.Generator().manual_seed(12)
+    full = torch.randperm(65535, generator=g)[:60].tolist() + [65534]
+    lens, lens_k = [0] * 65535, [0] * 65535
+    for n, m, d in zip(full, torch.randint(1, 160, (61,), generator=g).tolist(), torch.randint(-30, 60, (61,), generator=g).tolist()):
+        lens[n], lens_k[n] = m, max(0, m + d)
+    _run(lens, None, 2, 1, 128, causal, 13)
+    _run(lens, lens_k, 2, 2, 64, causal, 14)
+
+
+@pytest.mark.parametrize("HK", [15, 1])
+def test_as_many_heads_as_there_may_be(HK):
+    """65535 query heads, against 64 bits for all of them at once, on the GPU."""
+    gdn = _gdn()
+    T, HQ, D = 5, 65535, 64
+    q, k, v, do = (t.cuda() for t in _inputs([T], None, HQ, HK, D, 17))
+    o, lse, *grads = _all(q, k, v, do)
+    r, scale = {}, D ** -0.5
+    q, do = (t.double().view(T, HK, HQ // HK, D) for t in (q, do))
+    k, v = k.double(), v.double()
+    hidden = torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1)
+
+    def pairs(a, b):
+        return torch.einsum("ihgd,jhd->hgij", a, b)
+
+    def to_rows(p, b):
+        return torch.einsum("hgij,jhd->ihgd", p, b)
+
+    def to_keys(p, a):
+        return torch.einsum("hgij,ihgd->jhd", p, a)
+
+    s = (pairs(q, k) * scale).masked_fill(hidden, -math.inf)
+    size = 1 + (pairs(q.abs(), k.abs()) * scale).masked_fill(hidden, 0).amax(-1, keepdim=True)
+    p = s.softmax(-1)
+    r["o"], r["o_mag"], r["lse"], r["lse_mag"] = to_rows(p, v), to_rows(p, v.abs()), s.logsumexp(-1), size[..., 0]
+    delta = (do * r["o"]).sum(-1).permute(1, 2, 0)[..., None]
+    terms = (do * r["o"]).abs().sum(-1).permute(1, 2, 0)[..., None]
+    ds, mag = p * (pairs(do, v) - delta), p * (pairs(do.abs(), v.abs()) + terms) * size
+    for n, ways in (("", (scale * ds, p)), ("_round", (scale * ds.abs(), p)), ("_fp32", (scale * mag, p * size)), ("_delta", (scale * p * terms, p))):
+        f = (lambda t: t) if n == "" else torch.abs
+        r["dq" + n], r["dk" + n], r["dv" + n] = to_rows(ways[0], f(k)), to_keys(ways[0], f(q)), to_keys(ways[1], f(do))
+    rows = lambda t: t.reshape(T, HQ, D).cpu()  # noqa: E731
+    heads = lambda t: t.permute(2, 0, 1).reshape(T, HQ).cpu()  # noqa: E731
+    r = {n: heads(t) if n.startswith("lse") else rows(t) if n[0] == "o" or n.startswith("dq") else t.cpu() for n, t in r.items()}
+    _check_fwd(o, lse, r)
+    _check_bwd(grads, r)
