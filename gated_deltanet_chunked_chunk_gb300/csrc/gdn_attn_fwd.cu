@@ -47,11 +47,11 @@ constexpr float kFar = 1073741824.f;  // 2^30
 constexpr int kItems = 4;  // items between the warp that finds them and the others
 
 // An item, 32-bit words in shared memory: first row of q and of k of the sequence, its
-// keys; the item's first row in the sequence; keys - rows; rows and key tiles of both row
-// tiles; the head; whether it is one (0: there are no more); what the first row of both row
-// tiles sees last.  (What the softmax's loop rarely needs it reads there: the logits take
+// keys; the item's first row in the sequence; rows and key tiles of both row tiles; the
+// head; whether it is one (0: there are no more); what the first row of both row tiles sees
+// last.  (What the softmax's loop rarely needs it reads there: the logits take
 // the registers.)
-enum Word { W_Q = 0, W_K = 4, W_KEYS = 8, W_ROW0 = 12, W_PAST = 16, W_COUNT = 20, W_TILES = 28, W_HEAD = 36, W_ON = 40, W_LOW = 44, W_BYTES = 64 };
+enum Word { W_Q = 0, W_K = 4, W_KEYS = 8, W_ROW0 = 12, W_COUNT = 16, W_TILES = 24, W_HEAD = 32, W_ON = 36, W_LOW = 40, W_BYTES = 48 };
 
 template <int D> struct Lay {
   static constexpr int TB = tile_bytes<D>();
@@ -315,7 +315,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             sts_i(work + W_K, f.keys.first);
             sts_i(work + W_KEYS, f.keys.count);
             sts_i(work + W_ROW0, row0);
-            sts_i(work + W_PAST, past);
             sts_i(work + W_HEAD, f.in);
             for (int w = 0; w < 2; ++w) {
               const int count = w < tiles_an_item ? max(0, min(kTile, f.rows.count - row0 - w * kTile)) : 0;
