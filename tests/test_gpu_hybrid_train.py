@@ -203,7 +203,7 @@ def _kept(stack, T, save8):
 
 @pytest.mark.parametrize("layers,bf16,save8", [
     # bf16: the stream twice, the input, the projection, rotated q and k, o and lse; save8: three codes, q, k, v, o and lse
-    ("a", 2 * 1024 + 1024 + 3072 + 2560 + 2048 + 32, 3 * 528 + 3072 + 2048 + 32),
+    ("a", 2 * 1024 + 1024 + 12 * 256 + 2560 + 2048 + 32, 3 * 528 + 12 * 256 + 2048 + 32),
     # bf16: the stream twice, the input, the projection (for z), q, k, v, the recurrence's output, the normed one; save8:
     # three codes of the stream and the input, q, k, v, three codes of 8 heads of 128 (o, z and the projection's input);
     # both: gates in fp32
