@@ -5,9 +5,11 @@
 //   dQ = scale dS K,  dK = scale dS^T Q
 //
 // Five products, 10 D operations a (row, key, head); bound: the tensor cores, which
-// execute seven.  24 packed sequences of 200 to 2000 rows, 32 heads: 977 us (a pass over
-// the rows 71, dK and dV 510, dQ 400).  8192 rows of one sequence: 1210 to 1240 us,
-// 1.1 PFLOP/s by the five and 1.55 by the seven, at the power limit.
+// execute seven.  24 packed sequences of 200 to 2000 rows, 32 heads: 963 to 982 us (a pass
+// over the rows 71, dK and dV 510, dQ 400).  8192 rows of one sequence: 1210 to 1240 us,
+// 1.1 PFLOP/s by the five and 1.55 by the seven, at the power limit.  D = 64: 730 and 915 us,
+// with the tensor pipe busy for 35 % and 34 to 38 % of the issue slots taken: a step waits
+// in turn for products and for the arithmetic that reads and writes their columns.
 //
 // Two kernels, one with the keys fixed (dK, dV) and one with the rows fixed (dQ), each
 // of which forms S and dP itself: seven products instead of five.  In exchange every

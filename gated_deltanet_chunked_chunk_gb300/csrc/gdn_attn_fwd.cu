@@ -4,9 +4,9 @@
 //   lse = (c m + log2 l) ln 2,  c = scale log2 e
 //
 // with m the running maximum of S.  Bound: the tensor cores, 4 D operations a (row,
-// key, head).  16384 rows of one sequence, 32 heads, D = 128: 1370 us, 1.61 PFLOP/s, 83 %
-// of a large library matrix product's rate.  24 sequences of 200 to 2000 rows: 324
-// us.  A pair of tiles takes some 3000 cycles for 128 keys, of which the products alone
+// key, head).  16384 rows of one sequence, 32 heads, D = 128: 1385 to 1405 us, 1.57
+// PFLOP/s, 81 % of a large library matrix product's rate; D = 64: 1048 us, 1.05 PFLOP/s (half
+// the products, all of the arithmetic).  24 sequences of 200 to 2000 rows: 331 us.  A pair of tiles takes some 3000 cycles for 128 keys, of which the products alone
 // are 2050; the rest is S's wait for the P V that reads the same columns.
 //
 // An item is two tiles of 128 rows of one head, which share the keys and values
@@ -82,7 +82,7 @@ __device__ __forceinline__ float factor(float c, float m) {
 
 // Half a row of O, times inv, to dst; flags: 1: it is a row of the sequence, 2: it saw a
 // key (if not, what O's columns hold is not used).  Eight columns at a time: more of them
-// cost the softmax registers (spills: 1429 instead of 1370 us at 16384 rows).
+// cost the softmax registers (spills: 60 us more at 16384 rows).
 template <int D> __device__ __forceinline__ void store_half(uint32_t O, uint16_t *dst, float inv, int flags) {
 #pragma unroll 1
   for (int i = 0; i < D / 2; i += 8) {

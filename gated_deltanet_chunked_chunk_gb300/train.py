@@ -64,7 +64,7 @@ def gdn_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seql
                       dev_status: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Softmax attention of packed sequences: see include/gdn.h.
 
-    q bf16 [Tq, HQ, D], k, v bf16 [Tk, HK, D] (any token stride that is a multiple of 8), HQ a multiple of HK, D 64 or
+    q bf16 [Tq, HQ, D], k, v bf16 [Tk, HK, D] (from 16-byte boundaries on, any token stride that is a multiple of 8), HQ a multiple of HK, D 64 or
     128; cu_seqlens int32 [N + 1] (None: one sequence), cu_seqlens_k the keys' offsets where they are others (then the
     last row of a sequence sees all of its keys under ``causal``).  Returns (o bf16 [Tq, HQ, D], lse fp32 [Tq, HQ])."""
     return (stack._c or stack._load()).attention_fwd(q, k, v, cu_seqlens, cu_seqlens_k, 1 if causal else 0,

@@ -78,7 +78,8 @@ int gdn_version(void);
  * gdn_testing_force_wait_expiry -- a testing hook for the failure path of the
  * bounded waits; the pages have no counterpart.  Never set it in production.
  * While `on` is nonzero (process-wide), the first bounded wait of every block
- * of the decode kernels (gdn_recurrent_decode, _bf16, _mtp) and of every
+ * of the decode kernels (gdn_recurrent_decode, _bf16, _mtp) and of the attention
+ * kernels on the tensor cores (gdn_kv8_attention, gdn_attention_fwd, _bwd), and of every
  * chain of the chunked forward waits on a barrier that nothing completes,
  * with a limit of a few thousand cycles, so it runs out every time.  The block
  * then takes the path a real expiry takes: it waits, with the normal limit,
@@ -738,18 +739,17 @@ int gdn_norm_gate_bwd8(const uint16_t *dy, const uint8_t *h_codes, const float *
  * is one that begins before the end of an earlier one.
  * What other sequences hold, NaN and infinities among it, does not reach a
  * sequence; one of its own keys or values that is not finite may reach all of its
- * rows.  D 64 or 128 (else GDN_EUNSUPPORTED, as for N or HQ > 65535); HQ % HK
- * == 0; q, k, v and o must start on a 16-byte boundary and strides be multiples
- * of 8 (else GDN_EINVAL).  Tq = 0 is a no-op.  One launch.
+ * rows (and a row of dout all of its keys).  D 64 or 128 (else GDN_EUNSUPPORTED, as
+ * for N or HQ > 65535); HQ % HK == 0; q, k, v and o must start on a 16-byte boundary
+ * and strides be multiples of 8 (else GDN_EINVAL).  Tq = 0 is a no-op.  One launch.
  */
 int gdn_attention_fwd(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
                       const int32_t *cu_seqlens, const int32_t *cu_seqlens_k, int N, int Tq, int Tk, int HQ, int HK, int D,
                       int causal, float scale, uint16_t *o, float *lse, int32_t *dev_status, void *stream);
 
 /*
- * gdn_attention_bwd_workspace_size -- bytes of device workspace gdn_attention_bwd needs;
- * as much or more than with any of the sizes smaller, so one workspace serves all
- * smaller calls too.
+ * gdn_attention_bwd_workspace_size -- bytes of device workspace gdn_attention_bwd needs:
+ * no less than with any of the sizes smaller, so one workspace serves all smaller calls.
  */
 size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, int D);
 
@@ -765,14 +765,14 @@ size_t gdn_attention_bwd_workspace_size(int N, int Tq, int Tk, int HQ, int HK, i
  * Everything else as in gdn_attention_fwd (where offsets decrease somewhere, the
  * gradients of the whole call are unspecified); rows and keys behind the last sequence
  * have zero gradients.  P is off by some 2^-23 |lse| of itself, as lse is one fp32
- * number: 2^-8, as by its rounding to bf16, at |lse| = 2^15, a factor of e
- * at 2^23, and from 2^30 on it may be infinite.  P and dS enter the products in bf16, sums are fp32 and have a
- * fixed order: two calls agree bit for bit (where the sums of dk and dv are cut depends
- * on the lengths of the whole batch, so in another batch their last bits can differ).  dout, o, dq, dk, dv must start on a
- * 16-byte boundary; GDN_EWORKSPACE for a small workspace, GDN_EUNSUPPORTED (and a
- * workspace size of 0) where min(T, T / 128 + N + 1) heads, of the rows or of the
- * keys, pass 2^31 - 1.  Three launches, four
- * where few keys are cut between more blocks.
+ * number: 2^-8, as by its rounding to bf16, at |lse| = 2^15, a factor of e at 2^23, and
+ * from 2^30 on it may be infinite.  P and dS enter the products in bf16, sums are fp32
+ * and have a fixed order: two calls agree bit for bit (where the sums of dk and dv are
+ * cut depends on the lengths of the whole batch, so in another batch their last bits can
+ * differ).  dout, o, dq, dk, dv must start on a 16-byte boundary; GDN_EWORKSPACE for a
+ * small workspace, GDN_EUNSUPPORTED (and a workspace size of 0) where the tiles of all
+ * heads, HQ min(Tq, Tq / 128 + N + 1) or the same of the keys, pass 2^31 - 1.  Three
+ * launches, four where few keys are cut between more blocks.
  */
 int gdn_attention_bwd(const uint16_t *dout, const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v,
                       int64_t ldv, const uint16_t *o, const float *lse, const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
